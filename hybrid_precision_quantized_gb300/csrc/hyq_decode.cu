@@ -32,7 +32,7 @@
 #include <cooperative_groups.h>
 #include <math.h>
 
-#include "hyq_common.cuh"
+#include "hyq_qtile.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -60,8 +60,6 @@ struct Dec : QFmt<BK, BV> {
 };
 constexpr int kPart = 2 + HYQ_D;                              // m, l, acc[128] per head
 constexpr int kMaxSplits = 1024;
-// log2(e) / sqrt(128): logits are kept in the base-2 domain.
-constexpr float kScale = 0.1275174307366466f;
 constexpr float kSubScale = 1.0f / HYQ_F16_SUB_SCALE;         // 2^-24
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -229,229 +227,6 @@ __device__ __forceinline__ void step_ticket_finish(int old, const StepArgs& sa, 
     wc[HYQ_CNT_RING_N] = min(rn + 1, sa.period);
   }
   sa.tickets_b[b] = 0;
-}
-
-// Online-softmax state of one warp for the two heads (2t, 2t+1) a thread owns.
-// Logits live in a scaled base-2 domain, lambda' = 2^sigma log2(e) q.k / sqrt(d)
-// with one sigma per query head (QConst), chosen so that the per-group query
-// sums fit the fp16 operand of the zero-point product; p = 2^((lambda' - m) 2^-sigma).
-struct State {
-  float m[2];       // running maximum (scaled domain)
-  float nm[2];      // -m 2^-sigma (0 while m = -inf)
-  float l[2];       // running sum of this thread's probabilities
-  float acc[8][4];  // PV accumulators in units of 2^-24
-  float zd[4];      // sum_j p_j z_jq: rows g < 4 = group g, columns heads 2t, 2t+1
-};
-
-// 2^x on the special-function unit, one instruction (relative error about
-// 2^-22; 2^-inf = 0, results below 2^-126 flush to 0).
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Online-softmax update of the two heads (2t, 2t+1) this thread owns with the
-// logits of tokens (g, g+8); returns the probabilities p[2r + j].  The
-// accumulators are rescaled only when some head's running max moved (the
-// factor is exactly 1 otherwise).
-// kLazy: first test (one warp vote) whether any logit of the tile exceeds its
-// head's running maximum; if none does, the maximum stays, the correction is
-// 1 and no cross-lane maximum is needed (the full path would give the same
-// bits).  It pays off on long per-warp runs of tiles (one block per
-// sequence and KV head), not on short ones, where early tiles move the maximum.
-template <bool kLazy>
-__device__ __forceinline__ void softmax_update(const float (&lg)[4], State& st, float (&p)[4],
-                                               const float (&inv)[2]) {
-  if (kLazy) {
-    bool above = false;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) above |= fmaxf(lg[j], lg[2 + j]) > st.m[j];
-    if (!__any_sync(0xffffffffu, above)) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        p[j] = ex2(fmaf(lg[j], inv[j], st.nm[j]));
-        p[2 + j] = ex2(fmaf(lg[2 + j], inv[j], st.nm[j]));
-        st.l[j] += p[j] + p[2 + j];
-      }
-      return;
-    }
-  }
-  float corr[2];
-  bool moved = false;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float tm = fmaxf(lg[j], lg[2 + j]);
-    tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
-    tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
-    tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-    const float mn = fmaxf(st.m[j], tm);
-    const float nm = (mn == -INFINITY) ? 0.f : -mn * inv[j];
-    moved |= mn != st.m[j];
-    corr[j] = ex2(fmaf(st.m[j], inv[j], nm));
-    p[j] = ex2(fmaf(lg[j], inv[j], nm));
-    p[2 + j] = ex2(fmaf(lg[2 + j], inv[j], nm));
-    st.l[j] = fmaf(st.l[j], corr[j], p[j] + p[2 + j]);
-    st.m[j] = mn;
-    st.nm[j] = nm;
-  }
-  if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        st.acc[mt][j] *= corr[j];
-        st.acc[mt][2 + j] *= corr[j];
-      }
-      st.zd[j] *= corr[j];
-    }
-  }
-}
-
-// Binary exponent e of a finite x > 0 with x = f 2^e, f in [0.5, 1)
-// (subnormals included), 2^k for k in [-126, 127], and the clamp to that range.
-__device__ __forceinline__ int exp_of(float x) {
-  const int b = __float_as_int(x) >> 23;
-  return b != 0 ? b - 126 : (__float_as_int(x * 16777216.f) >> 23) - 150;
-}
-__device__ __forceinline__ int clamp_exp(int k) { return min(max(k, -126), 127); }
-__device__ __forceinline__ float pow2i(int k) { return __int_as_float((clamp_exp(k) + 127) << 23); }
-__device__ __forceinline__ bool pos_finite(float x) { return x > 0.f && x <= 3.402823466e38f; }
-
-// Per-block constants of the quantised path.
-struct QConst {
-  float ksc[2][2];  // scaled-domain factor of the code products [token g (x1) | g+8 (x16 codes)][head 2t + j]
-  float inv[2];     // 2^-sigma of heads 2t, 2t+1
-  float kss[2];     // scaled-domain factor of the BF16 products 2^sigma log2(e) / sqrt(d), heads 2t, 2t+1
-  // B fragment of the zero-point product for head g: the scaled query sums
-  // 2^sigma log2(e)/sqrt(d) sum(q over group) of groups 2(t&1), 2(t&1)+1 as
-  // an fp16 pair, their high parts for t < 2 and the remainders for t >= 2
-  // (hi + lo carries 22 bits).
-  uint32_t bz;
-};
-
-// The two codes of bytes 1 and 3 of w as the low bytes of two 16-bit halves.
-__device__ __forceinline__ uint32_t odd_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341); }
-
-__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// `n` 32-bit words of a code region: word u of this lane at
-// 512 (u / 4) + 16 lane + 4 (u % 4).
-template <int n>
-__device__ __forceinline__ void load_words(const uint8_t* region, int lane, uint32_t (&w)[n]) {
-#pragma unroll
-  for (int i = 0; i < n / 4; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(region + 512 * i + 16 * lane);
-    w[4 * i] = v.x;
-    w[4 * i + 1] = v.y;
-    w[4 * i + 2] = v.z;
-    w[4 * i + 3] = v.w;
-  }
-}
-
-__device__ __forceinline__ uint32_t u4c(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
-// One 16-row quantised tile at `tb` (byte layout QFmt<BK, BV>), `vr` valid
-// rows.  The codes enter the fp16 MMAs as subnormals c * 2^-24.  4-bit: the
-// low nibble of a byte as c * 2^-24, the high nibble, masked in place, as
-// 16 c * 2^-24; in both code orders the high nibbles are exactly fragment
-// rows g+8 (K: tokens g+8; V: output rows g+8), so the factor 16 is a
-// per-row constant: folded into ksc[1] for K and into the epilogue for V.
-// 8-bit: bytes 0 and 2 of a word by one AND, bytes 1 and 3 by one byte
-// permute, each a fragment register of two codes.  bq holds the query as
-// fp16, scaled by 2^e.
-//   logit = sum_q s_q (q.c)_q  (per-group code products scaled in fp32)
-//         + sum_q z_q (sum q)_q (one MMA: the zero pairs against qc.bz)
-//   out  += sum_j (p_j s_jq) c_jd  (P^T scaled by the V scale pairs in fp16)
-//         + sum_j p_j z_jq          (one MMA: the V zero pairs against P^T)
-template <int BK, int BV, bool kLazy>
-__device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, const uint32_t (&bq)[8][2],
-                                       const QConst& qc, State& st) {
-  using F = QFmt<BK, BV>;
-  const int g = lane >> 2, t = lane & 3;
-  float C[4][4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) C[q][0] = C[q][1] = C[q][2] = C[q][3] = 0.f;
-  if (BK == 4) {
-    uint32_t kw[8];
-    load_words<8>(tb, lane, kw);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const uint32_t w = kw[ks], w8 = w >> 8;
-      mma_f16(C[ks >> 1], w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u, bq[ks][0],
-              bq[ks][1]);
-    }
-  } else {
-    uint32_t kw[16];  // k-step ks: word 2ks (token g), 2ks + 1 (token g + 8)
-    load_words<16>(tb, lane, kw);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const uint32_t w0 = kw[2 * ks], w1 = kw[2 * ks + 1];
-      mma_f16(C[ks >> 1], w0 & 0x00FF00FFu, w1 & 0x00FF00FFu, odd_bytes(w0), odd_bytes(w1), bq[ks][0], bq[ks][1]);
-    }
-  }
-  // K metadata of tokens g and g+8: four scales, then four zeros.
-  const uint4 ma = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
-  const uint4 mb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
-  const float2 a01 = half2_to_float2(ma.x), a23 = half2_to_float2(ma.y);
-  const float2 b01 = half2_to_float2(mb.x), b23 = half2_to_float2(mb.y);
-  float lg[4];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    lg[c] = qc.ksc[0][c] * fmaf(a01.x, C[0][c], fmaf(a01.y, C[1][c], fmaf(a23.x, C[2][c], a23.y * C[3][c])));
-    lg[2 + c] = qc.ksc[1][c] *
-                fmaf(b01.x, C[0][2 + c], fmaf(b01.y, C[1][2 + c], fmaf(b23.x, C[2][2 + c], b23.y * C[3][2 + c])));
-  }
-  // + sum_q z_q (scaled query sum)_q: the A fragment's k slots 2t, 2t+1 are
-  // groups 2(t&1), 2(t&1)+1 (high parts of the sums for t < 2, remainders
-  // for t >= 2), so a lane passes the zero pair of those groups.
-  mma_f16(lg, (t & 1) ? ma.w : ma.z, (t & 1) ? mb.w : mb.z, 0u, 0u, qc.bz, 0u);
-  // A vertical-line position (held in BF16 elsewhere) has NaN key steps in
-  // the stream: its logit is NaN, and the row is left out.
-#pragma unroll
-  for (int i = 0; i < 4; ++i) lg[i] = lg[i] != lg[i] ? -INFINITY : lg[i];
-  if (vr < 16) {
-    if (g >= vr) lg[0] = lg[1] = -INFINITY;
-    if (g + 8 >= vr) lg[2] = lg[3] = -INFINITY;
-  }
-  float p[4];
-  softmax_update<kLazy>(lg, st, p, qc.inv);
-  // P^T fragments in fp16: tokens (2t, 2t+1) and (2t+8, 2t+9) of head g.
-  const uint32_t pt0 = movmatrix_trans(pack_f16x2(p[0], p[1]));
-  const uint32_t pt1 = movmatrix_trans(pack_f16x2(p[2], p[3]));
-  const uint8_t* vm = tb + F::kVMeta;
-  // V scale pairs of tokens (2t, 2t+1) and (2t+8, 2t+9), groups 0..3.
-  const uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
-  const uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
-  // sum_j p_j z_jq on the tensor core: A rows = groups (g < 4), k = tokens.
-  uint32_t z0 = 0u, z1 = 0u;
-  if (g < 4) {
-    z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * g);
-    z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * g);
-  }
-  mma_f16(st.zd, z0, 0u, z1, 0u, pt0, pt1);
-  uint32_t vw[BV == 4 ? 8 : 16];
-  load_words<BV == 4 ? 8 : 16>(tb + F::kVCode, lane, vw);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    // B operand (tokens x heads) of group q: p * s in packed fp16.
-    const uint32_t b0 = hmul2_u32(pt0, u4c(sv0, q)), b1 = hmul2_u32(pt1, u4c(sv1, q));
-#pragma unroll
-    for (int mm = 0; mm < 2; ++mm) {  // m-tile 2q + mm lies in group q
-      if (BV == 4) {
-        const uint32_t x = vw[2 * q + mm], x8 = x >> 8;
-        mma_f16(st.acc[2 * q + mm], x & 0x000F000Fu, x & 0x00F000F0u, x8 & 0x000F000Fu, x8 & 0x00F000F0u, b0, b1);
-      } else {  // m-tile mt: words 2mt (fragment rows g) and 2mt + 1 (rows g + 8)
-        const uint32_t y0 = vw[2 * (2 * q + mm)], y1 = vw[2 * (2 * q + mm) + 1];
-        mma_f16(st.acc[2 * q + mm], y0 & 0x00FF00FFu, y1 & 0x00FF00FFu, odd_bytes(y0), odd_bytes(y1), b0, b1);
-      }
-    }
-  }
 }
 
 // 16 x a bf16 pair (exact: a power of two); the identity for 8-bit values,
@@ -753,85 +528,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(
       reinterpret_cast<uint4*>(smem + D::kRingBytes + fw * kFTileBytes + (lane >= 16 ? 16 * kFKStride : 0) +
                                rin * kFKStride)[lane & 15] = nrow;
   }
-  // One warp per query row (rows past g stay zero): the row's fp16 B
-  // fragments, scaled by an exact power of two 2^qe so that max |q| lies in
-  // [2^13, 2^14), stored in the order lane (g, t) reads them; and the row's
-  // constants: sigma (its largest scaled group sum 2^sigma log2(e)/sqrt(d)
-  // |sum q| below 2^13, and sigma <= 23 - exponent(max |q|), which bounds the
-  // scaled logits), the code-product factors and the zero-point fragments.
+  // One warp per query row (rows past g stay zero).
   if (warp < HYQ_MAX_GQA) {
-    const int r = warp;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (r < gq) {
-      const uint2 v = *reinterpret_cast<const uint2*>(q_s + r * HYQ_D + 4 * lane);
-      const float2 x01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-      const float2 x23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-      x[0] = x01.x, x[1] = x01.y, x[2] = x23.x, x[3] = x23.y;
-    }
-    float gs = (x[0] + x[1]) + (x[2] + x[3]);  // group lane / 8
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) gs += __shfl_xor_sync(0xffffffffu, gs, o);
-    float am = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    float gm = fabsf(gs * kScale);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-#pragma unroll
-    for (int o = 8; o < 32; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
-    const int qe = pos_finite(am) ? clamp_exp(14 - exp_of(am)) : 14;
-    const float gmb = fmaxf(gm, am * 0.0009765625f);  // 2^-10 max |q|
-    const int sg = pos_finite(gmb) ? clamp_exp(13 - exp_of(gmb)) : 13;
-    const float qscale = pow2i(qe);
-#pragma unroll
-    for (int hp = 0; hp < 2; ++hp) {
-      const int e = 4 * lane + 2 * hp;  // pair (e, e + 1) -> lane t, k-step ks, half hh
-      const int hh = (e >> 1) & 1;
-      const int tt = BK == 4 ? (e >> 3) & 3 : (e >> 2) & 3;
-      const int ks = BK == 4 ? 2 * (e >> 5) + ((e >> 2) & 1) : e >> 4;
-      bq_s[ks >> 1][r][tt][2 * (ks & 1) + hh] = pack_f16x2(x[2 * hp] * qscale, x[2 * hp + 1] * qscale);
-    }
-    const float kss = kScale * pow2i(sg);
-    const float s0 = __shfl_sync(0xffffffffu, gs, 0) * kss, s1 = __shfl_sync(0xffffffffu, gs, 8) * kss;
-    const float s2 = __shfl_sync(0xffffffffu, gs, 16) * kss, s3 = __shfl_sync(0xffffffffu, gs, 24) * kss;
-    if (lane < 4) {  // lane = t of the reading thread
-      const float y0 = (lane & 1) ? s2 : s0, y1 = (lane & 1) ? s3 : s1;
-      const float h0 = __half2float(__float2half_rn(y0)), h1 = __half2float(__float2half_rn(y1));
-      bz_s[r][lane] = lane < 2 ? pack_f16x2(h0, h1) : pack_f16x2(y0 - h0, y1 - h1);
-    }
-    if (lane == 0) {
-      const float k0 = kScale * pow2i(clamp_exp(24 - qe)) * pow2i(sg);
-      rowc_s[r][0] = k0;
-      rowc_s[r][1] = BK == 4 ? k0 * 0.0625f : k0;  // 4-bit tokens g+8 carry 16 c
-      rowc_s[r][2] = pow2i(-sg);
-      rowc_s[r][3] = kss;
-    }
+    uint2 v = make_uint2(0, 0);
+    if (warp < gq) v = *reinterpret_cast<const uint2*>(q_s + warp * HYQ_D + 4 * lane);
+    prep_query_row<BK>(warp, lane, v, bq_s, rowc_s, bz_s);
   }
   __syncthreads();
-  // B fragments of q in the permuted k order of the key codes: kstep ks
-  // covers elements e + {0,1} and e + {2,3}, e = 8(t + 4(ks/2)) + 4(ks%2)
-  // for 4-bit keys, e = 16 ks + 4t for 8-bit keys.
   uint32_t bq[8][2];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = *reinterpret_cast<const uint4*>(&bq_s[i][g][t][0]);
-    bq[2 * i][0] = v.x, bq[2 * i][1] = v.y, bq[2 * i + 1][0] = v.z, bq[2 * i + 1][1] = v.w;
-  }
   QConst qc;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    qc.ksc[0][j] = rowc_s[2 * t + j][0];
-    qc.ksc[1][j] = rowc_s[2 * t + j][1];
-    qc.inv[j] = rowc_s[2 * t + j][2];
-    qc.kss[j] = rowc_s[2 * t + j][3];
-  }
-  qc.bz = bz_s[g][t];
+  load_query_consts(g, t, bq_s, rowc_s, bz_s, bq, qc);
 
   State st;
-  st.m[0] = st.m[1] = -INFINITY;
-  st.nm[0] = st.nm[1] = 0.f;
-  st.l[0] = st.l[1] = 0.f;
-#pragma unroll
-  for (int mt = 0; mt < 8; ++mt) st.acc[mt][0] = st.acc[mt][1] = st.acc[mt][2] = st.acc[mt][3] = 0.f;
-  st.zd[0] = st.zd[1] = st.zd[2] = st.zd[3] = 0.f;
+  reset_state(st);
 
   // Next-layer L2 prefetch (hyq_decode_step_prefetch): issued by the last
   // warp once its own tiles are read (the next layout's counters, loaded at
@@ -898,37 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(
   if (pf_warp) issue_prefetch();
   // ---- warp partial -> this warp's own ring (every copy into it has been
   // consumed): acc[head][128] with the zero-point terms, (m, l) per head -----
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) st.l[j] += __shfl_xor_sync(0xffffffffu, st.l[j], o);
-  // sum_j p_j z_jq of heads 2t, 2t+1 sits in lane (q, t): gather all four groups.
-  float zt[4][2];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    zt[q][0] = __shfl_sync(0xffffffffu, st.zd[0], 4 * q + t);
-    zt[q][1] = __shfl_sync(0xffffffffu, st.zd[1], 4 * q + t);
-  }
-  // [8 heads][128] = 4 KB <= the ring; element d of head hd at hd*128 + (d ^ (hd/2)),
-  // so that the 32 lanes' stores of one accumulator fall in 32 banks.
-  float* wpart = reinterpret_cast<float*>(ring);
-  // Accumulator (m-tile u, ci) of thread (g, t): element 32(u/2) + 4g +
-  // 2(u%2) + (ci >> 1), head 2t + (ci & 1); with 4-bit values the rows
-  // ci >= 2 carry 16 c.
-#pragma unroll
-  for (int u = 0; u < 8; ++u)
-#pragma unroll
-    for (int ci = 0; ci < 4; ++ci) {
-      const int d = 32 * (u >> 1) + 4 * g + 2 * (u & 1) + (ci >> 1), hd = 2 * t + (ci & 1);
-      const float f = (BV == 4 && ci >= 2) ? HYQ_F16_SUB_SCALE / 16.f : HYQ_F16_SUB_SCALE;
-      wpart[hd * HYQ_D + (d ^ t)] = fmaf(st.acc[u][ci], f, zt[u >> 1][ci & 1]);
-    }
-  if (g == 0)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      red_m[warp][2 * t + j] = st.m[j] == -INFINITY ? -INFINITY : st.m[j] * qc.inv[j];  // back to log2 units
-      red_l[warp][2 * t + j] = st.l[j];
-    }
+  store_warp_partial<BV>(st, qc, g, t, reinterpret_cast<float*>(ring), red_m[warp], red_l[warp]);
   __syncthreads();
   // ---- block partial: thread i takes elements i, i + 512 (a warp shares one
   // head); the warps' weights 2^(m_w - M) come from lanes 0..15 by shuffle --
