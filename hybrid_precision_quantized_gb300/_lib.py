@@ -24,6 +24,7 @@ DEVERR_COUNT = 0x2
 DEVERR_INDEX = 0x4
 DEVERR_SCORE = 0x8
 DEVERR_TIMEOUT = 0x10
+DEVERR_PAGES = 0x20
 
 QBLOCK_ROWS = 64
 QBLOCK_BYTES = 10240          # B_K = B_V = 4
@@ -43,6 +44,14 @@ OP_SELECT, OP_DECODE, OP_PREFILL, OP_SELECT_MASS, OP_PREFILL_BAND = 1, 2, 3, 4, 
 PREFILL_INT8, PREFILL_FP8, PREFILL_FP4 = 1, 2, 3
 VL_PER_KV_HEAD, VL_PER_QUERY_HEAD = 0, 1
 
+# Paged cache (include/hyq.h)
+PAGE_ROWS = 64
+BOUND_BYTES = 272
+BOUND_EXP_MIN = -40
+PAGED_MAX_BATCH, PAGED_MAX_Q = 1024, 64
+PAGES_FIELDS = ("pool", "bounds", "table", "lens", "refs", "err")
+OP_PAGED_ATTENTION, OP_PAGED_SELECT, OP_PAGES_RESERVE, OP_PAGES_COMPACT = 16, 17, 18, 19
+
 # Every symbol include/hyq.h declares.
 SYMBOLS = ("hyq_status_string", "hyq_config_check", "hyq_vl_count", "hyq_layout_sizes",
            "hyq_workspace_size", "hyq_layout_reset", "hyq_quantize_append",
@@ -50,7 +59,10 @@ SYMBOLS = ("hyq_status_string", "hyq_config_check", "hyq_vl_count", "hyq_layout_
            "hyq_decode_attention_noalloc", "hyq_read_device_error", "hyq_set_decode_plan",
            "hyq_prefill_attention", "hyq_decode_step", "hyq_set_decode_overlap",
            "hyq_decode_step_prefetch", "hyq_age_tail", "hyq_select_vertical_mass",
-           "hyq_prefill_attention_band", "hyq_select_vertical_heads")
+           "hyq_prefill_attention_band", "hyq_select_vertical_heads", "hyq_pages_sizes",
+           "hyq_pages_workspace_size", "hyq_pages_reset", "hyq_pages_reserve", "hyq_pages_fork",
+           "hyq_pages_truncate", "hyq_pages_compact", "hyq_paged_append", "hyq_paged_attention",
+           "hyq_paged_select", "hyq_paged_attention_blocks")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -63,6 +75,11 @@ class HyqConfig(ctypes.Structure):
 
 class HyqLayout(ctypes.Structure):
     _fields_ = [(name, c_void_p) for name in LAYOUT_FIELDS]
+
+
+class HyqPages(ctypes.Structure):
+    _fields_ = ([(name, c_int32) for name in ("n_layers", "n_pages", "n_seqs", "max_blocks")]
+                + [(name, c_void_p) for name in PAGES_FIELDS])
 
 
 class HyqError(RuntimeError):
@@ -127,6 +144,20 @@ def load() -> ctypes.CDLL:
                                                  c_int32, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                                  c_void_p, c_size_t, c_void_p]),
     }
+    C, G, i32, i64, vp = P(HyqConfig), P(HyqPages), c_int32, ctypes.c_int64, c_void_p
+    sig.update({
+        "hyq_pages_sizes": (i32, [C, G, P(c_size_t)]),
+        "hyq_pages_workspace_size": (c_size_t, [C, G, ctypes.c_int, i32, i32]),
+        "hyq_pages_reset": (i32, [C, G, vp]),
+        "hyq_pages_reserve": (i32, [C, G, vp, i32, vp, vp, c_size_t, vp]),
+        "hyq_pages_fork": (i32, [C, G, vp, vp, i32, vp]),
+        "hyq_pages_truncate": (i32, [C, G, vp, vp, i32, vp]),
+        "hyq_pages_compact": (i32, [C, G, vp, vp, vp, c_size_t, vp]),
+        "hyq_paged_append": (i32, [C, G, i32, vp, i32, vp, i32, vp, vp, i64, vp, vp, vp]),
+        "hyq_paged_attention": (i32, [C, G, i32, vp, i32, i32, vp, i64, vp, vp, c_size_t, vp]),
+        "hyq_paged_select": (i32, [C, G, i32, vp, i32, i32, vp, i64, i32, i32, i32, vp, vp, c_size_t, vp]),
+        "hyq_paged_attention_blocks": (i32, [C, G, i32, vp, i32, i32, vp, i64, vp, i32, vp, vp, c_size_t, vp]),
+    })
     for name in SYMBOLS:
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = sig[name]
@@ -330,3 +361,69 @@ def hyq_read_device_error(err_dev, stream=None) -> int:
     if st not in (0, 6):
         raise HyqError("hyq_read_device_error", st)
     return host.value
+
+
+# --- paged cache: pointers, sizes and strides as given (PagedCache checks them) ---
+
+def hyq_pages_sizes(cfg: HyqConfig, pages: HyqPages) -> list[int]:
+    out = (c_size_t * len(PAGES_FIELDS))()
+    _check("hyq_pages_sizes", load().hyq_pages_sizes(ctypes.byref(cfg), ctypes.byref(pages), out))
+    return list(out)
+
+
+def hyq_pages_workspace_size(cfg: HyqConfig, pages: HyqPages, op: int, batch: int, n_q: int = 1) -> int:
+    return load().hyq_pages_workspace_size(ctypes.byref(cfg), ctypes.byref(pages), op, batch, n_q)
+
+
+def hyq_pages_reset(cfg, pages: HyqPages, stream=None):
+    _check("hyq_pages_reset", load().hyq_pages_reset(ctypes.byref(cfg), ctypes.byref(pages), stream_ptr(stream)))
+
+
+def hyq_pages_reserve(cfg, pages: HyqPages, seqs, batch: int, n_new, ws, stream=None):
+    _check("hyq_pages_reserve", load().hyq_pages_reserve(
+        ctypes.byref(cfg), ctypes.byref(pages), ptr(seqs), batch, ptr(n_new), ptr(ws), ws.nbytes,
+        stream_ptr(stream)))
+
+
+def hyq_pages_fork(cfg, pages: HyqPages, src, dst, n: int, stream=None):
+    _check("hyq_pages_fork", load().hyq_pages_fork(
+        ctypes.byref(cfg), ctypes.byref(pages), ptr(src), ptr(dst), n, stream_ptr(stream)))
+
+
+def hyq_pages_truncate(cfg, pages: HyqPages, seqs, new_lens, n: int, stream=None):
+    _check("hyq_pages_truncate", load().hyq_pages_truncate(
+        ctypes.byref(cfg), ctypes.byref(pages), ptr(seqs), ptr(new_lens), n, stream_ptr(stream)))
+
+
+def hyq_pages_compact(cfg, pages: HyqPages, table_out, refs_out, ws, stream=None):
+    _check("hyq_pages_compact", load().hyq_pages_compact(
+        ctypes.byref(cfg), ctypes.byref(pages), ptr(table_out), ptr(refs_out), ptr(ws), ws.nbytes,
+        stream_ptr(stream)))
+
+
+def hyq_paged_append(cfg, pages: HyqPages, layer: int, seqs, batch: int, cu_rows, n_rows: int, k_rows, v_rows,
+                     ld: int, k_hat=None, v_hat=None, stream=None):
+    _check("hyq_paged_append", load().hyq_paged_append(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, ptr(cu_rows), n_rows, ptr(k_rows),
+        ptr(v_rows), ld, ptr(k_hat), ptr(v_hat), stream_ptr(stream)))
+
+
+def hyq_paged_attention(cfg, pages: HyqPages, layer: int, seqs, batch: int, n_q: int, q, ldq: int, out, ws,
+                        stream=None):
+    _check("hyq_paged_attention", load().hyq_paged_attention(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(q), ldq, ptr(out), ptr(ws),
+        ws.nbytes, stream_ptr(stream)))
+
+
+def hyq_paged_select(cfg, pages: HyqPages, layer: int, seqs, batch: int, n_q: int, q, ldq: int, k: int,
+                     n_first: int, n_last: int, sel, ws, stream=None):
+    _check("hyq_paged_select", load().hyq_paged_select(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(q), ldq, k, n_first, n_last,
+        ptr(sel), ptr(ws), ws.nbytes, stream_ptr(stream)))
+
+
+def hyq_paged_attention_blocks(cfg, pages: HyqPages, layer: int, seqs, batch: int, n_q: int, q, ldq: int, sel,
+                               k: int, out, ws, stream=None):
+    _check("hyq_paged_attention_blocks", load().hyq_paged_attention_blocks(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(q), ldq, ptr(sel), k, ptr(out),
+        ptr(ws), ws.nbytes, stream_ptr(stream)))

@@ -1,0 +1,62 @@
+// Shared by the paged cache's kernels: the pool as the kernels see it, launch
+// declarations and the exponents of bounds and query codes.
+#pragma once
+
+#include "hyq_common.cuh"
+
+// Device view of one layer of a pool.
+struct PageView {
+  uint8_t* pool;    // [n_pages][HKV][block bytes]
+  uint8_t* bounds;  // [n_pages][HKV][HYQ_BOUND_BYTES]
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t* err;
+  int32_t n_pages, n_seqs, max_blocks;
+};
+
+inline PageView hyq_page_view(const hyq_config* c, const hyq_pages* p, int32_t layer) {
+  const size_t pages = (size_t)layer * p->n_pages * c->num_kv_heads;
+  return PageView{p->pool + pages * hyq_qblock_bytes(c), p->bounds + pages * HYQ_BOUND_BYTES,
+                  p->table, p->lens, p->err, p->n_pages, p->n_seqs, p->max_blocks};
+}
+
+inline size_t hyq_align256(size_t x) { return (x + 255) / 256 * 256; }
+
+size_t hyq_paged_attention_ws_bytes(const hyq_config* c, int32_t batch, int32_t n_q);
+cudaError_t hyq_launch_paged_attention(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
+                                       int32_t n_q, const void* q, int64_t ldq, const int32_t* sel, int32_t k_sel,
+                                       void* out, void* ws, cudaStream_t s);
+cudaError_t hyq_launch_paged_append(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
+                                    const int32_t* cu, int32_t n_rows, const void* k, const void* v, int64_t ld,
+                                    void* k_hat, void* v_hat, cudaStream_t s);
+size_t hyq_paged_select_ws_bytes(const hyq_config* c, const hyq_pages* p, int32_t batch, int32_t n_q);
+cudaError_t hyq_launch_paged_select(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
+                                    int32_t n_q, const void* q, int64_t ldq, int32_t k, int32_t n_first,
+                                    int32_t n_last, int32_t* sel, void* ws, cudaStream_t s);
+size_t hyq_pages_reserve_ws_bytes(const hyq_pages* p);
+cudaError_t hyq_launch_pages_reserve(const hyq_config* c, const hyq_pages* p, const int32_t* seqs, int32_t batch,
+                                     const int32_t* n_new, void* ws, cudaStream_t s);
+cudaError_t hyq_launch_pages_fork(const hyq_pages* p, const int32_t* src, const int32_t* dst, int32_t n,
+                                  cudaStream_t s);
+cudaError_t hyq_launch_pages_truncate(const hyq_pages* p, const int32_t* seqs, const int32_t* new_lens, int32_t n,
+                                      cudaStream_t s);
+size_t hyq_pages_compact_ws_bytes(const hyq_pages* p);
+cudaError_t hyq_launch_pages_compact(const hyq_config* c, const hyq_pages* p, int32_t* table_out, int32_t* refs_out,
+                                     void* ws, cudaStream_t s);
+
+// Sequence of call row i, or -1 when it is out of range.
+__device__ __forceinline__ int32_t page_seq(const int32_t* seqs, int32_t i, int32_t n_seqs) {
+  const int32_t s = seqs ? __ldg(seqs + i) : i;
+  return s >= 0 && s < n_seqs ? s : -1;
+}
+
+// Smallest integer e >= HYQ_BOUND_EXP_MIN with amax <= 127 * 2^e, for a
+// finite amax >= 0: with amax = m 2^x, m in [1/2, 1), that is x - 7, or
+// x - 6 when m > 127/128.
+__device__ __forceinline__ int bound_exp(float amax) {
+  if (!(amax > 0.f)) return HYQ_BOUND_EXP_MIN;
+  int x;
+  const float m = frexpf(amax, &x);
+  const int e = x - (m > 0.9921875f ? 6 : 7);
+  return e > HYQ_BOUND_EXP_MIN ? e : HYQ_BOUND_EXP_MIN;
+}

@@ -1,0 +1,243 @@
+"""A pool of quantised pages for many sequences (include/hyq.h, "Paged cache").
+
+PyTorch only allocates memory and provides the stream; every step runs in
+libhyq's kernels.  One step of a model with ``n_layers`` layers:
+
+    cache.reserve(seqs, n_new)                        # lengths, pages, copies on write
+    for layer in range(n_layers):
+        cache.append(layer, k, v, seqs=seqs, ...)     # this step's rows
+        cache.attention(layer, q, out, seqs=seqs)     # or select + attention_blocks
+
+``fork`` lets sequences share what they have in common, ``truncate`` shortens
+or frees them, ``compact`` moves the pages in use to the front of the pool.
+Nothing synchronises; errors that only the GPU can see collect in
+``cache.err()`` (hyq_read_device_error).
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib as L
+from ._lib import HyqConfig, HyqPages
+
+_DTYPES = {"pool": torch.uint8, "bounds": torch.uint8, "table": torch.int32, "lens": torch.int32,
+           "refs": torch.int32, "err": torch.int32}
+
+
+class PagedCache:
+    """The buffers of a pool and the calls on it.
+
+    cfg        : heads and code widths (make_config; batch and capacity are not used)
+    n_pages    : pages of 64 positions, each for every layer
+    n_seqs     : rows of the table
+    max_blocks : pages a sequence may have
+    buffers    : tensors to use instead of new ones, by name (pool, bounds, table, lens, refs, err), contiguous, of
+                 the C layout's types and sizes; those not given are allocated (and, without any, reset)
+
+    The workspaces belong to the object and grow with the largest call: calls of one kind that may overlap on the
+    GPU (other streams, graphs replayed at once) need a PagedCache of their own over the same buffers.  Call each kind once at its
+    largest size before capturing it into a CUDA graph, and keep to that size while the graph lives.
+    """
+
+    def __init__(self, cfg: HyqConfig, n_pages: int, n_seqs: int, max_blocks: int, n_layers: int = 1, device="cuda",
+                 buffers: dict | None = None):
+        self.cfg = cfg
+        self.n_pages, self.n_seqs, self.max_blocks, self.n_layers = n_pages, n_seqs, max_blocks, n_layers
+        self.c = HyqPages(n_layers=n_layers, n_pages=n_pages, n_seqs=n_seqs, max_blocks=max_blocks)
+        sizes = dict(zip(L.PAGES_FIELDS, L.hyq_pages_sizes(cfg, self.c)))
+        block = L.qblock_bytes(cfg.bits_k, cfg.bits_v)
+        shapes = {"pool": (n_layers, n_pages, cfg.num_kv_heads, block),
+                  "bounds": (n_layers, n_pages, cfg.num_kv_heads, L.BOUND_BYTES), "table": (n_seqs, max_blocks),
+                  "lens": (n_seqs,), "refs": (n_pages,), "err": (1,)}
+        given = buffers or {}
+        if set(given) - set(shapes):
+            raise ValueError(f"unknown buffers: {sorted(set(given) - set(shapes))}")
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.buf = {}
+        for name, shape in shapes.items():
+            t = given.get(name)
+            if t is None:
+                n = sizes[name] // _DTYPES[name].itemsize
+                make = torch.empty if name in ("pool", "bounds") else torch.zeros
+                t = make(n, dtype=_DTYPES[name], device=dev)
+                t = t[: int(torch.Size(shape).numel())].view(shape)
+            elif t.dtype != _DTYPES[name] or tuple(t.shape) != shape or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"{name}: expected a contiguous {_DTYPES[name]} tensor of shape {shape} on {dev}")
+            self.buf[name] = t
+            setattr(self.c, name, t.data_ptr())
+        self._ws, self._kept = {}, []
+
+    # typed views -----------------------------------------------------------
+    def pool(self) -> torch.Tensor:
+        """uint8 [n_layers, n_pages, HKV, block bytes]"""
+        return self.buf["pool"]
+
+    def bounds(self) -> torch.Tensor:
+        """uint8 [n_layers, n_pages, HKV, 272]"""
+        return self.buf["bounds"]
+
+    def table(self) -> torch.Tensor:
+        return self.buf["table"]
+
+    def lens(self) -> torch.Tensor:
+        return self.buf["lens"]
+
+    def refs(self) -> torch.Tensor:
+        return self.buf["refs"]
+
+    def err(self) -> torch.Tensor:
+        return self.buf["err"]
+
+    # argument checks ---------------------------------------------------------
+    def _stream(self, stream):
+        """The stream to launch on: the given one, or the current one of the cache's device."""
+        if stream is not None:
+            return stream
+        return torch.cuda.current_stream(self.device)
+
+    def _here(self):
+        """A context in which the cache's device is the current one."""
+        return torch.cuda.device(self.device)
+
+    def _ints(self, t, name, n=None):
+        """Entries of an int32 index tensor (None: n)."""
+        if t is None:
+            return n
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name}: expected a contiguous int32 vector on {self.device}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name}: expected {n} entries, got {t.shape[0]}")
+        return t.shape[0]
+
+    def _heads(self, t, name, heads):
+        """Elements between consecutive tokens of a bf16 [..., heads, 128] tensor whose tokens are evenly spaced and whose
+        heads are dense."""
+        if t.dtype != torch.bfloat16 or t.shape[-2:] != (heads, 128) or t.device != self.device:
+            raise ValueError(f"{name}: expected a bf16 [..., {heads}, 128] tensor on {self.device}")
+        if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != 128):
+            raise ValueError(f"{name}: the heads of a token must be dense")
+        ld = None
+        for i in range(t.dim() - 3, -1, -1):
+            if t.shape[i] == 1:
+                continue
+            if ld is None:
+                ld, step = t.stride(i), t.stride(i) * t.shape[i]
+            elif t.stride(i) != step:
+                raise ValueError(f"{name}: the tokens must be evenly spaced")
+            else:
+                step *= t.shape[i]
+        return heads * 128 if ld is None else ld
+
+    def _dense(self, t, name, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {self.device}")
+
+    def workspace(self, op: int, batch: int, n_q: int = 1, stream=None) -> torch.Tensor:
+        """The zero-filled workspace of an operation for calls of batch * n_q tokens, kept and grown as needed.  One that
+        has been outgrown stays allocated: work queued earlier may still use it."""
+        w = self._ws.get(op)
+        if w is None or w[0] < batch * n_q:
+            n = L.hyq_pages_workspace_size(self.cfg, self.c, op, batch, n_q)
+            if n == 0:
+                raise ValueError(f"no call of this kind takes {batch} sequences with {n_q} tokens")
+            with torch.cuda.stream(self._stream(stream)):
+                t = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self._kept.append(t)
+            w = self._ws[op] = (batch * n_q, t)
+        return w[1]
+
+    # tables ------------------------------------------------------------------
+    def reset(self, stream=None):
+        """Empty pool."""
+        with self._here():
+            L.hyq_pages_reset(self.cfg, self.c, self._stream(stream))
+
+    def reserve(self, seqs=None, n_new=None, stream=None):
+        """Room for n_new[i] (default 1) more positions of sequence seqs[i] (default: sequence i)."""
+        n = self._ints(seqs, "seqs", None)
+        n = self._ints(n_new, "n_new", n)
+        n = self.n_seqs if n is None else n
+        with self._here():
+            L.hyq_pages_reserve(self.cfg, self.c, seqs, n, n_new,
+                                self.workspace(L.OP_PAGES_RESERVE, 1, stream=stream), self._stream(stream))
+
+    def fork(self, src, dst, stream=None):
+        """Let the empty sequences dst begin as copies of src, sharing their pages."""
+        n = self._ints(dst, "dst", self._ints(src, "src"))
+        with self._here():
+            L.hyq_pages_fork(self.cfg, self.c, src, dst, n, self._stream(stream))
+
+    def truncate(self, seqs=None, new_lens=None, stream=None):
+        """Shorten the sequences to new_lens (default 0: free them)."""
+        n = self._ints(seqs, "seqs", None)
+        n = self._ints(new_lens, "new_lens", n)
+        n = self.n_seqs if n is None else n
+        with self._here():
+            L.hyq_pages_truncate(self.cfg, self.c, seqs, new_lens, n, self._stream(stream))
+
+    def compact(self, table_out=None, refs_out=None, stream=None):
+        """Move the pages in use to the front of the pool; the new table and refs go to the given tensors, or in place."""
+        if table_out is not None:
+            self._dense(table_out, "table_out", torch.int32, (self.n_seqs, self.max_blocks))
+        if refs_out is not None:
+            self._dense(refs_out, "refs_out", torch.int32, (self.n_pages,))
+        with self._here():
+            L.hyq_pages_compact(self.cfg, self.c, table_out, refs_out,
+                                self.workspace(L.OP_PAGES_COMPACT, 1, stream=stream), self._stream(stream))
+
+    # one layer -----------------------------------------------------------------
+    def append(self, layer: int, k, v, seqs=None, cu_rows=None, k_hat=None, v_hat=None, stream=None):
+        """Quantise rows k, v [rows, HKV, 128] into the last positions of their sequences: one row per sequence, or rows
+        cu_rows[i] .. cu_rows[i + 1] for sequence seqs[i].  k_hat, v_hat: bf16 tensors for the rows as they are held."""
+        hkv = self.cfg.num_kv_heads
+        rows = k.shape[0]
+        if k.dim() != 3 or v.shape != k.shape:
+            raise ValueError("k and v: expected [rows, HKV, 128] each")
+        ld = self._heads(k, "k", hkv)
+        if self._heads(v, "v", hkv) != ld:
+            raise ValueError("k and v must share the spacing of their rows")
+        if cu_rows is None:
+            n = self._ints(seqs, "seqs", rows)
+        else:
+            n = self._ints(cu_rows, "cu_rows") - 1
+            self._ints(seqs, "seqs", n)
+        for t, name in ((k_hat, "k_hat"), (v_hat, "v_hat")):
+            if t is not None:
+                self._dense(t, name, torch.bfloat16, (rows, hkv, 128))
+        with self._here():
+            L.hyq_paged_append(self.cfg, self.c, layer, seqs, n, cu_rows, rows, k, v, ld, k_hat, v_hat,
+                               self._stream(stream))
+
+    def _query(self, q, seqs):
+        if q.dim() != 4:
+            raise ValueError("q: expected [sequences, tokens, HQ, 128]")
+        self._ints(seqs, "seqs", q.shape[0])
+        return q.shape[0], q.shape[1], self._heads(q, "q", self.cfg.num_q_heads)
+
+    def attention(self, layer: int, q, out, seqs=None, stream=None):
+        """Causal attention of the last n_q tokens of every sequence: q, out bf16 [sequences, n_q, HQ, 128]."""
+        b, n_q, ldq = self._query(q, seqs)
+        self._dense(out, "out", torch.bfloat16, tuple(q.shape))
+        with self._here():
+            L.hyq_paged_attention(self.cfg, self.c, layer, seqs, b, n_q, q, ldq, out,
+                                  self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream=stream), self._stream(stream))
+
+    def select(self, layer: int, q, sel, seqs=None, n_first: int = 1, n_last: int = 1, stream=None):
+        """The blocks worth reading for every token and KV head: sel int32 [sequences, n_q, HKV, k]."""
+        b, n_q, ldq = self._query(q, seqs)
+        self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, sel.shape[-1]))
+        with self._here():
+            L.hyq_paged_select(self.cfg, self.c, layer, seqs, b, n_q, q, ldq, sel.shape[-1], n_first, n_last, sel,
+                               self.workspace(L.OP_PAGED_SELECT, b, n_q, stream=stream), self._stream(stream))
+
+    def attention_blocks(self, layer: int, q, sel, out, seqs=None, stream=None):
+        """attention over the blocks that sel lists for each token and KV head."""
+        b, n_q, ldq = self._query(q, seqs)
+        self._dense(out, "out", torch.bfloat16, tuple(q.shape))
+        self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, sel.shape[-1]))
+        with self._here():
+            L.hyq_paged_attention_blocks(self.cfg, self.c, layer, seqs, b, n_q, q, ldq, sel, sel.shape[-1], out,
+                                         self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream=stream), self._stream(stream))

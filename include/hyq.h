@@ -56,6 +56,7 @@ typedef enum {
 #define HYQ_DEVERR_COUNT 0x2       /* a device-side count exceeded the layout capacity */
 #define HYQ_DEVERR_INDEX 0x4       /* an index list was not strictly ascending in range */
 #define HYQ_DEVERR_SCORE 0x8       /* a selection score was NaN */
+#define HYQ_DEVERR_PAGES 0x20      /* no free page left, or a sequence past its table row */
 #define HYQ_DEVERR_TIMEOUT 0x10    /* a bounded wait inside a kernel gave up (a bulk copy or a
                                       tensor-core commit did not complete); the kernel stopped
                                       issuing work, drained what it had in flight and returned */
@@ -530,6 +531,241 @@ hyq_status hyq_set_decode_plan(int32_t merge, int32_t splits);
 #define HYQ_NOALLOC_SCRATCH_BYTES (4u << 20)
 hyq_status hyq_decode_attention_noalloc(const hyq_config *cfg, const void *q, const hyq_layout *lay,
                                         void *out, int32_t len_hint, hyq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache: one pool of pages for many sequences of unlike lengths.
+ *
+ * A page holds HYQ_PAGE_ROWS = 64 consecutive positions of one sequence for
+ * every KV head of every layer, all of it quantised (no BF16 rows): per KV
+ * head one 64-row block of the quantised stream format above (row r of the
+ * page = row r of the block, codes c, value c s + z).  A sequence s owns row s
+ * of the table: its position p lies in page table[s][p / 64], row p % 64.
+ * Pages may be shared between sequences (hyq_pages_fork); refs counts the
+ * table rows that hold a page, and a page with refs = 0 is free.
+ *
+ * One step of a model: hyq_pages_reserve once (new lengths, new pages, copies
+ * of shared pages about to be written), then per layer hyq_paged_append with
+ * the rows of the new positions and hyq_paged_attention (or
+ * hyq_paged_select and hyq_paged_attention_blocks).
+ *
+ * Per (layer, page, KV head) a bound record of HYQ_BOUND_BYTES describes the
+ * keys that hyq_paged_append wrote, for hyq_paged_select:
+ *   [0, 128)    int8 lo_d = floor(min_j k_jd 2^-e)
+ *   [128, 256)  int8 hi_d = ceil(max_j k_jd 2^-e)
+ *   [256, 260)  int32 e = the smallest integer >= HYQ_BOUND_EXP_MIN with
+ *               max |k_jd| <= 127 2^e
+ *   [260, 272)  unused
+ * over the BF16 key rows j written to the page since its row 0 was last
+ * written (a group that raised HYQ_DEVERR_QUANT_RANGE counts as zeros).  A
+ * truncated sequence's dropped rows stay in the bounds of its last page:
+ * they remain bounds.  Rounding outward by powers of two commutes with taking
+ * more rows in, so the record does not depend on how the rows were divided
+ * into calls.
+ *
+ * Only num_q_heads, num_kv_heads, head_dim, group, bits_k and bits_v of
+ * hyq_config are used by these entry points (the config must pass
+ * hyq_config_check); every call gives its own number of sequences, at most
+ * HYQ_PAGED_MAX_BATCH.  The pool and the tables need no initial contents
+ * beyond hyq_pages_reset; whatever a page's unwritten rows hold, they do not
+ * reach a result.
+ *
+ * Calls that read (attention, select) or append may run while others of the
+ * same kind do, on other layers or sequences; the calls that change the
+ * tables (hyq_pages_*) must be ordered with every call on the same pool.  A
+ * sequence may be listed only once in a call that writes (append, reserve,
+ * truncate, the destinations of a fork).
+ * ------------------------------------------------------------------------ */
+#define HYQ_PAGE_ROWS 64
+#define HYQ_BOUND_BYTES 272
+#define HYQ_BOUND_EXP_MIN (-40)
+#define HYQ_PAGED_MAX_BATCH 1024
+#define HYQ_PAGED_MAX_Q 64
+#define HYQ_PAGED_MAX_PAGES (1 << 20)  /* pages of a pool (67 million positions a layer) */
+#define HYQ_PAGED_MAX_BLOCKS (1 << 22) /* pages of one sequence */
+
+/* A pool and its tables.  Sizes in bytes come from hyq_pages_sizes(); all
+ * pointers are device pointers, 256-byte aligned.
+ *   pool    [n_layers][n_pages][HKV][HYQ_QBLOCK_BYTES_BITS(B_K, B_V)]
+ *   bounds  [n_layers][n_pages][HKV][HYQ_BOUND_BYTES]
+ *   table   int32 [n_seqs][max_blocks]; entries past a sequence's length are not read
+ *   lens    int32 [n_seqs]  positions of each sequence
+ *   refs    int32 [n_pages]
+ *   err     int32 [1]       device error word
+ */
+typedef struct {
+  int32_t n_layers;
+  int32_t n_pages;
+  int32_t n_seqs;
+  int32_t max_blocks;
+  uint8_t *pool;
+  uint8_t *bounds;
+  int32_t *table;
+  int32_t *lens;
+  int32_t *refs;
+  int32_t *err;
+} hyq_pages;
+
+#define HYQ_PAGES_FIELDS 6 /* pool bounds table lens refs err */
+
+#define HYQ_OP_PAGED_ATTENTION 16 /* also hyq_paged_attention_blocks */
+#define HYQ_OP_PAGED_SELECT 17
+#define HYQ_OP_PAGES_RESERVE 18
+#define HYQ_OP_PAGES_COMPACT 19
+
+/* Bytes of each buffer, in the order of HYQ_PAGES_FIELDS (out[HYQ_PAGES_FIELDS],
+ * host), from the four sizes of `pages` (its pointers are not looked at). */
+hyq_status hyq_pages_sizes(const hyq_config *cfg, const hyq_pages *pages, size_t *out);
+
+/* Workspace bytes of an operation (HYQ_OP_PAGED_* / HYQ_OP_PAGES_*) for calls
+ * of at most `batch` sequences with n_q query tokens each (n_q is used by
+ * attention and select alone); 0 on invalid sizes.  A workspace must be zero-filled before its
+ * first use and is left ready for the next call; calls of any smaller size
+ * may share it, one at a time. */
+size_t hyq_pages_workspace_size(const hyq_config *cfg, const hyq_pages *pages, int op, int32_t batch,
+                                int32_t n_q);
+
+/* Empty pool: lens, refs and err become 0. */
+hyq_status hyq_pages_reset(const hyq_config *cfg, const hyq_pages *pages, hyq_stream_t stream);
+
+/*
+ * Make room for new positions.  For the sequences seqs[i], i < batch, as if
+ * one after another: n = n_new[i] positions are added behind the lens[s]
+ * present ones; the pages that they need are taken from the free ones, the
+ * lowest first; if the first new position falls into a page that is partly
+ * filled and held by another sequence too (refs > 1), the sequence gets a
+ * copy of that page (first in the order of its new pages) and leaves the shared one: per layer
+ * and KV head the 16-row tiles that hold rows, and the bound record, are copied.
+ * lens[s] += n.
+ *   seqs   device int32 [batch], distinct, or NULL (sequence i)
+ *   n_new  device int32 [batch], >= 0, or NULL (1 each)
+ * All or nothing: if the free pages do not suffice or a sequence would pass
+ * max_blocks pages (HYQ_DEVERR_PAGES), or a sequence number is out of range
+ * or listed twice, or an n_new is negative (HYQ_DEVERR_INDEX), nothing is
+ * changed but the error word.
+ * Workspace: HYQ_OP_PAGES_RESERVE.  Two launches.
+ */
+hyq_status hyq_pages_reserve(const hyq_config *cfg, const hyq_pages *pages, const int32_t *seqs, int32_t batch,
+                             const int32_t *n_new, void *ws, size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * Let the empty sequences dst[i] begin as copies of src[i], i < n: the table
+ * entries and the length are copied and each page's refs goes up; no page is
+ * copied (hyq_pages_reserve does so when one is written).  One source may
+ * appear any number of times.
+ * A pair whose numbers are out of range, whose dst is not empty (lens != 0),
+ * appears twice (the later ones) or also as a source, is left out and sets
+ * HYQ_DEVERR_INDEX.
+ *   src, dst  device int32 [n], n <= HYQ_PAGED_MAX_BATCH
+ */
+hyq_status hyq_pages_fork(const hyq_config *cfg, const hyq_pages *pages, const int32_t *src, const int32_t *dst,
+                          int32_t n, hyq_stream_t stream);
+
+/*
+ * Shorten sequences: seqs[i] keeps its first new_lens[i] positions (0 with
+ * new_lens = NULL: the sequence is freed); each page that it no longer
+ * reaches loses one of its refs.  A sequence number out of range or listed
+ * before, or a new length that is negative or above the present one, is left
+ * out and sets HYQ_DEVERR_INDEX.
+ *   seqs      device int32 [n] or NULL (sequence i)
+ *   new_lens  device int32 [n] or NULL (0 each)
+ */
+hyq_status hyq_pages_truncate(const hyq_config *cfg, const hyq_pages *pages, const int32_t *seqs,
+                              const int32_t *new_lens, int32_t n, hyq_stream_t stream);
+
+/*
+ * Move the pages in use to the front of the pool.  With N the number of
+ * pages with refs > 0, the r-th of them at or past N (ascending) moves to the
+ * r-th free page below N, in every layer, with its bound records; the table
+ * and the refs that describe the moved pool are written to
+ *   table_out  device int32 [n_seqs][max_blocks] or NULL (in place)
+ *   refs_out   device int32 [n_pages] or NULL (in place)
+ * (entries past a sequence's length are copied as they are).  The page
+ * contents at and past N stay as they were: until they are written again the
+ * pool serves the old table as well as the new one.
+ * Workspace: HYQ_OP_PAGES_COMPACT.  Two launches.
+ */
+hyq_status hyq_pages_compact(const hyq_config *cfg, const hyq_pages *pages, int32_t *table_out, int32_t *refs_out,
+                             void *ws, size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * Quantise new key and value rows (as hyq_quantize_append does) into the last
+ * positions of their sequences, and bring the bound records up to date.  Call
+ * row i (i < batch) is sequence seqs[i] with n_i = cu_rows[i + 1] - cu_rows[i]
+ * rows, rows cu_rows[i] .. of k_rows and v_rows, which become its positions
+ * lens - n_i .. lens - 1 (after hyq_pages_reserve).
+ *   seqs     device int32 [batch], distinct, or NULL (sequence i)
+ *   cu_rows  device int32 [batch + 1], ascending from 0 to n_rows, or NULL:
+ *            one row each (n_rows = batch)
+ *   n_rows   host, the total number of rows
+ *   k_rows, v_rows  device bf16: row r, KV head h, element d at
+ *            r ld + 128 h + d; ld >= 128 HKV, a multiple of 8
+ *   k_hat, v_hat    device bf16 [n_rows][HKV][128] or NULL (both or none):
+ *            the rows as the cache now holds them, c s + z rounded to BF16
+ * A sequence that is out of range, that has fewer than n_i positions, or whose
+ * table leaves the pool is left out and sets HYQ_DEVERR_INDEX; a pair of
+ * cu_rows that descends or leaves [0, n_rows] likewise.  Pages that other
+ * sequences share are written too: reserve first.  Other rows of the pages keep their bits.
+ */
+hyq_status hyq_paged_append(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
+                            int32_t batch, const int32_t *cu_rows, int32_t n_rows, const void *k_rows,
+                            const void *v_rows, int64_t ld, void *k_hat, void *v_hat, hyq_stream_t stream);
+
+/*
+ * Attention of the last n_q positions of every sequence over the sequence,
+ * causal: query token i < n_q of call row b stands at position
+ * lens - n_q + i of sequence seqs[b] and sees the positions up to its own
+ * (already appended).  out = softmax(q K^T / sqrt(128)) V over the
+ * dequantised rows; a token at a negative position sees nothing and gives
+ * zeros.  n_q = 1 is decoding, a few are drafted tokens or the end of a prompt.
+ *   seqs  device int32 [batch] or NULL (sequence i); may repeat
+ *   q     device bf16: token (b, i), head h, element d at
+ *         (b n_q + i) ldq + 128 h + d; ldq >= 128 HQ, a multiple of 8
+ *   out   device bf16 [batch][n_q][HQ][128]
+ * A sequence out of range or a table entry outside the pool sets
+ * HYQ_DEVERR_INDEX and counts as nothing to see.
+ * The sequences' tiles are shared out evenly over the GPU whatever their
+ * lengths are; partial results of a sequence that several blocks share are
+ * joined in a fixed order by the last of them, so results do not vary from run to run.
+ * Workspace: HYQ_OP_PAGED_ATTENTION, zero-filled before first use.
+ */
+hyq_status hyq_paged_attention(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
+                               int32_t batch, int32_t n_q, const void *q, int64_t ldq, void *out, void *ws,
+                               size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * Choose, for every query token and KV head, the blocks (pages of its
+ * sequence) worth reading, from the bound records alone.  With c the codes of
+ * the token's g queries, c = rint(q 2^-e'), e' the smallest integer >=
+ * HYQ_BOUND_EXP_MIN with max |q| <= 127 2^e' over the g heads, block j scores
+ *   S(j) = 2^e_j sum_heads sum_d max(c_d lo_jd, c_d hi_jd),
+ * up to a factor an upper bound of the summed logits of any of its rows
+ * (Algorithm 1's score, bounded per block).  The sum is an integer below 2^24,
+ * so S is exact.  Of the nb = ceil(visible / 64) blocks that the token sees,
+ * the first n_first and the last n_last are taken, then those of largest S,
+ * ties to the lower block, min(nb, k) in all.
+ *   seqs, q, ldq, n_q  as for hyq_paged_attention
+ *   k      1 .. HYQ_PAGED_MAX_BLOCKS, n_first + n_last <= k
+ *   sel    device int32 [batch][n_q][HKV][k]: block numbers, ascending, then -1
+ * A query that is not finite counts as zeros and sets HYQ_DEVERR_SCORE.
+ * Workspace: HYQ_OP_PAGED_SELECT, zero-filled before first use.
+ */
+hyq_status hyq_paged_select(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
+                            int32_t batch, int32_t n_q, const void *q, int64_t ldq, int32_t k, int32_t n_first,
+                            int32_t n_last, int32_t *sel, void *ws, size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * hyq_paged_attention over listed blocks alone: query token (b, i) and KV
+ * head h see the positions of the blocks sel[b][i][h][0..k) that
+ * hyq_paged_attention would let them see.  Arguments as there, and
+ *   sel  device int32 [batch][n_q][HKV][k], block numbers ascending, -1 from
+ *        the first unused entry on (e.g. from hyq_paged_select)
+ * A list that is not ascending or leaves the sequence sets HYQ_DEVERR_INDEX
+ * (that token's output is then unspecified).
+ */
+hyq_status hyq_paged_attention_blocks(const hyq_config *cfg, const hyq_pages *pages, int32_t layer,
+                                      const int32_t *seqs, int32_t batch, int32_t n_q, const void *q, int64_t ldq,
+                                      const int32_t *sel, int32_t k, void *out, void *ws, size_t ws_bytes,
+                                      hyq_stream_t stream);
 
 /*
  * Copy a device error word to the host (synchronises `stream`).
