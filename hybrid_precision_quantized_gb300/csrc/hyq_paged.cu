@@ -12,14 +12,18 @@
 // for 4-bit codes, against 4 * 128 * g flops: HBM, then instruction issue.
 //
 // Work split: a group is one (sequence, KV head, tile of up to 8 query rows)
-// and has ceil(len / 16) tiles of 16 rows.  The T tiles of all groups, laid
-// end to end, are cut into equal runs, one per block (two blocks an SM), so
-// that unlike lengths and single long sequences use the GPU alike and the
-// launch does not depend on the lengths (they live on the device; a captured
-// call stays valid as they grow).  A group inside one run is finished by its
-// block; one that several runs share is joined from their partials
-// (maximum, sum, accumulator) in run order by the last block to finish, an
-// atomic ticket that nobody waits for.
+// and has ceil(len / rows of a unit) units, a unit being what a warp copies
+// and multiplies in one go.  The units of all groups, laid end to end, are cut
+// into equal runs, one per block (two blocks an SM), so that unlike lengths
+// and single long sequences use the GPU alike and the launch does not depend
+// on the lengths (they live on the device; a captured call stays valid as
+// they grow).  In the line each group begins with kGroupCost units that are
+// not there, about what preparing its queries and joining its warps takes:
+// without them a block that meets many short groups finishes last (16
+// sequences, one of them a single token: 126 us instead of 181 us x 0.73).
+// A group inside one run is finished by its block; one that several runs share
+// is joined from their partials (maximum, sum, accumulator) in run order by
+// the last block to finish, an atomic ticket that nobody waits for.
 #include "hyq_paged.cuh"
 #include "hyq_qtile.cuh"
 
@@ -29,15 +33,21 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowsQ = HYQ_MAX_GQA;    // query rows per tile (MMA N)
 constexpr int kPart = 2 + HYQ_D;       // m, l, acc[128] per query row
-constexpr int kMinTiles = kWarps;      // tiles per block before work is split further
+constexpr int kGroupCost = 16;         // units that a group's fixed work is worth
+constexpr int kMinUnits = 32;          // units per block before a group is split further
 constexpr int kBlocksPerSm = 2;
 constexpr int kMaxGrid = 1024;         // two blocks on each of up to 512 SMs
 
-// Per-warp ring of tiles (bulk copies), as many as two blocks an SM allow.
+// A warp's units and its ring of bulk copies, as much as two blocks an SM
+// allow: units of two adjacent tiles for 4-bit codes.
 template <int BK, int BV>
 struct Ring : QFmt<BK, BV> {
-  static constexpr int kSlots = BK + BV == 8 ? 4 : BK + BV == 12 ? 3 : 2;
-  static constexpr int kWarpBytes = kSlots * QFmt<BK, BV>::kTile;
+  static constexpr int kTiles = BK + BV == 8 ? 2 : 1;  // tiles per unit
+  static constexpr int kSlots = BK + BV == 12 ? 3 : 2;
+  static constexpr int kUnit = kTiles * QFmt<BK, BV>::kTile;
+  static constexpr int kRows = 16 * kTiles;
+  static constexpr int kPerPage = HYQ_PAGE_ROWS / kRows;
+  static constexpr int kWarpBytes = kSlots * kUnit;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
   static_assert(kWarpBytes >= HYQ_MAX_GQA * HYQ_D * 4, "a warp's partial fits its ring");
 };
@@ -54,7 +64,7 @@ struct Params {
   int32_t batch, n_q, HQ, HKV, gq, QT, k_sel;
 };
 
-// Length of call row b (0 for a sequence out of range) and its tiles per group.
+// Length of call row b, 0 for a sequence out of range.
 __device__ __forceinline__ int row_len(const Params& p, int b, int* seq) {
   const int s = page_seq(p.seqs, b, p.pv.n_seqs);
   *seq = s;
@@ -63,17 +73,30 @@ __device__ __forceinline__ int row_len(const Params& p, int b, int* seq) {
   const int n = p.pv.lens[s];
   return n < 0 ? 0 : (int64_t)n > cap ? (int)cap : n;
 }
-__device__ __forceinline__ int row_tiles(const Params& p, int len) {
-  if (!p.sel) return (len + 15) >> 4;
-  return 4 * min(p.k_sel, (len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS);
+
+// a / b for 0 <= a, 0 < b: 32-bit arithmetic whenever both fit.
+__device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+  return a / b;
 }
+
+// T units over nb blocks: the first `more` blocks take `each` + 1 tiles, the others `each`.
+struct Shares {
+  int64_t each, more;
+  __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + min(c, more); }
+  __device__ __forceinline__ int owner(int64_t x) const {  // of unit x
+    const int64_t wide = more * (each + 1);
+    return (int)(x < wide ? div_fast(x, each + 1) : more + div_fast(x - wide, each));
+  }
+};
 
 template <int BK, int BV>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Params p) {
   using R = Ring<BK, BV>;
-  constexpr int kSlots = R::kSlots, kTile = R::kTile;
+  constexpr int kSlots = R::kSlots;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];  // tiles per (KV head, query tile) of the rows before b
+  __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];  // units per (KV head, query tile) of the rows before b
+  __shared__ int s_len[HYQ_PAGED_MAX_BATCH], s_seq[HYQ_PAGED_MAX_BATCH];
   __shared__ int64_t s_warp[kWarps];
   __shared__ __align__(16) uint32_t bq_s[4][kRowsQ][4][4];
   __shared__ float rowc_s[kRowsQ][4];
@@ -90,17 +113,28 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
   if (lane < kSlots) mbar_init(&wb[lane], 1);
   mbar_fence_init();
 
-  // ---- the rows' tiles, summed up: a block of 4 rows per thread -------------
+  // Units of a group of row b: its own and those of the fixed work; 0 when
+  // there is nothing to read.
+  auto units_of = [&](int len) {
+    int n = (len + R::kRows - 1) / R::kRows;
+    if (p.sel) n = R::kPerPage * min(p.k_sel, (len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS);
+    return n == 0 ? 0 : n + kGroupCost;
+  };
+  // ---- the rows' units, summed up: a block of 4 rows per thread --------------
   const int unit = p.HKV * p.QT;
   {
     int64_t w[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int b = 4 * tid + i;
-      int seq;
+      int seq = -1;
       const int len = b < p.batch ? row_len(p, b, &seq) : 0;
-      if (b < p.batch && seq < 0 && blockIdx.x == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-      w[i] = row_tiles(p, len);
+      if (b < p.batch) {
+        s_len[b] = len;
+        s_seq[b] = seq;
+        if (seq < 0 && blockIdx.x == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+      }
+      w[i] = units_of(len);
       sum += w[i];
       // a row without positions: its outputs are zero
       if (b < p.batch && w[i] == 0 && b % gridDim.x == blockIdx.x) {
@@ -126,16 +160,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
     if (tid == kThreads - 1 && p.batch == HYQ_PAGED_MAX_BATCH) s_cum[HYQ_PAGED_MAX_BATCH] = at;
   }
   __syncthreads();
+  // ---- this block's run -------------------------------------------------------
+  // With fewer groups than blocks every group gets the same number of blocks
+  // (equal lengths are then cut at the groups' borders), and no more than give
+  // each kMinUnits.
   const int64_t T = s_cum[p.batch] * unit;
-  const int64_t nb = min((int64_t)gridDim.x, max((int64_t)1, T / kMinTiles));  // blocks that take part
+  int64_t nb = gridDim.x;
+  {
+    const int64_t groups = (int64_t)p.batch * unit;
+    if (groups < nb) nb = groups * max((int64_t)1, min(div_fast(nb, groups), div_fast(T, groups * kMinUnits)));
+    nb = max((int64_t)1, min(nb, T));
+  }
   if ((int64_t)blockIdx.x >= nb) return;
-  int64_t pos = T * blockIdx.x / nb;
-  const int64_t end = T * (blockIdx.x + 1) / nb;
+  Shares sh;
+  sh.each = div_fast(T, nb);
+  sh.more = T - sh.each * nb;
+  int64_t pos = sh.begin(blockIdx.x);
+  const int64_t end = sh.begin(blockIdx.x + 1);
 
-  // Lane i < kSlots fills slot i of the warp's ring (copies that one thread
-  // issues complete one after another).  cur: position of its slot's tile,
-  // whether it was copied, and the parity to wait for.
-  uint32_t parity = 0, cur = 0;
+  uint32_t done = 0;  // units that this warp's ring has seen: slot done % kSlots, parity (done / kSlots) & 1
   bool dead = false;
 
   while (pos < end) {
@@ -147,26 +190,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
       else hi = m;
     }
     const int b = lo;
-    const int W = (int)(s_cum[b + 1] - s_cum[b]);
-    const int64_t off = pos - s_cum[b] * unit;
-    const int grp = (int)(off / W), w0 = (int)(off - (int64_t)grp * W);
-    const int w1 = (int)min((int64_t)W, w0 + (end - pos));
+    const int64_t cum = s_cum[b];
+    const int W = (int)(s_cum[b + 1] - cum);  // with the fixed work's units
+    const int64_t off = pos - cum * unit;
+    const int grp = (int)div_fast(off, W), x0 = (int)(off - (int64_t)grp * W);
+    const int x1 = (int)min((int64_t)W, x0 + (end - pos));
+    pos += x1 - x0;
+    const int n_units = W - kGroupCost, w0 = max(0, x0 - kGroupCost), w1 = x1 - kGroupCost;
+    if (w1 <= w0) continue;  // only units of the fixed work: another block's group
     const int h = grp / p.QT, qt = grp - h * p.QT;
-    int seq;
-    const int len = row_len(p, b, &seq);
+    const int seq = s_seq[b], len = s_len[b];
     const int32_t* table = p.pv.table + (size_t)seq * p.pv.max_blocks;
     const int32_t* sel = p.sel ? p.sel + (((size_t)b * p.n_q + qt) * p.HKV + h) * p.k_sel : nullptr;
     const int n_rows = p.sel ? p.gq : min(kRowsQ, p.n_q * p.gq - kRowsQ * qt);
-    const uint8_t* heads = p.pv.pool + (size_t)h * R::kBlock;  // this head's block of page 0
     const size_t page_bytes = (size_t)p.HKV * R::kBlock;
 
-    // ---- this warp's tiles: w0 + warp, + 8, ... ---------------------------
+    // ---- this warp's units: w0 + warp, + 8, ... ---------------------------
+    // kPerPage divides 8, so all of them take the same part of their pages.
     const int nj = w1 - w0 > warp ? (w1 - w0 - warp + kWarps - 1) / kWarps : 0;
-    // Entry of the block list that tile j lies in (dense: the block itself);
-    // -1 for one that must not be read.
+    const int part = (w0 + warp) % R::kPerPage, x_first = (w0 + warp) / R::kPerPage;
+    const uint8_t* heads = p.pv.pool + (size_t)h * R::kBlock + part * R::kUnit;
+    // Block of the sequence that unit j lies in, or -1 for one that must not
+    // be read.
     auto entry = [&](int j) -> int {
       if (j >= nj) return -1;
-      const int x = (w0 + warp + kWarps * j) >> 2;
+      const int x = x_first + j * (kWarps / R::kPerPage);
       if (!sel) return x;
       const int e = __ldg(sel + x), pe = x > 0 ? __ldg(sel + x - 1) : -1;
       if (e < 0) return -1;
@@ -176,36 +224,44 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
       }
       return e;
     };
-    auto page_of = [&](int e) -> int { return e >= 0 ? __ldg(table + e) : -1; };
-    // Lane pipeline: page of its next tile, list entry of the one after.
-    int e1 = -1, e2 = -1, pg1 = -1;
-    auto issue = [&](int j) {  // lane j % kSlots
-      const int x = (w0 + warp + kWarps * j) & 3;
-      const int at = e1 * HYQ_PAGE_ROWS + 16 * x;
-      bool ok = e1 >= 0 && at < len;
-      if (ok && (pg1 < 0 || pg1 >= p.pv.n_pages)) {
-        hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-        ok = false;
-      }
-      if (ok) {
-        uint64_t* bar = &wb[j % kSlots];
-        mbar_arrive_expect_tx(bar, kTile);
-        bulk_g2s(ring + (j % kSlots) * kTile, heads + (size_t)pg1 * page_bytes + x * kTile, kTile, bar);
-        cur = ((uint32_t)at << 2) | 2u | parity;
-        parity ^= 1u;
-      } else {
-        cur = 0;
-      }
-      e1 = e2;
-      pg1 = page_of(e1);
-      e2 = entry(j + 2 * kSlots);
+    auto page_of = [&](int e) -> int {
+      if (e < 0) return -1;
+      const int page = __ldg(table + e);
+      return page;
     };
-    if (lane < kSlots && !dead) {
-      e1 = entry(lane);
-      pg1 = page_of(e1);
-      e2 = entry(lane + kSlots);
-      if (lane < nj) issue(lane);
-    }
+    // Lane l holds block and page of unit 32 r + l of the present round r of 32
+    // units, and of the next one; the pages arrive while the round is worked off.
+    int e_cur = entry(lane), pg_cur = page_of(e_cur);
+    int e_nxt = entry(32 + lane), pg_nxt = page_of(e_nxt);
+    // Position of unit j's first row (of a unit that is there), else -1; issues its copy.
+    auto issue = [&](int j) -> int {
+      const int e = __shfl_sync(0xffffffffu, e_cur, j & 31), pg = __shfl_sync(0xffffffffu, pg_cur, j & 31);
+      const int at = e * HYQ_PAGE_ROWS + part * R::kRows;
+      const bool in = (uint32_t)pg < (uint32_t)p.pv.n_pages, ok = e >= 0 && at < len && in;
+      const uint32_t n = done + (uint32_t)j;
+      const int slot = n % kSlots;
+      if (lane == slot) {  // copies that one thread issues complete one after another
+        uint64_t* bar = &wb[slot];
+        if (ok) {
+          const uint32_t bytes = R::kTiles == 1 || at + 16 < len ? R::kUnit : R::kTile;
+          mbar_arrive_expect_tx(bar, bytes);
+          bulk_g2s(ring + slot * R::kUnit, heads + (size_t)pg * page_bytes, bytes, bar);
+        } else {
+          mbar_arrive_expect_tx(bar, 0);
+          if (e >= 0 && !in) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+        }
+      }
+      if ((j & 31) == 31) {
+        e_cur = e_nxt;
+        pg_cur = pg_nxt;
+        e_nxt = entry(j + 33 + lane);
+        pg_nxt = page_of(e_nxt);
+      }
+      return ok ? at : -1;
+    };
+    int at_slot[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) at_slot[j] = j < nj && !dead ? issue(j) : -1;
 
     // ---- the query rows: warp r prepares row r ----------------------------
     {
@@ -223,48 +279,54 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
     uint32_t bq[8][2];
     QConst qc;
     load_query_consts(g, t, bq_s, rowc_s, bz_s, bq, qc);
-    const int lim0 = lim_s[2 * t], lim1 = lim_s[2 * t + 1];
     const int minlim = lim_s[0];  // the rows' tokens ascend
     State st;
     reset_state(st);
 
     for (int j = 0; j < nj && !dead; ++j) {
-      const int slot = j % kSlots;
-      const uint32_t c = __shfl_sync(0xffffffffu, cur, slot);
-      if (c & 2u) {
-        const bool ok = mbar_wait(&wb[slot], c & 1u);
-        if (__any_sync(0xffffffffu, !ok)) {
-          // A copy did not arrive: flag it, let this warp's other copies land
-          // before shared memory is used for anything else, and stop.
-          if (lane == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
-          if (lane < kSlots && (cur & 2u)) (void)mbar_wait(&wb[lane], cur & 1u);
-          __syncwarp();
-          dead = true;
-          break;
+      const uint32_t n = done + (uint32_t)j;
+      const int slot = n % kSlots;
+      const bool ok = mbar_wait(&wb[slot], (n / kSlots) & 1u);
+      if (__any_sync(0xffffffffu, !ok)) {
+        // A copy did not arrive: flag it, let this warp's other copies land
+        // before shared memory is used for anything else, and stop.
+        if (lane == 0) {
+          hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
+          for (int k = j; k < nj && k < j + kSlots; ++k)
+            (void)mbar_wait(&wb[(done + k) % kSlots], ((done + k) / kSlots) & 1u);
         }
-        const int at = (int)(c >> 2);
-        const uint8_t* tb = ring + slot * kTile;
-        if (at + 16 <= minlim)
-          q_tile<BK, BV, true>(tb, lane, 16, bq, qc, st);
-        else
-          q_tile<BK, BV, true, true>(tb, lane, len - at, bq, qc, st, lim0 - at, lim1 - at);
         __syncwarp();
+        dead = true;
+        break;
       }
-      if (lane == slot) {
-        if (j + kSlots < nj) {
-          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-          issue(j + kSlots);
+      const int at = at_slot[0];
+      const uint8_t* tb = ring + slot * R::kUnit;
+      if (at >= 0) {
+        if (at + R::kRows <= minlim) {
+          q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st);
         } else {
-          cur = 0;
+          const int lim0 = lim_s[2 * t], lim1 = lim_s[2 * t + 1];
+          for (int x = 0; x < R::kTiles && at + 16 * x < len; ++x) {
+            const int a = at + 16 * x;
+            q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, len - a, bq, qc, st, lim0 - a, lim1 - a);
+          }
         }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k + 1 < kSlots; ++k) at_slot[k] = at_slot[k + 1];
+      if (j + kSlots < nj) {
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        at_slot[kSlots - 1] = issue(j + kSlots);
       }
     }
+    done += nj;
 
     // ---- the block's partial ------------------------------------------------
     __syncwarp();
     store_warp_partial<BV>(st, qc, g, t, reinterpret_cast<float*>(ring), red_m[warp], red_l[warp]);
     __syncthreads();
-    const bool whole = w0 == 0 && w1 == W;
+    const bool whole = w0 == 0 && w1 == n_units;
     float* pp = p.part + ((size_t)blockIdx.x * 2 + (w0 == 0 ? 1 : 0)) * (kRowsQ * kPart);
     auto out_at = [&](int r) {
       const int flat = kRowsQ * qt + r;
@@ -300,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
     }
     __syncthreads();  // the rings are free again
     if (!whole) {
-      // blocks that share this group: those holding its first and last tile
-      const int64_t base = s_cum[b] * unit + (int64_t)grp * W;
-      const int c0 = (int)(((base + 1) * nb - 1) / T), c1 = (int)(((base + W) * nb - 1) / T);
+      // blocks that share this group: those holding its first and last unit
+      const int64_t base = cum * unit + (int64_t)grp * W + kGroupCost;
+      const int c0 = sh.owner(base), c1 = sh.owner(base + n_units - 1);
       const size_t gi = ((size_t)b * p.HKV + h) * p.QT + qt;
       if (tid == 0) {
         int old;
@@ -312,22 +374,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
       }
       __syncthreads();
       if (s_last) {
-        // part of block c: slot 1 when its run begins the group (c == c0 and
-        // the run starts at or before it), else slot 0
         float* wts = reinterpret_cast<float*>(smem);  // [8][n] weights
         const int n = c1 - c0 + 1;
-        auto part_of = [&](int c) {
-          const bool first = T * c / nb <= base;
-          return p.part + ((size_t)c * 2 + (first ? 1 : 0)) * (kRowsQ * kPart);
-        };
+        // part i: slot 0 of block c0 + i, where its run ends this group; the
+        // first block's is slot 1 when its run holds the group's first unit
+        const float* parts = p.part + (size_t)c0 * 2 * (kRowsQ * kPart);
+        const int first = sh.begin(c0) <= base ? kRowsQ * kPart : 0;
+        auto part_of = [&](int i) { return parts + (size_t)i * (2 * kRowsQ * kPart) + (i == 0 ? first : 0); };
         if (warp < n_rows) {
           float M = -INFINITY;
-          for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(part_of(c0 + c) + warp * kPart));
+          for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(part_of(c) + warp * kPart));
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
           float L = 0.f;
           for (int c = lane; c < n; c += 32) {
-            const float* e = part_of(c0 + c) + warp * kPart;
+            const float* e = part_of(c) + warp * kPart;
             const float m = __ldcg(e), wt = m == -INFINITY ? 0.f : ex2(m - M);
             wts[warp * n + c] = wt;
             L = fmaf(__ldcg(e + 1), wt, L);
@@ -340,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
         for (int i = tid; i < n_rows * HYQ_D; i += kThreads) {
           const int r = i >> 7, d = i & (HYQ_D - 1);
           float a = 0.f;
-#pragma unroll 8
-          for (int c = 0; c < n; ++c) a = fmaf(__ldcg(part_of(c0 + c) + r * kPart + 2 + d), wts[r * n + c], a);
+#pragma unroll 16
+          for (int c = 0; c < n; ++c) a = fmaf(__ldcg(part_of(c) + r * kPart + 2 + d), wts[r * n + c], a);
           const float L = s_sum[r];
           out_at(r)[d] = __float2bfloat16_rn(L > 0.f ? a / L : 0.f);
         }
@@ -350,7 +411,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
     }
     // order this block's generic accesses to the rings before the next copies
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-    pos += w1 - w0;
   }
 }
 

@@ -254,6 +254,118 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   }
 }
 
+// q_tile for NT adjacent tiles, every row seen by every query row and no row
+// left out by NaN steps: the tiles' independent chains overlap, and the
+// running maximum is tested once for all of them.
+template <int BK, int BV, int NT>
+__device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint32_t (&bq)[8][2], const QConst& qc,
+                                        State& st) {
+  using F = QFmt<BK, BV>;
+  const int g = lane >> 2, t = lane & 3;
+  float lg[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint8_t* tb = tb0 + n * F::kTile;
+    float C[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) C[q][0] = C[q][1] = C[q][2] = C[q][3] = 0.f;
+    if (BK == 4) {
+      uint32_t kw[8];
+      load_words<8>(tb, lane, kw);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t w = kw[ks], w8 = w >> 8;
+        mma_f16(C[ks >> 1], w & 0x000F000Fu, w & 0x00F000F0u, w8 & 0x000F000Fu, w8 & 0x00F000F0u, bq[ks][0],
+                bq[ks][1]);
+      }
+    } else {
+      uint32_t kw[16];
+      load_words<16>(tb, lane, kw);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const uint32_t w0 = kw[2 * ks], w1 = kw[2 * ks + 1];
+        mma_f16(C[ks >> 1], w0 & 0x00FF00FFu, w1 & 0x00FF00FFu, odd_bytes(w0), odd_bytes(w1), bq[ks][0], bq[ks][1]);
+      }
+    }
+    const uint4 ma = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
+    const uint4 mb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
+    const float2 a01 = half2_to_float2(ma.x), a23 = half2_to_float2(ma.y);
+    const float2 b01 = half2_to_float2(mb.x), b23 = half2_to_float2(mb.y);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      lg[n][c] =
+          qc.ksc[0][c] * fmaf(a01.x, C[0][c], fmaf(a01.y, C[1][c], fmaf(a23.x, C[2][c], a23.y * C[3][c])));
+      lg[n][2 + c] = qc.ksc[1][c] * fmaf(b01.x, C[0][2 + c],
+                                         fmaf(b01.y, C[1][2 + c], fmaf(b23.x, C[2][2 + c], b23.y * C[3][2 + c])));
+    }
+    mma_f16(lg[n], (t & 1) ? ma.w : ma.z, (t & 1) ? mb.w : mb.z, 0u, 0u, qc.bz, 0u);
+  }
+  // ---- running maximum ------------------------------------------------------
+  float tm[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    tm[j] = fmaxf(lg[0][j], lg[0][2 + j]);
+#pragma unroll
+    for (int n = 1; n < NT; ++n) tm[j] = fmaxf(tm[j], fmaxf(lg[n][j], lg[n][2 + j]));
+  }
+  if (__any_sync(0xffffffffu, tm[0] > st.m[0] || tm[1] > st.m[1])) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 4));
+      tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 8));
+      tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 16));
+      const float mn = fmaxf(st.m[j], tm[j]);
+      const float nm = mn == -INFINITY ? 0.f : -mn * qc.inv[j];
+      const float corr = ex2(fmaf(st.m[j], qc.inv[j], nm));
+      st.m[j] = mn;
+      st.nm[j] = nm;
+      st.l[j] *= corr;
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        st.acc[mt][j] *= corr;
+        st.acc[mt][2 + j] *= corr;
+      }
+      st.zd[j] *= corr;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const uint8_t* tb = tb0 + n * F::kTile;
+    float p[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      p[j] = ex2(fmaf(lg[n][j], qc.inv[j], st.nm[j]));
+      p[2 + j] = ex2(fmaf(lg[n][2 + j], qc.inv[j], st.nm[j]));
+      st.l[j] += p[j] + p[2 + j];
+    }
+    const uint32_t pt0 = movmatrix_trans(pack_f16x2(p[0], p[1]));
+    const uint32_t pt1 = movmatrix_trans(pack_f16x2(p[2], p[3]));
+    const uint8_t* vm = tb + F::kVMeta;
+    const uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
+    const uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
+    // rows g < 4 carry the zeros of group g; rows 4 .. 7 repeat them and are not used
+    const uint32_t z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * (g & 3));
+    const uint32_t z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * (g & 3));
+    mma_f16(st.zd, z0, 0u, z1, 0u, pt0, pt1);
+    uint32_t vw[BV == 4 ? 8 : 16];
+    load_words<BV == 4 ? 8 : 16>(tb + F::kVCode, lane, vw);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t b0 = hmul2_u32(pt0, u4c(sv0, q)), b1 = hmul2_u32(pt1, u4c(sv1, q));
+#pragma unroll
+      for (int mm = 0; mm < 2; ++mm) {
+        if (BV == 4) {
+          const uint32_t x = vw[2 * q + mm], x8 = x >> 8;
+          mma_f16(st.acc[2 * q + mm], x & 0x000F000Fu, x & 0x00F000F0u, x8 & 0x000F000Fu, x8 & 0x00F000F0u, b0, b1);
+        } else {
+          const uint32_t y0 = vw[2 * (2 * q + mm)], y1 = vw[2 * (2 * q + mm) + 1];
+          mma_f16(st.acc[2 * q + mm], y0 & 0x00FF00FFu, y1 & 0x00FF00FFu, odd_bytes(y0), odd_bytes(y1), b0, b1);
+        }
+      }
+    }
+  }
+}
+
 // A query row's operands: its fp16 B fragments (bq_s), scaled by an exact
 // power of two 2^qe so that max |q| lies in [2^13, 2^14), stored in the order
 // lane (g, t) reads them; and its constants: sigma (its largest scaled group

@@ -15,6 +15,8 @@ Nothing synchronises; errors that only the GPU can see collect in
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib as L
@@ -69,6 +71,8 @@ class PagedCache:
             self.buf[name] = t
             setattr(self.c, name, t.data_ptr())
         self._ws, self._kept = {}, []
+        self._lib, self._index = L.load(), dev.index
+        self._cfg, self._pages = ctypes.byref(cfg), ctypes.byref(self.c)
 
     # typed views -----------------------------------------------------------
     def pool(self) -> torch.Tensor:
@@ -92,15 +96,20 @@ class PagedCache:
         return self.buf["err"]
 
     # argument checks ---------------------------------------------------------
-    def _stream(self, stream):
-        """The stream to launch on: the given one, or the current one of the cache's device."""
-        if stream is not None:
-            return stream
-        return torch.cuda.current_stream(self.device)
-
-    def _here(self):
-        """A context in which the cache's device is the current one."""
-        return torch.cuda.device(self.device)
+    # A decode step makes these calls for every layer, a few microseconds apart:
+    # the common forms (contiguous tensors, the cache's device being the
+    # current one) are tested first and cost well under a microsecond each.
+    def _run(self, name, args, stream):
+        """Call the C entry point on the given stream, or the current one of the cache's device."""
+        fn = getattr(self._lib, name)
+        raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
+        if torch.cuda.current_device() == self._index:
+            st = fn(self._cfg, self._pages, *args, raw)
+        else:
+            with torch.cuda.device(self.device):
+                st = fn(self._cfg, self._pages, *args, raw)
+        if st:
+            raise L.HyqError(name, st)
 
     def _ints(self, t, name, n=None):
         """Entries of an int32 index tensor (None: n)."""
@@ -108,42 +117,48 @@ class PagedCache:
             return n
         if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != self.device:
             raise ValueError(f"{name}: expected a contiguous int32 vector on {self.device}")
-        if n is not None and t.shape[0] != n:
-            raise ValueError(f"{name}: expected {n} entries, got {t.shape[0]}")
-        return t.shape[0]
+        m = t.shape[0]
+        if n is not None and m != n:
+            raise ValueError(f"{name}: expected {n} entries, got {m}")
+        return m
 
     def _heads(self, t, name, heads):
         """Elements between consecutive tokens of a bf16 [..., heads, 128] tensor whose tokens are evenly spaced and whose
         heads are dense."""
-        if t.dtype != torch.bfloat16 or t.shape[-2:] != (heads, 128) or t.device != self.device:
+        shape = t.shape
+        if t.dtype != torch.bfloat16 or shape[-1] != 128 or shape[-2] != heads or t.device != self.device:
             raise ValueError(f"{name}: expected a bf16 [..., {heads}, 128] tensor on {self.device}")
-        if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != 128):
+        if t.is_contiguous():
+            return heads * 128
+        strides = t.stride()
+        if strides[-1] != 1 or (heads > 1 and strides[-2] != 128):
             raise ValueError(f"{name}: the heads of a token must be dense")
         ld = None
         for i in range(t.dim() - 3, -1, -1):
-            if t.shape[i] == 1:
+            if shape[i] == 1:
                 continue
             if ld is None:
-                ld, step = t.stride(i), t.stride(i) * t.shape[i]
-            elif t.stride(i) != step:
+                ld, step = strides[i], strides[i] * shape[i]
+            elif strides[i] != step:
                 raise ValueError(f"{name}: the tokens must be evenly spaced")
             else:
-                step *= t.shape[i]
+                step *= shape[i]
         return heads * 128 if ld is None else ld
 
     def _dense(self, t, name, dtype, shape):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
-            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {self.device}")
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}")
+        return t.data_ptr()
 
     def workspace(self, op: int, batch: int, n_q: int = 1, stream=None) -> torch.Tensor:
         """The zero-filled workspace of an operation for calls of batch * n_q tokens, kept and grown as needed.  One that
         has been outgrown stays allocated: work queued earlier may still use it."""
         w = self._ws.get(op)
         if w is None or w[0] < batch * n_q:
-            n = L.hyq_pages_workspace_size(self.cfg, self.c, op, batch, n_q)
+            n = L.hyq_pages_workspace_size(self.cfg, self.c, op, max(batch, 1), n_q)
             if n == 0:
                 raise ValueError(f"no call of this kind takes {batch} sequences with {n_q} tokens")
-            with torch.cuda.stream(self._stream(stream)):
+            with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 t = torch.zeros(n, dtype=torch.uint8, device=self.device)
             self._kept.append(t)
             w = self._ws[op] = (batch * n_q, t)
@@ -152,50 +167,43 @@ class PagedCache:
     # tables ------------------------------------------------------------------
     def reset(self, stream=None):
         """Empty pool."""
-        with self._here():
-            L.hyq_pages_reset(self.cfg, self.c, self._stream(stream))
+        self._run("hyq_pages_reset", (), stream)
 
     def reserve(self, seqs=None, n_new=None, stream=None):
         """Room for n_new[i] (default 1) more positions of sequence seqs[i] (default: sequence i)."""
-        n = self._ints(seqs, "seqs", None)
-        n = self._ints(n_new, "n_new", n)
-        n = self.n_seqs if n is None else n
-        with self._here():
-            L.hyq_pages_reserve(self.cfg, self.c, seqs, n, n_new,
-                                self.workspace(L.OP_PAGES_RESERVE, 1, stream=stream), self._stream(stream))
+        n = self._ints(n_new, "n_new", self._ints(seqs, "seqs"))
+        ws = self.workspace(L.OP_PAGES_RESERVE, 1, stream=stream)
+        self._run("hyq_pages_reserve", (L.ptr(seqs), self.n_seqs if n is None else n, L.ptr(n_new), ws.data_ptr(),
+                                        ws.nbytes), stream)
 
     def fork(self, src, dst, stream=None):
         """Let the empty sequences dst begin as copies of src, sharing their pages."""
         n = self._ints(dst, "dst", self._ints(src, "src"))
-        with self._here():
-            L.hyq_pages_fork(self.cfg, self.c, src, dst, n, self._stream(stream))
+        self._run("hyq_pages_fork", (src.data_ptr(), dst.data_ptr(), n), stream)
 
     def truncate(self, seqs=None, new_lens=None, stream=None):
         """Shorten the sequences to new_lens (default 0: free them)."""
-        n = self._ints(seqs, "seqs", None)
-        n = self._ints(new_lens, "new_lens", n)
-        n = self.n_seqs if n is None else n
-        with self._here():
-            L.hyq_pages_truncate(self.cfg, self.c, seqs, new_lens, n, self._stream(stream))
+        n = self._ints(new_lens, "new_lens", self._ints(seqs, "seqs"))
+        self._run("hyq_pages_truncate", (L.ptr(seqs), L.ptr(new_lens), self.n_seqs if n is None else n), stream)
 
     def compact(self, table_out=None, refs_out=None, stream=None):
         """Move the pages in use to the front of the pool; the new table and refs go to the given tensors, or in place."""
+        table = refs = None
         if table_out is not None:
-            self._dense(table_out, "table_out", torch.int32, (self.n_seqs, self.max_blocks))
+            table = self._dense(table_out, "table_out", torch.int32, (self.n_seqs, self.max_blocks))
         if refs_out is not None:
-            self._dense(refs_out, "refs_out", torch.int32, (self.n_pages,))
-        with self._here():
-            L.hyq_pages_compact(self.cfg, self.c, table_out, refs_out,
-                                self.workspace(L.OP_PAGES_COMPACT, 1, stream=stream), self._stream(stream))
+            refs = self._dense(refs_out, "refs_out", torch.int32, (self.n_pages,))
+        ws = self.workspace(L.OP_PAGES_COMPACT, 1, stream=stream)
+        self._run("hyq_pages_compact", (table, refs, ws.data_ptr(), ws.nbytes), stream)
 
     # one layer -----------------------------------------------------------------
     def append(self, layer: int, k, v, seqs=None, cu_rows=None, k_hat=None, v_hat=None, stream=None):
         """Quantise rows k, v [rows, HKV, 128] into the last positions of their sequences: one row per sequence, or rows
         cu_rows[i] .. cu_rows[i + 1] for sequence seqs[i].  k_hat, v_hat: bf16 tensors for the rows as they are held."""
         hkv = self.cfg.num_kv_heads
-        rows = k.shape[0]
         if k.dim() != 3 or v.shape != k.shape:
             raise ValueError("k and v: expected [rows, HKV, 128] each")
+        rows = k.shape[0]
         ld = self._heads(k, "k", hkv)
         if self._heads(v, "v", hkv) != ld:
             raise ValueError("k and v must share the spacing of their rows")
@@ -204,40 +212,45 @@ class PagedCache:
         else:
             n = self._ints(cu_rows, "cu_rows") - 1
             self._ints(seqs, "seqs", n)
-        for t, name in ((k_hat, "k_hat"), (v_hat, "v_hat")):
-            if t is not None:
-                self._dense(t, name, torch.bfloat16, (rows, hkv, 128))
-        with self._here():
-            L.hyq_paged_append(self.cfg, self.c, layer, seqs, n, cu_rows, rows, k, v, ld, k_hat, v_hat,
-                               self._stream(stream))
+        kh = vh = None
+        if k_hat is not None:
+            kh = self._dense(k_hat, "k_hat", torch.bfloat16, k.shape)
+        if v_hat is not None:
+            vh = self._dense(v_hat, "v_hat", torch.bfloat16, k.shape)
+        self._run("hyq_paged_append", (layer, L.ptr(seqs), n, L.ptr(cu_rows), rows, k.data_ptr(), v.data_ptr(), ld, kh,
+                                       vh), stream)
 
     def _query(self, q, seqs):
+        """(batch, n_q, elements between tokens) of q."""
         if q.dim() != 4:
             raise ValueError("q: expected [sequences, tokens, HQ, 128]")
-        self._ints(seqs, "seqs", q.shape[0])
-        return q.shape[0], q.shape[1], self._heads(q, "q", self.cfg.num_q_heads)
+        b, n_q = q.shape[0], q.shape[1]
+        self._ints(seqs, "seqs", b)
+        return b, n_q, self._heads(q, "q", self.cfg.num_q_heads)
 
     def attention(self, layer: int, q, out, seqs=None, stream=None):
         """Causal attention of the last n_q tokens of every sequence: q, out bf16 [sequences, n_q, HQ, 128]."""
         b, n_q, ldq = self._query(q, seqs)
-        self._dense(out, "out", torch.bfloat16, tuple(q.shape))
-        with self._here():
-            L.hyq_paged_attention(self.cfg, self.c, layer, seqs, b, n_q, q, ldq, out,
-                                  self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream=stream), self._stream(stream))
+        o = self._dense(out, "out", torch.bfloat16, q.shape)
+        ws = self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream)
+        self._run("hyq_paged_attention", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, o, ws.data_ptr(), ws.nbytes),
+                  stream)
 
     def select(self, layer: int, q, sel, seqs=None, n_first: int = 1, n_last: int = 1, stream=None):
         """The blocks worth reading for every token and KV head: sel int32 [sequences, n_q, HKV, k]."""
         b, n_q, ldq = self._query(q, seqs)
-        self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, sel.shape[-1]))
-        with self._here():
-            L.hyq_paged_select(self.cfg, self.c, layer, seqs, b, n_q, q, ldq, sel.shape[-1], n_first, n_last, sel,
-                               self.workspace(L.OP_PAGED_SELECT, b, n_q, stream=stream), self._stream(stream))
+        k = sel.shape[-1]
+        p = self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, k))
+        ws = self.workspace(L.OP_PAGED_SELECT, b, n_q, stream)
+        self._run("hyq_paged_select", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, k, n_first, n_last, p,
+                                       ws.data_ptr(), ws.nbytes), stream)
 
     def attention_blocks(self, layer: int, q, sel, out, seqs=None, stream=None):
         """attention over the blocks that sel lists for each token and KV head."""
         b, n_q, ldq = self._query(q, seqs)
-        self._dense(out, "out", torch.bfloat16, tuple(q.shape))
-        self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, sel.shape[-1]))
-        with self._here():
-            L.hyq_paged_attention_blocks(self.cfg, self.c, layer, seqs, b, n_q, q, ldq, sel, sel.shape[-1], out,
-                                         self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream=stream), self._stream(stream))
+        o = self._dense(out, "out", torch.bfloat16, q.shape)
+        k = sel.shape[-1]
+        p = self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, k))
+        ws = self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream)
+        self._run("hyq_paged_attention_blocks", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, p, k, o, ws.data_ptr(),
+                                                 ws.nbytes), stream)
