@@ -51,12 +51,12 @@ __device__ __forceinline__ int32_t page_seq(const int32_t* seqs, int32_t i, int3
 }
 
 // Smallest integer e >= HYQ_BOUND_EXP_MIN with amax <= 127 * 2^e, for a
-// finite amax >= 0: with amax = m 2^x, m in [1/2, 1), that is x - 7, or
-// x - 6 when m > 127/128.
+// finite amax >= 0: with amax = f 2^x, f in [1, 2), that is x - 6, or x - 5
+// when f > 127/64.  (Zeros and subnormals lie far below the least exponent.)
 __device__ __forceinline__ int bound_exp(float amax) {
-  if (!(amax > 0.f)) return HYQ_BOUND_EXP_MIN;
-  int x;
-  const float m = frexpf(amax, &x);
-  const int e = x - (m > 0.9921875f ? 6 : 7);
+  const int u = __float_as_int(amax);
+  const int e = (u >> 23) - 127 - 6 + ((u & 0x7FFFFF) > 0x7E0000 ? 1 : 0);
   return e > HYQ_BOUND_EXP_MIN ? e : HYQ_BOUND_EXP_MIN;
 }
+// 2^k for -126 <= k <= 127.
+__device__ __forceinline__ float pow2_int(int k) { return __int_as_float((k + 127) << 23); }

@@ -6,13 +6,14 @@
 // (x - z) / s, decided exactly (hyq_qcode.cuh).  Reads 512 bytes per (row, KV
 // head), writes 160 (4-bit codes), and 512 more with the dequantised rows.
 //
-// One block per (page that gets rows, KV head), one warp per (16-row tile, K
-// or V): a lane holds the four elements of a row that share a code word, so a
-// tile's words are assembled in registers, without shared memory.  Steps and
-// zeros take a division each: eight rows are reduced together, the halves
-// exchanged so that each of a group's eight lanes ends with one row's
-// (min, max) (7 exchanges for 8 rows instead of 24) and derives that row's
-// step, once per (row, group) instead of once per lane.
+// One warp per (page that gets rows, KV head, K or V), working through the
+// page's 16-row tiles.  A lane holds eight elements (one 16-byte load) of the
+// rows 2t, 2t + 1, 2t + 8, 2t + 9 for two t: those whose codes share words in
+// either fragment order, so that a tile's words are assembled in registers,
+// without shared memory or barriers; a key warp carries the page's bounds.
+// Steps and zeros take a division each: the rows are reduced together, halves
+// exchanged, so that each of a group's four lanes ends with two rows' (min, max)
+// and derives their steps, once per (row, group) instead of once per lane.
 #include "hyq_paged.cuh"
 #include "hyq_qcode.cuh"
 
@@ -72,64 +73,154 @@ __device__ __forceinline__ PageRows page_rows(const AppendParams& p, const CallR
   return r;
 }
 
-// First of the four elements of a row that lane `lane` holds: the ones whose
-// codes lie in one 32-bit word (K, 4-bit) or simply 4 lane .. 4 lane + 3.
-// Group lane / 8 in both.
-template <int T, int BITS>
-__device__ __forceinline__ int first_element(int lane) {
-  return T == 0 && BITS == 4 ? 8 * (lane & 3) + 32 * (lane >> 3) + 4 * ((lane >> 2) & 1) : 4 * lane;
-}
-
 __device__ __forceinline__ uint32_t u32_of(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
 __device__ __forceinline__ __nv_bfloat162 bf2_of(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
 
-// (min, -max) of a lane's four elements, NaN if one is.
-__device__ __forceinline__ uint32_t min_negmax(uint2 v) {
-  const __nv_bfloat162 a = bf2_of(v.x), b = bf2_of(v.y);
-  const __nv_bfloat162 mn = __hmin2_nan(a, b), mx = __hmax2_nan(a, b);
-  const __nv_bfloat16 lo = __hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn));
-  const __nv_bfloat16 hi = __hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx));
-  return u32_of(__halves2bfloat162(lo, __hneg(hi)));
-}
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) { return u32_of(__hmin2_nan(bf2_of(a), bf2_of(b))); }
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return u32_of(__hmax2_nan(bf2_of(a), bf2_of(b))); }
 
-// Step, zero and reciprocal of a group from (min, -max).  r = -1 marks a group
-// that FP16 metadata cannot hold (or a NaN): codes, step and zero become 0.
+// (min, -max) of a lane's eight elements, NaN if one is.
+__device__ __forceinline__ uint32_t min_negmax(uint4 v) {
+  const uint32_t mn = min2(min2(v.x, v.y), min2(v.z, v.w));
+  const uint32_t nx = max2(max2(v.x, v.y), max2(v.z, v.w)) ^ 0x80008000u;
+  return min2(__byte_perm(mn, nx, 0x5410), __byte_perm(mn, nx, 0x7632));
+}
+
+// Step, zero and reciprocal of a group from (min, -max).  The sign of r tells
+// how the codes are found: r >= 0, the group's extremes lie within half a step
+// of codes 0 and qmax, so no code needs a clamp; r < 0, one may (|r| is the
+// reciprocal); -infinity, a group that FP16 metadata cannot hold (or a NaN):
+// codes, step and zero are 0.
 struct GroupQ {
   uint32_t sz;  // FP16 step | zero << 16
   float r;
 };
-__device__ __forceinline__ GroupQ group_q(uint32_t mm, float qmax) {
+// A code argument t = fl(fl(x - z) r) is off by at most 2^-24 (difference),
+// 2^-23 (reciprocal) and 2^-24 (product) of its size: below 2^-17 for codes up to
+// 15 and 2^-13 up to 255.  An argument that far from a midpoint rounds to the
+// right code; the others are decided exactly.
+template <int BITS>
+struct Near {
+  static constexpr float kTie = BITS == 4 ? 0.5f - 0x1p-17f : 0.5f - 0x1p-13f;
+  static constexpr float kMax = BITS == 4 ? 15.f : 255.f;
+  static constexpr float kInv = BITS == 4 ? 0x1.111112p-4f : 0x1.010102p-8f;  // 1 / kMax, rounded up
+};
+template <int BITS>
+__device__ __forceinline__ GroupQ group_q(uint32_t mm) {
+  constexpr float qmax = Near<BITS>::kMax;
   const float2 m = __bfloat1622float2(bf2_of(mm));
   const float mn = m.x, mx = -m.y;
-  const __half sh = group_step(mn, mx, qmax), zh = __float2half_rn(mn);
-  const float s = __half2float(sh), z = __half2float(zh);
+  // s: the smallest FP16 value with qmax s >= d, d = mx - mn rounded up (qmax s
+  // is exact in float32, so no such product lies between mx - mn and d).  The
+  // rounded-up quotient is at most one FP16 step too large.
+  const float d = __fsub_ru(mx, mn);
+  uint32_t sb = __half_as_ushort(__float2half_ru(__fmul_ru(d, Near<BITS>::kInv)));
+  if (sb > 0 && __fmul_rn(__half2float(__ushort_as_half((unsigned short)(sb - 1))), qmax) >= d) --sb;
+  const float s = __half2float(__ushort_as_half((unsigned short)sb));
+  const __half zh = __float2half_rn(mn);
+  const float z = __half2float(zh);
   GroupQ o;
   if (isnan(m.x) || isnan(m.y) || isinf(s) || isinf(z)) {
     o.sz = 0u;
-    o.r = -1.f;
+    o.r = -INFINITY;
   } else {
-    o.sz = (uint32_t)__half_as_ushort(sh) | ((uint32_t)__half_as_ushort(zh) << 16);
-    o.r = s > 0.f ? __frcp_rn(s) : 0.f;
+    o.sz = sb | ((uint32_t)__half_as_ushort(zh) << 16);
+    float r = 0.f;
+    if (s > 0.f) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const float tl = __fmul_rn(__fsub_rn(mn, z), r), th = __fmul_rn(__fsub_rn(mx, z), r);
+    o.r = tl > -0.5f && th < qmax + 0.5f ? r : -r;
+  }
+  return o;
+}
+__device__ __forceinline__ bool marked(float r) { return r == -INFINITY; }
+
+// The code of x from its argument t: rint(t), and near the midpoint
+// m = (k + 1/2) s the sign of x - z - m, in float32 without a rounding that
+// counts.  m is exact (9 + 11 bits).  x - z = a + e with a = fl(x - z) and e its
+// error (a two-sum); a lies within a factor of two of m there, so a - m is exact
+// and x - z > m just when a - m > -e.  Ties go to the even code.
+template <int BITS>
+__device__ __forceinline__ float exact_code4(float x, float z, float s, float t) {
+  float c = rintf(t);
+  if (fabsf(__fsub_rn(t, c)) > Near<BITS>::kTie) {
+    const float k = floorf(t), m = __fmul_rn(__fadd_rn(k, 0.5f), s);
+    const float a = __fsub_rn(x, z), bb = __fsub_rn(a, x);
+    const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(a, bb)), __fadd_rn(z, bb));
+    const float d = __fsub_rn(a, m);
+    const bool odd = __float2int_rz(k) & 1;
+    c = d > -e || (d == -e && odd) ? __fadd_rn(k, 1.f) : k;
+  }
+  return fminf(fmaxf(c, 0.f), Near<BITS>::kMax);
+}
+
+// The codes of eight elements as bytes, decided exactly (r < 0: with clamps).
+// Out of line: it is called for about one row in 25 (the midpoints that a
+// coarse BF16 grid meets).
+template <int BITS>
+__device__ __noinline__ uint2 exact_codes(uint4 v, float s, float z, float r) {
+  uint32_t o[2] = {0u, 0u};
+  if (!marked(r)) {
+    const float ra = fabsf(r);
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const float x = __uint_as_float(v.x << 16);
+      const uint32_t c = (uint32_t)exact_code4<BITS>(x, z, s, __fmul_rn(__fsub_rn(x, z), ra));
+      o[0] = __funnelshift_r(o[0], o[1], 8);  // bytes move down, the new one enters at the top
+      o[1] = o[1] >> 8 | c << 24;
+      v.x = __funnelshift_r(v.x, v.y, 16);
+      v.y = __funnelshift_r(v.y, v.z, 16);
+      v.z = __funnelshift_r(v.z, v.w, 16);
+      v.w >>= 16;
+    }
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+// Codes of a lane's eight elements: c as float pairs and, for packing, as the
+// low bytes of b (the bits of 1.5 * 2^23 + c).  v becomes zeros in a marked group.
+struct Codes8 {
+  uint64_t c[4];
+  uint32_t b[8];
+};
+template <int BITS>
+__device__ __forceinline__ Codes8 codes8(uint4& v, float s, float z, float r) {
+  Codes8 o;
+  const uint64_t nz2 = f2_splat(-z), r2 = f2_splat(r), m2 = f2_splat(kMagic), nm2 = f2_splat(-kMagic);
+  const uint64_t no2 = f2_splat(-1.f);
+  float far = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = (&v.x)[k];
+    const uint64_t x = (uint64_t)(w << 16) | ((uint64_t)(w & 0xFFFF0000u) << 32);
+    const uint64_t t = f2_mul(f2_add(x, nz2), r2), b = f2_add(t, m2);
+    o.c[k] = f2_add(b, nm2);
+    o.b[2 * k] = lo32(b), o.b[2 * k + 1] = hi32(b);
+    const uint64_t d = f2_fma(o.c[k], no2, t);  // exact
+    far = fmax3(far, fabsf(f2_lo(d)), fabsf(f2_hi(d)));
+  }
+  if (r < 0.f || far > Near<BITS>::kTie) {
+    const uint2 e = exact_codes<BITS>(v, s, z, r);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o.b[k] = __byte_perm(k < 4 ? e.x : e.y, 0x4B400000u, 0x7650 + (k & 3));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o.c[k] = f2_add(f2_pack(__uint_as_float(o.b[2 * k]), __uint_as_float(o.b[2 * k + 1])), nm2);
+    if (marked(r)) v = make_uint4(0u, 0u, 0u, 0u);
   }
   return o;
 }
 
-// Codes of a lane's four elements.  x becomes zeros when the group is marked.
-__device__ __forceinline__ void codes4(uint2& v, uint32_t sz, float r, float qmax, float& s, float& z,
-                                       uint32_t (&c)[4]) {
-  if (r < 0.f) {
-    v = make_uint2(0u, 0u);
-    r = 0.f;
-  }
-  const float2 f = half2_to_float2(sz);
-  s = f.x;
-  z = f.y;
-  const float2 a = __bfloat1622float2(bf2_of(v.x)), b = __bfloat1622float2(bf2_of(v.y));
-  c[0] = code_of(a.x, z, r, s, qmax);
-  c[1] = code_of(a.y, z, r, s, qmax);
-  c[2] = code_of(b.x, z, r, s, qmax);
-  c[3] = code_of(b.y, z, r, s, qmax);
+// Bytes: the codes of elements 0, 2, 1, 3 of four (the order of a key word).
+__device__ __forceinline__ uint32_t key_word(const uint32_t* b) {
+  return __byte_perm(__byte_perm(b[0], b[2], 0x0040), __byte_perm(b[1], b[3], 0x0040), 0x5410);
+}
+// w with its byte `at` replaced by the low byte of x.
+template <int at>
+__device__ __forceinline__ uint32_t put_byte(uint32_t w, uint32_t x) {
+  return __byte_perm(w, x, (0x3210u & ~(0xFu << (4 * at))) | (0x4u << (4 * at)));
+}
+__device__ __forceinline__ uint32_t put_byte(uint32_t w, uint32_t x, int at) {  // at: a constant after unrolling
+  return at == 0 ? put_byte<0>(w, x) : at == 1 ? put_byte<1>(w, x) : at == 2 ? put_byte<2>(w, x) : put_byte<3>(w, x);
 }
 
 // Metadata of (row r of the tile, group q).
@@ -140,184 +231,226 @@ __device__ __forceinline__ void store_meta(uint8_t* meta, int r, int q, uint32_t
   *reinterpret_cast<uint16_t*>(meta + so + (T == 0 ? 8 : 128)) = (uint16_t)(sz >> 16);
 }
 
-__device__ __forceinline__ void store_hat(__nv_bfloat16* hat, const uint32_t (&c)[4], float s, float z) {
-  const uint32_t lo = pack_bf16x2(fmaf((float)c[0], s, z), fmaf((float)c[1], s, z));
-  const uint32_t hi = pack_bf16x2(fmaf((float)c[2], s, z), fmaf((float)c[3], s, z));
-  *reinterpret_cast<uint2*>(hat) = make_uint2(lo, hi);
+__device__ __forceinline__ void store_hat(__nv_bfloat16* hat, const Codes8& c, float s, float z) {
+  const uint64_t s2 = f2_splat(s), z2 = f2_splat(z);
+  uint4 o;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint64_t x = f2_fma(c.c[k], s2, z2);
+    (&o.x)[k] = pack_bf16x2(f2_lo(x), f2_hi(x));
+  }
+  *reinterpret_cast<uint4*>(hat) = o;
 }
 
-// Running bounds of a lane's four key elements (BF16 pairs).
-struct Bounds4 {
-  __nv_bfloat162 mn[2], mx[2];
+// Running bounds of a lane's eight key elements (BF16 pairs).
+struct Bounds8 {
+  uint32_t mn[4], mx[4];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mn[k] = 0x7F807F80u, mx[k] = 0xFF80FF80u;  // +inf, -inf
+  }
+  __device__ __forceinline__ void take(const uint4& v) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      mn[k] = u32_of(__hmin2(bf2_of(mn[k]), bf2_of((&v.x)[k])));
+      mx[k] = u32_of(__hmax2(bf2_of(mx[k]), bf2_of((&v.x)[k])));
+    }
+  }
 };
 
-// Rows `nm` (bits 0..15) of one tile, tensor T (0 = K, 1 = V): row i comes
-// from src + i ld.  bnd: bounds of the rows taken (K).
-template <int T, int BITS, int kTile, int kCode, int kMeta>
-__device__ void tile_rows(uint8_t* tile, const __nv_bfloat16* src, int64_t ld, __nv_bfloat16* hat, int64_t ldh,
-                          uint32_t nm, int lane, Bounds4& bnd, int32_t* err) {
-  constexpr float qmax = BITS == 8 ? 255.f : 15.f;
-  constexpr int kWords = T == 0 ? (BITS == 4 ? 8 : 1) : (BITS == 4 ? 8 : 16);
-  const int e0 = first_element<T, BITS>(lane), q = lane >> 3, i8 = lane & 7;
-  uint32_t w[kWords];
-#pragma unroll
-  for (int k = 0; k < kWords; ++k) w[k] = 0u;
-  bool bad = false;
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const uint32_t hm = (nm >> (8 * half)) & 0xFFu;
-    if (hm == 0) continue;
-    uint2 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[i] = (hm >> i) & 1 ? __ldg(reinterpret_cast<const uint2*>(src + (8 * half + i) * ld + e0)) : make_uint2(0u, 0u);
-    // eight rows' (min, -max): lane i8 of a group ends with row i8's
-    uint32_t m[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = min_negmax(v[i]);
-#pragma unroll
-    for (int o = 4; o >= 1; o >>= 1) {
-      const bool up = i8 & o;
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const uint32_t keep = up ? m[i + o] : m[i], give = up ? m[i] : m[i + o];
-        m[i] = min2(keep, __shfl_xor_sync(0xffffffffu, give, o));
-      }
-    }
-    const GroupQ gq = group_q(m[0], qmax);
-    const bool mine = (hm >> i8) & 1;
-    bad |= mine && gq.r < 0.f;
-    if (mine) store_meta<T>(tile + kMeta, 8 * half + i8, q, gq.sz);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t sz = __shfl_sync(0xffffffffu, gq.sz, (lane & 24) | i);
-      const float r = __shfl_sync(0xffffffffu, gq.r, (lane & 24) | i);
-      if (!((hm >> i) & 1)) continue;  // the same for the whole warp
-      float s, z;
-      uint32_t c[4];
-      codes4(v[i], sz, r, qmax, s, z, c);
-      if (T == 0) {
-        bnd.mn[0] = __hmin2(bnd.mn[0], bf2_of(v[i].x));
-        bnd.mn[1] = __hmin2(bnd.mn[1], bf2_of(v[i].y));
-        bnd.mx[0] = __hmax2(bnd.mx[0], bf2_of(v[i].x));
-        bnd.mx[1] = __hmax2(bnd.mx[1], bf2_of(v[i].y));
-      }
-      if (hat) store_hat(hat + (8 * half + i) * ldh + e0, c, s, z);
-      if (T == 0) {  // bytes: elements 0, 2, 1, 3
-        const uint32_t word = c[0] | (c[2] << 8) | (c[1] << 16) | (c[3] << 24);
-        if (BITS == 4)
-          w[i % kWords] |= word << (4 * half);  // row i + 8 in the high nibbles of row i's word
-        else
-          *reinterpret_cast<uint32_t*>(tile + kCode + 512 * (lane >> 3) + 16 * (4 * i + (lane & 3)) +
-                                       4 * (2 * ((lane >> 2) & 1) + half)) = word;
-      } else if (BITS == 4) {  // row 2t + 8b + c: byte b + 2c of the words of t
-        const int sh = 8 * (half + 2 * (i & 1));
-        w[(2 * (i >> 1)) % kWords] |= (c[0] | (c[1] << 4)) << sh;
-        w[(2 * (i >> 1) + 1) % kWords] |= (c[2] | (c[3] << 4)) << sh;
-      } else {
-        const int sh = 8 * (half + 2 * (i & 1));
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[(4 * (i >> 1) + k) % kWords] |= c[k] << sh;
-      }
-    }
+__device__ __forceinline__ void merge_store(uint2* dst, uint2 x, uint32_t mask) {
+  if (mask != 0xFFFFFFFFu) {
+    const uint2 old = *dst;
+    x.x = (old.x & ~mask) | (x.x & mask);
+    x.y = (old.y & ~mask) | (x.y & mask);
   }
-  if (T == 0 && BITS == 4) {
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(tile + kCode + 512 * (lane >> 4) + 16 * (4 * g + (lane & 3)) +
-                                                  4 * ((lane >> 2) & 3));
-      const uint32_t mask = ((nm >> g) & 1 ? 0x0F0F0F0Fu : 0u) | ((nm >> (g + 8)) & 1 ? 0xF0F0F0F0u : 0u);
-      if (mask == 0u) continue;
-      *dst = mask == 0xFFFFFFFFu ? w[g % kWords] : (*dst & ~mask) | w[g % kWords];
-    }
-  } else if (T == 1) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      uint32_t mask = 0u;  // bytes b + 2c: rows 2t, 2t + 8, 2t + 1, 2t + 9
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if ((nm >> (2 * t + 8 * (j & 1) + (j >> 1))) & 1) mask |= 0xFFu << (8 * j);
-      if (mask == 0u) continue;
-      const int at = 16 * (4 * (lane & 7) + t);
-      if (BITS == 4) {
-        uint2* dst = reinterpret_cast<uint2*>(tile + kCode + 512 * (q >> 1) + at + 8 * (q & 1));
-        uint2 x = make_uint2(w[(2 * t) % kWords], w[(2 * t + 1) % kWords]);
-        if (mask != 0xFFFFFFFFu) {
-          const uint2 old = *dst;
-          x.x |= old.x & ~mask;
-          x.y |= old.y & ~mask;
-        }
-        *dst = x;
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(tile + kCode + 512 * q + at);
-        uint4 x = make_uint4(w[(4 * t) % kWords], w[(4 * t + 1) % kWords], w[(4 * t + 2) % kWords],
-                             w[(4 * t + 3) % kWords]);
-        if (mask != 0xFFFFFFFFu) {
-          const uint4 old = *dst;
-          x.x |= old.x & ~mask;
-          x.y |= old.y & ~mask;
-          x.z |= old.z & ~mask;
-          x.w |= old.w & ~mask;
-        }
-        *dst = x;
-      }
-    }
-  }
-  if (bad) hyq_set_err(err, HYQ_DEVERR_QUANT_RANGE);
+  *dst = x;
 }
 
-// One warp: the bound record of one (page, KV head) from the min / max of four
-// elements per lane, joined with the present record unless `fresh`.  Codes at
-// a coarser step follow from those at a finer one by an outward shift.
-__device__ __forceinline__ void store_bounds(uint8_t* rec, int e0, const Bounds4& b, bool fresh) {
-  float mn[4], mx[4], am = 0.f;
+// Rows `nm` (bits 0..15) of one tile, tensor T (0 = K, 1 = V): row i comes
+// from src + i ld.  bnd: bounds of the rows taken (K).  Returns whether a group
+// could not be held.
+template <int T, int BITS, int kCode, int kMeta>
+__device__ __forceinline__ bool tile_rows(uint8_t* tile, const __nv_bfloat16* src, int64_t ld, __nv_bfloat16* hat,
+                                          int64_t ldh, uint32_t nm, int lane, Bounds8& bnd) {
+  const int hw = lane >> 4, c = lane & 15, q = c >> 2, t4 = c & 3;
+  // row of step j = 4 tt + 2 b + odd: 2 (2 tt + hw) + 8 b + odd
+  const int row0 = 2 * hw;
+  src += row0 * ld + 8 * c;
+  if (hat) hat += row0 * ldh + 8 * c;
+  const uint32_t mine = nm >> row0;  // bit 4 tt + 8 b + odd: the lane's rows
+  uint4 v[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float2 a = __bfloat1622float2(b.mn[i]), c = __bfloat1622float2(b.mx[i]);
-    mn[2 * i] = a.x, mn[2 * i + 1] = a.y, mx[2 * i] = c.x, mx[2 * i + 1] = c.y;
+  for (int j = 0; j < 8; ++j) {
+    const int row = 4 * (j >> 2) + 8 * ((j >> 1) & 1) + (j & 1);
+    v[j] = make_uint4(0u, 0u, 0u, 0u);
+    if ((mine >> row) & 1) v[j] = __ldg(reinterpret_cast<const uint4*>(src + row * ld));
+  }
+  // ---- steps and zeros: lane t4 of a group ends with steps 2 t4 and 2 t4 + 1 --
+  uint32_t m[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m[j] = min_negmax(v[j]);
+#pragma unroll
+  for (int o = 2; o >= 1; o >>= 1) {
+    const bool up = t4 & o;
+#pragma unroll
+    for (int i = 0; i < 2 * o; ++i) {
+      const uint32_t keep = up ? m[i + 2 * o] : m[i], give = up ? m[i] : m[i + 2 * o];
+      m[i] = min2(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  GroupQ gq[2];
+  bool bad = false;
+#pragma unroll
+  for (int odd = 0; odd < 2; ++odd) {
+    gq[odd] = group_q<BITS>(m[odd]);
+    const int row = 4 * (t4 >> 1) + 8 * (t4 & 1) + odd;
+    if ((mine >> row) & 1) {
+      bad |= marked(gq[odd].r);
+      store_meta<T>(tile + kMeta, row0 + row, q, gq[odd].sz);
+    }
+  }
+  // ---- codes (rolled: the unrolled tile does not fit the instruction cache) ---
+#pragma unroll 1
+  for (int tt = 0; tt < 2; ++tt) {
+    const uint32_t tm = mine >> (4 * tt);  // bits 0, 1, 8, 9
+    uint32_t kw[2][2][2] = {};             // K: [odd][word][b]
+    uint32_t vw[2][4] = {};                // V: [half of the elements][word]
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = j >> 1, odd = j & 1, from = (lane & 28) | (2 * tt + b);
+      const uint32_t sz = __shfl_sync(0xffffffffu, gq[odd].sz, from);
+      const float r = __shfl_sync(0xffffffffu, gq[odd].r, from);
+      const float2 f = half2_to_float2(sz);
+      uint4& x = v[j];
+      const Codes8 cd = codes8<BITS>(x, f.x, f.y, r);
+      if ((tm >> (8 * b + odd)) & 1) {
+        if (T == 0) bnd.take(x);
+        if (hat) store_hat(hat + (4 * tt + 8 * b + odd) * ldh, cd, f.x, f.y);
+      }
+      if (T == 0) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) kw[odd][w][b] = key_word(cd.b + 4 * w);
+      } else {
+        const int at = b + 2 * odd;  // row 2t + 8b + odd: byte b + 2 odd of the words
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (BITS == 4) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t* e = cd.b + 4 * half + 2 * w;
+              vw[half][w] = put_byte(vw[half][w], (e[1] << 4) + e[0], at);
+            }
+          } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) vw[half][w] = put_byte(vw[half][w], cd.b[4 * half + w], at);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = v[j + 4];
+    if (T == 0) {
+#pragma unroll
+      for (int odd = 0; odd < 2; ++odd) {
+        const int g = row0 + 4 * tt + odd;  // rows g and g + 8
+        const bool lo = (tm >> odd) & 1, hi = (tm >> (8 + odd)) & 1;
+        if (BITS == 4) {  // row g + 8 in the high nibbles of row g's words
+          const uint2 x = make_uint2(kw[odd][0][0] | kw[odd][0][1] << 4, kw[odd][1][0] | kw[odd][1][1] << 4);
+          if (lo || hi)
+            merge_store(reinterpret_cast<uint2*>(tile + kCode + 512 * (q >> 1) + 16 * (4 * g + t4) + 8 * (q & 1)), x,
+                        (lo ? 0x0F0F0F0Fu : 0u) | (hi ? 0xF0F0F0F0u : 0u));
+        } else {  // a word of row g, then one of row g + 8
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            uint8_t* dst = tile + kCode + 512 * q + 16 * (4 * g + 2 * (c & 1) + w) + 8 * ((c >> 1) & 1);
+            if (lo && hi)
+              *reinterpret_cast<uint2*>(dst) = make_uint2(kw[odd][w][0], kw[odd][w][1]);
+            else if (lo || hi)
+              *reinterpret_cast<uint32_t*>(dst + (hi ? 4 : 0)) = kw[odd][w][hi ? 1 : 0];
+          }
+        }
+      }
+    } else {
+      const uint32_t mask = ((tm & 1) ? 0xFFu : 0u) | ((tm >> 8) & 1 ? 0xFF00u : 0u) | ((tm & 2) ? 0xFF0000u : 0u) |
+                            ((tm >> 9) & 1 ? 0xFF000000u : 0u);
+      const int t = 2 * tt + hw;
+      if (mask) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int at = 16 * (4 * (2 * t4 + half) + t);
+          if (BITS == 4) {
+            merge_store(reinterpret_cast<uint2*>(tile + kCode + 512 * (q >> 1) + at + 8 * (q & 1)),
+                        make_uint2(vw[half][0], vw[half][1]), mask);
+          } else {
+            uint2* dst = reinterpret_cast<uint2*>(tile + kCode + 512 * q + at);
+            merge_store(dst, make_uint2(vw[half][0], vw[half][1]), mask);
+            merge_store(dst + 1, make_uint2(vw[half][2], vw[half][3]), mask);
+          }
+        }
+      }
+    }
+  }
+  return bad;
+}
+
+// One warp: the bound record of one (page, KV head) from the min / max of eight
+// elements per lane (both half-warps hold the same elements: the first
+// stores), joined with the present record unless `fresh`.  Codes at a coarser
+// step follow from those at a finer one by an outward shift.
+__device__ __forceinline__ void store_bounds(uint8_t* rec, int lane, const Bounds8& b, bool fresh) {
+  float mn[8], mx[8], am = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = __bfloat1622float2(bf2_of(b.mn[k])), y = __bfloat1622float2(bf2_of(b.mx[k]));
+    mn[2 * k] = x.x, mn[2 * k + 1] = x.y, mx[2 * k] = y.x, mx[2 * k + 1] = y.y;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) am = fmaxf(am, fmaxf(fabsf(mn[i]), fabsf(mx[i])));
+  for (int k = 0; k < 8; ++k) am = fmaxf(am, fmaxf(fabsf(mn[k]), fabsf(mx[k])));
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+  for (int o = 1; o < 16; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+  const int c = lane & 15;
   int e = bound_exp(am), oe = 0;
-  uint32_t ol = 0u, oh = 0u;
+  uint2 ol = make_uint2(0u, 0u), oh = ol;
   if (!fresh) {
     oe = *reinterpret_cast<const int32_t*>(rec + 256);
-    ol = *reinterpret_cast<const uint32_t*>(rec + e0);
-    oh = *reinterpret_cast<const uint32_t*>(rec + 128 + e0);
+    ol = *reinterpret_cast<const uint2*>(rec + 8 * c);
+    oh = *reinterpret_cast<const uint2*>(rec + 128 + 8 * c);
     e = max(e, oe);
   }
   __syncwarp();
-  const float inv = ldexpf(1.f, -e);
+  const float inv = pow2_int(min(max(-e, -126), 127));
   const int sh = min(max(e - oe, 0), 31);
-  uint32_t l = 0u, h = 0u;
+  uint32_t l[2] = {0u, 0u}, h[2] = {0u, 0u};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    int lo = (int)floorf(mn[i] * inv), hi = (int)ceilf(mx[i] * inv);
+  for (int k = 0; k < 8; ++k) {
+    int lo = (int)floorf(mn[k] * inv), hi = (int)ceilf(mx[k] * inv);
     if (!fresh) {
-      lo = min(lo, (int)(int8_t)(ol >> (8 * i)) >> sh);
-      hi = max(hi, -(-(int)(int8_t)(oh >> (8 * i)) >> sh));
+      const uint32_t wl = k < 4 ? ol.x : ol.y, wh = k < 4 ? oh.x : oh.y;
+      lo = min(lo, (int)(int8_t)(wl >> (8 * (k & 3))) >> sh);
+      hi = max(hi, -(-(int)(int8_t)(wh >> (8 * (k & 3))) >> sh));
     }
-    l |= ((uint32_t)lo & 0xFFu) << (8 * i);
-    h |= ((uint32_t)hi & 0xFFu) << (8 * i);
+    l[k >> 2] |= ((uint32_t)lo & 0xFFu) << (8 * (k & 3));
+    h[k >> 2] |= ((uint32_t)hi & 0xFFu) << (8 * (k & 3));
   }
-  *reinterpret_cast<uint32_t*>(rec + e0) = l;
-  *reinterpret_cast<uint32_t*>(rec + 128 + e0) = h;
-  if ((threadIdx.x & 31) == 0) *reinterpret_cast<int4*>(rec + 256) = make_int4(e, 0, 0, 0);
+  if (lane < 16) {
+    *reinterpret_cast<uint2*>(rec + 8 * c) = make_uint2(l[0], l[1]);
+    *reinterpret_cast<uint2*>(rec + 128 + 8 * c) = make_uint2(h[0], h[1]);
+    if (lane == 0) *reinterpret_cast<int4*>(rec + 256) = make_int4(e, 0, 0, 0);
+  }
 }
 
-constexpr int kThreads = 256;  // 4 tiles x {K, V}
+constexpr int kThreads = 256;  // 4 KV heads x {K, V}
+constexpr int kHeads = kThreads / 64;
 
-// grid (pages that the call may reach, KV heads' share): block x takes the
-// x-th page that gets rows, in the order of the call's rows.
+// grid (pages that the call may reach, KV heads / 4): block x takes the x-th
+// page that gets rows, in the order of the call's rows.
 template <int BK, int BV>
-__global__ void __launch_bounds__(kThreads) append_pages_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendParams p) {
   using F = QFmt<BK, BV>;
   __shared__ int s_warp[kThreads / 32];
   __shared__ PageRows s_rows;
   __shared__ bool s_found;
-  __shared__ Bounds4 s_b[4][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // pages of the call rows 4 tid .. 4 tid + 3, summed up
   CallRows c[4];
@@ -356,113 +489,116 @@ __global__ void __launch_bounds__(kThreads) append_pages_kernel(const AppendPara
   if (!s_found) return;
   const PageRows r = s_rows;
   if (r.r1 <= r.r0) return;
-  const int tile = warp & 3, T = warp >> 2;
-  // rows of this tile: bits of [r0, r1) in [16 tile, 16 tile + 16)
-  const int a = min(max(r.r0 - 16 * tile, 0), 16), z = min(max(r.r1 - 16 * tile, 0), 16);
-  const uint32_t nm = ((1u << z) - 1u) & ~((1u << a) - 1u);
-  const int64_t row0 = (int64_t)r.tok0 + 16 * tile - r.r0;  // call row of the tile's row 0 (may lie before tok0)
-  for (int h = blockIdx.y; h < p.HKV; h += gridDim.y) {
-    const size_t ph = (size_t)r.page * p.HKV + h;
-    uint8_t* tp = p.pv.pool + ph * F::kBlock + tile * F::kTile;
-    const int64_t ldh = (int64_t)p.HKV * HYQ_D;
-    Bounds4 b;
-    b.mn[0] = b.mn[1] = __floats2bfloat162_rn(INFINITY, INFINITY);
-    b.mx[0] = b.mx[1] = __floats2bfloat162_rn(-INFINITY, -INFINITY);
-    if (nm) {
-      if (T == 0)
-        tile_rows<0, BK, F::kTile, 0, F::kKMeta>(tp, p.k + row0 * p.ld + (int64_t)h * HYQ_D, p.ld,
-                                                 p.k_hat ? p.k_hat + row0 * ldh + (int64_t)h * HYQ_D : nullptr, ldh,
-                                                 nm, lane, b, p.pv.err);
-      else
-        tile_rows<1, BV, F::kTile, F::kVCode, F::kVMeta>(
-            tp, p.v + row0 * p.ld + (int64_t)h * HYQ_D, p.ld,
-            p.v_hat ? p.v_hat + row0 * ldh + (int64_t)h * HYQ_D : nullptr, ldh, nm, lane, b, p.pv.err);
-    }
-    if (T == 0) s_b[tile][lane] = b;
-    __syncthreads();
-    if (warp == 0) {
+  const int h = blockIdx.y * kHeads + (warp >> 1), T = warp & 1;
+  if (h >= p.HKV) return;
+  const size_t ph = (size_t)r.page * p.HKV + h;
+  uint8_t* block = p.pv.pool + ph * F::kBlock;
+  const int64_t ldh = (int64_t)p.HKV * HYQ_D;
+  const __nv_bfloat16* src = (T == 0 ? p.k : p.v) + (int64_t)h * HYQ_D;
+  __nv_bfloat16* hat = T == 0 ? p.k_hat : p.v_hat;
+  if (hat) hat += (int64_t)h * HYQ_D;
+  Bounds8 b;
+  b.clear();
+  bool bad = false;
+#pragma unroll 1
+  for (int tile = r.r0 >> 4; 16 * tile < r.r1; ++tile) {
+    // rows of this tile: bits of [r0, r1) in [16 tile, 16 tile + 16)
+    const int a = max(r.r0 - 16 * tile, 0), z = min(r.r1 - 16 * tile, 16);
+    const uint32_t nm = ((1u << z) - 1u) & ~((1u << a) - 1u);
+    const int64_t row0 = (int64_t)r.tok0 + 16 * tile - r.r0;  // call row of the tile's row 0 (may lie before tok0)
+    uint8_t* tp = block + tile * F::kTile;
+    if (T == 0)
+      bad |= tile_rows<0, BK, 0, F::kKMeta>(tp, src + row0 * p.ld, p.ld, hat ? hat + row0 * ldh : nullptr, ldh, nm, lane, b);
+    else
+      bad |= tile_rows<1, BV, F::kVCode, F::kVMeta>(tp, src + row0 * p.ld, p.ld, hat ? hat + row0 * ldh : nullptr, ldh,
+                                                    nm, lane, b);
+  }
+  if (bad) hyq_set_err(p.pv.err, HYQ_DEVERR_QUANT_RANGE);
+  if (T == 0) {
 #pragma unroll
-      for (int i = 1; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          b.mn[j] = __hmin2(b.mn[j], s_b[i][lane].mn[j]);
-          b.mx[j] = __hmax2(b.mx[j], s_b[i][lane].mx[j]);
-        }
-      store_bounds(p.pv.bounds + ph * HYQ_BOUND_BYTES, first_element<0, BK>(lane), b, r.r0 == 0);
+    for (int k = 0; k < 4; ++k) {  // the half-warps' rows
+      b.mn[k] = u32_of(__hmin2(bf2_of(b.mn[k]), bf2_of(__shfl_xor_sync(0xffffffffu, b.mn[k], 16))));
+      b.mx[k] = u32_of(__hmax2(bf2_of(b.mx[k]), bf2_of(__shfl_xor_sync(0xffffffffu, b.mx[k], 16))));
     }
-    __syncthreads();
+    store_bounds(p.pv.bounds + ph * HYQ_BOUND_BYTES, lane, b, r.r0 == 0);
   }
 }
 
-// One row per sequence: grid (batch, HKV), warp 0 the key, warp 1 the value.
+// One row per sequence: a warp per (sequence, KV head), the key in its first
+// half and the value in its second, eight elements a lane.
+// grid (batch, KV heads / kHeadsOne)
+constexpr int kHeadsOne = 4;
+
 template <int BK, int BV>
-__global__ void __launch_bounds__(64) append_one_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(32 * kHeadsOne) append_one_kernel(const AppendParams p) {
   using F = QFmt<BK, BV>;
-  const int h = blockIdx.y, T = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const CallRows c = call_rows(p, blockIdx.x);
-  if (c.bad && threadIdx.x == 0 && h == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-  if (c.n <= 0) return;
-  const PageRows r = page_rows(p, c, 0);
-  if (r.r1 <= r.r0) return;
-  const size_t ph = (size_t)r.page * p.HKV + h;
-  const int row = r.r0 & 15, q = lane >> 3;
-  const float qmax = (T == 0 ? BK : BV) == 8 ? 255.f : 15.f;
-  const int e0 = T == 0 ? first_element<0, BK>(lane) : first_element<1, BV>(lane);
-  uint8_t* tile = p.pv.pool + ph * F::kBlock + (r.r0 >> 4) * F::kTile;
-  uint2 v = __ldg(reinterpret_cast<const uint2*>((T == 0 ? p.k : p.v) + (int64_t)r.tok0 * p.ld + (int64_t)h * HYQ_D + e0));
+  const int lane = threadIdx.x & 31, h = blockIdx.y * kHeadsOne + (threadIdx.x >> 5);
+  const CallRows cr = call_rows(p, blockIdx.x);
+  if (cr.bad && threadIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+  if (cr.n <= 0 || h >= p.HKV) return;
+  const PageRows pr = page_rows(p, cr, 0);
+  if (pr.r1 <= pr.r0) return;
+  const size_t ph = (size_t)pr.page * p.HKV + h;
+  const int T = lane >> 4, c = lane & 15, q = c >> 2, t4 = c & 3, row = pr.r0 & 15;
+  uint8_t* tile = p.pv.pool + ph * F::kBlock + (pr.r0 >> 4) * F::kTile;
+  uint4 v = __ldg(reinterpret_cast<const uint4*>((T == 0 ? p.k : p.v) + (int64_t)pr.tok0 * p.ld + (int64_t)h * HYQ_D + 8 * c));
   uint32_t m = min_negmax(v);
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) m = min2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const GroupQ gq = group_q(m, qmax);
-  if (gq.r < 0.f) hyq_set_err(p.pv.err, HYQ_DEVERR_QUANT_RANGE);
-  float s, z;
-  uint32_t cd[4];
-  codes4(v, gq.sz, gq.r, qmax, s, z, cd);
+  m = min2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = min2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const GroupQ gq = (T == 0 ? BK : BV) == 4 ? group_q<4>(m) : group_q<8>(m);
+  if (marked(gq.r)) hyq_set_err(p.pv.err, HYQ_DEVERR_QUANT_RANGE);
+  const float2 f = half2_to_float2(gq.sz);
+  const Codes8 cd = (T == 0 ? BK : BV) == 4 ? codes8<4>(v, f.x, f.y, gq.r) : codes8<8>(v, f.x, f.y, gq.r);
   __nv_bfloat16* hat = T == 0 ? p.k_hat : p.v_hat;
-  if (hat) store_hat(hat + ((int64_t)r.tok0 * p.HKV + h) * HYQ_D + e0, cd, s, z);
+  if (hat) store_hat(hat + ((int64_t)pr.tok0 * p.HKV + h) * HYQ_D + 8 * c, cd, f.x, f.y);
   if (T == 0) {
-    if ((lane & 7) == 0) store_meta<0>(tile + F::kKMeta, row, q, gq.sz);
-    const uint32_t word = cd[0] | (cd[2] << 8) | (cd[1] << 16) | (cd[3] << 24);
-    const int g = row & 7, half = row >> 3;
+    if (t4 == 0) store_meta<0>(tile + F::kKMeta, row, q, gq.sz);
+    const int g = row & 7, b = row >> 3;
+    const uint32_t w0 = key_word(cd.b), w1 = key_word(cd.b + 4);
     if (BK == 4) {
-      uint32_t* dst = reinterpret_cast<uint32_t*>(tile + 512 * (lane >> 4) + 16 * (4 * g + (lane & 3)) + 4 * ((lane >> 2) & 3));
-      *dst = (*dst & ~(0x0F0F0F0Fu << (4 * half))) | (word << (4 * half));
+      merge_store(reinterpret_cast<uint2*>(tile + 512 * (q >> 1) + 16 * (4 * g + t4) + 8 * (q & 1)),
+                  make_uint2(w0 << (4 * b), w1 << (4 * b)), 0x0F0F0F0Fu << (4 * b));
     } else {
-      *reinterpret_cast<uint32_t*>(tile + 512 * (lane >> 3) + 16 * (4 * g + (lane & 3)) +
-                                   4 * (2 * ((lane >> 2) & 1) + half)) = word;
+      uint8_t* dst = tile + 512 * q + 16 * (4 * g + 2 * (c & 1)) + 8 * ((c >> 1) & 1) + 4 * b;
+      *reinterpret_cast<uint32_t*>(dst) = w0;
+      *reinterpret_cast<uint32_t*>(dst + 16) = w1;
     }
-    Bounds4 b;
-    b.mn[0] = b.mx[0] = bf2_of(v.x);
-    b.mn[1] = b.mx[1] = bf2_of(v.y);
-    store_bounds(p.pv.bounds + ph * HYQ_BOUND_BYTES, e0, b, r.r0 == 0);
   } else {
-    if ((lane & 7) == 0) store_meta<1>(tile + F::kVMeta, row, q, gq.sz);
-    const int t = (row & 7) >> 1, j = (row >> 3) + 2 * (row & 1);
-    uint8_t* at = tile + F::kVCode + 16 * (4 * (lane & 7) + t) + j;
-    if (BV == 4) {
-      at += 512 * (q >> 1) + 8 * (q & 1);
-      at[0] = (uint8_t)(cd[0] | (cd[1] << 4));
-      at[4] = (uint8_t)(cd[2] | (cd[3] << 4));
-    } else {
-      at += 512 * q;
+    if (t4 == 0) store_meta<1>(tile + F::kVMeta, row, q, gq.sz);
+    const int t = (row & 7) >> 1;
+    uint8_t* dst = tile + F::kVCode + 16 * (8 * t4 + t) + (row >> 3) + 2 * (row & 1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) at[4 * k] = (uint8_t)cd[k];
+    for (int half = 0; half < 2; ++half) {
+      uint8_t* at = dst + 64 * half;
+      if (BV == 4) {
+        at += 512 * (q >> 1) + 8 * (q & 1);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t* e = cd.b + 4 * half + 2 * w;
+          at[4 * w] = (uint8_t)((e[1] << 4) + e[0]);
+        }
+      } else {
+        at += 512 * q;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) at[4 * w] = (uint8_t)cd.b[4 * half + w];
+      }
     }
   }
+  // the key half's bounds, in both halves (store_bounds takes the whole warp)
+  Bounds8 bnd;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) bnd.mn[k] = bnd.mx[k] = __shfl_sync(0xffffffffu, (&v.x)[k], c);
+  store_bounds(p.pv.bounds + ph * HYQ_BOUND_BYTES, lane, bnd, pr.r0 == 0);
 }
 
 template <int BK, int BV>
 cudaError_t launch(const AppendParams& p, cudaStream_t s) {
   if (!p.cu) {
-    append_one_kernel<BK, BV><<<dim3(p.batch, p.HKV), 64, 0, s>>>(p);
+    append_one_kernel<BK, BV><<<dim3(p.batch, (p.HKV + kHeadsOne - 1) / kHeadsOne), 32 * kHeadsOne, 0, s>>>(p);
   } else {
     // a sequence with n rows reaches at most n / 64 + 2 pages
     const int pages = p.n_rows / HYQ_PAGE_ROWS + 2 * min(p.batch, p.n_rows);
-    // every head its own block while that does not give far more blocks than
-    // can be resident; then a block takes several heads in turn
-    int hs = p.HKV;
-    while (hs > 1 && (int64_t)pages * hs > 16 * hyq_num_sms()) hs = (hs + 1) / 2;
-    append_pages_kernel<BK, BV><<<dim3(pages, hs), kThreads, 0, s>>>(p);
+    append_pages_kernel<BK, BV><<<dim3(pages, (p.HKV + kHeads - 1) / kHeads), kThreads, 0, s>>>(p);
   }
   return cudaGetLastError();
 }

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
   odd = __syncthreads_or(odd);
   if (tid < HYQ_D) {
     am = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-    const float inv = ldexpf(1.f, -bound_exp(odd ? 0.f : am));
+    const float inv = pow2_int(min(-bound_exp(odd ? 0.f : am), 127));
     int pos = 0, neg = 0;
 #pragma unroll
     for (int r = 0; r < HYQ_MAX_GQA; ++r) {
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     if (j < nb && part == 0) {
       const bool forced = j < p.n_first || j >= nb - p.n_last;
       // 0 and all ones lie outside the keys of finite scores
-      keys[j] = forced ? 0xFFFFFFFFu : ok ? key_of(ldexpf((float)acc, e)) : 0u;
+      keys[j] = forced ? 0xFFFFFFFFu : ok ? key_of((float)acc * pow2_int(min(max(e, -126), 127))) : 0u;
     }
   }
   // ---- the last block of the list selects ------------------------------------
