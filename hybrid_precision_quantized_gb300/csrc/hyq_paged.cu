@@ -17,7 +17,7 @@
 // into equal runs, one per block (two blocks an SM), so that unlike lengths
 // and single long sequences use the GPU alike and the launch does not depend
 // on the lengths (they live on the device; a captured call stays valid as
-// they grow).  In the line each group begins with kGroupCost units that are
+// they grow).  In the line each group begins with R::kCost units that are
 // not there, about what preparing its queries and joining its warps takes:
 // without them a block that meets many short groups finishes last (16
 // sequences, one of them a single token: 126 us instead of 181 us x 0.73).
@@ -33,23 +33,28 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowsQ = HYQ_MAX_GQA;    // query rows per tile (MMA N)
 constexpr int kPart = 2 + HYQ_D;       // m, l, acc[128] per query row
-constexpr int kGroupCost = 16;         // units that a group's fixed work is worth
-constexpr int kMinUnits = 32;          // units per block before a group is split further
-constexpr int kBlocksPerSm = 2;
-constexpr int kMaxGrid = 1024;         // two blocks on each of up to 512 SMs
+constexpr int kMinUnits = 16;          // units per block before a group is split further
+constexpr int kMaxNQ = 4;             // query tiles that one block takes together
 
-// A warp's units and its ring of bulk copies, as much as two blocks an SM
-// allow: units of two adjacent tiles for 4-bit codes.
-template <int BK, int BV>
+// The kernel's shape for NQ query tiles a group.  One tile: two blocks an SM
+// (one's group change hides behind the other), units of two adjacent 16-row tiles for 4-bit codes.
+// More: the accumulators of NQ tiles leave registers for one block an SM, whose
+// ring is deeper; units of one tile.
+template <int BK, int BV, int NQ>
 struct Ring : QFmt<BK, BV> {
-  static constexpr int kTiles = BK + BV == 8 ? 2 : 1;  // tiles per unit
-  static constexpr int kSlots = BK + BV == 12 ? 3 : 2;
+  static constexpr int kPerSm = NQ == 1 ? 2 : 1;
+  static constexpr int kTiles = BK + BV == 8 && NQ == 1 ? 2 : 1;  // tiles per unit
+  static constexpr int kSlots = NQ > 1 ? 4 : BK + BV == 12 ? 3 : 2;
   static constexpr int kUnit = kTiles * QFmt<BK, BV>::kTile;
+  static constexpr int kCost = (NQ == 1 ? 48 : 16 * NQ) / kTiles;  // units that a group's fixed work is worth
   static constexpr int kRows = 16 * kTiles;
   static constexpr int kPerPage = HYQ_PAGE_ROWS / kRows;
   static constexpr int kWarpBytes = kSlots * kUnit;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  static_assert(kWarpBytes >= HYQ_MAX_GQA * HYQ_D * 4, "a warp's partial fits its ring");
+  // query tiles whose partials a warp's ring holds at once
+  static constexpr int kJoin = NQ * 4096 <= kWarpBytes ? NQ : NQ > 2 && 2 * 4096 <= kWarpBytes ? 2 : 1;
+  static_assert(kJoin * 4096 <= kWarpBytes && NQ % kJoin == 0, "a warp's partial fits its ring");
+  static_assert(kWarps % kPerPage == 0, "a warp's units take the same part of their pages");
 };
 
 struct Params {
@@ -59,9 +64,10 @@ struct Params {
   int64_t ldq;
   const int32_t* sel;  // [batch][n_q][HKV][k_sel] or nullptr
   __nv_bfloat16* out;
-  float* part;         // [grid][2][8][kPart]
+  float* part;         // [grid][2][NQ][8][kPart]
   int32_t* tickets;    // [groups]
-  int32_t batch, n_q, HQ, HKV, gq, QT, k_sel;
+  int32_t batch, n_q, HQ, HKV, gq, k_sel;
+  int32_t QT;          // groups per (sequence, KV head)
 };
 
 // Length of call row b, 0 for a sequence out of range.
@@ -90,21 +96,22 @@ struct Shares {
   }
 };
 
-template <int BK, int BV>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Params p) {
-  using R = Ring<BK, BV>;
-  constexpr int kSlots = R::kSlots;
+template <int BK, int BV, int NQ>
+__global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kernel(const Params p) {
+  using R = Ring<BK, BV, NQ>;
+  constexpr int kSlots = R::kSlots, kRowsG = NQ * kRowsQ;  // query rows per group
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];  // units per (KV head, query tile) of the rows before b
   __shared__ int s_len[HYQ_PAGED_MAX_BATCH], s_seq[HYQ_PAGED_MAX_BATCH];
   __shared__ int64_t s_warp[kWarps];
-  __shared__ __align__(16) uint32_t bq_s[4][kRowsQ][4][4];
-  __shared__ float rowc_s[kRowsQ][4];
-  __shared__ uint32_t bz_s[kRowsQ][4];
-  __shared__ int lim_s[kRowsQ];
+  __shared__ __align__(16) uint32_t bq_s[NQ][4][kRowsQ][4][4];
+  __shared__ __align__(16) float rowc_s[NQ][kRowsQ][4];
+  __shared__ uint32_t bz_s[NQ][kRowsQ][4];
+  __shared__ int lim_s[NQ][kRowsQ];
   __shared__ __align__(8) uint64_t bars[kWarps * kSlots];
-  __shared__ float red_m[kWarps][kRowsQ], red_l[kWarps][kRowsQ];
-  __shared__ float s_sum[kRowsQ];
+  __shared__ float red_m[kWarps][R::kJoin][kRowsQ], red_l[kWarps][R::kJoin][kRowsQ];
+  __shared__ float s_wt[R::kJoin * kRowsQ][kWarps];     // weights of the warps' partials
+  __shared__ float s_sum[R::kJoin * kRowsQ];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -118,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
   auto units_of = [&](int len) {
     int n = (len + R::kRows - 1) / R::kRows;
     if (p.sel) n = R::kPerPage * min(p.k_sel, (len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS);
-    return n == 0 ? 0 : n + kGroupCost;
+    return n == 0 ? 0 : n + R::kCost;
   };
   // ---- the rows' units, summed up: a block of 4 rows per thread --------------
   const int unit = p.HKV * p.QT;
@@ -161,14 +168,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
   }
   __syncthreads();
   // ---- this block's run -------------------------------------------------------
-  // With fewer groups than blocks every group gets the same number of blocks
-  // (equal lengths are then cut at the groups' borders), and no more than give
-  // each kMinUnits.
+  // No more blocks than give each kMinUnits.  With few groups every group gets
+  // the same number of blocks: equal lengths are then cut at the groups'
+  // borders.  (Not where rounding down would leave a quarter of the blocks out.)
   const int64_t T = s_cum[p.batch] * unit;
   int64_t nb = gridDim.x;
   {
-    const int64_t groups = (int64_t)p.batch * unit;
-    if (groups < nb) nb = groups * max((int64_t)1, min(div_fast(nb, groups), div_fast(T, groups * kMinUnits)));
+    const int64_t groups = (int64_t)p.batch * unit, want = max((int64_t)1, div_fast(T, kMinUnits));
+    if (groups <= nb) {
+      const int64_t most = div_fast(nb, groups), by_size = max((int64_t)1, div_fast(want, groups));
+      if (by_size < most || most >= 4) nb = groups * min(most, by_size);
+    }
     nb = max((int64_t)1, min(nb, T));
   }
   if ((int64_t)blockIdx.x >= nb) return;
@@ -196,13 +206,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
     const int grp = (int)div_fast(off, W), x0 = (int)(off - (int64_t)grp * W);
     const int x1 = (int)min((int64_t)W, x0 + (end - pos));
     pos += x1 - x0;
-    const int n_units = W - kGroupCost, w0 = max(0, x0 - kGroupCost), w1 = x1 - kGroupCost;
+    const int n_units = W - R::kCost, w0 = max(0, x0 - R::kCost), w1 = x1 - R::kCost;
     if (w1 <= w0) continue;  // only units of the fixed work: another block's group
     const int h = grp / p.QT, qt = grp - h * p.QT;
     const int seq = s_seq[b], len = s_len[b];
     const int32_t* table = p.pv.table + (size_t)seq * p.pv.max_blocks;
     const int32_t* sel = p.sel ? p.sel + (((size_t)b * p.n_q + qt) * p.HKV + h) * p.k_sel : nullptr;
-    const int n_rows = p.sel ? p.gq : min(kRowsQ, p.n_q * p.gq - kRowsQ * qt);
+    const int n_rows = p.sel ? p.gq : min(kRowsG, p.n_q * p.gq - kRowsG * qt);
     const size_t page_bytes = (size_t)p.HKV * R::kBlock;
 
     // ---- this warp's units: w0 + warp, + 8, ... ---------------------------
@@ -263,25 +273,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) at_slot[j] = j < nj && !dead ? issue(j) : -1;
 
-    // ---- the query rows: warp r prepares row r ----------------------------
-    {
-      const int r = warp;
-      const int flat = kRowsQ * qt + r;
-      const int tok = p.sel ? qt : flat / p.gq, head = p.sel ? r : flat - tok * p.gq;
+    // ---- the query rows: warp r prepares row r of each query tile ----------
+    // Token and head of row r of the group: rows are (token, head) pairs in
+    // order; with block lists a group is one token's heads.
+    auto token_of = [&](int r) { return p.sel ? qt : (kRowsG * qt + r) / p.gq; };
+    auto head_of = [&](int r, int tok) { return p.sel ? r : kRowsG * qt + r - tok * p.gq; };
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+      const int r = kRowsQ * k + warp;
+      const int tok = token_of(r), head = head_of(r, tok);
       uint2 v = make_uint2(0, 0);
       if (r < n_rows)
         v = __ldg(reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.n_q + tok) * p.ldq +
                                                  (size_t)(h * p.gq + head) * HYQ_D + 4 * lane));
-      prep_query_row<BK>(r, lane, v, bq_s, rowc_s, bz_s);
-      if (lane == 0) lim_s[r] = r < n_rows ? max(0, len - p.n_q + 1 + tok) : len;
+      prep_query_row<BK>(warp, lane, v, bq_s[k], rowc_s[k], bz_s[k]);
+      if (lane == 0) lim_s[k][warp] = r < n_rows ? max(0, len - p.n_q + 1 + tok) : len;
     }
     __syncthreads();
     uint32_t bq[8][2];
     QConst qc;
-    load_query_consts(g, t, bq_s, rowc_s, bz_s, bq, qc);
-    const int minlim = lim_s[0];  // the rows' tokens ascend
-    State st;
-    reset_state(st);
+    if (NQ == 1) load_query_consts(g, t, bq_s[0], rowc_s[0], bz_s[0], bq, qc);
+    const int minlim = lim_s[0][0];  // the rows' tokens ascend
+    State st[NQ];
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) reset_state(st[k]);
 
     for (int j = 0; j < nj && !dead; ++j) {
       const uint32_t n = done + (uint32_t)j;
@@ -302,14 +317,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
       const int at = at_slot[0];
       const uint8_t* tb = ring + slot * R::kUnit;
       if (at >= 0) {
-        if (at + R::kRows <= minlim) {
-          q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st);
-        } else {
-          const int lim0 = lim_s[2 * t], lim1 = lim_s[2 * t + 1];
-          for (int x = 0; x < R::kTiles && at + 16 * x < len; ++x) {
-            const int a = at + 16 * x;
-            q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, len - a, bq, qc, st, lim0 - a, lim1 - a);
+        if constexpr (NQ == 1) {
+          if (at + R::kRows <= minlim) {
+            q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st[0]);
+          } else {
+            const int lim0 = lim_s[0][2 * t], lim1 = lim_s[0][2 * t + 1];
+            for (int x = 0; x < R::kTiles && at + 16 * x < len; ++x) {
+              const int a = at + 16 * x;
+              q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, len - a, bq, qc, st[0], lim0 - a, lim1 - a);
+            }
           }
+        } else if (at + R::kRows <= minlim) {
+          q_tile_multi<BK, BV, NQ, false>(tb, lane, 16, bq_s, rowc_s, bz_s, lim_s, at, st);
+        } else {
+          q_tile_multi<BK, BV, NQ, true>(tb, lane, len - at, bq_s, rowc_s, bz_s, lim_s, at, st);
         }
       }
       __syncwarp();
@@ -322,48 +343,74 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
     }
     done += nj;
 
-    // ---- the block's partial ------------------------------------------------
+    // ---- the block's partial, a query tile at a time -------------------------
     __syncwarp();
-    store_warp_partial<BV>(st, qc, g, t, reinterpret_cast<float*>(ring), red_m[warp], red_l[warp]);
-    __syncthreads();
     const bool whole = w0 == 0 && w1 == n_units;
-    float* pp = p.part + ((size_t)blockIdx.x * 2 + (w0 == 0 ? 1 : 0)) * (kRowsQ * kPart);
+    float* pp = p.part + ((size_t)blockIdx.x * 2 + (w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
     auto out_at = [&](int r) {
-      const int flat = kRowsQ * qt + r;
-      const int tok = p.sel ? qt : flat / p.gq, head = p.sel ? r : flat - tok * p.gq;
-      return p.out + (((size_t)b * p.n_q + tok) * p.HQ + (size_t)h * p.gq + head) * HYQ_D;
+      const int tok = token_of(r);
+      return p.out + (((size_t)b * p.n_q + tok) * p.HQ + (size_t)h * p.gq + head_of(r, tok)) * HYQ_D;
     };
-    for (int i = tid; i < n_rows * HYQ_D; i += kThreads) {
-      const int r = i >> 7, d = i & (HYQ_D - 1);
-      const float mw = lane < kWarps ? red_m[lane][r] : -INFINITY;
-      float M = mw;
+    constexpr int kJoin = R::kJoin;
 #pragma unroll
-      for (int o = 1; o < kWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      M = __shfl_sync(0xffffffffu, M, 0);
-      const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
-      float L = lane < kWarps ? red_l[lane][r] * wt : 0.f;
+    for (int k0 = 0; k0 < NQ; k0 += kJoin) {
+      if (NQ > 1 && kRowsQ * k0 >= n_rows) break;
 #pragma unroll
-      for (int o = 1; o < kWarps; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      L = __shfl_sync(0xffffffffu, L, 0);
-      float a = 0.f;
+      for (int k = 0; k < kJoin; ++k) {
+        if (NQ > 1) load_query_consts(g, t, bq_s[k0 + k], rowc_s[k0 + k], bz_s[k0 + k], bq, qc);
+        store_warp_partial<BV>(st[k0 + k], qc, g, t, reinterpret_cast<float*>(ring + 4096 * k), red_m[warp][k],
+                               red_l[warp][k]);
+      }
+      __syncthreads();
+      // eight lanes a row: its weights 2^(m_w - M) and its sum
+      if (tid < kJoin * kRowsQ * kWarps) {
+        const int r = tid >> 3, w = tid & 7;
+        const float mw = red_m[w][r >> 3][r & 7];
+        float M = mw;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w)
-        a = fmaf(__shfl_sync(0xffffffffu, wt, w),
-                 reinterpret_cast<const float*>(smem + w * R::kWarpBytes)[r * HYQ_D + (d ^ (r >> 1))], a);
-      if (whole) {
-        out_at(r)[d] = __float2bfloat16_rn(L > 0.f ? a / L : 0.f);
-      } else {
-        pp[r * kPart + 2 + d] = a;
-        if (d == 0) {
-          pp[r * kPart + 0] = M;
-          pp[r * kPart + 1] = L;
+        for (int o = 1; o < kWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
+        float L = red_l[w][r >> 3][r & 7] * wt;
+#pragma unroll
+        for (int o = 1; o < kWarps; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        s_wt[r][w] = wt;
+        if (w == 0) {
+          s_sum[r] = L;
+          if (!whole && kRowsQ * k0 + r < n_rows) {
+            pp[(kRowsQ * k0 + r) * kPart + 0] = M;
+            pp[(kRowsQ * k0 + r) * kPart + 1] = L;
+          }
         }
       }
+      __syncthreads();
+      // four elements of a row a thread (the warps' partials hold element d at d ^ (row / 2))
+      for (int i = tid; i < min(kJoin * kRowsQ, n_rows - kRowsQ * k0) * (HYQ_D / 4); i += kThreads) {
+        const int r = i >> 5, d = 4 * (i & 31), x = (r & 7) >> 1;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(smem + w * R::kWarpBytes + 4096 * (r >> 3) +
+                                                            4 * ((r & 7) * HYQ_D + d));
+          const float wt = s_wt[r][w];
+          a.x = fmaf(wt, v.x, a.x), a.y = fmaf(wt, v.y, a.y), a.z = fmaf(wt, v.z, a.z), a.w = fmaf(wt, v.w, a.w);
+        }
+        if (x & 1) a = make_float4(a.y, a.x, a.w, a.z);
+        if (x & 2) a = make_float4(a.z, a.w, a.x, a.y);
+        if (whole) {
+          const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
+          *reinterpret_cast<uint2*>(out_at(kRowsQ * k0 + r) + d) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+        } else {
+          float2* to = reinterpret_cast<float2*>(pp + (kRowsQ * k0 + r) * kPart + 2 + d);
+          to[0] = make_float2(a.x, a.y);
+          to[1] = make_float2(a.z, a.w);
+        }
+      }
+      __syncthreads();  // the rings are free again
     }
-    __syncthreads();  // the rings are free again
     if (!whole) {
       // blocks that share this group: those holding its first and last unit
-      const int64_t base = cum * unit + (int64_t)grp * W + kGroupCost;
+      const int64_t base = cum * unit + (int64_t)grp * W + R::kCost;
       const int c0 = sh.owner(base), c1 = sh.owner(base + n_units - 1);
       const size_t gi = ((size_t)b * p.HKV + h) * p.QT + qt;
       if (tid == 0) {
@@ -378,35 +425,43 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
         const int n = c1 - c0 + 1;
         // part i: slot 0 of block c0 + i, where its run ends this group; the
         // first block's is slot 1 when its run holds the group's first unit
-        const float* parts = p.part + (size_t)c0 * 2 * (kRowsQ * kPart);
-        const int first = sh.begin(c0) <= base ? kRowsQ * kPart : 0;
-        auto part_of = [&](int i) { return parts + (size_t)i * (2 * kRowsQ * kPart) + (i == 0 ? first : 0); };
-        if (warp < n_rows) {
-          float M = -INFINITY;
-          for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(part_of(c) + warp * kPart));
+        constexpr size_t kSlot = (size_t)NQ * kRowsQ * kPart;
+        const float* parts = p.part + (size_t)c0 * 2 * kSlot;
+        const size_t first = sh.begin(c0) <= base ? kSlot : 0;
+        auto part_of = [&](int i) { return parts + (size_t)i * (2 * kSlot) + (i == 0 ? first : 0); };
+        for (int r0 = 0; r0 < n_rows; r0 += kRowsQ) {
+          const int rows = min(kRowsQ, n_rows - r0);
+          if (warp < rows) {
+            float M = -INFINITY;
+            for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(part_of(c) + (r0 + warp) * kPart));
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-          float L = 0.f;
-          for (int c = lane; c < n; c += 32) {
-            const float* e = part_of(c) + warp * kPart;
-            const float m = __ldcg(e), wt = m == -INFINITY ? 0.f : ex2(m - M);
-            wts[warp * n + c] = wt;
-            L = fmaf(__ldcg(e + 1), wt, L);
+            for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            float L = 0.f;
+            for (int c = lane; c < n; c += 32) {
+              const float* e = part_of(c) + (r0 + warp) * kPart;
+              const float m = __ldcg(e), wt = m == -INFINITY ? 0.f : ex2(m - M);
+              wts[warp * n + c] = wt;
+              L = fmaf(__ldcg(e + 1), wt, L);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+            if (lane == 0) s_sum[warp] = L;
           }
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-          if (lane == 0) s_sum[warp] = L;
-        }
-        __syncthreads();
-        for (int i = tid; i < n_rows * HYQ_D; i += kThreads) {
-          const int r = i >> 7, d = i & (HYQ_D - 1);
-          float a = 0.f;
+          __syncthreads();
+          for (int i = tid; i < rows * (HYQ_D / 2); i += kThreads) {
+            const int r = i >> 6, d = 2 * (i & 63);
+            float2 a = make_float2(0.f, 0.f);
 #pragma unroll 16
-          for (int c = 0; c < n; ++c) a = fmaf(__ldcg(part_of(c) + r * kPart + 2 + d), wts[r * n + c], a);
-          const float L = s_sum[r];
-          out_at(r)[d] = __float2bfloat16_rn(L > 0.f ? a / L : 0.f);
+            for (int c = 0; c < n; ++c) {
+              const float2 v = __ldcg(reinterpret_cast<const float2*>(part_of(c) + (r0 + r) * kPart + 2 + d));
+              const float wt = wts[r * n + c];
+              a.x = fmaf(v.x, wt, a.x), a.y = fmaf(v.y, wt, a.y);
+            }
+            const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
+            *reinterpret_cast<uint32_t*>(out_at(r0 + r) + d) = pack_bf16x2(a.x * inv, a.y * inv);
+          }
+          __syncthreads();
         }
-        __syncthreads();
       }
     }
     // order this block's generic accesses to the rings before the next copies
@@ -414,24 +469,32 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_kernel(const Par
   }
 }
 
-int paged_grid() { return min(kBlocksPerSm * hyq_num_sms(), kMaxGrid); }
+// Query tiles that a group takes together.
+int group_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
+  const int gq = c->num_q_heads / c->num_kv_heads, tiles = (n_q * gq + kRowsQ - 1) / kRowsQ;
+  return blocks || tiles == 1 ? 1 : tiles == 2 ? 2 : kMaxNQ;
+}
 
-int query_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
-  const int gq = c->num_q_heads / c->num_kv_heads;
-  return blocks ? n_q : (n_q * gq + kRowsQ - 1) / kRowsQ;
+template <int BK, int BV, int NQ>
+cudaError_t launch(const Params& p, cudaStream_t s) {
+  using R = Ring<BK, BV, NQ>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = hyq_once_per_device(done, [] {
+    return cudaFuncSetAttribute(paged_kernel<BK, BV, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  paged_kernel<BK, BV, NQ><<<R::kPerSm * hyq_num_sms(), kThreads, R::kSmemBytes, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <int BK, int BV>
-cudaError_t launch(const Params& p, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = hyq_once_per_device(done, [] {
-    return cudaFuncSetAttribute(paged_kernel<BK, BV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Ring<BK, BV>::kSmemBytes);
-  });
-  if (e != cudaSuccess) return e;
-  paged_kernel<BK, BV><<<paged_grid(), kThreads, Ring<BK, BV>::kSmemBytes, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_nq(const Params& p, int nq, cudaStream_t s) {
+  return nq == 1 ? launch<BK, BV, 1>(p, s) : nq == 2 ? launch<BK, BV, 2>(p, s) : launch<BK, BV, kMaxNQ>(p, s);
 }
+
+// Partials of the largest grid: two slots of kMaxNQ query tiles on each SM
+// (one tile a block takes two blocks an SM, which is less).
+size_t part_bytes() { return hyq_align256((size_t)hyq_num_sms() * 2 * kMaxNQ * kRowsQ * kPart * 4); }
 
 }  // namespace
 
@@ -439,13 +502,14 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
 // group: calls of other shapes may share the workspace, since no call's
 // partials lie where another's tickets are.
 size_t hyq_paged_attention_ws_bytes(const hyq_config* c, int32_t batch, int32_t n_q) {
-  const size_t groups = (size_t)batch * c->num_kv_heads * n_q;  // n_q >= the dense query tiles
-  return hyq_align256((size_t)paged_grid() * 2 * kRowsQ * kPart * 4) + hyq_align256(groups * 4);
+  const size_t groups = (size_t)batch * c->num_kv_heads * n_q;  // at most a group a token
+  return part_bytes() + hyq_align256(groups * 4);
 }
 
 cudaError_t hyq_launch_paged_attention(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
                                        int32_t n_q, const void* q, int64_t ldq, const int32_t* sel, int32_t k_sel,
                                        void* out, void* ws, cudaStream_t s) {
+  const int nq = group_tiles(c, n_q, sel != nullptr);
   Params p;
   p.pv = pv;
   p.seqs = seqs;
@@ -454,16 +518,15 @@ cudaError_t hyq_launch_paged_attention(const hyq_config* c, const PageView& pv, 
   p.sel = sel;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.part = static_cast<float*>(ws);
-  p.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws) +
-                                         hyq_align256((size_t)paged_grid() * 2 * kRowsQ * kPart * 4));
+  p.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + part_bytes());
   p.batch = batch;
   p.n_q = n_q;
   p.HQ = c->num_q_heads;
   p.HKV = c->num_kv_heads;
   p.gq = c->num_q_heads / c->num_kv_heads;
-  p.QT = query_tiles(c, n_q, sel != nullptr);
+  p.QT = sel ? n_q : (n_q * p.gq + nq * kRowsQ - 1) / (nq * kRowsQ);
   p.k_sel = k_sel;
   const int bk = hyq_bits_k(c), bv = hyq_bits_v(c);
-  if (bk == 4) return bv == 4 ? launch<4, 4>(p, s) : launch<4, 8>(p, s);
-  return bv == 4 ? launch<8, 4>(p, s) : launch<8, 8>(p, s);
+  if (bk == 4) return bv == 4 ? launch_nq<4, 4>(p, nq, s) : launch_nq<4, 8>(p, nq, s);
+  return bv == 4 ? launch_nq<8, 4>(p, nq, s) : launch_nq<8, 8>(p, nq, s);
 }

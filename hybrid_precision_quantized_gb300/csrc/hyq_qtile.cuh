@@ -254,6 +254,20 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   }
 }
 
+// The running maximum of q_tiles and q_tile_multi is a reference that may lag:
+// it moves (and the accumulators are rescaled) only when a logit passes it by
+// more than kSlack<BV> in log2 units.  A probability is then at most 2^kSlack,
+// and p s still fits fp16: s is at most 2 * 65504 / qmax, 8734 for 4-bit and 514
+// for 8-bit values.  The first maximum of a row is seldom its last, so without
+// the slack short runs of tiles rescale at most of their tiles.
+template <int BV>
+constexpr float kSlack = BV == 4 ? 2.f : 6.f;
+// The slack in the scaled domain of a row with inv = 2^-sigma.
+template <int BV>
+__device__ __forceinline__ float slack_of(float inv) {
+  return kSlack<BV> * __int_as_float((254 << 23) - __float_as_int(inv));
+}
+
 // q_tile for NT adjacent tiles, every row seen by every query row and no row
 // left out by NaN steps: the tiles' independent chains overlap, and the
 // running maximum is tested once for all of them.
@@ -308,7 +322,7 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
 #pragma unroll
     for (int n = 1; n < NT; ++n) tm[j] = fmaxf(tm[j], fmaxf(lg[n][j], lg[n][2 + j]));
   }
-  if (__any_sync(0xffffffffu, tm[0] > st.m[0] || tm[1] > st.m[1])) {
+  if (__any_sync(0xffffffffu, tm[0] > st.m[0] + slack_of<BV>(qc.inv[0]) || tm[1] > st.m[1] + slack_of<BV>(qc.inv[1]))) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 4));
@@ -362,6 +376,167 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
           mma_f16(st.acc[2 * q + mm], y0 & 0x00FF00FFu, y1 & 0x00FF00FFu, odd_bytes(y0), odd_bytes(y1), b0, b1);
         }
       }
+    }
+  }
+}
+
+// q_tile for NQ tiles of query rows at once: a tile's codes are unpacked once
+// (the keys' once per two query tiles) and its scales converted once for all of
+// them.  The query operands stay in shared memory: bq_s, rowc_s and bz_s of
+// query tile k.  kRows as in q_tile, with lim[k] the number of the tile's rows that
+// heads 2t, 2t+1 of query tile k see.
+template <int BK, int BV, int NQ, bool kRows>
+__device__ __forceinline__ void q_tile_multi(const uint8_t* tb, int lane, int vr, const uint32_t (*bq_s)[4][HYQ_MAX_GQA][4][4],
+                                             const float (*rowc_s)[HYQ_MAX_GQA][4],
+                                             const uint32_t (*bz_s)[HYQ_MAX_GQA][4], const int (*lim_s)[HYQ_MAX_GQA],
+                                             int at, State (&st)[NQ]) {
+  using F = QFmt<BK, BV>;
+  const int g = lane >> 2, t = lane & 3;
+  float lg[NQ][4];
+  {
+    constexpr int kW = BK == 4 ? 8 : 16;
+    uint32_t kw[kW];
+    load_words<kW>(tb, lane, kw);
+    const uint4 ma = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
+    const uint4 mb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
+    const float2 a01 = half2_to_float2(ma.x), a23 = half2_to_float2(ma.y);
+    const float2 b01 = half2_to_float2(mb.x), b23 = half2_to_float2(mb.y);
+    const uint32_t za = (t & 1) ? ma.w : ma.z, zb = (t & 1) ? mb.w : mb.z;
+    constexpr int kStep = NQ < 2 ? 1 : 2;
+#pragma unroll
+    for (int k0 = 0; k0 < NQ; k0 += kStep) {
+      float C[kStep][4][4];
+#pragma unroll
+      for (int k = 0; k < kStep; ++k)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) C[k][q][0] = C[k][q][1] = C[k][q][2] = C[k][q][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 b[kStep];
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) b[k] = *reinterpret_cast<const uint4*>(&bq_s[k0 + k][i][g][t][0]);
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int ks = 2 * i + hf;
+          uint32_t x0, x1, x2, x3;
+          if (BK == 4) {
+            const uint32_t w = kw[ks % kW], w8 = w >> 8;
+            x0 = w & 0x000F000Fu, x1 = w & 0x00F000F0u, x2 = w8 & 0x000F000Fu, x3 = w8 & 0x00F000F0u;
+          } else {
+            const uint32_t w0 = kw[(2 * ks) % kW], w1 = kw[(2 * ks + 1) % kW];
+            x0 = w0 & 0x00FF00FFu, x1 = w1 & 0x00FF00FFu, x2 = odd_bytes(w0), x3 = odd_bytes(w1);
+          }
+#pragma unroll
+          for (int k = 0; k < kStep; ++k)
+            mma_f16(C[k][ks >> 1], x0, x1, x2, x3, hf ? b[k].z : b[k].x, hf ? b[k].w : b[k].y);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kStep; ++k) {
+        float(&l)[4] = lg[k0 + k];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float2 ksc = *reinterpret_cast<const float2*>(&rowc_s[k0 + k][2 * t + c][0]);
+          l[c] = ksc.x *
+                 fmaf(a01.x, C[k][0][c], fmaf(a01.y, C[k][1][c], fmaf(a23.x, C[k][2][c], a23.y * C[k][3][c])));
+          l[2 + c] = ksc.y * fmaf(b01.x, C[k][0][2 + c],
+                                  fmaf(b01.y, C[k][1][2 + c], fmaf(b23.x, C[k][2][2 + c], b23.y * C[k][3][2 + c])));
+        }
+        mma_f16(l, za, zb, 0u, 0u, bz_s[k0 + k][g][t], 0u);
+        if (kRows) {
+          const int v0 = lim_s[k0 + k][2 * t] - at, v1 = lim_s[k0 + k][2 * t + 1] - at;
+          if (g >= v0) l[0] = -INFINITY;
+          if (g >= v1) l[1] = -INFINITY;
+          if (g + 8 >= v0) l[2] = -INFINITY;
+          if (g + 8 >= v1) l[3] = -INFINITY;
+        }
+      }
+    }
+  }
+  // ---- running maxima, tested together, moved tile by tile --------------------
+  float inv[NQ][2], tm[NQ][2];
+  bool above[NQ], any = false;
+#pragma unroll
+  for (int k = 0; k < NQ; ++k) {
+    above[k] = false;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      inv[k][j] = rowc_s[k][2 * t + j][2];
+      tm[k][j] = fmaxf(lg[k][j], lg[k][2 + j]);
+      above[k] |= tm[k][j] > st[k].m[j] + slack_of<BV>(inv[k][j]);
+    }
+    any |= above[k];
+  }
+  if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+      if (!__any_sync(0xffffffffu, above[k])) continue;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float x = fmaxf(tm[k][j], __shfl_xor_sync(0xffffffffu, tm[k][j], 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        const float mn = fmaxf(st[k].m[j], x);
+        const float nm = mn == -INFINITY ? 0.f : -mn * inv[k][j];
+        const float corr = ex2(fmaf(st[k].m[j], inv[k][j], nm));
+        st[k].m[j] = mn;
+        st[k].nm[j] = nm;
+        st[k].l[j] *= corr;
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+          st[k].acc[mt][j] *= corr;
+          st[k].acc[mt][2 + j] *= corr;
+        }
+        st[k].zd[j] *= corr;
+      }
+    }
+  }
+  uint32_t pt0[NQ], pt1[NQ];
+#pragma unroll
+  for (int k = 0; k < NQ; ++k) {
+    float p[4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      p[j] = ex2(fmaf(lg[k][j], inv[k][j], st[k].nm[j]));
+      p[2 + j] = ex2(fmaf(lg[k][2 + j], inv[k][j], st[k].nm[j]));
+      st[k].l[j] += p[j] + p[2 + j];
+    }
+    pt0[k] = movmatrix_trans(pack_f16x2(p[0], p[1]));
+    pt1[k] = movmatrix_trans(pack_f16x2(p[2], p[3]));
+  }
+  const uint8_t* vm = tb + F::kVMeta;
+  uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
+  uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
+  uint32_t z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * (g & 3));
+  uint32_t z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * (g & 3));
+  if (kRows) {
+    const uint32_t k0 = (2 * t < vr ? 0xFFFFu : 0u) | (2 * t + 1 < vr ? 0xFFFF0000u : 0u);
+    const uint32_t k1 = (2 * t + 8 < vr ? 0xFFFFu : 0u) | (2 * t + 9 < vr ? 0xFFFF0000u : 0u);
+    sv0.x &= k0, sv0.y &= k0, sv0.z &= k0, sv0.w &= k0, z0 &= k0;
+    sv1.x &= k1, sv1.y &= k1, sv1.z &= k1, sv1.w &= k1, z1 &= k1;
+  }
+#pragma unroll
+  for (int k = 0; k < NQ; ++k) mma_f16(st[k].zd, z0, 0u, z1, 0u, pt0[k], pt1[k]);
+  constexpr int kV = BV == 4 ? 8 : 16;
+  uint32_t vw[kV];
+  load_words<kV>(tb + F::kVCode, lane, vw);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t b0[NQ], b1[NQ];
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) b0[k] = hmul2_u32(pt0[k], u4c(sv0, q)), b1[k] = hmul2_u32(pt1[k], u4c(sv1, q));
+#pragma unroll
+    for (int mm = 0; mm < 2; ++mm) {
+      uint32_t x0, x1, x2, x3;
+      if (BV == 4) {
+        const uint32_t x = vw[(2 * q + mm) % kV], x8 = x >> 8;
+        x0 = x & 0x000F000Fu, x1 = x & 0x00F000F0u, x2 = x8 & 0x000F000Fu, x3 = x8 & 0x00F000F0u;
+      } else {
+        const uint32_t y0 = vw[(2 * (2 * q + mm)) % kV], y1 = vw[(2 * (2 * q + mm) + 1) % kV];
+        x0 = y0 & 0x00FF00FFu, x1 = y1 & 0x00FF00FFu, x2 = odd_bytes(y0), x3 = odd_bytes(y1);
+      }
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) mma_f16(st[k].acc[2 * q + mm], x0, x1, x2, x3, b0[k], b1[k]);
     }
   }
 }
