@@ -32,8 +32,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowsQ = HYQ_MAX_GQA;    // query rows per tile (MMA N)
-constexpr int kPart = 2 + HYQ_D;       // m, l, acc[128] per query row
-constexpr int kMinUnits = 16;          // units per block before a group is split further
+constexpr int kPart = HYQ_D + 4;       // acc[128], m, l and two unused floats per query row
+constexpr int kMinUnits = 8;           // units per block before a group is split further
+constexpr int kMaxParts = 1024;        // blocks of the largest grid (two on each of 512 SMs)
 constexpr int kMaxNQ = 4;             // query tiles that one block takes together
 
 // The kernel's shape for NQ query tiles a group.  One tile: two blocks an SM
@@ -53,6 +54,7 @@ struct Ring : QFmt<BK, BV> {
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
   // query tiles whose partials a warp's ring holds at once
   static constexpr int kJoin = NQ * 4096 <= kWarpBytes ? NQ : NQ > 2 && 2 * 4096 <= kWarpBytes ? 2 : 1;
+  static_assert(kSmemBytes >= 32 * kMaxParts + kThreads * 16, "the join's weights and sums");
   static_assert(kJoin * 4096 <= kWarpBytes && NQ % kJoin == 0, "a warp's partial fits its ring");
   static_assert(kWarps % kPerPage == 0, "a warp's units take the same part of their pages");
 };
@@ -95,6 +97,83 @@ struct Shares {
     return (int)(x < wide ? div_fast(x, each + 1) : more + div_fast(x - wide, each));
   }
 };
+
+// Output row of (token, head) pair `flat` of a KV head whose first row is `out`.
+__device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, int gq, int flat) {
+  const int tok = flat / gq;
+  return out + ((size_t)tok * HQ + (flat - tok * gq)) * HYQ_D;
+}
+
+// One block: joins the n partials of a group's n_rows rows.  Part i lies at
+// parts + i stride, the first one `first` further.  Out of line, so that its
+// registers are its own: a thread takes four elements of a row over every
+// S-th part and has kHold of them under way before the weights are known.
+__device__ __noinline__ void join_parts(const float* parts, int first, int stride, int n, int n_rows, uint8_t* smem,
+                                        float* s_sum, __nv_bfloat16* out, int HQ, int gq, int flat0) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* wts = reinterpret_cast<float*>(smem);                           // [8][n] weights
+  float4* sums = reinterpret_cast<float4*>(smem + 8 * 4 * kMaxParts);  // [S][rows * 32]
+  auto part_of = [&](int i) { return parts + (size_t)i * stride + (i == 0 ? first : 0); };
+  constexpr int kHold = 20;
+  for (int r0 = 0; r0 < n_rows; r0 += kRowsQ) {
+    const int rows = min(kRowsQ, n_rows - r0);
+    const int items = rows * (HYQ_D / 4), S = kThreads / items, share = tid / items, item = tid - share * items;
+    const int r = item >> 5, d = 4 * (item & 31);
+    const int mine = share < S ? (n - share + S - 1) / S : 0;  // parts share, share + S, ...
+    const float* at = parts + (size_t)share * stride + (r0 + r) * kPart + d;
+    float4 v[kHold];
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+      v[k] = k < mine ? __ldcg(reinterpret_cast<const float4*>(at + (size_t)k * S * stride + (share + k == 0 ? first : 0)))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (warp < rows) {
+      float M = -INFINITY, L = 0.f;
+      for (int c = lane; c < n; c += 32) {
+        const float m = __ldcg(part_of(c) + (r0 + warp) * kPart + HYQ_D);
+        wts[warp * n + c] = m;
+        M = fmaxf(M, m);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      for (int c = lane; c < n; c += 32) {
+        const float m = wts[warp * n + c], wt = m == -INFINITY ? 0.f : ex2(m - M);
+        wts[warp * n + c] = wt;
+        L = fmaf(__ldcg(part_of(c) + (r0 + warp) * kPart + HYQ_D + 1), wt, L);
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      if (lane == 0) s_sum[warp] = L;
+    }
+    __syncthreads();
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float* wr = wts + r * n + share;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const float wt = k < mine ? wr[S * k] : 0.f;
+      a.x = fmaf(wt, v[k].x, a.x), a.y = fmaf(wt, v[k].y, a.y), a.z = fmaf(wt, v[k].z, a.z), a.w = fmaf(wt, v[k].w, a.w);
+    }
+#pragma unroll 8
+    for (int k = kHold; k < mine; ++k) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(at + (size_t)k * S * stride));
+      const float wt = wr[S * k];
+      a.x = fmaf(wt, x.x, a.x), a.y = fmaf(wt, x.y, a.y), a.z = fmaf(wt, x.z, a.z), a.w = fmaf(wt, x.w, a.w);
+    }
+    if (S > 1) {
+      if (share < S) sums[tid] = a;
+      __syncthreads();
+    }
+    if (share == 0) {
+      for (int k = 1; k < S; ++k) {
+        const float4 x = sums[k * items + item];
+        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+      }
+      const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
+      *reinterpret_cast<uint2*>(out_row(out, HQ, gq, flat0 + r0 + r) + d) =
+          make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    }
+    __syncthreads();
+  }
+}
 
 template <int BK, int BV, int NQ>
 __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kernel(const Params p) {
@@ -215,6 +294,23 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     const int n_rows = p.sel ? p.gq : min(kRowsG, p.n_q * p.gq - kRowsG * qt);
     const size_t page_bytes = (size_t)p.HKV * R::kBlock;
 
+    // Row r of the group is (token, head) pair flat0 + r of the KV head's, in
+    // order; with block lists a group is one token's heads.
+    const int flat0 = p.sel ? qt * p.gq : qt * kRowsG;
+    auto token_of = [&](int r) { return (flat0 + r) / p.gq; };
+    __nv_bfloat16* out_bh = p.out + ((size_t)b * p.n_q * p.HQ + (size_t)h * p.gq) * HYQ_D;
+    // the query rows, row `warp` of each query tile: loaded ahead of the page
+    // numbers, prepared while the first copies are under way
+    uint2 qv[NQ];
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+      const int r = kRowsQ * k + warp, tok = token_of(r);
+      qv[k] = make_uint2(0, 0);
+      if (r < n_rows)
+        qv[k] = __ldg(reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.n_q + tok) * p.ldq +
+                                                     (size_t)(h * p.gq + flat0 + r - tok * p.gq) * HYQ_D + 4 * lane));
+    }
+
     // ---- this warp's units: w0 + warp, + 8, ... ---------------------------
     // kPerPage divides 8, so all of them take the same part of their pages.
     const int nj = w1 - w0 > warp ? (w1 - w0 - warp + kWarps - 1) / kWarps : 0;
@@ -274,20 +370,11 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     for (int j = 0; j < kSlots; ++j) at_slot[j] = j < nj && !dead ? issue(j) : -1;
 
     // ---- the query rows: warp r prepares row r of each query tile ----------
-    // Token and head of row r of the group: rows are (token, head) pairs in
-    // order; with block lists a group is one token's heads.
-    auto token_of = [&](int r) { return p.sel ? qt : (kRowsG * qt + r) / p.gq; };
-    auto head_of = [&](int r, int tok) { return p.sel ? r : kRowsG * qt + r - tok * p.gq; };
 #pragma unroll
     for (int k = 0; k < NQ; ++k) {
       const int r = kRowsQ * k + warp;
-      const int tok = token_of(r), head = head_of(r, tok);
-      uint2 v = make_uint2(0, 0);
-      if (r < n_rows)
-        v = __ldg(reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.n_q + tok) * p.ldq +
-                                                 (size_t)(h * p.gq + head) * HYQ_D + 4 * lane));
-      prep_query_row<BK>(warp, lane, v, bq_s[k], rowc_s[k], bz_s[k]);
-      if (lane == 0) lim_s[k][warp] = r < n_rows ? max(0, len - p.n_q + 1 + tok) : len;
+      prep_query_row<BK>(warp, lane, qv[k], bq_s[k], rowc_s[k], bz_s[k]);
+      if (lane == 0) lim_s[k][warp] = r < n_rows ? max(0, len - p.n_q + 1 + token_of(r)) : len;
     }
     __syncthreads();
     uint32_t bq[8][2];
@@ -347,10 +434,6 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     __syncwarp();
     const bool whole = w0 == 0 && w1 == n_units;
     float* pp = p.part + ((size_t)blockIdx.x * 2 + (w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
-    auto out_at = [&](int r) {
-      const int tok = token_of(r);
-      return p.out + (((size_t)b * p.n_q + tok) * p.HQ + (size_t)h * p.gq + head_of(r, tok)) * HYQ_D;
-    };
     constexpr int kJoin = R::kJoin;
 #pragma unroll
     for (int k0 = 0; k0 < NQ; k0 += kJoin) {
@@ -377,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
         if (w == 0) {
           s_sum[r] = L;
           if (!whole && kRowsQ * k0 + r < n_rows) {
-            pp[(kRowsQ * k0 + r) * kPart + 0] = M;
-            pp[(kRowsQ * k0 + r) * kPart + 1] = L;
+            pp[(kRowsQ * k0 + r) * kPart + HYQ_D] = M;
+            pp[(kRowsQ * k0 + r) * kPart + HYQ_D + 1] = L;
           }
         }
       }
@@ -398,12 +481,10 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
         if (x & 2) a = make_float4(a.z, a.w, a.x, a.y);
         if (whole) {
           const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
-          *reinterpret_cast<uint2*>(out_at(kRowsQ * k0 + r) + d) =
+          *reinterpret_cast<uint2*>(out_row(out_bh, p.HQ, p.gq, flat0 + kRowsQ * k0 + r) + d) =
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
         } else {
-          float2* to = reinterpret_cast<float2*>(pp + (kRowsQ * k0 + r) * kPart + 2 + d);
-          to[0] = make_float2(a.x, a.y);
-          to[1] = make_float2(a.z, a.w);
+          *reinterpret_cast<float4*>(pp + (kRowsQ * k0 + r) * kPart + d) = a;
         }
       }
       __syncthreads();  // the rings are free again
@@ -421,47 +502,11 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       }
       __syncthreads();
       if (s_last) {
-        float* wts = reinterpret_cast<float*>(smem);  // [8][n] weights
-        const int n = c1 - c0 + 1;
         // part i: slot 0 of block c0 + i, where its run ends this group; the
         // first block's is slot 1 when its run holds the group's first unit
-        constexpr size_t kSlot = (size_t)NQ * kRowsQ * kPart;
-        const float* parts = p.part + (size_t)c0 * 2 * kSlot;
-        const size_t first = sh.begin(c0) <= base ? kSlot : 0;
-        auto part_of = [&](int i) { return parts + (size_t)i * (2 * kSlot) + (i == 0 ? first : 0); };
-        for (int r0 = 0; r0 < n_rows; r0 += kRowsQ) {
-          const int rows = min(kRowsQ, n_rows - r0);
-          if (warp < rows) {
-            float M = -INFINITY;
-            for (int c = lane; c < n; c += 32) M = fmaxf(M, __ldcg(part_of(c) + (r0 + warp) * kPart));
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float L = 0.f;
-            for (int c = lane; c < n; c += 32) {
-              const float* e = part_of(c) + (r0 + warp) * kPart;
-              const float m = __ldcg(e), wt = m == -INFINITY ? 0.f : ex2(m - M);
-              wts[warp * n + c] = wt;
-              L = fmaf(__ldcg(e + 1), wt, L);
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (lane == 0) s_sum[warp] = L;
-          }
-          __syncthreads();
-          for (int i = tid; i < rows * (HYQ_D / 2); i += kThreads) {
-            const int r = i >> 6, d = 2 * (i & 63);
-            float2 a = make_float2(0.f, 0.f);
-#pragma unroll 16
-            for (int c = 0; c < n; ++c) {
-              const float2 v = __ldcg(reinterpret_cast<const float2*>(part_of(c) + (r0 + r) * kPart + 2 + d));
-              const float wt = wts[r * n + c];
-              a.x = fmaf(v.x, wt, a.x), a.y = fmaf(v.y, wt, a.y);
-            }
-            const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
-            *reinterpret_cast<uint32_t*>(out_at(r0 + r) + d) = pack_bf16x2(a.x * inv, a.y * inv);
-          }
-          __syncthreads();
-        }
+        constexpr int kSlot = NQ * kRowsQ * kPart;
+        join_parts(p.part + (size_t)c0 * 2 * kSlot, sh.begin(c0) <= base ? kSlot : 0, 2 * kSlot, c1 - c0 + 1, n_rows,
+                   smem, s_sum, out_bh, p.HQ, p.gq, flat0);
       }
     }
     // order this block's generic accesses to the rings before the next copies
@@ -483,7 +528,8 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
     return cudaFuncSetAttribute(paged_kernel<BK, BV, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  paged_kernel<BK, BV, NQ><<<R::kPerSm * hyq_num_sms(), kThreads, R::kSmemBytes, s>>>(p);
+  const int grid = min(R::kPerSm * hyq_num_sms(), kMaxParts);
+  paged_kernel<BK, BV, NQ><<<grid, kThreads, R::kSmemBytes, s>>>(p);
   return cudaGetLastError();
 }
 
