@@ -13,16 +13,19 @@
 // per byte; at one sequence the latency of the launch, the dependent loads
 // (table, record) and the selection.
 //
-// One block scores a strided share of one list's blocks (eight lanes per
-// record, 16-byte loads) into the workspace; the last block of the list to
-// finish selects: the k-th largest key bit by bit, then one ordered pass.
+// One block scores a strided share of one list's blocks into the workspace:
+// a warp has 16 records under way (eight lanes each, 16-byte loads), asked for
+// before the query's codes are made.  The last block of the list to finish
+// selects: the k-th largest key by 8-bit histograms from the highest bit in
+// which the keys differ (two passes as a rule), then one ordered pass.
 #include "hyq_paged.cuh"
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPerIter = kThreads / 8;  // records scored per block and pass
+constexpr int kBatch = 16;              // records that a warp has under way
+constexpr int kPerIter = kWarps * kBatch;  // records scored per block and pass
 constexpr int kKeys = 8192;             // keys of a list held in shared memory (32 KB)
 
 struct SelectParams {
@@ -59,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
   extern __shared__ uint32_t s_keys[];  // kKeys
   __shared__ __align__(16) int16_t s_a[HYQ_D], s_n[HYQ_D];
   __shared__ float s_red[kWarps];
-  __shared__ int s_cnt[kWarps];
+  __shared__ int s_cnt[kWarps], s_hist[256], s_pick[3];
   __shared__ uint32_t s_and[kWarps], s_or[kWarps];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -77,6 +80,31 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
       for (int i = tid; i < p.k; i += kThreads) sel[i] = i < nb ? i : -1;
     return;
   }
+  // ---- the first records: lane i < 16 holds the page of record i, eight lanes
+  // then read a record each time, 16 elements a lane ---------------------------
+  const int part = lane & 7, which = lane >> 3;  // record 4 x + which in step x
+  const int32_t* table = p.pv.table + (size_t)seq * p.pv.max_blocks;
+  uint32_t* keys = p.keys + list * p.pv.max_blocks;
+  int j0 = blockIdx.x * kPerIter + warp * kBatch;
+  auto page_at = [&](int j) { return lane < kBatch && j + lane < nb ? __ldg(table + j + lane) : -1; };
+  int page = page_at(j0), page_next = page_at(j0 + gridDim.x * kPerIter);
+  int4 lo[kBatch / 4], hi[kBatch / 4];
+  int ex[kBatch / 4];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int x = 0; x < kBatch / 4; ++x) {
+      const int pg = __shfl_sync(0xffffffffu, page, 4 * x + which);
+      lo[x] = hi[x] = make_int4(0, 0, 0, 0);
+      ex[x] = INT32_MIN;  // no record
+      if ((uint32_t)pg < (uint32_t)p.pv.n_pages) {
+        const uint8_t* rec = p.pv.bounds + ((size_t)pg * p.HKV + h) * HYQ_BOUND_BYTES;
+        lo[x] = __ldg(reinterpret_cast<const int4*>(rec) + part);
+        hi[x] = __ldg(reinterpret_cast<const int4*>(rec + HYQ_D) + part);
+        ex[x] = __ldg(reinterpret_cast<const int*>(rec + 2 * HYQ_D));
+      }
+    }
+  };
+  fetch();
   // ---- the query's codes: thread i < 128 holds element i of every head ------
   float x[HYQ_MAX_GQA], am = 0.f;
   const __nv_bfloat16* q = p.q + ((size_t)b * p.n_q + tok) * p.ldq + (size_t)h * p.gq * HYQ_D;
@@ -108,27 +136,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
   }
   if (odd && tid == 0 && blockIdx.x == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_SCORE);
   __syncthreads();
-  // ---- scores: eight lanes a record, 16 elements each -----------------------
-  const int part = lane & 7;
   int a[8], n[8];  // pairs of int16
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     a[i] = reinterpret_cast<const int*>(s_a)[8 * part + i];
     n[i] = reinterpret_cast<const int*>(s_n)[8 * part + i];
   }
-  const int32_t* table = p.pv.table + (size_t)seq * p.pv.max_blocks;
-  uint32_t* keys = p.keys + list * p.pv.max_blocks;
-  for (int j0 = blockIdx.x * kPerIter; j0 < nb; j0 += gridDim.x * kPerIter) {
-    const int j = j0 + (tid >> 3);
-    const int page = j < nb ? __ldg(table + j) : 0;
-    const bool ok = j < nb && page >= 0 && page < p.pv.n_pages;
-    int acc = 0, e = 0;
-    if (ok) {
-      const uint8_t* rec = p.pv.bounds + ((size_t)page * p.HKV + h) * HYQ_BOUND_BYTES;
-      const int4 lo = __ldg(reinterpret_cast<const int4*>(rec) + part);
-      const int4 hi = __ldg(reinterpret_cast<const int4*>(rec + HYQ_D) + part);
-      if (part == 0) e = __ldg(reinterpret_cast<const int*>(rec + 2 * HYQ_D));
-      const int l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
+  // ---- scores -----------------------------------------------------------------
+  for (; j0 < nb; j0 += gridDim.x * kPerIter) {
+#pragma unroll
+    for (int s = 0; s < kBatch / 4; ++s) {
+      const int l[4] = {lo[s].x, lo[s].y, lo[s].z, lo[s].w}, u[4] = {hi[s].x, hi[s].y, hi[s].z, hi[s].w};
+      int acc = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         acc = __dp2a_lo(a[2 * i], u[i], acc);
@@ -136,16 +155,19 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
         acc = __dp2a_lo(n[2 * i], l[i], acc);
         acc = __dp2a_hi(n[2 * i + 1], l[i], acc);
       }
-    } else if (j < nb && part == 0) {
-      hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-    }
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (j < nb && part == 0) {
-      const bool forced = j < p.n_first || j >= nb - p.n_last;
-      // 0 and all ones lie outside the keys of finite scores
-      keys[j] = forced ? 0xFFFFFFFFu : ok ? key_of((float)acc * pow2_int(min(max(e, -126), 127))) : 0u;
+      for (int o = 1; o < 8; o <<= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+      const int j = j0 + 4 * s + which;
+      if (j < nb && part == 0) {
+        const bool forced = j < p.n_first || j >= nb - p.n_last, ok = ex[s] != INT32_MIN;
+        if (!ok) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+        // 0 and all ones lie outside the keys of finite scores
+        keys[j] = forced ? 0xFFFFFFFFu : ok ? key_of((float)acc * pow2_int(min(max(ex[s], -126), 127))) : 0u;
+      }
     }
+    page = page_next;
+    page_next = page_at(j0 + 2 * gridDim.x * kPerIter);
+    if (j0 + gridDim.x * kPerIter < nb) fetch();
   }
   // ---- the last block of the list selects ------------------------------------
   __syncthreads();
@@ -179,35 +201,62 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) all_and &= s_and[i], all_or |= s_or[i];
   auto key = [&](int i) { return held ? s_keys[i] : __ldcg(keys + i); };
-  // The largest value v with at least `want` keys >= v among those not forced
-  // (want >= 1 as fewer blocks than k are forced or all keys are): bit by bit
-  // from the highest in which they differ.
-  const int want = p.k - forced;
+  // The bound v and the number `take` of keys equal to it that make `want`
+  // selected keys among those not forced: digit by digit, `want` the keys still
+  // to be found among those that agree with v above `shift`.
+  int want = p.k - forced;
   uint32_t v = all_and;
-  if (want > 0) {
-    const uint32_t diff = all_and ^ all_or;
-    if (diff) {
-      const int top = 31 - __clz(diff);
-      v = all_and & ~((2u << top) - 1u);
-      for (int bit = top; bit >= 0; --bit) {
-        const uint32_t c = v | (1u << bit);
-        int n_ge = 0;
-        for (int i = tid; i < nb; i += kThreads) {
-          const uint32_t u = key(i);
-          n_ge += u >= c && u != 0xFFFFFFFFu;
+  if (want <= 0) {
+    v = 0xFFFFFFFEu;  // the forced blocks alone
+  } else if (all_and != all_or) {
+    const int top = 31 - __clz(all_and ^ all_or);
+    v = all_and & ~((2u << top) - 1u);
+    for (int high = top + 1; high > 0;) {
+      const int shift = max(high - 8, 0);
+      const uint32_t digits = (1u << (high - shift)) - 1u;
+      for (int i = tid; i < 256; i += kThreads) s_hist[i] = 0;
+      __syncthreads();
+      for (int i = tid; i < nb; i += kThreads) {
+        const uint32_t u = key(i);
+        if (u != 0xFFFFFFFFu && (high == 32 || (u >> high) == (v >> high))) atomicAdd(&s_hist[(u >> shift) & digits], 1);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        // lane l: digits 255 - 8 l .. 248 - 8 l, the largest first
+        int c[8], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += c[i] = s_hist[255 - 8 * lane - i];
+        int pre = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += y;
         }
-        if (block_sum(n_ge, s_cnt) >= want) v = c;
+        int before = pre - sum;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (before < want && before + c[i] >= want) s_pick[0] = 255 - 8 * lane - i, s_pick[1] = before, s_pick[2] = c[i];
+          before += c[i];
+        }
+      }
+      __syncthreads();
+      v |= (uint32_t)s_pick[0] << shift;
+      want -= s_pick[1];
+      const bool whole = s_pick[2] == want;
+      high = shift;
+      if (whole && shift > 0) {  // every key of this digit is selected: a bound just below them
+        v -= 1u;
+        want = 0;
+        break;
       }
     }
-  } else {
-    v = 0xFFFFFFFEu;  // the forced blocks alone
   }
   // ranks: every key above v, and the first `want - above` equal to it
   int gt = 0, eq = 0;
   for (int i = i0; i < i1; ++i) {
     const uint32_t u = key(i);
     gt += u > v;
-    eq += u == v && want > 0;
+    eq += u == v && want > 0;  // want > 0: ties are left to take
   }
   const int above = block_sum(gt, s_cnt);
   // exclusive prefix of (gt, eq) over the threads

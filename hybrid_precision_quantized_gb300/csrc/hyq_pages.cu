@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
   __shared__ int s_seq[kThreads], s_last[kThreads];
   __shared__ int s_scan[kWarps];
   __shared__ int s_have[kThreads], s_need[kThreads], s_off[kThreads], s_copy[kThreads];
+  let_next_start();
   const int i = threadIdx.x;
   const bool row = i < batch;
   int err = 0, s = -1, len = 0, n = 0, have = 0, last = -1, old_refs = 0;
@@ -194,35 +195,48 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
 
 constexpr int kCopyThreads = 128;
 
-// Copies `bytes` (a multiple of 16, 16-byte aligned) with the whole block.
-__device__ __forceinline__ void copy_block(uint8_t* dst, const uint8_t* src, int bytes) {
+// One block: `bytes` of a page's block for one KV head and layer (a multiple of
+// 16) and its bound record, all loads of a thread ahead of its stores: a whole
+// block of any code width is at most kDeep loads a thread.
+constexpr int kDeep = 9;
+static_assert(HYQ_QBLOCK_BYTES_BITS(8, 8) <= kDeep * 16 * kCopyThreads, "a block in one go");
+static_assert(HYQ_BOUND_BYTES / 16 <= kCopyThreads, "a record in one go");
+__device__ __forceinline__ void copy_block(uint8_t* dst, const uint8_t* src, int bytes, uint8_t* rec_dst,
+                                           const uint8_t* rec_src) {
   const uint4* a = reinterpret_cast<const uint4*>(src);
   uint4* b = reinterpret_cast<uint4*>(dst);
-  const int n = bytes / 16;
-  int i = threadIdx.x;
-  for (; i + 3 * kCopyThreads < n; i += 4 * kCopyThreads) {
-    uint4 v[4];
+  const int n = bytes / 16, i = threadIdx.x;
+  uint4 v[kDeep], r;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __ldcs(a + i + k * kCopyThreads);
+  for (int k = 0; k < kDeep; ++k)
+    if (i + k * kCopyThreads < n) v[k] = __ldcs(a + i + k * kCopyThreads);
+  if (i < HYQ_BOUND_BYTES / 16) r = *(reinterpret_cast<const uint4*>(rec_src) + i);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) b[i + k * kCopyThreads] = v[k];
-  }
-  for (; i < n; i += kCopyThreads) b[i] = __ldcs(a + i);
+  for (int k = 0; k < kDeep; ++k)
+    if (i + k * kCopyThreads < n) b[i + k * kCopyThreads] = v[k];
+  if (i < HYQ_BOUND_BYTES / 16) *(reinterpret_cast<uint4*>(rec_dst) + i) = r;
+}
+// a / b and the remainder, in 32 bits when they fit.
+__device__ __forceinline__ int split(int64_t a, int b, int* rest) {
+  const int q = a >> 32 ? (int)(a / b) : (int)((uint32_t)a / (uint32_t)b);
+  *rest = (int)(a - (int64_t)q * b);
+  return q;
 }
 
 // The copies of a reserve: an item is one (row, layer, KV head).
 __global__ void __launch_bounds__(kCopyThreads) reserve_copy_kernel(const hyq_pages p, ReserveWs ws, int HKV,
                                                                     int block_bytes) {
-  const int n = *ws.count;
-  const int64_t items = (int64_t)n * p.n_layers * HKV;
+  wait_previous();
+  const int n = *ws.count, per = p.n_layers * HKV;
+  const int64_t items = (int64_t)n * per;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int per = p.n_layers * HKV;
-    const int row = (int)(it / per), x = (int)(it - (int64_t)row * per), layer = x / HKV, h = x - layer * HKV;
+    int x;
+    const int row = split(it, per, &x), layer = x / HKV, h = x - layer * HKV;
     const int src = ws.src[row];
     if (src < 0) continue;
     const size_t a = ((size_t)layer * p.n_pages + src) * HKV + h, b = ((size_t)layer * p.n_pages + ws.dst[row]) * HKV + h;
-    copy_block(p.pool + b * block_bytes, p.pool + a * block_bytes, ws.tiles[row] * (block_bytes / 4));
-    copy_block(p.bounds + b * HYQ_BOUND_BYTES, p.bounds + a * HYQ_BOUND_BYTES, HYQ_BOUND_BYTES);
+    copy_block(p.pool + b * block_bytes, p.pool + a * block_bytes, ws.tiles[row] * (block_bytes / 4),
+               p.bounds + b * HYQ_BOUND_BYTES, p.bounds + a * HYQ_BOUND_BYTES);
   }
 }
 
@@ -309,6 +323,7 @@ CompactWs compact_ws(void* ws, int n_pages) {
 // One block: the number of pages in use N, the two lists, the map and the new refs.
 __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const hyq_pages p, int32_t* refs_out, CompactWs ws) {
   __shared__ int s_scan[kWarps];
+  let_next_start();
   const int tid = threadIdx.x, np = p.n_pages;
   constexpr int kPass = kThreads * kScan;
   int mine = 0;
@@ -346,6 +361,7 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const hyq_pages 
 // The table through the map, and the pages: an item is one (move, layer, KV head).
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const hyq_pages p, int32_t* table_out,
                                                                     CompactWs ws, int HKV, int block_bytes) {
+  wait_previous();
   const int64_t entries = (int64_t)p.n_seqs * p.max_blocks;
   for (int64_t x = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; x < entries;
        x += (int64_t)gridDim.x * kCopyThreads) {
@@ -360,11 +376,12 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const hyq_pa
   const int n = *ws.count, per = p.n_layers * HKV;
   const int64_t items = (int64_t)n * per;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int m = (int)(it / per), x = (int)(it - (int64_t)m * per), layer = x / HKV, h = x - layer * HKV;
+    int x;
+    const int m = split(it, per, &x), layer = x / HKV, h = x - layer * HKV;
     const size_t a = ((size_t)layer * p.n_pages + ws.src[m]) * HKV + h,
                  b = ((size_t)layer * p.n_pages + ws.dst[m]) * HKV + h;
-    copy_block(p.pool + b * block_bytes, p.pool + a * block_bytes, block_bytes);
-    copy_block(p.bounds + b * HYQ_BOUND_BYTES, p.bounds + a * HYQ_BOUND_BYTES, HYQ_BOUND_BYTES);
+    copy_block(p.pool + b * block_bytes, p.pool + a * block_bytes, block_bytes, p.bounds + b * HYQ_BOUND_BYTES,
+               p.bounds + a * HYQ_BOUND_BYTES);
   }
 }
 
@@ -385,9 +402,8 @@ cudaError_t hyq_launch_pages_reserve(const hyq_config* c, const hyq_pages* p, co
   reserve_kernel<<<1, kThreads, 0, s>>>(*p, seqs, batch, n_new, w);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  reserve_copy_kernel<<<copy_grid((int64_t)batch * p->n_layers * c->num_kv_heads), kCopyThreads, 0, s>>>(
-      *p, w, c->num_kv_heads, (int)hyq_qblock_bytes(c));
-  return cudaGetLastError();
+  return hyq_launch_second(reserve_copy_kernel, dim3(copy_grid((int64_t)batch * p->n_layers * c->num_kv_heads)),
+                           kCopyThreads, s, *p, w, (int)c->num_kv_heads, (int)hyq_qblock_bytes(c));
 }
 
 cudaError_t hyq_launch_pages_fork(const hyq_pages* p, const int32_t* src, const int32_t* dst, int32_t n,
@@ -411,7 +427,6 @@ cudaError_t hyq_launch_pages_compact(const hyq_config* c, const hyq_pages* p, in
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t half = ((int64_t)p->n_pages / 2 + 1) * p->n_layers * c->num_kv_heads;  // moves are at most n_pages / 2
-  compact_move_kernel<<<copy_grid(half), kCopyThreads, 0, s>>>(*p, table_out ? table_out : p->table, w,
-                                                               c->num_kv_heads, (int)hyq_qblock_bytes(c));
-  return cudaGetLastError();
+  return hyq_launch_second(compact_move_kernel, dim3(copy_grid(half)), kCopyThreads, s, *p,
+                           table_out ? table_out : p->table, w, (int)c->num_kv_heads, (int)hyq_qblock_bytes(c));
 }
