@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 16;              // records that a warp has under way
 constexpr int kPerIter = kWarps * kBatch;  // records scored per block and pass
+constexpr int kPerSm = 4;               // resident blocks an SM
 constexpr int kKeys = 8192;             // keys of a list held in shared memory (32 KB)
 
 struct SelectParams {
@@ -58,7 +59,7 @@ __device__ __forceinline__ int block_sum(int v, int* s) {
 }
 
 // grid (shares, n_q * HKV, batch)
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t s_keys[];  // kKeys
   __shared__ __align__(16) int16_t s_a[HYQ_D], s_n[HYQ_D];
   __shared__ float s_red[kWarps];
@@ -285,8 +286,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 }
 
 int shares_of(int64_t lists, int32_t max_blocks) {
-  // enough blocks to fill the GPU, and no more than there are passes
-  const int64_t fill = (4 * (int64_t)hyq_num_sms() + lists - 1) / lists;
+  // at most the blocks that are resident together (a second wave costs more
+  // than longer shares: 256 lists of a thousand blocks 22.3 against 20.6 us), and
+  // no more than there are passes
+  const int64_t fill = kPerSm * (int64_t)hyq_num_sms() / lists;
   const int64_t most = (max_blocks + kPerIter - 1) / kPerIter;
   return (int)(fill < most ? (fill > 1 ? fill : 1) : most);
 }

@@ -82,16 +82,19 @@ __host__ __device__ __forceinline__ ReserveWs reserve_ws(void* ws) {
   return r;
 }
 
+constexpr int kTakeHeld = 4096;  // pages taken that are listed in shared memory
+
 // One block; thread i handles call row i (batch <= kThreads).
 __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, const int32_t* seqs, int batch,
                                                            const int32_t* n_new, ReserveWs ws) {
   static_assert(HYQ_PAGED_MAX_BATCH <= kThreads, "one row per thread");
-  __shared__ int s_seq[kThreads], s_last[kThreads];
-  __shared__ int s_scan[kWarps];
+  __shared__ __align__(16) int s_seq[kThreads], s_last[kThreads];
+  __shared__ int s_scan[kWarps], s_take[kTakeHeld];
   __shared__ int s_have[kThreads], s_need[kThreads], s_off[kThreads], s_copy[kThreads];
   let_next_start();
   const int i = threadIdx.x;
   const bool row = i < batch;
+  uint32_t used = used_mask(p.refs, i * kScan, p.n_pages);  // the scan's first pass, under way with the rows
   int err = 0, s = -1, len = 0, n = 0, have = 0, last = -1, old_refs = 0;
   int64_t need64 = 0;
   if (row) {
@@ -125,9 +128,14 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
   // the same sequence before this row; rows before it that leave the same page
   int rank = 0;
   if (row && s >= 0)
-    for (int j = 0; j < i; ++j) {
-      if (s_seq[j] == s) err |= HYQ_DEVERR_INDEX;
-      rank += last >= 0 && s_last[j] == last;
+    for (int j = 0; j < i; j += 4) {
+      const int4 a = *reinterpret_cast<const int4*>(s_seq + j), b = *reinterpret_cast<const int4*>(s_last + j);
+      const int sj[4] = {a.x, a.y, a.z, a.w}, lj[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (j + k < i && sj[k] == s) err |= HYQ_DEVERR_INDEX;
+        rank += j + k < i && last >= 0 && lj[k] == last;
+      }
     }
   // as if in order: each leaves the page while another still holds it
   const bool copy = last >= 0 && old_refs - rank > 1;
@@ -140,15 +148,17 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
     return;
   }
   const Scan sc = block_scan(want, s_scan);  // below 2^31: at most 1024 rows of at most n_pages each
-  // the lowest free pages
+  // the lowest free pages, listed in shared memory when they fit
+  int32_t* take = sc.total <= kTakeHeld ? s_take : ws.take;
   int got = 0;
   for (int base = 0; base < p.n_pages && got < sc.total; base += kThreads * kScan) {
     const int p0 = base + i * kScan;
     const int in = min(max(p.n_pages - p0, 0), kScan);
-    uint32_t f = ~used_mask(p.refs, p0, p.n_pages) & ((1u << in) - 1u);
+    if (base > 0) used = used_mask(p.refs, p0, p.n_pages);
+    uint32_t f = ~used & ((1u << in) - 1u);
     const Scan fs = block_scan(__popc(f), s_scan);
     int at = got + fs.before;
-    for (; f && at < sc.total; f &= f - 1, ++at) ws.take[at] = p0 + __ffs(f) - 1;
+    for (; f && at < sc.total; f &= f - 1, ++at) take[at] = p0 + __ffs(f) - 1;
     got += fs.total;
   }
   failed = got < sc.total;
@@ -156,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
   s_need[i] = row ? need : 0;
   s_off[i] = sc.before;
   s_copy[i] = copy;
-  __syncthreads();  // ws.take and the rows are complete
+  __syncthreads();  // the list and the rows are complete
   if (failed) {
     if (i == 0) {
       *ws.count = 0;
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
   if (row) {
     int32_t* table = p.table + (size_t)s * p.max_blocks;
     if (copy) {
-      const int to = ws.take[sc.before];
+      const int to = take[sc.before];
       ws.src[i] = last;
       ws.dst[i] = to;
       ws.tiles[i] = (len % HYQ_PAGE_ROWS + 15) / 16;
@@ -186,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
     const int from = s_off[r] + s_copy[r], cnt = s_need[r] - s_have[r];
     int32_t* table = p.table + (size_t)s_seq[r] * p.max_blocks + s_have[r];
     for (int k = lane; k < cnt; k += 32) {
-      const int to = ws.take[from + k];
+      const int to = take[from + k];
       table[k] = to;
       p.refs[to] = 1;
     }
