@@ -34,7 +34,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kRowsQ = HYQ_MAX_GQA;    // query rows per tile (MMA N)
 constexpr int kPart = HYQ_D + 4;       // acc[128], m, l and two unused floats per query row
 constexpr int kMinUnits = 8;           // units per block before a group is split further
-constexpr int kMaxParts = 1024;        // blocks of the largest grid (two on each of 512 SMs)
 constexpr int kMaxNQ = 4;             // query tiles that one block takes together
 
 // The kernel's shape for NQ query tiles a group.  One tile: two blocks an SM
@@ -54,7 +53,6 @@ struct Ring : QFmt<BK, BV> {
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
   // query tiles whose partials a warp's ring holds at once
   static constexpr int kJoin = NQ * 4096 <= kWarpBytes ? NQ : NQ > 2 && 2 * 4096 <= kWarpBytes ? 2 : 1;
-  static_assert(kSmemBytes >= 32 * kMaxParts + kThreads * 16, "the join's weights and sums");
   static_assert(kJoin * 4096 <= kWarpBytes && NQ % kJoin == 0, "a warp's partial fits its ring");
   static_assert(kWarps % kPerPage == 0, "a warp's units take the same part of their pages");
 };
@@ -98,6 +96,22 @@ struct Shares {
   }
 };
 
+// A block's run of units and what it is doing: kept in shared memory, where
+// thread 0 keeps it up, so that the main loop's registers are its own.
+struct Run {
+  Shares sh;
+  int64_t pos, end;
+};
+struct Segment {
+  int b, h, qt, len;        // row of the call, KV head, group of its query rows; positions
+  int w0, w1, n_units;      // units [w0, w1) of the group's n_units (w0 < 0: none are left)
+  int n_rows, flat0;        // query rows of the group, the first one's (token, head) pair
+  const int32_t* table;     // of the sequence
+  const int32_t* sel;       // the group's list of blocks, or nullptr
+  __nv_bfloat16* out;       // of (row b, KV head h)
+  int64_t base;             // of the group's first unit in the line
+};
+
 // Output row of (token, head) pair `flat` of a KV head whose first row is `out`.
 __device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, int gq, int flat) {
   const int tok = flat / gq;
@@ -105,74 +119,72 @@ __device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, in
 }
 
 // One block: joins the n partials of a group's n_rows rows.  Part i lies at
-// parts + i stride, the first one `first` further.  Out of line, so that its
-// registers are its own: a thread takes four elements of a row over every
-// S-th part and has kHold of them under way before the weights are known.
+// parts + i stride, the first one `first` further.  A thread takes four elements
+// of a row over every S-th part, kHold parts at a time, with an online softmax
+// of its own (each part's maximum and sum come with its elements, so there is
+// one round of loads and nothing to wait for between them).  Out of line and
+// short: the code runs once a launch, cold, and its instructions are fetched
+// while the call waits (unrolled further it was slower).
 __device__ __noinline__ void join_parts(const float* parts, int first, int stride, int n, int n_rows, uint8_t* smem,
-                                        float* s_sum, __nv_bfloat16* out, int HQ, int gq, int flat0) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  float* wts = reinterpret_cast<float*>(smem);                           // [8][n] weights
-  float4* sums = reinterpret_cast<float4*>(smem + 8 * 4 * kMaxParts);  // [S][rows * 32]
-  auto part_of = [&](int i) { return parts + (size_t)i * stride + (i == 0 ? first : 0); };
-  constexpr int kHold = 20;
+                                        __nv_bfloat16* out, int HQ, int gq, int flat0) {
+  const int tid = threadIdx.x;
+  float4* sums = reinterpret_cast<float4*>(smem);                                // [kThreads]
+  float2* stats = reinterpret_cast<float2*>(smem + kThreads * sizeof(float4));  // [kThreads]
+  constexpr int kHold = 10;
   for (int r0 = 0; r0 < n_rows; r0 += kRowsQ) {
-    const int rows = min(kRowsQ, n_rows - r0);
-    const int items = rows * (HYQ_D / 4), S = kThreads / items, share = tid / items, item = tid - share * items;
-    const int r = item >> 5, d = 4 * (item & 31);
+    const int items = min(kRowsQ, n_rows - r0) * (HYQ_D / 4), S = kThreads / items, share = tid / items;
+    const int item = tid - share * items, r = r0 + (item >> 5), d = 4 * (item & 31);
     const int mine = share < S ? (n - share + S - 1) / S : 0;  // parts share, share + S, ...
-    const float* at = parts + (size_t)share * stride + (r0 + r) * kPart + d;
-    float4 v[kHold];
-#pragma unroll
-    for (int k = 0; k < kHold; ++k)
-      v[k] = k < mine ? __ldcg(reinterpret_cast<const float4*>(at + (size_t)k * S * stride + (share + k == 0 ? first : 0)))
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
-    if (warp < rows) {
-      float M = -INFINITY, L = 0.f;
-      for (int c = lane; c < n; c += 32) {
-        const float m = __ldcg(part_of(c) + (r0 + warp) * kPart + HYQ_D);
-        wts[warp * n + c] = m;
-        M = fmaxf(M, m);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      for (int c = lane; c < n; c += 32) {
-        const float m = wts[warp * n + c], wt = m == -INFINITY ? 0.f : ex2(m - M);
-        wts[warp * n + c] = wt;
-        L = fmaf(__ldcg(part_of(c) + (r0 + warp) * kPart + HYQ_D + 1), wt, L);
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-      if (lane == 0) s_sum[warp] = L;
-    }
-    __syncthreads();
+    const size_t step = (size_t)S * stride;
+    const float* at = parts + (size_t)share * stride + r * kPart;
+    float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* wr = wts + r * n + share;
+    for (int k0 = 0; k0 < mine; k0 += kHold) {
+      float2 ml[kHold];
+      float4 v[kHold];
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-      const float wt = k < mine ? wr[S * k] : 0.f;
-      a.x = fmaf(wt, v[k].x, a.x), a.y = fmaf(wt, v[k].y, a.y), a.z = fmaf(wt, v[k].z, a.z), a.w = fmaf(wt, v[k].w, a.w);
+      for (int k = 0; k < kHold; ++k, at += step) {
+        const bool in = k0 + k < mine;
+        const float* e = at + (share + k0 + k == 0 ? first : 0);
+        ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(e + HYQ_D)) : make_float2(-INFINITY, 0.f);
+        v[k] = in ? __ldcg(reinterpret_cast<const float4*>(e + d)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) top = fmaxf(top, ml[k].x);
+      const float ref = top == -INFINITY ? 0.f : top, corr = ex2(M - ref);
+      M = top;
+      L *= corr, a.x *= corr, a.y *= corr, a.z *= corr, a.w *= corr;
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const float w = ex2(ml[k].x - ref);
+        L = fmaf(ml[k].y, w, L);
+        a.x = fmaf(w, v[k].x, a.x), a.y = fmaf(w, v[k].y, a.y), a.z = fmaf(w, v[k].z, a.z), a.w = fmaf(w, v[k].w, a.w);
+      }
     }
-#pragma unroll 8
-    for (int k = kHold; k < mine; ++k) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(at + (size_t)k * S * stride));
-      const float wt = wr[S * k];
-      a.x = fmaf(wt, x.x, a.x), a.y = fmaf(wt, x.y, a.y), a.z = fmaf(wt, x.z, a.z), a.w = fmaf(wt, x.w, a.w);
-    }
-    if (S > 1) {
-      if (share < S) sums[tid] = a;
+    if (S > 1) {  // fewer than eight rows, or the last ones of a group
+      sums[tid] = a;
+      stats[tid] = make_float2(M, L);
       __syncthreads();
     }
     if (share == 0) {
+      float top = M;
+      for (int k = 1; k < S; ++k) top = fmaxf(top, stats[k * items + item].x);
+      const float ref = top == -INFINITY ? 0.f : top, own = ex2(M - ref);
+      L *= own, a.x *= own, a.y *= own, a.z *= own, a.w *= own;
       for (int k = 1; k < S; ++k) {
         const float4 x = sums[k * items + item];
-        a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
+        const float2 ml = stats[k * items + item];
+        const float w = ex2(ml.x - ref);
+        L = fmaf(ml.y, w, L);
+        a.x = fmaf(w, x.x, a.x), a.y = fmaf(w, x.y, a.y), a.z = fmaf(w, x.z, a.z), a.w = fmaf(w, x.w, a.w);
       }
-      const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
-      *reinterpret_cast<uint2*>(out_row(out, HQ, gq, flat0 + r0 + r) + d) =
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      *reinterpret_cast<uint2*>(out_row(out, HQ, gq, flat0 + r) + d) =
           make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
     }
-    __syncthreads();
   }
+  __syncthreads();
 }
 
 template <int BK, int BV, int NQ>
@@ -192,6 +204,8 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
   __shared__ float s_wt[R::kJoin * kRowsQ][kWarps];     // weights of the warps' partials
   __shared__ float s_sum[R::kJoin * kRowsQ];
   __shared__ int s_last;
+  __shared__ Run run;
+  __shared__ Segment seg;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * R::kWarpBytes;
@@ -250,55 +264,64 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
   // No more blocks than give each kMinUnits.  With few groups every group gets
   // the same number of blocks: equal lengths are then cut at the groups'
   // borders.  (Not where rounding down would leave a quarter of the blocks out.)
-  const int64_t T = s_cum[p.batch] * unit;
-  int64_t nb = gridDim.x;
-  {
-    const int64_t groups = (int64_t)p.batch * unit, want = max((int64_t)1, div_fast(T, kMinUnits));
+  if (tid == 0) {
+    const int64_t T = s_cum[p.batch] * unit, groups = (int64_t)p.batch * unit;
+    const int64_t want = max((int64_t)1, div_fast(T, kMinUnits));
+    int64_t nb = gridDim.x;
     if (groups <= nb) {
       const int64_t most = div_fast(nb, groups), by_size = max((int64_t)1, div_fast(want, groups));
       if (by_size < most || most >= 4) nb = groups * min(most, by_size);
     }
     nb = max((int64_t)1, min(nb, T));
+    run.sh.each = div_fast(T, nb);
+    run.sh.more = T - run.sh.each * nb;
+    run.pos = run.sh.begin(min((int64_t)blockIdx.x, nb));  // blocks past nb: an empty run
+    run.end = run.sh.begin(min((int64_t)blockIdx.x + 1, nb));
   }
-  if ((int64_t)blockIdx.x >= nb) return;
-  Shares sh;
-  sh.each = div_fast(T, nb);
-  sh.more = T - sh.each * nb;
-  int64_t pos = sh.begin(blockIdx.x);
-  const int64_t end = sh.begin(blockIdx.x + 1);
 
   uint32_t done = 0;  // units that this warp's ring has seen: slot done % kSlots, parity (done / kSlots) & 1
   bool dead = false;
 
-  while (pos < end) {
-    // ---- the group at pos -----------------------------------------------
-    int lo = 0, hi = p.batch;  // the last b with unit * s_cum[b] <= pos
-    while (hi - lo > 1) {
-      const int m = (lo + hi) >> 1;
-      if (s_cum[m] * unit <= pos) lo = m;
-      else hi = m;
+  while (true) {
+    // ---- the next group that the run meets (not only its fixed work) ----------
+    if (tid == 0) {
+      seg.w0 = -1;
+      while (run.pos < run.end) {
+        int lo = 0, hi = p.batch;  // the last b with unit * s_cum[b] <= pos
+        while (hi - lo > 1) {
+          const int m = (lo + hi) >> 1;
+          if (s_cum[m] * unit <= run.pos) lo = m;
+          else hi = m;
+        }
+        const int W = (int)(s_cum[lo + 1] - s_cum[lo]);  // with the fixed work's units
+        const int64_t off = run.pos - s_cum[lo] * unit;
+        const int grp = (int)div_fast(off, W), x0 = (int)(off - (int64_t)grp * W);
+        const int x1 = (int)min((int64_t)W, x0 + (run.end - run.pos));
+        run.pos += x1 - x0;
+        if (x1 <= R::kCost) continue;  // the group is the next blocks'
+        const int h = grp / p.QT, qt = grp - h * p.QT;
+        seg.b = lo;
+        seg.h = h;
+        seg.qt = qt;
+        seg.len = s_len[lo];
+        seg.w0 = max(0, x0 - R::kCost);
+        seg.w1 = x1 - R::kCost;
+        seg.n_units = W - R::kCost;
+        seg.n_rows = p.sel ? p.gq : min(kRowsG, p.n_q * p.gq - kRowsG * qt);
+        seg.flat0 = p.sel ? qt * p.gq : qt * kRowsG;  // with block lists a group is one token's heads
+        seg.table = p.pv.table + (size_t)s_seq[lo] * p.pv.max_blocks;
+        seg.sel = p.sel ? p.sel + (((size_t)lo * p.n_q + qt) * p.HKV + h) * p.k_sel : nullptr;
+        seg.out = p.out + ((size_t)lo * p.n_q * p.HQ + (size_t)h * p.gq) * HYQ_D;
+        seg.base = s_cum[lo] * unit + (int64_t)grp * W + R::kCost;
+        break;
+      }
     }
-    const int b = lo;
-    const int64_t cum = s_cum[b];
-    const int W = (int)(s_cum[b + 1] - cum);  // with the fixed work's units
-    const int64_t off = pos - cum * unit;
-    const int grp = (int)div_fast(off, W), x0 = (int)(off - (int64_t)grp * W);
-    const int x1 = (int)min((int64_t)W, x0 + (end - pos));
-    pos += x1 - x0;
-    const int n_units = W - R::kCost, w0 = max(0, x0 - R::kCost), w1 = x1 - R::kCost;
-    if (w1 <= w0) continue;  // only units of the fixed work: another block's group
-    const int h = grp / p.QT, qt = grp - h * p.QT;
-    const int seq = s_seq[b], len = s_len[b];
-    const int32_t* table = p.pv.table + (size_t)seq * p.pv.max_blocks;
-    const int32_t* sel = p.sel ? p.sel + (((size_t)b * p.n_q + qt) * p.HKV + h) * p.k_sel : nullptr;
-    const int n_rows = p.sel ? p.gq : min(kRowsG, p.n_q * p.gq - kRowsG * qt);
-    const size_t page_bytes = (size_t)p.HKV * R::kBlock;
-
-    // Row r of the group is (token, head) pair flat0 + r of the KV head's, in
-    // order; with block lists a group is one token's heads.
-    const int flat0 = p.sel ? qt * p.gq : qt * kRowsG;
-    auto token_of = [&](int r) { return (flat0 + r) / p.gq; };
-    __nv_bfloat16* out_bh = p.out + ((size_t)b * p.n_q * p.HQ + (size_t)h * p.gq) * HYQ_D;
+    __syncthreads();
+    const int w0 = seg.w0, w1 = seg.w1;
+    if (w0 < 0) break;
+    const int len = seg.len;
+    // Row r of the group is (token, head) pair flat0 + r of the KV head's.
+    auto token_of = [&](int r) { return (seg.flat0 + r) / p.gq; };
     // the query rows, row `warp` of each query tile: loaded ahead of the page
     // numbers, prepared while the first copies are under way
     uint2 qv[NQ];
@@ -306,23 +329,24 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     for (int k = 0; k < NQ; ++k) {
       const int r = kRowsQ * k + warp, tok = token_of(r);
       qv[k] = make_uint2(0, 0);
-      if (r < n_rows)
-        qv[k] = __ldg(reinterpret_cast<const uint2*>(p.q + ((size_t)b * p.n_q + tok) * p.ldq +
-                                                     (size_t)(h * p.gq + flat0 + r - tok * p.gq) * HYQ_D + 4 * lane));
+      if (r < seg.n_rows)
+        qv[k] = __ldg(reinterpret_cast<const uint2*>(
+            p.q + ((size_t)seg.b * p.n_q + tok) * p.ldq +
+            (size_t)(seg.h * p.gq + seg.flat0 + r - tok * p.gq) * HYQ_D + 4 * lane));
     }
 
     // ---- this warp's units: w0 + warp, + 8, ... ---------------------------
     // kPerPage divides 8, so all of them take the same part of their pages.
     const int nj = w1 - w0 > warp ? (w1 - w0 - warp + kWarps - 1) / kWarps : 0;
     const int part = (w0 + warp) % R::kPerPage, x_first = (w0 + warp) / R::kPerPage;
-    const uint8_t* heads = p.pv.pool + (size_t)h * R::kBlock + part * R::kUnit;
+    const uint8_t* heads = p.pv.pool + (size_t)seg.h * R::kBlock + part * R::kUnit;
     // Block of the sequence that unit j lies in, or -1 for one that must not
     // be read.
     auto entry = [&](int j) -> int {
       if (j >= nj) return -1;
       const int x = x_first + j * (kWarps / R::kPerPage);
-      if (!sel) return x;
-      const int e = __ldg(sel + x), pe = x > 0 ? __ldg(sel + x - 1) : -1;
+      if (!seg.sel) return x;
+      const int e = __ldg(seg.sel + x), pe = x > 0 ? __ldg(seg.sel + x - 1) : -1;
       if (e < 0) return -1;
       if ((x > 0 && pe < 0) || pe >= e || (int64_t)e * HYQ_PAGE_ROWS >= len) {
         hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
@@ -330,11 +354,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       }
       return e;
     };
-    auto page_of = [&](int e) -> int {
-      if (e < 0) return -1;
-      const int page = __ldg(table + e);
-      return page;
-    };
+    auto page_of = [&](int e) -> int { return e < 0 ? -1 : __ldg(seg.table + e); };
     // Lane l holds block and page of unit 32 r + l of the present round r of 32
     // units, and of the next one; the pages arrive while the round is worked off.
     int e_cur = entry(lane), pg_cur = page_of(e_cur);
@@ -351,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
         if (ok) {
           const uint32_t bytes = R::kTiles == 1 || at + 16 < len ? R::kUnit : R::kTile;
           mbar_arrive_expect_tx(bar, bytes);
-          bulk_g2s(ring + slot * R::kUnit, heads + (size_t)pg * page_bytes, bytes, bar);
+          bulk_g2s(ring + slot * R::kUnit, heads + (size_t)pg * ((size_t)p.HKV * R::kBlock), bytes, bar);
         } else {
           mbar_arrive_expect_tx(bar, 0);
           if (e >= 0 && !in) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
@@ -374,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     for (int k = 0; k < NQ; ++k) {
       const int r = kRowsQ * k + warp;
       prep_query_row<BK>(warp, lane, qv[k], bq_s[k], rowc_s[k], bz_s[k]);
-      if (lane == 0) lim_s[k][warp] = r < n_rows ? max(0, len - p.n_q + 1 + token_of(r)) : len;
+      if (lane == 0) lim_s[k][warp] = r < seg.n_rows ? max(0, len - p.n_q + 1 + token_of(r)) : len;
     }
     __syncthreads();
     uint32_t bq[8][2];
@@ -432,8 +452,9 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
 
     // ---- the block's partial, a query tile at a time -------------------------
     __syncwarp();
-    const bool whole = w0 == 0 && w1 == n_units;
-    float* pp = p.part + ((size_t)blockIdx.x * 2 + (w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
+    const int n_rows = seg.n_rows;
+    const bool whole = seg.w0 == 0 && seg.w1 == seg.n_units;
+    float* pp = p.part + ((size_t)blockIdx.x * 2 + (seg.w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
     constexpr int kJoin = R::kJoin;
 #pragma unroll
     for (int k0 = 0; k0 < NQ; k0 += kJoin) {
@@ -481,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
         if (x & 2) a = make_float4(a.z, a.w, a.x, a.y);
         if (whole) {
           const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
-          *reinterpret_cast<uint2*>(out_row(out_bh, p.HQ, p.gq, flat0 + kRowsQ * k0 + r) + d) =
+          *reinterpret_cast<uint2*>(out_row(seg.out, p.HQ, p.gq, seg.flat0 + kRowsQ * k0 + r) + d) =
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
         } else {
           *reinterpret_cast<float4*>(pp + (kRowsQ * k0 + r) * kPart + d) = a;
@@ -491,24 +512,25 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     }
     if (!whole) {
       // blocks that share this group: those holding its first and last unit
-      const int64_t base = cum * unit + (int64_t)grp * W + R::kCost;
-      const int c0 = sh.owner(base), c1 = sh.owner(base + n_units - 1);
-      const size_t gi = ((size_t)b * p.HKV + h) * p.QT + qt;
+      const int64_t base = seg.base;
+      const int c0 = run.sh.owner(base), c1 = run.sh.owner(base + seg.n_units - 1);
       if (tid == 0) {
+        int32_t* ticket = p.tickets + ((size_t)seg.b * p.HKV + seg.h) * p.QT + seg.qt;
         int old;
-        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;\n" : "=r"(old) : "l"(p.tickets + gi) : "memory");
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;\n" : "=r"(old) : "l"(ticket) : "memory");
         s_last = old == c1 - c0;
-        if (s_last) p.tickets[gi] = 0;
+        if (s_last) *ticket = 0;
       }
       __syncthreads();
       if (s_last) {
         // part i: slot 0 of block c0 + i, where its run ends this group; the
         // first block's is slot 1 when its run holds the group's first unit
         constexpr int kSlot = NQ * kRowsQ * kPart;
-        join_parts(p.part + (size_t)c0 * 2 * kSlot, sh.begin(c0) <= base ? kSlot : 0, 2 * kSlot, c1 - c0 + 1, n_rows,
-                   smem, s_sum, out_bh, p.HQ, p.gq, flat0);
+        join_parts(p.part + (size_t)c0 * 2 * kSlot, run.sh.begin(c0) <= base ? kSlot : 0, 2 * kSlot, c1 - c0 + 1, n_rows,
+                   smem, seg.out, p.HQ, p.gq, seg.flat0);
       }
     }
+    __syncthreads();  // the segment is done with
     // order this block's generic accesses to the rings before the next copies
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
   }
@@ -528,7 +550,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
     return cudaFuncSetAttribute(paged_kernel<BK, BV, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  const int grid = min(R::kPerSm * hyq_num_sms(), kMaxParts);
+  const int grid = R::kPerSm * hyq_num_sms();
   paged_kernel<BK, BV, NQ><<<grid, kThreads, R::kSmemBytes, s>>>(p);
   return cudaGetLastError();
 }
