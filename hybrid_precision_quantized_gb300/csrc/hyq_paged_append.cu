@@ -153,27 +153,16 @@ __device__ __forceinline__ float exact_code4(float x, float z, float s, float t)
   return fminf(fmaxf(c, 0.f), Near<BITS>::kMax);
 }
 
-// The codes of eight elements as bytes, decided exactly (r < 0: with clamps).
-// Out of line: it is called for about one row in 25 (the midpoints that a
+// The codes of the two elements of w, decided exactly (r < 0: with clamps).
+// Out of line: about one row in 25 has such an element (the midpoints that a
 // coarse BF16 grid meets).
 template <int BITS>
-__device__ __noinline__ uint2 exact_codes(uint4 v, float s, float z, float r) {
-  uint32_t o[2] = {0u, 0u};
-  if (!marked(r)) {
-    const float ra = fabsf(r);
-#pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-      const float x = __uint_as_float(v.x << 16);
-      const uint32_t c = (uint32_t)exact_code4<BITS>(x, z, s, __fmul_rn(__fsub_rn(x, z), ra));
-      o[0] = __funnelshift_r(o[0], o[1], 8);  // bytes move down, the new one enters at the top
-      o[1] = o[1] >> 8 | c << 24;
-      v.x = __funnelshift_r(v.x, v.y, 16);
-      v.y = __funnelshift_r(v.y, v.z, 16);
-      v.z = __funnelshift_r(v.z, v.w, 16);
-      v.w >>= 16;
-    }
-  }
-  return make_uint2(o[0], o[1]);
+__device__ __noinline__ float2 exact_pair(uint32_t w, float s, float z, float r) {
+  if (marked(r)) return make_float2(0.f, 0.f);
+  const float2 x = __bfloat1622float2(bf2_of(w));
+  const float ra = fabsf(r);
+  return make_float2(exact_code4<BITS>(x.x, z, s, __fmul_rn(__fsub_rn(x.x, z), ra)),
+                     exact_code4<BITS>(x.y, z, s, __fmul_rn(__fsub_rn(x.y, z), ra)));
 }
 
 // Codes of a lane's eight elements: c as float pairs and, for packing, as the
@@ -188,23 +177,28 @@ __device__ __forceinline__ Codes8 codes8(uint4& v, float s, float z, float r) {
   const uint64_t nz2 = f2_splat(-z), r2 = f2_splat(r), m2 = f2_splat(kMagic), nm2 = f2_splat(-kMagic);
   const uint64_t no2 = f2_splat(-1.f);
   float far = 0.f;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  // distance of an element pair's arguments from their codes, exact
+  auto code_pair = [&](int k) {
     const uint32_t w = (&v.x)[k];
     const uint64_t x = (uint64_t)(w << 16) | ((uint64_t)(w & 0xFFFF0000u) << 32);
     const uint64_t t = f2_mul(f2_add(x, nz2), r2), b = f2_add(t, m2);
     o.c[k] = f2_add(b, nm2);
     o.b[2 * k] = lo32(b), o.b[2 * k + 1] = hi32(b);
-    const uint64_t d = f2_fma(o.c[k], no2, t);  // exact
-    far = fmax3(far, fabsf(f2_lo(d)), fabsf(f2_hi(d)));
-  }
+    const uint64_t d = f2_fma(o.c[k], no2, t);
+    return fmaxf(fabsf(f2_lo(d)), fabsf(f2_hi(d)));
+  };
+#pragma unroll
+  for (int k = 0; k < 4; ++k) far = fmaxf(far, code_pair(k));
   if (r < 0.f || far > Near<BITS>::kTie) {
-    const uint2 e = exact_codes<BITS>(v, s, z, r);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o.b[k] = __byte_perm(k < 4 ? e.x : e.y, 0x4B400000u, 0x7650 + (k & 3));
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      o.c[k] = f2_add(f2_pack(__uint_as_float(o.b[2 * k]), __uint_as_float(o.b[2 * k + 1])), nm2);
+    for (int k = 0; k < 4; ++k) {
+      if (code_pair(k) > Near<BITS>::kTie || r < 0.f) {
+        const float2 c = exact_pair<BITS>((&v.x)[k], s, z, r);
+        o.c[k] = f2_pack(c.x, c.y);
+        o.b[2 * k] = __float_as_uint(__fadd_rn(c.x, kMagic));
+        o.b[2 * k + 1] = __float_as_uint(__fadd_rn(c.y, kMagic));
+      }
+    }
     if (marked(r)) v = make_uint4(0u, 0u, 0u, 0u);
   }
   return o;
@@ -440,17 +434,18 @@ __device__ __forceinline__ void store_bounds(uint8_t* rec, int lane, const Bound
   }
 }
 
-constexpr int kThreads = 256;  // 4 KV heads x {K, V}
-constexpr int kHeads = kThreads / 64;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 
-// grid (pages that the call may reach, KV heads / 4): block x takes the x-th
-// page that gets rows, in the order of the call's rows.
+// grid (pages that the call may reach / (8 / hb), KV heads / hb, {K, V}), with
+// hb = 1, 2, 4 or 8 heads a block: a block takes 8 / hb pages that get rows, in
+// the order of the call's rows, a warp for each (page, head).  Keys and values
+// in blocks of their own: the warps of a block run the same code (5% faster).
 template <int BK, int BV>
-__global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendParams p, int hb) {
   using F = QFmt<BK, BV>;
   __shared__ int s_warp[kThreads / 32];
-  __shared__ PageRows s_rows;
-  __shared__ bool s_found;
+  __shared__ PageRows s_rows[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // pages of the call rows 4 tid .. 4 tid + 3, summed up
   CallRows c[4];
@@ -472,25 +467,20 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
     if (lane >= o) pre += y;
   }
   if (lane == 31) s_warp[warp] = pre;
-  if (tid == 0) s_found = false;
+  const int per = kWarps / hb, first = (int)blockIdx.x * per;
+  if (tid < kWarps) s_rows[tid].r0 = s_rows[tid].r1 = 0;  // no rows
   __syncthreads();
   int at = pre - sum;
   for (int i = 0; i < warp; ++i) at += s_warp[i];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int nth = (int)blockIdx.x - at;
-    if (nth >= 0 && nth < n[i]) {
-      s_rows = page_rows(p, c[i], nth);
-      s_found = true;
-    }
+    for (int j = max(at - first, 0); j < per && first + j - at < n[i]; ++j) s_rows[j] = page_rows(p, c[i], first + j - at);
     at += n[i];
   }
   __syncthreads();
-  if (!s_found) return;
-  const PageRows r = s_rows;
-  if (r.r1 <= r.r0) return;
-  const int h = blockIdx.y * kHeads + (warp >> 1), T = warp & 1;
-  if (h >= p.HKV) return;
+  const int h = blockIdx.y * hb + warp % hb, T = blockIdx.z;
+  const PageRows r = s_rows[warp / hb];
+  if (r.r1 <= r.r0 || h >= p.HKV) return;
   const size_t ph = (size_t)r.page * p.HKV + h;
   uint8_t* block = p.pv.pool + ph * F::kBlock;
   const int64_t ldh = (int64_t)p.HKV * HYQ_D;
@@ -598,7 +588,8 @@ cudaError_t launch(const AppendParams& p, cudaStream_t s) {
   } else {
     // a sequence with n rows reaches at most n / 64 + 2 pages
     const int pages = p.n_rows / HYQ_PAGE_ROWS + 2 * min(p.batch, p.n_rows);
-    append_pages_kernel<BK, BV><<<dim3(pages, (p.HKV + kHeads - 1) / kHeads), kThreads, 0, s>>>(p);
+    const int hb = p.HKV >= 8 ? 8 : p.HKV > 2 ? 4 : p.HKV, per = kWarps / hb;
+    append_pages_kernel<BK, BV><<<dim3((pages + per - 1) / per, (p.HKV + hb - 1) / hb, 2), kThreads, 0, s>>>(p, hb);
   }
   return cudaGetLastError();
 }
