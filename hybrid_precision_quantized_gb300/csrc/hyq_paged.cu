@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
   uint64_t* wb = bars + warp * kSlots;
   if (lane < kSlots) mbar_init(&wb[lane], 1);
   mbar_fence_init();
+  chain_kernel();
 
   // Units of a group of row b: its own and those of the fixed work; 0 when
   // there is nothing to read.
@@ -551,8 +552,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   const int grid = R::kPerSm * hyq_num_sms();
-  paged_kernel<BK, BV, NQ><<<grid, kThreads, R::kSmemBytes, s>>>(p);
-  return cudaGetLastError();
+  return hyq_launch_chained(paged_kernel<BK, BV, NQ>, dim3(grid), kThreads, R::kSmemBytes, s, p);
 }
 
 template <int BK, int BV>

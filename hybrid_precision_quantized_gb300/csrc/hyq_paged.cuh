@@ -44,15 +44,20 @@ size_t hyq_pages_compact_ws_bytes(const hyq_pages* p);
 cudaError_t hyq_launch_pages_compact(const hyq_config* c, const hyq_pages* p, int32_t* table_out, int32_t* refs_out,
                                      void* ws, cudaStream_t s);
 
-// Launch of a call's second kernel: it may start while the first one (which
-// has let its dependents go, let_next_start) still runs and waits for all of it
-// (wait_previous) before it reads or writes anything, so that only its launch
-// overlaps.
+// Every kernel of the paged cache is launched as a programmatic dependent: it
+// may be scheduled while the kernel before it on the stream still runs, and
+// begins with chain_kernel(), which waits until all of that kernel's work is done
+// and visible, before it reads or writes anything.  Only the launch overlaps (a
+// kernel that lets its dependents go early; after any other kernel the order
+// is the usual one).  It lets the next launch go only after its own wait, so that all
+// kernels but the immediately preceding one have finished whenever a launch
+// starts.
 template <class... Ks, class... As>
-inline cudaError_t hyq_launch_second(void (*k)(Ks...), dim3 grid, int threads, cudaStream_t s, As... args) {
+inline cudaError_t hyq_launch_chained(void (*k)(Ks...), dim3 grid, int threads, size_t smem, cudaStream_t s, As... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -61,8 +66,10 @@ inline cudaError_t hyq_launch_second(void (*k)(Ks...), dim3 grid, int threads, c
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
 }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void chain_kernel() {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
 
 // Sequence of call row i, or -1 when it is out of range.
 __device__ __forceinline__ int32_t page_seq(const int32_t* seqs, int32_t i, int32_t n_seqs) {

@@ -447,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
   __shared__ int s_warp[kThreads / 32];
   __shared__ PageRows s_rows[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  chain_kernel();
   // pages of the call rows 4 tid .. 4 tid + 3, summed up
   CallRows c[4];
   int n[4], sum = 0;
@@ -523,6 +524,7 @@ template <int BK, int BV>
 __global__ void __launch_bounds__(32 * kHeadsOne) append_one_kernel(const AppendParams p) {
   using F = QFmt<BK, BV>;
   const int lane = threadIdx.x & 31, h = blockIdx.y * kHeadsOne + (threadIdx.x >> 5);
+  chain_kernel();
   const CallRows cr = call_rows(p, blockIdx.x);
   if (cr.bad && threadIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
   if (cr.n <= 0 || h >= p.HKV) return;
@@ -583,15 +585,14 @@ __global__ void __launch_bounds__(32 * kHeadsOne) append_one_kernel(const Append
 
 template <int BK, int BV>
 cudaError_t launch(const AppendParams& p, cudaStream_t s) {
-  if (!p.cu) {
-    append_one_kernel<BK, BV><<<dim3(p.batch, (p.HKV + kHeadsOne - 1) / kHeadsOne), 32 * kHeadsOne, 0, s>>>(p);
-  } else {
-    // a sequence with n rows reaches at most n / 64 + 2 pages
-    const int pages = p.n_rows / HYQ_PAGE_ROWS + 2 * min(p.batch, p.n_rows);
-    const int hb = p.HKV >= 8 ? 8 : p.HKV > 2 ? 4 : p.HKV, per = kWarps / hb;
-    append_pages_kernel<BK, BV><<<dim3((pages + per - 1) / per, (p.HKV + hb - 1) / hb, 2), kThreads, 0, s>>>(p, hb);
-  }
-  return cudaGetLastError();
+  if (!p.cu)
+    return hyq_launch_chained(append_one_kernel<BK, BV>, dim3(p.batch, (p.HKV + kHeadsOne - 1) / kHeadsOne),
+                              32 * kHeadsOne, 0, s, p);
+  // a sequence with n rows reaches at most n / 64 + 2 pages
+  const int pages = p.n_rows / HYQ_PAGE_ROWS + 2 * min(p.batch, p.n_rows);
+  const int hb = p.HKV >= 8 ? 8 : p.HKV > 2 ? 4 : p.HKV, per = kWarps / hb;
+  return hyq_launch_chained(append_pages_kernel<BK, BV>, dim3((pages + per - 1) / per, (p.HKV + hb - 1) / hb, 2), kThreads,
+                            0, s, p, hb);
 }
 
 }  // namespace

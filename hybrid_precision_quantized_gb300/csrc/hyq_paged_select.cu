@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const SelectPa
   __shared__ uint32_t s_and[kWarps], s_or[kWarps];
   __shared__ int s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  chain_kernel();
   const int b = blockIdx.z, tok = blockIdx.y / p.HKV, h = blockIdx.y - tok * p.HKV;
   const size_t list = ((size_t)b * p.n_q + tok) * p.HKV + h;
   const int seq = page_seq(p.seqs, b, p.pv.n_seqs);
@@ -325,6 +326,5 @@ cudaError_t hyq_launch_paged_select(const hyq_config* c, const PageView& pv, con
   p.n_last = n_last;
   const int64_t lists = (int64_t)batch * n_q * p.HKV;
   const dim3 grid(shares_of(lists, pv.max_blocks), n_q * p.HKV, batch);
-  select_kernel<<<grid, kThreads, kKeys * 4, s>>>(p);
-  return cudaGetLastError();
+  return hyq_launch_chained(select_kernel, grid, kThreads, kKeys * 4, s, p);
 }

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) reserve_kernel(const hyq_pages p, co
   __shared__ __align__(16) int s_seq[kThreads], s_last[kThreads];
   __shared__ int s_scan[kWarps], s_take[kTakeHeld];
   __shared__ int s_have[kThreads], s_need[kThreads], s_off[kThreads], s_copy[kThreads];
-  let_next_start();
+  chain_kernel();
   const int i = threadIdx.x;
   const bool row = i < batch;
   uint32_t used = used_mask(p.refs, i * kScan, p.n_pages);  // the scan's first pass, under way with the rows
@@ -236,7 +236,7 @@ __device__ __forceinline__ int split(int64_t a, int b, int* rest) {
 // The copies of a reserve: an item is one (row, layer, KV head).
 __global__ void __launch_bounds__(kCopyThreads) reserve_copy_kernel(const hyq_pages p, ReserveWs ws, int HKV,
                                                                     int block_bytes) {
-  wait_previous();
+  chain_kernel();
   const int n = *ws.count, per = p.n_layers * HKV;
   const int64_t items = (int64_t)n * per;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -255,6 +255,7 @@ constexpr int kRowThreads = 128;
 // One block per pair.
 __global__ void __launch_bounds__(kRowThreads) fork_kernel(const hyq_pages p, const int32_t* src, const int32_t* dst,
                                                            int n) {
+  chain_kernel();
   const int i = blockIdx.x, s = src[i], d = dst[i];
   bool bad = s < 0 || s >= p.n_seqs || d < 0 || d >= p.n_seqs;
   for (int j = threadIdx.x; j < n; j += kRowThreads) bad |= (j < i && dst[j] == d) || src[j] == d;
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kRowThreads) fork_kernel(const hyq_pages p, co
 // One block per sequence.
 __global__ void __launch_bounds__(kRowThreads) truncate_kernel(const hyq_pages p, const int32_t* seqs,
                                                                const int32_t* new_lens, int n) {
+  chain_kernel();
   const int i = blockIdx.x, s = seqs ? seqs[i] : i;
   bool bad = s < 0 || s >= p.n_seqs;
   if (seqs)
@@ -333,7 +335,7 @@ CompactWs compact_ws(void* ws, int n_pages) {
 // One block: the number of pages in use N, the two lists, the map and the new refs.
 __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const hyq_pages p, int32_t* refs_out, CompactWs ws) {
   __shared__ int s_scan[kWarps];
-  let_next_start();
+  chain_kernel();
   const int tid = threadIdx.x, np = p.n_pages;
   constexpr int kPass = kThreads * kScan;
   int mine = 0;
@@ -371,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) compact_plan_kernel(const hyq_pages 
 // The table through the map, and the pages: an item is one (move, layer, KV head).
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const hyq_pages p, int32_t* table_out,
                                                                     CompactWs ws, int HKV, int block_bytes) {
-  wait_previous();
+  chain_kernel();
   const int64_t entries = (int64_t)p.n_seqs * p.max_blocks;
   for (int64_t x = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; x < entries;
        x += (int64_t)gridDim.x * kCopyThreads) {
@@ -409,23 +411,20 @@ size_t hyq_pages_reserve_ws_bytes(const hyq_pages* p) {
 cudaError_t hyq_launch_pages_reserve(const hyq_config* c, const hyq_pages* p, const int32_t* seqs, int32_t batch,
                                      const int32_t* n_new, void* ws, cudaStream_t s) {
   const ReserveWs w = reserve_ws(ws);
-  reserve_kernel<<<1, kThreads, 0, s>>>(*p, seqs, batch, n_new, w);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = hyq_launch_chained(reserve_kernel, dim3(1), kThreads, 0, s, *p, seqs, (int)batch, n_new, w);
   if (e != cudaSuccess) return e;
-  return hyq_launch_second(reserve_copy_kernel, dim3(copy_grid((int64_t)batch * p->n_layers * c->num_kv_heads)),
-                           kCopyThreads, s, *p, w, (int)c->num_kv_heads, (int)hyq_qblock_bytes(c));
+  return hyq_launch_chained(reserve_copy_kernel, dim3(copy_grid((int64_t)batch * p->n_layers * c->num_kv_heads)),
+                            kCopyThreads, 0, s, *p, w, (int)c->num_kv_heads, (int)hyq_qblock_bytes(c));
 }
 
 cudaError_t hyq_launch_pages_fork(const hyq_pages* p, const int32_t* src, const int32_t* dst, int32_t n,
                                   cudaStream_t s) {
-  fork_kernel<<<n, kRowThreads, 0, s>>>(*p, src, dst, n);
-  return cudaGetLastError();
+  return hyq_launch_chained(fork_kernel, dim3(n), kRowThreads, 0, s, *p, src, dst, (int)n);
 }
 
 cudaError_t hyq_launch_pages_truncate(const hyq_pages* p, const int32_t* seqs, const int32_t* new_lens, int32_t n,
                                       cudaStream_t s) {
-  truncate_kernel<<<n, kRowThreads, 0, s>>>(*p, seqs, new_lens, n);
-  return cudaGetLastError();
+  return hyq_launch_chained(truncate_kernel, dim3(n), kRowThreads, 0, s, *p, seqs, new_lens, (int)n);
 }
 
 size_t hyq_pages_compact_ws_bytes(const hyq_pages* p) { return 256 + hyq_align256((size_t)p->n_pages * 3 * 4); }
@@ -433,10 +432,9 @@ size_t hyq_pages_compact_ws_bytes(const hyq_pages* p) { return 256 + hyq_align25
 cudaError_t hyq_launch_pages_compact(const hyq_config* c, const hyq_pages* p, int32_t* table_out, int32_t* refs_out,
                                      void* ws, cudaStream_t s) {
   const CompactWs w = compact_ws(ws, p->n_pages);
-  compact_plan_kernel<<<1, kThreads, 0, s>>>(*p, refs_out ? refs_out : p->refs, w);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = hyq_launch_chained(compact_plan_kernel, dim3(1), kThreads, 0, s, *p, refs_out ? refs_out : p->refs, w);
   if (e != cudaSuccess) return e;
   const int64_t half = ((int64_t)p->n_pages / 2 + 1) * p->n_layers * c->num_kv_heads;  // moves are at most n_pages / 2
-  return hyq_launch_second(compact_move_kernel, dim3(copy_grid(half)), kCopyThreads, s, *p,
-                           table_out ? table_out : p->table, w, (int)c->num_kv_heads, (int)hyq_qblock_bytes(c));
+  return hyq_launch_chained(compact_move_kernel, dim3(copy_grid(half)), kCopyThreads, 0, s, *p,
+                            table_out ? table_out : p->table, w, (int)c->num_kv_heads, (int)hyq_qblock_bytes(c));
 }
