@@ -99,10 +99,17 @@ class PagedCache:
     # A decode step makes these calls for every layer, a few microseconds apart:
     # the common forms (contiguous tensors, the cache's device being the
     # current one) are tested first and cost well under a microsecond each.
-    def _run(self, name, args, stream):
-        """Call the C entry point on the given stream, or the current one of the cache's device."""
+    def _run(self, name, args, stream, *tensors):
+        """Call the C entry point on the given stream, or the current one of the cache's device.  A given stream is noted on
+        the call's tensors: one that the caller drops is not reused before the call has read it."""
         fn = getattr(self._lib, name)
-        raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(self._index)
+        else:
+            raw = stream.cuda_stream
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
         if torch.cuda.current_device() == self._index:
             st = fn(self._cfg, self._pages, *args, raw)
         else:
@@ -174,17 +181,18 @@ class PagedCache:
         n = self._ints(n_new, "n_new", self._ints(seqs, "seqs"))
         ws = self.workspace(L.OP_PAGES_RESERVE, 1, stream=stream)
         self._run("hyq_pages_reserve", (L.ptr(seqs), self.n_seqs if n is None else n, L.ptr(n_new), ws.data_ptr(),
-                                        ws.nbytes), stream)
+                                        ws.nbytes), stream, seqs, n_new)
 
     def fork(self, src, dst, stream=None):
         """Let the empty sequences dst begin as copies of src, sharing their pages."""
         n = self._ints(dst, "dst", self._ints(src, "src"))
-        self._run("hyq_pages_fork", (src.data_ptr(), dst.data_ptr(), n), stream)
+        self._run("hyq_pages_fork", (src.data_ptr(), dst.data_ptr(), n), stream, src, dst)
 
     def truncate(self, seqs=None, new_lens=None, stream=None):
         """Shorten the sequences to new_lens (default 0: free them)."""
         n = self._ints(new_lens, "new_lens", self._ints(seqs, "seqs"))
-        self._run("hyq_pages_truncate", (L.ptr(seqs), L.ptr(new_lens), self.n_seqs if n is None else n), stream)
+        self._run("hyq_pages_truncate", (L.ptr(seqs), L.ptr(new_lens), self.n_seqs if n is None else n), stream, seqs,
+                  new_lens)
 
     def compact(self, table_out=None, refs_out=None, stream=None):
         """Move the pages in use to the front of the pool; the new table and refs go to the given tensors, or in place."""
@@ -194,7 +202,7 @@ class PagedCache:
         if refs_out is not None:
             refs = self._dense(refs_out, "refs_out", torch.int32, (self.n_pages,))
         ws = self.workspace(L.OP_PAGES_COMPACT, 1, stream=stream)
-        self._run("hyq_pages_compact", (table, refs, ws.data_ptr(), ws.nbytes), stream)
+        self._run("hyq_pages_compact", (table, refs, ws.data_ptr(), ws.nbytes), stream, table_out, refs_out)
 
     # one layer -----------------------------------------------------------------
     def append(self, layer: int, k, v, seqs=None, cu_rows=None, k_hat=None, v_hat=None, stream=None):
@@ -218,7 +226,7 @@ class PagedCache:
         if v_hat is not None:
             vh = self._dense(v_hat, "v_hat", torch.bfloat16, k.shape)
         self._run("hyq_paged_append", (layer, L.ptr(seqs), n, L.ptr(cu_rows), rows, k.data_ptr(), v.data_ptr(), ld, kh,
-                                       vh), stream)
+                                       vh), stream, seqs, cu_rows, k, v, k_hat, v_hat)
 
     def _query(self, q, seqs):
         """(batch, n_q, elements between tokens) of q."""
@@ -234,7 +242,7 @@ class PagedCache:
         o = self._dense(out, "out", torch.bfloat16, q.shape)
         ws = self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream)
         self._run("hyq_paged_attention", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, o, ws.data_ptr(), ws.nbytes),
-                  stream)
+                  stream, seqs, q, out)
 
     def select(self, layer: int, q, sel, seqs=None, n_first: int = 1, n_last: int = 1, stream=None):
         """The blocks worth reading for every token and KV head: sel int32 [sequences, n_q, HKV, k]."""
@@ -243,7 +251,7 @@ class PagedCache:
         p = self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, k))
         ws = self.workspace(L.OP_PAGED_SELECT, b, n_q, stream)
         self._run("hyq_paged_select", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, k, n_first, n_last, p,
-                                       ws.data_ptr(), ws.nbytes), stream)
+                                       ws.data_ptr(), ws.nbytes), stream, seqs, q, sel)
 
     def attention_blocks(self, layer: int, q, sel, out, seqs=None, stream=None):
         """attention over the blocks that sel lists for each token and KV head."""
@@ -253,4 +261,4 @@ class PagedCache:
         p = self._dense(sel, "sel", torch.int32, (b, n_q, self.cfg.num_kv_heads, k))
         ws = self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream)
         self._run("hyq_paged_attention_blocks", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, p, k, o, ws.data_ptr(),
-                                                 ws.nbytes), stream)
+                                                 ws.nbytes), stream, seqs, q, sel, out)

@@ -694,3 +694,128 @@ def test_refused_calls_raise_and_change_nothing(hyq):
         cache.attention(0, q, out, seqs=torch.zeros(1, dtype=torch.int64, device="cuda"))
     torch.cuda.synchronize()
     assert (out == 7.0).all() and (sel == 9).all() and hyq_read_device_error(cache.err()) == 0
+
+
+def test_calls_on_several_streams_at_once(hyq):
+    """Appends into two layers, then attention and choice on both, from two streams at once (a PagedCache of its own
+    over the same buffers for each, as their workspaces need), equal the same calls made in turn."""
+    HQ, HKV, lens = 8, 2, [900, 64, 333]
+    base = make(HQ, HKV, 40, 3, 16, n_layers=2)
+    base.reserve(None, ints(lens))
+    rows = [mixed_rows(s, (HKV, sum(lens), 128)).transpose(0, 1).contiguous().cuda() for s in range(4)]
+    cu = ints(np.concatenate([[0], np.cumsum(lens)]).tolist())
+    q = [queries(s, 3, 1, HQ) for s in (1, 2)]
+    views = [PagedCache(base.cfg, 40, 3, 16, 2, buffers=base.buf) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    results = []
+    for together in (False, True):
+        base.pool().fill_(0xFF)
+        base.bounds().fill_(0xFF)
+        outs = [[torch.full_like(q[0], float("nan")), torch.zeros(3, 1, HKV, 4, dtype=torch.int32, device="cuda")]
+                for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for l in range(2):
+                v, s = views[l], streams[l] if together else None
+                v.append(l, rows[2 * l], rows[2 * l + 1], cu_rows=cu, stream=s)
+                v.attention(l, q[l], outs[l][0], stream=s)
+                v.select(l, q[l], outs[l][1], stream=s)
+        torch.cuda.synchronize()
+        results.append([base.pool()[:, base.table()[0, :14].long()].clone(), base.bounds()[:, base.table()[0, :14].long()].clone()]
+                       + [x.clone() for o in outs for x in o])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    hist = History(3, HKV)
+    hist.add(range(3), lens, rows[2], rows[3])
+    check_attention(base, hist, q[1], results[1][4], range(3), layer=1)
+    assert hyq_read_device_error(base.err()) == 0
+
+
+def test_a_call_on_a_stream_of_its_own_follows_that_stream(hyq):
+    """Work queued on the given stream before the call (here the rows' and queries' copies behind a long kernel) is seen by it,
+    with the default stream idle."""
+    cache = make(4, 2, 8, 2, 4)
+    k, v = (mixed_rows(s, (2, 150, 128)).transpose(0, 1).contiguous() for s in (3, 4))
+    hist = History(2, 2)
+    hist.add([1], [150], k, v)
+    kd, vd = (torch.zeros(150, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, out = (torch.zeros(1, 1, 4, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ks, vs, qs = k.cuda(), v.cuda(), queries(5, 1, 1, 4)
+    big = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big = big @ big * 1e-3
+        kd.copy_(ks)
+        vd.copy_(vs)
+        q.copy_(qs)
+    cache.reserve(ints([1]), ints([150]), stream=side)
+    cache.append(0, kd, vd, seqs=ints([1]), cu_rows=ints([0, 150]), stream=side)
+    cache.attention(0, q, out, seqs=ints([1]), stream=side)
+    side.synchronize()
+    check_attention(cache, hist, qs, out, [1])
+
+
+@pytest.mark.parametrize("HKV", [1, 2, 4, 5, 8, 12])
+def test_append_for_any_number_of_heads(hyq, HKV):
+    counts, seqs = [70, 0, 200, 3, 64, 1], [5, 4, 3, 2, 1, 0]
+    cache, hist = make(HKV, HKV, 24, 6, 8), History(6, HKV)
+    for step in range(2):
+        k, v, _, _ = grow(cache, seqs, counts, 7 * step + HKV)
+        hist.add(seqs, counts, k, v)
+    for s in range(6):
+        for h in range(HKV):
+            check_rows(cache, s, h, hist.k[s][:, h], hist.v[s][:, h])
+            check_bounds(cache, s, h, hist.k[s][:, h])
+    assert hyq_read_device_error(cache.err()) == 0
+
+
+@pytest.mark.parametrize("one", [False, True])
+def test_append_to_the_most_sequences(hyq, one):
+    """1024 sequences in one call, a row each or none to two."""
+    n = 1024
+    cache, hist = make(2, 2, 1100, n, 3), History(n, 2)
+    for step in range(2):
+        counts = [1] * n if one else [(i + step) % 3 for i in range(n)]
+        k, v, _, _ = grow(cache, list(range(n))[::-1], counts, step, one=one)
+        hist.add(list(range(n))[::-1], counts, k, v)
+    for s in (0, 1, 2, 511, 1022, 1023):
+        if len(hist.k[s]):
+            check_rows(cache, s, 1, hist.k[s][:, 1], hist.v[s][:, 1])
+            check_bounds(cache, s, 1, hist.k[s][:, 1])
+    q = queries(3, n, 1, 2)
+    out = torch.full_like(q, float("nan"))
+    cache.attention(0, q, out)
+    check_attention(cache, hist, q, out, range(n))
+
+
+@pytest.mark.parametrize("HQ,HKV,n_q", [(8, 1, 64), (5, 1, 13), (64, 8, 3)])
+def test_many_query_tokens(hyq, HQ, HKV, n_q):
+    """Up to the largest number of tokens: several passes of four query tiles, rows that end inside a tile."""
+    lens = [40, 700, 64, n_q, n_q - 1]
+    cache, hist = make(HQ, HKV, 24, 5, 12), History(5, HKV)
+    k, v, _, _ = grow(cache, list(range(5)), lens, 2)
+    hist.add(range(5), lens, k, v)
+    q = queries(9, 5, n_q, HQ)
+    out = torch.full_like(q, float("nan"))
+    cache.attention(0, q, out)
+    check_attention(cache, hist, q, out, range(5))
+
+
+def test_queries_that_are_not_finite_stay_in_their_rows(hyq):
+    """A NaN or infinite query gives NaN in its own output row; all others are as without it."""
+    cache = make(8, 2, 8, 2, 4)
+    grow(cache, [0, 1], [200, 100], 3)
+    q = queries(4, 2, 2, 8)
+    outs = []
+    for bad in (False, True):
+        if bad:
+            q[0, 1, 3, 5], q[1, 0, 6, 100] = float("nan"), float("inf")
+        out = torch.zeros_like(q)
+        cache.attention(0, q, out)
+        outs.append(out)
+    hit = torch.zeros(2, 2, 8, dtype=torch.bool, device="cuda")
+    hit[0, 1, 3] = hit[1, 0, 6] = True
+    assert outs[1][hit].isnan().any(1).all()
+    assert torch.equal(outs[0][~hit], outs[1][~hit])
