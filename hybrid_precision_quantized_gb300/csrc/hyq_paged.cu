@@ -37,9 +37,9 @@ constexpr int kMinUnits = 8;           // units per block before a group is spli
 constexpr int kMaxNQ = 4;             // query tiles that one block takes together
 
 // The kernel's shape for NQ query tiles a group.  One tile: two blocks an SM
-// (one's group change hides behind the other), units of two adjacent 16-row tiles for 4-bit codes.
-// More: the accumulators of NQ tiles leave registers for one block an SM, whose
-// ring is deeper; units of one tile.
+// (one's group change hides behind the other) and, for 4-bit codes, units of
+// two adjacent 16-row tiles.  kMaxNQ: the accumulators leave registers for one
+// block an SM, whose ring is deeper.
 template <int BK, int BV, int NQ>
 struct Ring : QFmt<BK, BV> {
   static constexpr int kPerSm = NQ == 1 ? 2 : 1;
@@ -263,15 +263,15 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
   __syncthreads();
   // ---- this block's run -------------------------------------------------------
   // No more blocks than give each kMinUnits.  With few groups every group gets
-  // the same number of blocks: equal lengths are then cut at the groups'
-  // borders.  (Not where rounding down would leave a quarter of the blocks out.)
+  // the same number of blocks, unless that would leave more than a sixteenth of
+  // the blocks out: equal lengths are then cut at the groups' borders.
   if (tid == 0) {
     const int64_t T = s_cum[p.batch] * unit, groups = (int64_t)p.batch * unit;
     const int64_t want = max((int64_t)1, div_fast(T, kMinUnits));
     int64_t nb = gridDim.x;
     if (groups <= nb) {
       const int64_t most = div_fast(nb, groups), by_size = max((int64_t)1, div_fast(want, groups));
-      if (by_size < most || most >= 4) nb = groups * min(most, by_size);
+      if (by_size < most || 16 * groups * most >= 15 * nb) nb = groups * min(most, by_size);
     }
     nb = max((int64_t)1, min(nb, T));
     run.sh.each = div_fast(T, nb);
@@ -537,10 +537,17 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
   }
 }
 
-// Query tiles that a group takes together.
+// Query tiles that a group takes together.  A pass of its own for each tile (the
+// groups of one KV head lie side by side and meet most of each other's reads in
+// L2) is as fast as four tiles a pass, whose one block an SM has eight warps to
+// hide latency with: 4-bit codes, 8 sequences of up to 16 thousand positions,
+// 8 KV heads, 4 / 8 / 16 tiles: 74 / 131 / 246 us one by one, 80 / 134 / 242 by
+// fours; 32 sequences of 2000: 58 / 99 / 184 against 65 / 107 / 189.  Only for wider codes, whose
+// cache passes L2 sooner, do full fours pay: 8-bit 89 / 164 / 313 us one by one,
+// 77 / 132 / 239 by fours (6 tiles, two passes of four: 113 against 132).
 int group_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
   const int gq = c->num_q_heads / c->num_kv_heads, tiles = (n_q * gq + kRowsQ - 1) / kRowsQ;
-  return blocks || tiles == 1 ? 1 : tiles == 2 ? 2 : kMaxNQ;
+  return !blocks && hyq_bits_k(c) + hyq_bits_v(c) > 8 && tiles % kMaxNQ == 0 ? kMaxNQ : 1;
 }
 
 template <int BK, int BV, int NQ>
@@ -557,7 +564,9 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
 
 template <int BK, int BV>
 cudaError_t launch_nq(const Params& p, int nq, cudaStream_t s) {
-  return nq == 1 ? launch<BK, BV, 1>(p, s) : nq == 2 ? launch<BK, BV, 2>(p, s) : launch<BK, BV, kMaxNQ>(p, s);
+  if constexpr (BK + BV > 8)
+    if (nq == kMaxNQ) return launch<BK, BV, kMaxNQ>(p, s);
+  return launch<BK, BV, 1>(p, s);
 }
 
 // Partials of the largest grid: two slots of kMaxNQ query tiles on each SM

@@ -402,7 +402,8 @@ __device__ __forceinline__ void q_tile_multi(const uint8_t* tb, int lane, int vr
     const float2 a01 = half2_to_float2(ma.x), a23 = half2_to_float2(ma.y);
     const float2 b01 = half2_to_float2(mb.x), b23 = half2_to_float2(mb.y);
     const uint32_t za = (t & 1) ? ma.w : ma.z, zb = (t & 1) ? mb.w : mb.z;
-    constexpr int kStep = NQ < 2 ? 1 : 2;
+    constexpr int kStep = 2;
+    static_assert(NQ % kStep == 0, "query tiles in pairs");
 #pragma unroll
     for (int k0 = 0; k0 < NQ; k0 += kStep) {
       float C[kStep][4][4];
