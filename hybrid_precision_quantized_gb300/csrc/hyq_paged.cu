@@ -17,10 +17,11 @@
 // into equal runs, one per block (two blocks an SM), so that unlike lengths
 // and single long sequences use the GPU alike and the launch does not depend
 // on the lengths (they live on the device; a captured call stays valid as
-// they grow).  In the line each group begins with R::kCost units that are
-// not there, about what preparing its queries and joining its warps takes:
-// without them a block that meets many short groups finishes last (16
-// sequences, one of them a single token: 126 us instead of 181 us x 0.73).
+// they grow).  In the line each group begins with kCost units that are not
+// there, about what preparing its queries and joining its warps takes: with too
+// few of them a block that meets many short groups finishes last (two tokens of
+// 16 sequences over chosen blocks: 142 us with 8 tiles' worth, 118 with 16, 102
+// with 48).
 // A group inside one run is finished by its block; one that several runs share
 // is joined from their partials (maximum, sum, accumulator) in run order by
 // the last block to finish, an atomic ticket that nobody waits for.
@@ -237,11 +238,6 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       }
       w[i] = units_of(len);
       sum += w[i];
-      // a row without positions: its outputs are zero
-      if (b < p.batch && w[i] == 0 && b % gridDim.x == blockIdx.x) {
-        uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * p.HQ * HYQ_D);
-        for (int k = 0; k < p.n_q * p.HQ * (HYQ_D / 8); ++k) o[k] = make_uint4(0, 0, 0, 0);
-      }
     }
     int64_t pre = sum;
 #pragma unroll
@@ -261,6 +257,12 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     if (tid == kThreads - 1 && p.batch == HYQ_PAGED_MAX_BATCH) s_cum[HYQ_PAGED_MAX_BATCH] = at;
   }
   __syncthreads();
+  // rows without positions: their outputs are zero
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    if (s_cum[b] == s_cum[b + 1]) {
+      uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * p.HQ * HYQ_D);
+      for (int k = tid; k < p.n_q * p.HQ * (HYQ_D / 8); k += kThreads) o[k] = make_uint4(0, 0, 0, 0);
+    }
   // ---- this block's run -------------------------------------------------------
   // No more blocks than give each kMinUnits.  With few groups every group gets
   // the same number of blocks, unless that would leave more than a sixteenth of
@@ -331,9 +333,9 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       const int r = kRowsQ * k + warp, tok = token_of(r);
       qv[k] = make_uint2(0, 0);
       if (r < seg.n_rows)
-        qv[k] = __ldg(reinterpret_cast<const uint2*>(
+        qv[k] = *reinterpret_cast<const uint2*>(
             p.q + ((size_t)seg.b * p.n_q + tok) * p.ldq +
-            (size_t)(seg.h * p.gq + seg.flat0 + r - tok * p.gq) * HYQ_D + 4 * lane));
+            (size_t)(seg.h * p.gq + seg.flat0 + r - tok * p.gq) * HYQ_D + 4 * lane);
     }
 
     // ---- this warp's units: w0 + warp, + 8, ... ---------------------------
@@ -347,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       if (j >= nj) return -1;
       const int x = x_first + j * (kWarps / R::kPerPage);
       if (!seg.sel) return x;
-      const int e = __ldg(seg.sel + x), pe = x > 0 ? __ldg(seg.sel + x - 1) : -1;
+      const int e = seg.sel[x], pe = x > 0 ? seg.sel[x - 1] : -1;
       if (e < 0) return -1;
       if ((x > 0 && pe < 0) || pe >= e || (int64_t)e * HYQ_PAGE_ROWS >= len) {
         hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       }
       return e;
     };
-    auto page_of = [&](int e) -> int { return e < 0 ? -1 : __ldg(seg.table + e); };
+    auto page_of = [&](int e) -> int { return e < 0 ? -1 : seg.table[e]; };
     // Lane l holds block and page of unit 32 r + l of the present round r of 32
     // units, and of the next one; the pages arrive while the round is worked off.
     int e_cur = entry(lane), pg_cur = page_of(e_cur);
@@ -524,10 +526,11 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       }
       __syncthreads();
       if (s_last) {
-        // part i: slot 0 of block c0 + i, where its run ends this group; the
-        // first block's is slot 1 when its run holds the group's first unit
+        // part i: slot 0 of block c0 + i, where its run ends or goes through this
+        // group; the first block, whose run holds the group's first unit, has it
+        // in slot 1
         constexpr int kSlot = NQ * kRowsQ * kPart;
-        join_parts(p.part + (size_t)c0 * 2 * kSlot, run.sh.begin(c0) <= base ? kSlot : 0, 2 * kSlot, c1 - c0 + 1, n_rows,
+        join_parts(p.part + (size_t)c0 * 2 * kSlot, kSlot, 2 * kSlot, c1 - c0 + 1, n_rows,
                    smem, seg.out, p.HQ, p.gq, seg.flat0);
       }
     }

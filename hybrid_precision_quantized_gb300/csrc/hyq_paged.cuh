@@ -51,7 +51,8 @@ cudaError_t hyq_launch_pages_compact(const hyq_config* c, const hyq_pages* p, in
 // kernel that lets its dependents go early; after any other kernel the order
 // is the usual one).  It lets the next launch go only after its own wait, so that all
 // kernels but the immediately preceding one have finished whenever a launch
-// starts.
+// starts.  What an earlier kernel may have written is read by plain loads: one
+// through the read-only path could be moved ahead of the wait.
 template <class... Ks, class... As>
 inline cudaError_t hyq_launch_chained(void (*k)(Ks...), dim3 grid, int threads, size_t smem, cudaStream_t s, As... args) {
   cudaLaunchConfig_t cfg = {};
@@ -73,7 +74,7 @@ __device__ __forceinline__ void chain_kernel() {
 
 // Sequence of call row i, or -1 when it is out of range.
 __device__ __forceinline__ int32_t page_seq(const int32_t* seqs, int32_t i, int32_t n_seqs) {
-  const int32_t s = seqs ? __ldg(seqs + i) : i;
+  const int32_t s = seqs ? seqs[i] : i;
   return s >= 0 && s < n_seqs ? s : -1;
 }
 

@@ -45,8 +45,8 @@ struct CallRows {
 };
 __device__ __forceinline__ CallRows call_rows(const AppendParams& p, int i) {
   CallRows c;
-  c.tok = p.cu ? __ldg(p.cu + i) : i;
-  const int end = p.cu ? __ldg(p.cu + i + 1) : i + 1;
+  c.tok = p.cu ? p.cu[i] : i;
+  const int end = p.cu ? p.cu[i + 1] : i + 1;
   c.n = end - c.tok;
   c.seq = page_seq(p.seqs, i, p.pv.n_seqs);
   c.start = 0;
@@ -278,7 +278,7 @@ __device__ __forceinline__ bool tile_rows(uint8_t* tile, const __nv_bfloat16* sr
   for (int j = 0; j < 8; ++j) {
     const int row = 4 * (j >> 2) + 8 * ((j >> 1) & 1) + (j & 1);
     v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if ((mine >> row) & 1) v[j] = __ldg(reinterpret_cast<const uint4*>(src + row * ld));
+    if ((mine >> row) & 1) v[j] = *reinterpret_cast<const uint4*>(src + row * ld);
   }
   // ---- steps and zeros: lane t4 of a group ends with steps 2 t4 and 2 t4 + 1 --
   uint32_t m[8];
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(32 * kHeadsOne) append_one_kernel(const Append
   const size_t ph = (size_t)pr.page * p.HKV + h;
   const int T = lane >> 4, c = lane & 15, q = c >> 2, t4 = c & 3, row = pr.r0 & 15;
   uint8_t* tile = p.pv.pool + ph * F::kBlock + (pr.r0 >> 4) * F::kTile;
-  uint4 v = __ldg(reinterpret_cast<const uint4*>((T == 0 ? p.k : p.v) + (int64_t)pr.tok0 * p.ld + (int64_t)h * HYQ_D + 8 * c));
+  uint4 v = *reinterpret_cast<const uint4*>((T == 0 ? p.k : p.v) + (int64_t)pr.tok0 * p.ld + (int64_t)h * HYQ_D + 8 * c);
   uint32_t m = min_negmax(v);
   m = min2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = min2(m, __shfl_xor_sync(0xffffffffu, m, 2));

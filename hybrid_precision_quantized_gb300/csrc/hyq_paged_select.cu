@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const SelectPa
   const int32_t* table = p.pv.table + (size_t)seq * p.pv.max_blocks;
   uint32_t* keys = p.keys + list * p.pv.max_blocks;
   int j0 = blockIdx.x * kPerIter + warp * kBatch;
-  auto page_at = [&](int j) { return lane < kBatch && j + lane < nb ? __ldg(table + j + lane) : -1; };
+  auto page_at = [&](int j) { return lane < kBatch && j + lane < nb ? table[j + lane] : -1; };
   int page = page_at(j0), page_next = page_at(j0 + gridDim.x * kPerIter);
   int4 lo[kBatch / 4], hi[kBatch / 4];
   int ex[kBatch / 4];
@@ -100,9 +100,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const SelectPa
       ex[x] = INT32_MIN;  // no record
       if ((uint32_t)pg < (uint32_t)p.pv.n_pages) {
         const uint8_t* rec = p.pv.bounds + ((size_t)pg * p.HKV + h) * HYQ_BOUND_BYTES;
-        lo[x] = __ldg(reinterpret_cast<const int4*>(rec) + part);
-        hi[x] = __ldg(reinterpret_cast<const int4*>(rec + HYQ_D) + part);
-        ex[x] = __ldg(reinterpret_cast<const int*>(rec + 2 * HYQ_D));
+        lo[x] = reinterpret_cast<const int4*>(rec)[part];
+        hi[x] = reinterpret_cast<const int4*>(rec + HYQ_D)[part];
+        ex[x] = *reinterpret_cast<const int*>(rec + 2 * HYQ_D);
       }
     }
   };

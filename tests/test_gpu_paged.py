@@ -819,3 +819,43 @@ def test_queries_that_are_not_finite_stay_in_their_rows(hyq):
     hit[0, 1, 3] = hit[1, 0, 6] = True
     assert outs[1][hit].isnan().any(1).all()
     assert torch.equal(outs[0][~hit], outs[1][~hit])
+
+
+def test_calls_captured_between_other_nodes(hyq):
+    """A captured step whose calls follow copies, fills and joined branches of another stream (and are followed by such)
+    replays to what the same calls give one by one."""
+    cache = make(8, 2, 24, 3, 8)
+    lens = [200, 64, 31]
+    k, v, _, _ = grow(cache, [0, 1, 2], lens, 4)
+    hist = History(3, 2)
+    hist.add(range(3), lens, k, v)
+    qs, q = queries(5, 3, 1, 8), torch.zeros(3, 1, 8, 128, dtype=torch.bfloat16, device="cuda")
+    out, copy = (torch.zeros_like(q) for _ in range(2))
+    other = PagedCache(cache.cfg, 24, 3, 8, buffers=cache.buf)
+    out2, sel = torch.zeros_like(q), torch.zeros(3, 1, 2, 2, dtype=torch.int32, device="cuda")
+    for c in (cache, other):
+        for op in (L.OP_PAGED_ATTENTION, L.OP_PAGED_SELECT):
+            c.workspace(op, 3)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        q.copy_(qs)
+        out.fill_(float("nan"))
+        cache.attention(0, q, out)              # after a fill
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other.select(0, q, sel)             # begins a branch
+            other.attention_blocks(0, q, sel, out2)
+        copy.copy_(out)
+        cache.attention(0, q, out)              # after a kernel of another library, beside the branch
+        torch.cuda.current_stream().wait_stream(side)
+        cache.attention(0, q, out)              # after a join
+        cache.truncate(ints([]))                # nothing
+    for _ in range(3):
+        q.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(cache, hist, qs, out, range(3))
+        check_attention(cache, hist, qs, out2, range(3), sel=sel.cpu().tolist())
+        assert torch.equal(copy, out)
+    assert hyq_read_device_error(cache.err()) == 0
