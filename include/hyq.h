@@ -569,8 +569,13 @@ hyq_status hyq_decode_attention_noalloc(const hyq_config *cfg, const void *q, co
  * beyond hyq_pages_reset; whatever a page's unwritten rows hold, they do not
  * reach a result.
  *
+ * The kernels are launched as programmatic dependents: a call's launch may
+ * overlap the end of the kernel before it on the stream, its work begins when
+ * all of that kernel's is done and visible (stream order as usual).
+ *
  * Calls that read (attention, select) or append may run while others of the
- * same kind do, on other layers or sequences; the calls that change the
+ * same kind do (appends on other layers or sequences), each with a workspace of
+ * its own; the calls that change the
  * tables (hyq_pages_*) must be ordered with every call on the same pool.  A
  * sequence may be listed only once in a call that writes (append, reserve,
  * truncate, the destinations of a fork).

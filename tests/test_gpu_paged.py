@@ -859,3 +859,30 @@ def test_calls_captured_between_other_nodes(hyq):
         check_attention(cache, hist, qs, out2, range(3), sel=sel.cpu().tolist())
         assert torch.equal(copy, out)
     assert hyq_read_device_error(cache.err()) == 0
+
+
+@pytest.mark.parametrize("bits", [(4, 4), (8, 8), (4, 8), (8, 4)])
+def test_pages_hold_the_bytes_of_the_stream(hyq, bits):
+    """The same rows appended to the fixed-batch stream and to pages give the same bytes: rows of many scales, offsets
+    much larger than their range (codes that need the clamp), coarse grids with planted midpoints, few distinct values."""
+    from hybrid_precision_quantized_gb300 import HybridLayer, hyq_quantize_append
+    HKV, n = 4, 64 * 24
+    gen = torch.Generator().manual_seed(bits[0] * 16 + bits[1])
+    parts = []
+    for scale in (1e-4, 0.03, 1.0, 20.0, 3000.0):
+        x = torch.randn(2, HKV, 192, 128, generator=gen) * scale
+        parts.append(x)
+        parts.append(x * 0.01 + scale * 3 * torch.randn(2, HKV, 192, 4, 1, generator=gen).expand(-1, -1, -1, -1, 32).flatten(-2))
+    rows = torch.cat(parts, 2)[:, :, : n - 192].to(torch.bfloat16)
+    ties = torch.stack([tie_rows(7 + i, (HKV, 192, 128), bits[i]) for i in range(2)])
+    k, v = torch.cat([rows, ties], 2).cuda()
+    assert k.shape[1] == n
+    layer = HybridLayer(make_config(1, HKV, HKV, capacity=n, window=0, bits_k=bits[0], bits_v=bits[1]))
+    layer.reset()
+    hyq_quantize_append(layer.cfg, k[None].contiguous(), v[None].contiguous(), n, layer.c)
+    cache = make(HKV, HKV, n // 64, 1, n // 64, bits=bits)
+    cache.reserve(ints([0]), ints([n]))
+    cache.append(0, k.transpose(0, 1).contiguous(), v.transpose(0, 1).contiguous(), cu_rows=ints([0, n]))
+    assert hyq_read_device_error(layer.err()) == 0 and hyq_read_device_error(cache.err()) == 0
+    pages = cache.pool()[0, cache.table()[0].long()]          # [blocks, HKV, bytes]
+    assert torch.equal(pages.transpose(0, 1), layer.qblocks()[0])
