@@ -30,7 +30,7 @@
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;              // warps that share out a group's units, each with a ring of its own
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowsQ = HYQ_MAX_GQA;    // query rows per tile (MMA N)
 constexpr int kPart = HYQ_D + 4;       // acc[128], m, l and two unused floats per query row
@@ -39,22 +39,28 @@ constexpr int kMaxNQ = 4;             // query tiles that one block takes togeth
 
 // The kernel's shape for NQ query tiles a group.  One tile: two blocks an SM
 // (one's group change hides behind the other) and, for 4-bit codes, units of
-// two adjacent 16-row tiles.  kMaxNQ: the accumulators leave registers for one
-// block an SM, whose ring is deeper.
+// two adjacent 16-row tiles.  kMaxNQ: one block an SM, and two warps to a ring,
+// each with half of the query tiles, whose accumulators leave 16 warps' worth of
+// registers (one warp with all four at 8 warps an SM waited more than the codes
+// unpacked twice cost: 79 against 73 us for 32 query rows a KV head, 8-bit codes,
+// 8 sequences of 4 to 16 thousand positions).
 template <int BK, int BV, int NQ>
 struct Ring : QFmt<BK, BV> {
+  static constexpr int kHalves = NQ == 1 ? 1 : 2;  // warps that work on one ring
+  static constexpr int kNW = NQ / kHalves;         // query tiles of a warp
+  static constexpr int kQuery = NQ == 1 ? 2048 : kPairQuery;  // bytes of a query tile's operands
+  static_assert(kNW <= 2, "one query tile, or a pair");
   static constexpr int kPerSm = NQ == 1 ? 2 : 1;
+  static constexpr int kBlockThreads = kThreads * kHalves;
   static constexpr int kTiles = BK + BV == 8 && NQ == 1 ? 2 : 1;  // tiles per unit
-  static constexpr int kSlots = NQ > 1 ? 4 : BK + BV == 12 ? 3 : 2;
   static constexpr int kUnit = kTiles * QFmt<BK, BV>::kTile;
+  static constexpr int kSlots = NQ > 1 ? (4096 * NQ + kUnit - 1) / kUnit : BK + BV == 12 ? 3 : 2;
   static constexpr int kCost = (NQ == 1 ? 48 : 16 * NQ) / kTiles;  // units that a group's fixed work is worth
   static constexpr int kRows = 16 * kTiles;
   static constexpr int kPerPage = HYQ_PAGE_ROWS / kRows;
   static constexpr int kWarpBytes = kSlots * kUnit;
   static constexpr int kSmemBytes = kWarps * kWarpBytes;
-  // query tiles whose partials a warp's ring holds at once
-  static constexpr int kJoin = NQ * 4096 <= kWarpBytes ? NQ : NQ > 2 && 2 * 4096 <= kWarpBytes ? 2 : 1;
-  static_assert(kJoin * 4096 <= kWarpBytes && NQ % kJoin == 0, "a warp's partial fits its ring");
+  static_assert(NQ * 4096 <= kWarpBytes && kSlots <= 32, "the query tiles' partials fit a ring");
   static_assert(kWarps % kPerPage == 0, "a warp's units take the same part of their pages");
 };
 
@@ -113,26 +119,55 @@ struct Segment {
   int64_t base;             // of the group's first unit in the line
 };
 
+// What the two warps of a ring share beside its bytes.
+template <int kSlots>
+struct Ctl {
+  uint64_t full[kSlots];  // the slot's copy is there
+  uint64_t free[kSlots];  // the second half's warp is done with it
+  int at[kSlots];         // position of the slot's first row, or -1 (nothing was copied)
+};
+// Barriers by their shared memory addresses.
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done;
+}
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity) {  // bounded, like mbar_wait
+  bool done = mbar_try_at(bar, parity);  // as a rule
+  for (int it = 0; !done && it < (1 << 22); ++it) done = mbar_try_at(bar, parity);
+  return done;
+}
+
 // Output row of (token, head) pair `flat` of a KV head whose first row is `out`.
 __device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, int gq, int flat) {
   const int tok = flat / gq;
   return out + ((size_t)tok * HQ + (flat - tok * gq)) * HYQ_D;
 }
 
-// One block: joins the n partials of a group's n_rows rows.  Part i lies at
+// One block: joins the n partials of a group's n_rows rows, eight rows per 256 threads.  Part i lies at
 // parts + i stride, the first one `first` further.  A thread takes four elements
 // of a row over every S-th part, kHold parts at a time, with an online softmax
 // of its own (each part's maximum and sum come with its elements, so there is
 // one round of loads and nothing to wait for between them).  Out of line and
 // short: the code runs once a launch, cold, and its instructions are fetched
 // while the call waits (unrolled further it was slower).
+template <int kHalves>
 __device__ __noinline__ void join_parts(const float* parts, int first, int stride, int n, int n_rows, uint8_t* smem,
                                         __nv_bfloat16* out, int HQ, int gq, int flat0) {
-  const int tid = threadIdx.x;
+  const int half = kHalves > 1 ? threadIdx.x / kThreads : 0, tid = threadIdx.x - kThreads * half;
+  smem += half * kThreads * (sizeof(float4) + sizeof(float2));
   float4* sums = reinterpret_cast<float4*>(smem);                                // [kThreads]
   float2* stats = reinterpret_cast<float2*>(smem + kThreads * sizeof(float4));  // [kThreads]
   constexpr int kHold = 10;
-  for (int r0 = 0; r0 < n_rows; r0 += kRowsQ) {
+  for (int r0 = half * kRowsQ; r0 < n_rows; r0 += kHalves * kRowsQ) {
     const int items = min(kRowsQ, n_rows - r0) * (HYQ_D / 4), S = kThreads / items, share = tid / items;
     const int item = tid - share * items, r = r0 + (item >> 5), d = 4 * (item & 31);
     const int mine = share < S ? (n - share + S - 1) / S : 0;  // parts share, share + S, ...
@@ -166,7 +201,7 @@ __device__ __noinline__ void join_parts(const float* parts, int first, int strid
     if (S > 1) {  // fewer than eight rows, or the last ones of a group
       sums[tid] = a;
       stats[tid] = make_float2(M, L);
-      __syncthreads();
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + half), "n"(kThreads) : "memory");  // this half's threads
     }
     if (share == 0) {
       float top = M;
@@ -189,29 +224,42 @@ __device__ __noinline__ void join_parts(const float* parts, int first, int strid
 }
 
 template <int BK, int BV, int NQ>
-__global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kernel(const Params p) {
+__global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, NQ>::kPerSm)
+    paged_kernel(const Params p) {
   using R = Ring<BK, BV, NQ>;
   constexpr int kSlots = R::kSlots, kRowsG = NQ * kRowsQ;  // query rows per group
+  constexpr int kHalves = R::kHalves, kNW = R::kNW;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];  // units per (KV head, query tile) of the rows before b
   __shared__ int s_len[HYQ_PAGED_MAX_BATCH], s_seq[HYQ_PAGED_MAX_BATCH];
-  __shared__ int64_t s_warp[kWarps];
-  __shared__ __align__(16) uint32_t bq_s[NQ][4][kRowsQ][4][4];
+  __shared__ int64_t s_warp[kWarps * kHalves];
+  using Fragments = uint32_t[4][kRowsQ][4][4];
+  __shared__ __align__(16) uint8_t query_s[NQ][R::kQuery];  // each begins with Fragments
+  auto bq_s = [&](int k) -> Fragments& { return *reinterpret_cast<Fragments*>(query_s[k]); };
   __shared__ __align__(16) float rowc_s[NQ][kRowsQ][4];
   __shared__ uint32_t bz_s[NQ][kRowsQ][4];
   __shared__ int lim_s[NQ][kRowsQ];
-  __shared__ __align__(8) uint64_t bars[kWarps * kSlots];
-  __shared__ float red_m[kWarps][R::kJoin][kRowsQ], red_l[kWarps][R::kJoin][kRowsQ];
-  __shared__ float s_wt[R::kJoin * kRowsQ][kWarps];     // weights of the warps' partials
-  __shared__ float s_sum[R::kJoin * kRowsQ];
+  __shared__ Ctl<kSlots> s_ctl[kWarps];
+  __shared__ float red_m[kWarps][NQ][kRowsQ], red_l[kWarps][NQ][kRowsQ];
+  __shared__ float s_wt[kRowsG][kWarps];                // weights of the warps' partials
+  __shared__ float s_sum[kRowsG];
   __shared__ int s_last;
   __shared__ Run run;
   __shared__ Segment seg;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x;
+  int lane = tid & 31, half = kHalves > 1 ? tid / kThreads : 0, warp = (tid >> 5) - kWarps * half;
+  // (not to be derived anew from the thread's number in each pass of the loop)
+  if (kHalves > 1) asm volatile("" : "+r"(lane), "+r"(half), "+r"(warp));
+  const int g = lane >> 2, t = lane & 3;
+  // The warps w and w + 8 of two halves work on the same ring, w filling it.
+  const int kq = kNW * half;
   uint8_t* ring = smem + warp * R::kWarpBytes;
-  uint64_t* wb = bars + warp * kSlots;
-  if (lane < kSlots) mbar_init(&wb[lane], 1);
+  uint64_t* wb = s_ctl[warp].full;
+  if (half == 0 && lane < kSlots) {
+    mbar_init(&wb[lane], 1);
+    if (kHalves > 1) mbar_init(&s_ctl[warp].free[lane], 1);
+  }
   mbar_fence_init();
   chain_kernel();
 
@@ -245,23 +293,23 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       const int64_t y = __shfl_up_sync(0xffffffffu, pre, o);
       if (lane >= o) pre += y;
     }
-    if (lane == 31) s_warp[warp] = pre;
+    if (lane == 31) s_warp[tid >> 5] = pre;
     __syncthreads();
     int64_t at = pre - sum;
-    for (int i = 0; i < warp; ++i) at += s_warp[i];
+    for (int i = 0; i < tid >> 5; ++i) at += s_warp[i];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (4 * tid + i <= p.batch) s_cum[4 * tid + i] = at;
       at += w[i];
     }
-    if (tid == kThreads - 1 && p.batch == HYQ_PAGED_MAX_BATCH) s_cum[HYQ_PAGED_MAX_BATCH] = at;
+    if (tid == R::kBlockThreads - 1 && p.batch == HYQ_PAGED_MAX_BATCH) s_cum[HYQ_PAGED_MAX_BATCH] = at;
   }
   __syncthreads();
   // rows without positions: their outputs are zero
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
     if (s_cum[b] == s_cum[b + 1]) {
       uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * p.HQ * HYQ_D);
-      for (int k = tid; k < p.n_q * p.HQ * (HYQ_D / 8); k += kThreads) o[k] = make_uint4(0, 0, 0, 0);
+      for (int k = tid; k < p.n_q * p.HQ * (HYQ_D / 8); k += R::kBlockThreads) o[k] = make_uint4(0, 0, 0, 0);
     }
   // ---- this block's run -------------------------------------------------------
   // No more blocks than give each kMinUnits.  With few groups every group gets
@@ -327,10 +375,10 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     auto token_of = [&](int r) { return (seg.flat0 + r) / p.gq; };
     // the query rows, row `warp` of each query tile: loaded ahead of the page
     // numbers, prepared while the first copies are under way
-    uint2 qv[NQ];
+    uint2 qv[kNW];
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int r = kRowsQ * k + warp, tok = token_of(r);
+    for (int k = 0; k < kNW; ++k) {
+      const int r = kRowsQ * (kq + k) + warp, tok = token_of(r);
       qv[k] = make_uint2(0, 0);
       if (r < seg.n_rows)
         qv[k] = *reinterpret_cast<const uint2*>(
@@ -348,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     auto entry = [&](int j) -> int {
       if (j >= nj) return -1;
       const int x = x_first + j * (kWarps / R::kPerPage);
-      if (!seg.sel) return x;
+      if (NQ > 1 || !seg.sel) return x;  // several query tiles: never with lists
       const int e = seg.sel[x], pe = x > 0 ? seg.sel[x - 1] : -1;
       if (e < 0) return -1;
       if ((x > 0 && pe < 0) || pe >= e || (int64_t)e * HYQ_PAGE_ROWS >= len) {
@@ -360,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     auto page_of = [&](int e) -> int { return e < 0 ? -1 : seg.table[e]; };
     // Lane l holds block and page of unit 32 r + l of the present round r of 32
     // units, and of the next one; the pages arrive while the round is worked off.
-    int e_cur = entry(lane), pg_cur = page_of(e_cur);
-    int e_nxt = entry(32 + lane), pg_nxt = page_of(e_nxt);
+    int e_cur = half == 0 ? entry(lane) : -1, pg_cur = page_of(e_cur);
+    int e_nxt = half == 0 ? entry(32 + lane) : -1, pg_nxt = page_of(e_nxt);
     // Position of unit j's first row (of a unit that is there), else -1; issues its copy.
     auto issue = [&](int j) -> int {
       const int e = __shfl_sync(0xffffffffu, e_cur, j & 31), pg = __shfl_sync(0xffffffffu, pg_cur, j & 31);
@@ -369,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       const bool in = (uint32_t)pg < (uint32_t)p.pv.n_pages, ok = e >= 0 && at < len && in;
       const uint32_t n = done + (uint32_t)j;
       const int slot = n % kSlots;
+      if (kHalves > 1 && lane == 0) s_ctl[warp].at[slot] = ok ? at : -1;
+      if (kHalves > 1) __syncwarp();
       if (lane == slot) {  // copies that one thread issues complete one after another
         uint64_t* bar = &wb[slot];
         if (ok) {
@@ -388,67 +438,104 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
       }
       return ok ? at : -1;
     };
-    int at_slot[kSlots];
+    int at_slot[kSlots];  // one half: the slots' positions from the next unit's on
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) at_slot[j] = j < nj && !dead ? issue(j) : -1;
+    for (int j = 0; j < kSlots; ++j) at_slot[j] = half == 0 && j < nj && !dead ? issue(j) : -1;
 
-    // ---- the query rows: warp r prepares row r of each query tile ----------
+    // ---- the query rows: warp r prepares row r of each of its half's tiles --
 #pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      const int r = kRowsQ * k + warp;
-      prep_query_row<BK>(warp, lane, qv[k], bq_s[k], rowc_s[k], bz_s[k]);
-      if (lane == 0) lim_s[k][warp] = r < seg.n_rows ? max(0, len - p.n_q + 1 + token_of(r)) : len;
+    for (int k = 0; k < kNW; ++k) {
+      const int r = kRowsQ * (kq + k) + warp;
+      prep_query_row<BK>(warp, lane, qv[k], bq_s(kq + k), rowc_s[kq + k], bz_s[kq + k]);
+      if (lane == 0) lim_s[kq + k][warp] = r < seg.n_rows ? max(0, len - p.n_q + 1 + token_of(r)) : len;
     }
     __syncthreads();
     uint32_t bq[8][2];
     QConst qc;
-    if (NQ == 1) load_query_consts(g, t, bq_s[0], rowc_s[0], bz_s[0], bq, qc);
     const int minlim = lim_s[0][0];  // the rows' tokens ascend
-    State st[NQ];
-#pragma unroll
-    for (int k = 0; k < NQ; ++k) reset_state(st[k]);
+    std::conditional_t<NQ == 1, State, PairState> st;
+    if constexpr (NQ == 1) {
+      load_query_consts(g, t, bq_s(0), rowc_s[0], bz_s[0], bq, qc);
+      reset_state(st);
+    } else {
+      if (tid < 32 * NQ) spread_query_consts(query_s[tid >> 5], lane, rowc_s[tid >> 5], bz_s[tid >> 5]);
+      __syncthreads();
+      reset_pair(st);
+    }
 
-    for (int j = 0; j < nj && !dead; ++j) {
-      const uint32_t n = done + (uint32_t)j;
-      const int slot = n % kSlots;
-      const bool ok = mbar_wait(&wb[slot], (n / kSlots) & 1u);
-      if (__any_sync(0xffffffffu, !ok)) {
-        // A copy did not arrive: flag it, let this warp's other copies land
-        // before shared memory is used for anything else, and stop.
-        if (lane == 0) {
-          hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
-          for (int k = j; k < nj && k < j + kSlots; ++k)
+    // A wait ran out: flag it, let this warp's other copies (units j0 .. j1 - 1)
+    // land before shared memory is used for anything else, and stop.
+    auto give_up = [&](int j0, int j1) {
+      if (lane == 0) {
+        hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
+        if (half == 0)
+          for (int k = j0; k < nj && k < j1; ++k)
             (void)mbar_wait(&wb[(done + k) % kSlots], ((done + k) / kSlots) & 1u);
-        }
-        __syncwarp();
-        dead = true;
-        break;
       }
-      const int at = at_slot[0];
-      const uint8_t* tb = ring + slot * R::kUnit;
-      if (at >= 0) {
-        if constexpr (NQ == 1) {
+      __syncwarp();
+      dead = true;
+    };
+    if constexpr (kHalves == 1) {
+      for (int j = 0; j < nj && !dead; ++j) {
+        const uint32_t n = done + (uint32_t)j;
+        const int slot = n % kSlots;
+        if (__any_sync(0xffffffffu, !mbar_wait(&wb[slot], (n / kSlots) & 1u))) {
+          give_up(j, j + kSlots);
+          break;
+        }
+        const int at = at_slot[0];
+        const uint8_t* tb = ring + slot * R::kUnit;
+        if (at >= 0) {
           if (at + R::kRows <= minlim) {
-            q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st[0]);
+            q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st);
           } else {
             const int lim0 = lim_s[0][2 * t], lim1 = lim_s[0][2 * t + 1];
             for (int x = 0; x < R::kTiles && at + 16 * x < len; ++x) {
               const int a = at + 16 * x;
-              q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, len - a, bq, qc, st[0], lim0 - a, lim1 - a);
+              q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, len - a, bq, qc, st, lim0 - a, lim1 - a);
             }
           }
-        } else if (at + R::kRows <= minlim) {
-          q_tile_multi<BK, BV, NQ, false>(tb, lane, 16, bq_s, rowc_s, bz_s, lim_s, at, st);
-        } else {
-          q_tile_multi<BK, BV, NQ, true>(tb, lane, len - at, bq_s, rowc_s, bz_s, lim_s, at, st);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k + 1 < kSlots; ++k) at_slot[k] = at_slot[k + 1];
+        if (j + kSlots < nj) {
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          at_slot[kSlots - 1] = issue(j + kSlots);
         }
       }
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k + 1 < kSlots; ++k) at_slot[k] = at_slot[k + 1];
-      if (j + kSlots < nj) {
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        at_slot[kSlots - 1] = issue(j + kSlots);
+    } else {
+      uint32_t slot = done % kSlots, par = (done / kSlots) & 1u;
+      uint32_t ctl = smem_u32(&s_ctl[warp]), tiles = smem_u32(ring), query = smem_u32(query_s[kq]);
+      asm volatile("" : "+r"(ctl), "+r"(tiles), "+r"(query));  // kept, not formed anew in each pass
+      constexpr uint32_t kFree = offsetof(Ctl<kSlots>, free), kAt = offsetof(Ctl<kSlots>, at);
+      for (int j = 0; j < nj && !dead; ++j) {
+        if (__any_sync(0xffffffffu, !mbar_wait_at(ctl + 8 * slot, par))) {
+          give_up(j, j + kSlots - (j > 0 ? 1 : 0));
+          break;
+        }
+        const int at = (int)lds32<kAt>(ctl + 4 * slot);
+        const uint32_t tb = tiles + slot * R::kUnit;
+        if (at >= 0) {
+          if (at + R::kRows <= minlim)
+            q_tile_pair<BK, BV, false>(tb, lane, query, 16, lim_s + kq, at, st);
+          else
+            q_tile_pair<BK, BV, true>(tb, lane, query, len - at, lim_s + kq, at, st);
+        }
+        __syncwarp();
+        if (half == 1) {
+          if (lane == 0) mbar_arrive_at(ctl + kFree + 8 * slot);
+        } else if (j > 0 && j - 1 + kSlots < nj) {
+          // the slot of the unit before, which the other half has mostly left too
+          const uint32_t s0 = slot ? slot - 1 : kSlots - 1, p0 = slot ? par : par ^ 1u;
+          if (__any_sync(0xffffffffu, !mbar_wait_at(ctl + kFree + 8 * s0, p0))) {
+            give_up(j + 1, j - 1 + kSlots);
+            break;
+          }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          (void)issue(j - 1 + kSlots);
+        }
+        if (++slot == kSlots) slot = 0, par ^= 1u;
       }
     }
     done += nj;
@@ -458,61 +545,62 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
     const int n_rows = seg.n_rows;
     const bool whole = seg.w0 == 0 && seg.w1 == seg.n_units;
     float* pp = p.part + ((size_t)blockIdx.x * 2 + (seg.w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
-    constexpr int kJoin = R::kJoin;
+    if (kHalves > 1) __syncthreads();  // both halves are done with the rings
+    if constexpr (NQ == 1) {
+      store_warp_partial<BV>(st, qc, g, t, reinterpret_cast<float*>(ring), red_m[warp][0], red_l[warp][0]);
+    } else {
 #pragma unroll
-    for (int k0 = 0; k0 < NQ; k0 += kJoin) {
-      if (NQ > 1 && kRowsQ * k0 >= n_rows) break;
-#pragma unroll
-      for (int k = 0; k < kJoin; ++k) {
-        if (NQ > 1) load_query_consts(g, t, bq_s[k0 + k], rowc_s[k0 + k], bz_s[k0 + k], bq, qc);
-        store_warp_partial<BV>(st[k0 + k], qc, g, t, reinterpret_cast<float*>(ring + 4096 * k), red_m[warp][k],
-                               red_l[warp][k]);
+      for (int k = 0; k < 2; ++k) {
+        load_query_consts(g, t, bq_s(kq + k), rowc_s[kq + k], bz_s[kq + k], bq, qc);
+        State one = pair_state(st, k, qc);
+        store_warp_partial<BV>(one, qc, g, t, reinterpret_cast<float*>(ring + 4096 * (kq + k)), red_m[warp][kq + k],
+                               red_l[warp][kq + k]);
       }
-      __syncthreads();
-      // eight lanes a row: its weights 2^(m_w - M) and its sum
-      if (tid < kJoin * kRowsQ * kWarps) {
-        const int r = tid >> 3, w = tid & 7;
-        const float mw = red_m[w][r >> 3][r & 7];
-        float M = mw;
-#pragma unroll
-        for (int o = 1; o < kWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
-        float L = red_l[w][r >> 3][r & 7] * wt;
-#pragma unroll
-        for (int o = 1; o < kWarps; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        s_wt[r][w] = wt;
-        if (w == 0) {
-          s_sum[r] = L;
-          if (!whole && kRowsQ * k0 + r < n_rows) {
-            pp[(kRowsQ * k0 + r) * kPart + HYQ_D] = M;
-            pp[(kRowsQ * k0 + r) * kPart + HYQ_D + 1] = L;
-          }
-        }
-      }
-      __syncthreads();
-      // four elements of a row a thread (the warps' partials hold element d at d ^ (row / 2))
-      for (int i = tid; i < min(kJoin * kRowsQ, n_rows - kRowsQ * k0) * (HYQ_D / 4); i += kThreads) {
-        const int r = i >> 5, d = 4 * (i & 31), x = (r & 7) >> 1;
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(smem + w * R::kWarpBytes + 4096 * (r >> 3) +
-                                                            4 * ((r & 7) * HYQ_D + d));
-          const float wt = s_wt[r][w];
-          a.x = fmaf(wt, v.x, a.x), a.y = fmaf(wt, v.y, a.y), a.z = fmaf(wt, v.z, a.z), a.w = fmaf(wt, v.w, a.w);
-        }
-        if (x & 1) a = make_float4(a.y, a.x, a.w, a.z);
-        if (x & 2) a = make_float4(a.z, a.w, a.x, a.y);
-        if (whole) {
-          const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
-          *reinterpret_cast<uint2*>(out_row(seg.out, p.HQ, p.gq, seg.flat0 + kRowsQ * k0 + r) + d) =
-              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        } else {
-          *reinterpret_cast<float4*>(pp + (kRowsQ * k0 + r) * kPart + d) = a;
-        }
-      }
-      __syncthreads();  // the rings are free again
     }
+    __syncthreads();
+    // eight lanes a row: its weights 2^(m_w - M) and its sum
+    if (tid < kRowsG * kWarps) {
+      const int r = tid >> 3, w = tid & 7;
+      const float mw = red_m[w][r >> 3][r & 7];
+      float M = mw;
+#pragma unroll
+      for (int o = 1; o < kWarps; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float wt = mw == -INFINITY ? 0.f : ex2(mw - M);
+      float L = red_l[w][r >> 3][r & 7] * wt;
+#pragma unroll
+      for (int o = 1; o < kWarps; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      s_wt[r][w] = wt;
+      if (w == 0) {
+        s_sum[r] = L;
+        if (!whole && r < n_rows) {
+          pp[r * kPart + HYQ_D] = M;
+          pp[r * kPart + HYQ_D + 1] = L;
+        }
+      }
+    }
+    __syncthreads();
+    // four elements of a row a thread (the warps' partials hold element d at d ^ (row / 2))
+    for (int i = tid; i < n_rows * (HYQ_D / 4); i += R::kBlockThreads) {
+      const int r = i >> 5, d = 4 * (i & 31), x = (r & 7) >> 1;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(smem + w * R::kWarpBytes + 4096 * (r >> 3) +
+                                                          4 * ((r & 7) * HYQ_D + d));
+        const float wt = s_wt[r][w];
+        a.x = fmaf(wt, v.x, a.x), a.y = fmaf(wt, v.y, a.y), a.z = fmaf(wt, v.z, a.z), a.w = fmaf(wt, v.w, a.w);
+      }
+      if (x & 1) a = make_float4(a.y, a.x, a.w, a.z);
+      if (x & 2) a = make_float4(a.z, a.w, a.x, a.y);
+      if (whole) {
+        const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<uint2*>(out_row(seg.out, p.HQ, p.gq, seg.flat0 + r) + d) =
+            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(pp + r * kPart + d) = a;
+      }
+    }
+    __syncthreads();  // the rings are free again
     if (!whole) {
       // blocks that share this group: those holding its first and last unit
       const int64_t base = seg.base;
@@ -530,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
         // group; the first block, whose run holds the group's first unit, has it
         // in slot 1
         constexpr int kSlot = NQ * kRowsQ * kPart;
-        join_parts(p.part + (size_t)c0 * 2 * kSlot, kSlot, 2 * kSlot, c1 - c0 + 1, n_rows,
-                   smem, seg.out, p.HQ, p.gq, seg.flat0);
+        join_parts<kHalves>(p.part + (size_t)c0 * 2 * kSlot, kSlot, 2 * kSlot, c1 - c0 + 1, n_rows,
+                            smem, seg.out, p.HQ, p.gq, seg.flat0);
       }
     }
     __syncthreads();  // the segment is done with
@@ -544,10 +632,10 @@ __global__ void __launch_bounds__(kThreads, Ring<BK, BV, NQ>::kPerSm) paged_kern
 // groups of one KV head lie side by side and meet most of each other's reads in
 // L2) is as fast as four tiles a pass, whose one block an SM has eight warps to
 // hide latency with: 4-bit codes, 8 sequences of up to 16 thousand positions,
-// 8 KV heads, 4 / 8 / 16 tiles: 74 / 131 / 246 us one by one, 80 / 134 / 242 by
-// fours; 32 sequences of 2000: 58 / 99 / 184 against 65 / 107 / 189.  Only for wider codes, whose
-// cache passes L2 sooner, do full fours pay: 8-bit 89 / 164 / 313 us one by one,
-// 77 / 132 / 239 by fours (6 tiles, two passes of four: 113 against 132).
+// 8 KV heads, 4 / 8 / 16 tiles: 72 / 129 / 243 us one by one, 71 / 126 / 232 by
+// fours; one sequence of 32768: 36 / 57 / 102 against 38 / 61 / 101.  For wider
+// codes, whose cache passes L2 sooner, full fours pay: 8-bit 89 / 164 / 313 us one
+// by one, 69 / 120 / 221 by fours (6 tiles, two passes of four: 113 against 111).
 int group_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
   const int gq = c->num_q_heads / c->num_kv_heads, tiles = (n_q * gq + kRowsQ - 1) / kRowsQ;
   return !blocks && hyq_bits_k(c) + hyq_bits_v(c) > 8 && tiles % kMaxNQ == 0 ? kMaxNQ : 1;
@@ -562,7 +650,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   const int grid = R::kPerSm * hyq_num_sms();
-  return hyq_launch_chained(paged_kernel<BK, BV, NQ>, dim3(grid), kThreads, R::kSmemBytes, s, p);
+  return hyq_launch_chained(paged_kernel<BK, BV, NQ>, dim3(grid), R::kBlockThreads, R::kSmemBytes, s, p);
 }
 
 template <int BK, int BV>

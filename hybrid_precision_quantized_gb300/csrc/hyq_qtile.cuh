@@ -6,6 +6,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "hyq_common.cuh"
 
 namespace {
@@ -254,12 +256,14 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   }
 }
 
-// The running maximum of q_tiles and q_tile_multi is a reference that may lag:
+// The running maximum of q_tiles and q_tile_pair is a reference that may lag:
 // it moves (and the accumulators are rescaled) only when a logit passes it by
 // more than kSlack<BV> in log2 units.  A probability is then at most 2^kSlack,
 // and p s still fits fp16: s is at most 2 * 65504 / qmax, 8734 for 4-bit and 514
 // for 8-bit values.  The first maximum of a row is seldom its last, so without
-// the slack short runs of tiles rescale at most of their tiles.
+// the slack short runs of tiles rescale at most of their tiles.  Each row's
+// maximum moves for its own logits alone: its result does not depend on the rows
+// that share its tile.
 template <int BV>
 constexpr float kSlack = BV == 4 ? 2.f : 6.f;
 // The slack in the scaled domain of a row with inv = 2^-sigma.
@@ -328,7 +332,7 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
       tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 4));
       tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 8));
       tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 16));
-      const float mn = fmaxf(st.m[j], tm[j]);
+      const float mn = tm[j] > st.m[j] + slack_of<BV>(qc.inv[j]) ? tm[j] : st.m[j];
       const float nm = mn == -INFINITY ? 0.f : -mn * qc.inv[j];
       const float corr = ex2(fmaf(st.m[j], qc.inv[j], nm));
       st.m[j] = mn;
@@ -380,136 +384,176 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
   }
 }
 
-// q_tile for NQ tiles of query rows at once: a tile's codes are unpacked once
-// (the keys' once per two query tiles) and its scales converted once for all of
-// them.  The query operands stay in shared memory: bq_s, rowc_s and bz_s of
-// query tile k.  kRows as in q_tile, with lim[k] the number of the tile's rows that
-// heads 2t, 2t+1 of query tile k see.
-template <int BK, int BV, int NQ, bool kRows>
-__device__ __forceinline__ void q_tile_multi(const uint8_t* tb, int lane, int vr, const uint32_t (*bq_s)[4][HYQ_MAX_GQA][4][4],
-                                             const float (*rowc_s)[HYQ_MAX_GQA][4],
-                                             const uint32_t (*bz_s)[HYQ_MAX_GQA][4], const int (*lim_s)[HYQ_MAX_GQA],
-                                             int at, State (&st)[NQ]) {
+// q_tile_pair: two tiles of query rows at once, their operands in shared
+// memory, laid out so that a lane's parts lie at constant offsets from two
+// addresses (the loop has no registers to spare for more):
+//   [0, 2048)     bq_s, 16 bytes per k-step pair and lane
+//   [2048, 2112)  per t: the code-product factor and 2^-sigma of head 2t, then of 2t + 1
+//   [2112, 2240)  per lane: the zero-point fragment
+constexpr int kPairQuery = 2240;  // bytes of a query tile
+struct PairState {
+  float nm[2][2];       // minus the running maximum in log2 units (kNoMax before the first)
+  float l[2][2];        // running sums of this thread's probabilities
+  float acc[2][8][4];   // as in State
+  float zd[2][4];       // sum_j p_j z_jq: rows g < 4, as in State
+};
+constexpr float kNoMax = 1e30f;  // above any slack, and finite: a masked logit less it is still minus infinity
+
+__device__ __forceinline__ void reset_pair(PairState& st) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    st.nm[k][0] = st.nm[k][1] = kNoMax;
+    st.l[k][0] = st.l[k][1] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) st.acc[k][mt][0] = st.acc[k][mt][1] = st.acc[k][mt][2] = st.acc[k][mt][3] = 0.f;
+    st.zd[k][0] = st.zd[k][1] = st.zd[k][2] = st.zd[k][3] = 0.f;
+  }
+}
+
+// The lane's constants of a query tile from what prep_query_row left.
+__device__ __forceinline__ void spread_query_consts(uint8_t* query, int lane, const float (&rowc_s)[HYQ_MAX_GQA][4],
+                                                    const uint32_t (&bz_s)[HYQ_MAX_GQA][4]) {
+  const int g = lane >> 2, t = lane & 3;
+  const float *a = rowc_s[2 * t], *b = rowc_s[2 * t + 1];
+  if (g == 0) *reinterpret_cast<float4*>(query + 2048 + 16 * t) = make_float4(a[0], a[2], b[0], b[2]);
+  *reinterpret_cast<uint32_t*>(query + 2112 + 4 * lane) = bz_s[g][t];
+}
+
+// Loads from a shared memory address in a register, at a constant offset.  (An
+// address formed from a shared variable's name costs three instructions and a
+// special register each time that the compiler forms it anew.)
+template <int kOff>
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a), "n"(kOff));
+  return v;
+}
+template <int kOff>
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1 + %2];\n" : "=r"(v) : "r"(a), "n"(kOff));
+  return v;
+}
+
+// One 16-row tile at address `tb` for two query tiles: a tile's codes are unpacked
+// and its scales converted once for both.  query: address of the first query tile's
+// operands.  kRows as in q_tile, with lim_s[k] the rows that query
+// tile k's heads see, less `at`.
+template <int BK, int BV, bool kRows>
+__device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t query, int vr,
+                                            const int (*lim_s)[HYQ_MAX_GQA], int at, PairState& st) {
   using F = QFmt<BK, BV>;
   const int g = lane >> 2, t = lane & 3;
-  float lg[NQ][4];
-  {
-    constexpr int kW = BK == 4 ? 8 : 16;
-    uint32_t kw[kW];
-    load_words<kW>(tb, lane, kw);
-    const uint4 ma = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
-    const uint4 mb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
-    const float2 a01 = half2_to_float2(ma.x), a23 = half2_to_float2(ma.y);
-    const float2 b01 = half2_to_float2(mb.x), b23 = half2_to_float2(mb.y);
-    const uint32_t za = (t & 1) ? ma.w : ma.z, zb = (t & 1) ? mb.w : mb.z;
-    constexpr int kStep = 2;
-    static_assert(NQ % kStep == 0, "query tiles in pairs");
+  const uint32_t tl = tb + 16 * lane, tg = tb + 16 * g, tt = tb + 16 * t, tz = tt + 4 * (g & 3);
+  const uint32_t qa = query + 16 * lane, qt = query + 16 * t, qz = query + 4 * lane;
+  float lg[2][4];
+  const uint4 ma = lds128<F::kKMeta>(tg), mb = lds128<F::kKMeta + 128>(tg);
+  // group by group, each scaled as soon as its two products are there: few
+  // accumulators are alive at a time
+  auto key_group = [&](auto group) {
+    constexpr int q = decltype(group)::value;
+    const uint4 w = lds128<512 * (BK == 8 ? q : q >> 1)>(tl);
+    const uint4 b0 = lds128<512 * q>(qa), b1 = lds128<kPairQuery + 512 * q>(qa);
+    float C[2][4];
 #pragma unroll
-    for (int k0 = 0; k0 < NQ; k0 += kStep) {
-      float C[kStep][4][4];
+    for (int k = 0; k < 2; ++k) C[k][0] = C[k][1] = C[k][2] = C[k][3] = 0.f;
 #pragma unroll
-      for (int k = 0; k < kStep; ++k)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) C[k][q][0] = C[k][q][1] = C[k][q][2] = C[k][q][3] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 b[kStep];
-#pragma unroll
-        for (int k = 0; k < kStep; ++k) b[k] = *reinterpret_cast<const uint4*>(&bq_s[k0 + k][i][g][t][0]);
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int ks = 2 * i + hf;
-          uint32_t x0, x1, x2, x3;
-          if (BK == 4) {
-            const uint32_t w = kw[ks % kW], w8 = w >> 8;
-            x0 = w & 0x000F000Fu, x1 = w & 0x00F000F0u, x2 = w8 & 0x000F000Fu, x3 = w8 & 0x00F000F0u;
-          } else {
-            const uint32_t w0 = kw[(2 * ks) % kW], w1 = kw[(2 * ks + 1) % kW];
-            x0 = w0 & 0x00FF00FFu, x1 = w1 & 0x00FF00FFu, x2 = odd_bytes(w0), x3 = odd_bytes(w1);
-          }
-#pragma unroll
-          for (int k = 0; k < kStep; ++k)
-            mma_f16(C[k][ks >> 1], x0, x1, x2, x3, hf ? b[k].z : b[k].x, hf ? b[k].w : b[k].y);
-        }
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t x0, x1, x2, x3;
+      if (BK == 4) {
+        const uint32_t v = u4c(w, 2 * (q & 1) + hf), v8 = v >> 8;
+        x0 = v & 0x000F000Fu, x1 = v & 0x00F000F0u, x2 = v8 & 0x000F000Fu, x3 = v8 & 0x00F000F0u;
+      } else {
+        const uint32_t w0 = u4c(w, 2 * hf), w1 = u4c(w, 2 * hf + 1);
+        x0 = w0 & 0x00FF00FFu, x1 = w1 & 0x00FF00FFu, x2 = odd_bytes(w0), x3 = odd_bytes(w1);
       }
+      mma_f16(C[0], x0, x1, x2, x3, hf ? b0.z : b0.x, hf ? b0.w : b0.y);
+      mma_f16(C[1], x0, x1, x2, x3, hf ? b1.z : b1.x, hf ? b1.w : b1.y);
+    }
+    // the group's steps of tokens g and g + 8
+    const float2 fa = half2_to_float2(q < 2 ? ma.x : ma.y), fb = half2_to_float2(q < 2 ? mb.x : mb.y);
+    const float sa = q & 1 ? fa.y : fa.x, sb = q & 1 ? fb.y : fb.x;
 #pragma unroll
-      for (int k = 0; k < kStep; ++k) {
-        float(&l)[4] = lg[k0 + k];
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float2 ksc = *reinterpret_cast<const float2*>(&rowc_s[k0 + k][2 * t + c][0]);
-          l[c] = ksc.x *
-                 fmaf(a01.x, C[k][0][c], fmaf(a01.y, C[k][1][c], fmaf(a23.x, C[k][2][c], a23.y * C[k][3][c])));
-          l[2 + c] = ksc.y * fmaf(b01.x, C[k][0][2 + c],
-                                  fmaf(b01.y, C[k][1][2 + c], fmaf(b23.x, C[k][2][2 + c], b23.y * C[k][3][2 + c])));
-        }
-        mma_f16(l, za, zb, 0u, 0u, bz_s[k0 + k][g][t], 0u);
-        if (kRows) {
-          const int v0 = lim_s[k0 + k][2 * t] - at, v1 = lim_s[k0 + k][2 * t + 1] - at;
-          if (g >= v0) l[0] = -INFINITY;
-          if (g >= v1) l[1] = -INFINITY;
-          if (g + 8 >= v0) l[2] = -INFINITY;
-          if (g + 8 >= v1) l[3] = -INFINITY;
-        }
+      for (int c = 0; c < 2; ++c) {
+        lg[k][c] = q == 3 ? sa * C[k][c] : fmaf(sa, C[k][c], lg[k][c]);
+        lg[k][2 + c] = q == 3 ? sb * C[k][2 + c] : fmaf(sb, C[k][2 + c], lg[k][2 + c]);
       }
+  };
+  key_group(std::integral_constant<int, 3>{});
+  key_group(std::integral_constant<int, 2>{});
+  key_group(std::integral_constant<int, 1>{});
+  key_group(std::integral_constant<int, 0>{});
+  const uint32_t za = (t & 1) ? ma.w : ma.z, zb = (t & 1) ? mb.w : mb.z;
+  float x[2][4];  // lambda 2^-sigma - max, in log2 units
+  bool above = false;
+  auto logits = [&](auto tile) {
+    constexpr int k = decltype(tile)::value;
+    float(&l)[4] = lg[k];
+    const uint4 c = lds128<kPairQuery * k + 2048>(qt);
+    const float f0 = __uint_as_float(c.x), f1 = __uint_as_float(c.z);
+    constexpr float kHigh = BK == 4 ? 0.0625f : 1.f;  // 4-bit tokens g + 8 carry 16 c
+    l[0] *= f0, l[1] *= f1, l[2] *= f0 * kHigh, l[3] *= f1 * kHigh;
+    mma_f16(l, za, zb, 0u, 0u, lds32<kPairQuery * k + 2112>(qz), 0u);
+    if (kRows) {
+      const int v0 = lim_s[k][2 * t] - at, v1 = lim_s[k][2 * t + 1] - at;
+      if (g >= v0) l[0] = -INFINITY;
+      if (g >= v1) l[1] = -INFINITY;
+      if (g + 8 >= v0) l[2] = -INFINITY;
+      if (g + 8 >= v1) l[3] = -INFINITY;
     }
-  }
-  // ---- running maxima, tested together, moved tile by tile --------------------
-  float inv[NQ][2], tm[NQ][2];
-  bool above[NQ], any = false;
 #pragma unroll
-  for (int k = 0; k < NQ; ++k) {
-    above[k] = false;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      inv[k][j] = rowc_s[k][2 * t + j][2];
-      tm[k][j] = fmaxf(lg[k][j], lg[k][2 + j]);
-      above[k] |= tm[k][j] > st[k].m[j] + slack_of<BV>(inv[k][j]);
-    }
-    any |= above[k];
-  }
-  if (__any_sync(0xffffffffu, any)) {
-#pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-      if (!__any_sync(0xffffffffu, above[k])) continue;
+    for (int i = 0; i < 4; ++i) x[k][i] = fmaf(l[i], __uint_as_float(i & 1 ? c.w : c.y), st.nm[k][i & 1]);
+    above |= fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3])) > kSlack<BV>;
+  };
+  logits(std::integral_constant<int, 0>{});
+  logits(std::integral_constant<int, 1>{});
+  if (__any_sync(0xffffffffu, above)) {
+    auto raise = [&](auto tile) {
+      constexpr int k = decltype(tile)::value;
+      const uint4 c = lds128<kPairQuery * k + 2048>(qt);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x = fmaxf(tm[k][j], __shfl_xor_sync(0xffffffffu, tm[k][j], 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        const float mn = fmaxf(st[k].m[j], x);
-        const float nm = mn == -INFINITY ? 0.f : -mn * inv[k][j];
-        const float corr = ex2(fmaf(st[k].m[j], inv[k][j], nm));
-        st[k].m[j] = mn;
-        st[k].nm[j] = nm;
-        st[k].l[j] *= corr;
+        const float inv = __uint_as_float(j ? c.w : c.y);
+        float tm = fmaxf(lg[k][j], lg[k][2 + j]);
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+        // inv is a power of two: the product is exact
+        const float old = st.nm[k][j], nm = fmaf(tm, inv, old) > kSlack<BV> ? -tm * inv : old;
+        const float corr = ex2(nm - old);
+        st.nm[k][j] = nm;
+        st.l[k][j] *= corr;
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) {
-          st[k].acc[mt][j] *= corr;
-          st[k].acc[mt][2 + j] *= corr;
+          st.acc[k][mt][j] *= corr;
+          st.acc[k][mt][2 + j] *= corr;
         }
-        st[k].zd[j] *= corr;
+        st.zd[k][j] *= corr;
+        x[k][j] = fmaf(lg[k][j], inv, nm);
+        x[k][2 + j] = fmaf(lg[k][2 + j], inv, nm);
       }
-    }
+    };
+    raise(std::integral_constant<int, 0>{});
+    raise(std::integral_constant<int, 1>{});
   }
-  uint32_t pt0[NQ], pt1[NQ];
+  uint32_t pt0[2], pt1[2];
 #pragma unroll
-  for (int k = 0; k < NQ; ++k) {
+  for (int k = 0; k < 2; ++k) {
     float p[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      p[j] = ex2(fmaf(lg[k][j], inv[k][j], st[k].nm[j]));
-      p[2 + j] = ex2(fmaf(lg[k][2 + j], inv[k][j], st[k].nm[j]));
-      st[k].l[j] += p[j] + p[2 + j];
-    }
+    for (int i = 0; i < 4; ++i) p[i] = ex2(x[k][i]);
+    st.l[k][0] += p[0] + p[2];
+    st.l[k][1] += p[1] + p[3];
     pt0[k] = movmatrix_trans(pack_f16x2(p[0], p[1]));
     pt1[k] = movmatrix_trans(pack_f16x2(p[2], p[3]));
   }
-  const uint8_t* vm = tb + F::kVMeta;
-  uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
-  uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
-  uint32_t z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * (g & 3));
-  uint32_t z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * (g & 3));
+  uint4 sv0 = lds128<F::kVMeta>(tt), sv1 = lds128<F::kVMeta + 64>(tt);
+  // rows g < 4 carry the zeros of group g; rows 4 .. 7 repeat them and are not used
+  uint32_t z0 = lds32<F::kVMeta + 128>(tz), z1 = lds32<F::kVMeta + 192>(tz);
   if (kRows) {
     const uint32_t k0 = (2 * t < vr ? 0xFFFFu : 0u) | (2 * t + 1 < vr ? 0xFFFF0000u : 0u);
     const uint32_t k1 = (2 * t + 8 < vr ? 0xFFFFu : 0u) | (2 * t + 9 < vr ? 0xFFFF0000u : 0u);
@@ -517,29 +561,48 @@ __device__ __forceinline__ void q_tile_multi(const uint8_t* tb, int lane, int vr
     sv1.x &= k1, sv1.y &= k1, sv1.z &= k1, sv1.w &= k1, z1 &= k1;
   }
 #pragma unroll
-  for (int k = 0; k < NQ; ++k) mma_f16(st[k].zd, z0, 0u, z1, 0u, pt0[k], pt1[k]);
-  constexpr int kV = BV == 4 ? 8 : 16;
-  uint32_t vw[kV];
-  load_words<kV>(tb + F::kVCode, lane, vw);
+  for (int k = 0; k < 2; ++k) mma_f16(st.zd[k], z0, 0u, z1, 0u, pt0[k], pt1[k]);
+  auto value_group = [&](auto group) {
+    constexpr int q = decltype(group)::value;
+    const uint4 w = lds128<F::kVCode + 512 * (BV == 8 ? q : q >> 1)>(tl);
+    uint32_t b0[2], b1[2];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t b0[NQ], b1[NQ];
-#pragma unroll
-    for (int k = 0; k < NQ; ++k) b0[k] = hmul2_u32(pt0[k], u4c(sv0, q)), b1[k] = hmul2_u32(pt1[k], u4c(sv1, q));
+    for (int k = 0; k < 2; ++k) b0[k] = hmul2_u32(pt0[k], u4c(sv0, q)), b1[k] = hmul2_u32(pt1[k], u4c(sv1, q));
 #pragma unroll
     for (int mm = 0; mm < 2; ++mm) {
       uint32_t x0, x1, x2, x3;
       if (BV == 4) {
-        const uint32_t x = vw[(2 * q + mm) % kV], x8 = x >> 8;
-        x0 = x & 0x000F000Fu, x1 = x & 0x00F000F0u, x2 = x8 & 0x000F000Fu, x3 = x8 & 0x00F000F0u;
+        const uint32_t v = u4c(w, 2 * (q & 1) + mm), v8 = v >> 8;
+        x0 = v & 0x000F000Fu, x1 = v & 0x00F000F0u, x2 = v8 & 0x000F000Fu, x3 = v8 & 0x00F000F0u;
       } else {
-        const uint32_t y0 = vw[(2 * (2 * q + mm)) % kV], y1 = vw[(2 * (2 * q + mm) + 1) % kV];
+        const uint32_t y0 = u4c(w, 2 * mm), y1 = u4c(w, 2 * mm + 1);
         x0 = y0 & 0x00FF00FFu, x1 = y1 & 0x00FF00FFu, x2 = odd_bytes(y0), x3 = odd_bytes(y1);
       }
 #pragma unroll
-      for (int k = 0; k < NQ; ++k) mma_f16(st[k].acc[2 * q + mm], x0, x1, x2, x3, b0[k], b1[k]);
+      for (int k = 0; k < 2; ++k) mma_f16(st.acc[k][2 * q + mm], x0, x1, x2, x3, b0[k], b1[k]);
     }
+  };
+  value_group(std::integral_constant<int, 0>{});
+  value_group(std::integral_constant<int, 1>{});
+  value_group(std::integral_constant<int, 2>{});
+  value_group(std::integral_constant<int, 3>{});
+}
+
+// Query tile k of a pair as a State, for store_warp_partial.
+__device__ __forceinline__ State pair_state(const PairState& p, int k, const QConst& qc) {
+  State st;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    st.m[j] = p.nm[k][j] == kNoMax ? -INFINITY : -p.nm[k][j] / qc.inv[j];
+    st.l[j] = p.l[k][j];
+    st.zd[j] = p.zd[k][j];
+    st.nm[j] = st.zd[2 + j] = 0.f;
   }
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st.acc[mt][i] = p.acc[k][mt][i];
+  return st;
 }
 
 // A query row's operands: its fp16 B fragments (bq_s), scaled by an exact

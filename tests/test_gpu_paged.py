@@ -886,3 +886,98 @@ def test_pages_hold_the_bytes_of_the_stream(hyq, bits):
     assert hyq_read_device_error(layer.err()) == 0 and hyq_read_device_error(cache.err()) == 0
     pages = cache.pool()[0, cache.table()[0].long()]          # [blocks, HKV, bytes]
     assert torch.equal(pages.transpose(0, 1), layer.qblocks()[0])
+
+
+# --- wide codes with 25 to 32 query rows a KV head (and multiples): four query tiles a pass ------------------------------
+
+WIDE = [(8, 1, (8, 8), 4), (5, 1, (4, 8), 5), (14, 2, (8, 4), 4), (16, 2, (8, 8), 8), (6, 3, (8, 4), 14)]
+
+
+@pytest.mark.parametrize("HQ,HKV,bits,n_q", WIDE)
+def test_wide_codes_and_many_query_rows_over_ragged_lengths(hyq, HQ, HKV, bits, n_q):
+    cache = make(HQ, HKV, 30, len(LENS), 6, bits=bits)
+    hist = History(len(LENS), HKV)
+    k, v, _, _ = grow(cache, list(range(len(LENS))), LENS, HQ + n_q)
+    hist.add(range(len(LENS)), LENS, k, v)
+    order = [7, 3, 9, 0, 1, 8, 2, 5, 6, 4, 9, 9]
+    q = queries(HQ, len(order), n_q, HQ)
+    outs = []
+    for _ in range(2):
+        out = torch.full_like(q, float("nan"))
+        cache.attention(0, q, out, seqs=ints(order))
+        outs.append(out)
+    assert hyq_read_device_error(cache.err()) == 0
+    print(f"error / bound: {check_attention(cache, hist, q, outs[0], order):.3f}")
+    assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("B,HQ,HKV,bits,n,n_q", [(1, 8, 1, (8, 8), 20011, 4), (2, 7, 1, (8, 4), 9000, 4), (1, 5, 1, (4, 8), 7777, 6)])
+def test_wide_codes_and_many_query_rows_joined(hyq, B, HQ, HKV, bits, n, n_q):
+    """Split over many blocks, whose partials (of 32, 28 and 30 rows) are joined; the same bits every time."""
+    nb = -(-n // 64)
+    cache = make(HQ, HKV, B * nb, B, nb, bits=bits)
+    k = torch.randn(n * B, HKV, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    v = torch.randn(n * B, HKV, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    grow(cache, list(range(B)), [n] * B, 0, rows=(k, v))
+    hist = History(B, HKV)
+    hist.add(range(B), [n] * B, k, v)
+    q = queries(3, B, n_q, HQ)
+    outs = []
+    for _ in range(3):
+        out = torch.full_like(q, float("nan"))
+        cache.attention(0, q, out)
+        outs.append(out)
+    print(f"error / bound: {check_attention(cache, hist, q, outs[0], range(B)):.3f}")
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_wide_codes_and_many_query_rows_of_extreme_values(hyq):
+    """Peaked logits late in the sequence (the maximum moves), equal ones, zero queries, large and tiny values."""
+    cache = make(8, 1, 25, 5, 5, bits=(8, 8))     # 290 rows: five pages each
+    n = 290
+    base = torch.randn(n, 1, 128, generator=torch.Generator().manual_seed(8))
+    ks = [base * 200, torch.ones(n, 1, 128), base, base * 1e-5, base]
+    ks[0][240] *= 3
+    vs = [base * 1000, base, base * 30000 / base.abs().max(), base * 1e-6, base]
+    hist = History(5, 1)
+    for s in range(5):
+        k, v = ks[s].to(torch.bfloat16), vs[s].to(torch.bfloat16)
+        grow(cache, [s], [n], 0, rows=(k, v))
+        hist.add([s], [n], k, v)
+    q = queries(9, 5, 4, 8)
+    q[4] = 0
+    out = torch.full_like(q, float("nan"))
+    cache.attention(0, q, out)
+    check_attention(cache, hist, q, out, range(5))
+
+
+def test_wide_codes_and_many_query_rows_that_are_not_finite(hyq):
+    """A NaN or infinite query gives NaN in its own output row; all others are as without it."""
+    cache = make(8, 1, 8, 2, 4, bits=(8, 8))
+    grow(cache, [0, 1], [200, 100], 3)
+    q = queries(4, 2, 4, 8)
+    outs = []
+    for bad in (False, True):
+        if bad:
+            q[0, 1, 3, 5], q[1, 3, 6, 100] = float("nan"), float("inf")
+        out = torch.zeros_like(q)
+        cache.attention(0, q, out)
+        outs.append(out)
+    same = torch.ones(2, 4, 8, dtype=torch.bool, device="cuda")
+    same[0, 1, 3] = same[1, 3, 6] = False
+    assert torch.equal(outs[0][same], outs[1][same])
+    assert outs[1][~same].isnan().any(1).all()
+
+
+def test_wide_codes_and_many_query_rows_skip_pages_outside_the_pool(hyq):
+    """A table entry outside the pool counts as nothing to see and is reported; the other sequences are as before."""
+    cache, hist = make(8, 1, 12, 2, 6, bits=(8, 8)), History(2, 1)
+    k, v, _, _ = grow(cache, [0, 1], [300, 300], 3)
+    hist.add([0, 1], [300, 300], k, v)
+    q = queries(4, 2, 4, 8)
+    cache.table()[0, 1], cache.table()[0, 3] = -5, 12
+    out = torch.full_like(q, float("nan"))
+    cache.attention(0, q, out)
+    assert hyq_read_device_error(cache.err()) == L.DEVERR_INDEX
+    sel = [[[np.array([0, 2, 4])]] * 4, [[np.arange(5)]] * 4]
+    check_attention(cache, hist, q, out, [0, 1], sel=sel)
