@@ -42,8 +42,8 @@ constexpr int kMaxNQ = 4;             // query tiles that one block takes togeth
 // two adjacent 16-row tiles.  kMaxNQ: one block an SM, and two warps to a ring,
 // each with half of the query tiles, whose accumulators leave 16 warps' worth of
 // registers (one warp with all four at 8 warps an SM waited more than the codes
-// unpacked twice cost: 79 against 73 us for 32 query rows a KV head, 8-bit codes,
-// 8 sequences of 4 to 16 thousand positions).
+// unpacked twice cost: 74 against 66 us for 32 query rows a KV head, 8-bit codes,
+// 8 sequences of up to 16 thousand positions).
 template <int BK, int BV, int NQ>
 struct Ring : QFmt<BK, BV> {
   static constexpr int kHalves = NQ == 1 ? 1 : 2;  // warps that work on one ring
@@ -140,10 +140,23 @@ __device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
       : "memory");
   return done;
 }
-__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity) {  // bounded, like mbar_wait
-  bool done = mbar_try_at(bar, parity);  // as a rule
+// A warp's wait, bounded like mbar_wait; false for every lane if one gave up.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_at(bar, parity))) return true;  // as a rule
+  bool done = false;
   for (int it = 0; !done && it < (1 << 22); ++it) done = mbar_try_at(bar, parity);
-  return done;
+  return __all_sync(0xffffffffu, done);
+}
+__device__ __forceinline__ void mbar_expect_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void sts32(uint32_t a, int v) {
+  asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(a), "r"(v) : "memory");
 }
 
 // Output row of (token, head) pair `flat` of a KV head whose first row is `out`.
@@ -249,8 +262,10 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
 
   const int tid = threadIdx.x;
   int lane = tid & 31, half = kHalves > 1 ? tid / kThreads : 0, warp = (tid >> 5) - kWarps * half;
-  // (not to be derived anew from the thread's number in each pass of the loop)
-  if (kHalves > 1) asm volatile("" : "+r"(lane), "+r"(half), "+r"(warp));
+  // What a shuffle returns is kept: it cannot be formed anew, from the thread's
+  // number or a variable's address, in each pass of the loop.
+  auto kept = [&](uint32_t x) { return kHalves > 1 ? __shfl_sync(0xffffffffu, x, tid & 31) : x; };
+  lane = (int)kept(lane), warp = (int)kept(warp), half = (int)kept(half);
   const int g = lane >> 2, t = lane & 3;
   // The warps w and w + 8 of two halves work on the same ring, w filling it.
   const int kq = kNW * half;
@@ -410,6 +425,13 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     // units, and of the next one; the pages arrive while the round is worked off.
     int e_cur = half == 0 ? entry(lane) : -1, pg_cur = page_of(e_cur);
     int e_nxt = half == 0 ? entry(32 + lane) : -1, pg_nxt = page_of(e_nxt);
+    auto next_pages = [&](int j) {  // after unit j
+      if ((j & 31) != 31) return;
+      e_cur = e_nxt;
+      pg_cur = pg_nxt;
+      e_nxt = entry(j + 33 + lane);
+      pg_nxt = page_of(e_nxt);
+    };
     // Position of unit j's first row (of a unit that is there), else -1; issues its copy.
     auto issue = [&](int j) -> int {
       const int e = __shfl_sync(0xffffffffu, e_cur, j & 31), pg = __shfl_sync(0xffffffffu, pg_cur, j & 31);
@@ -417,8 +439,6 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       const bool in = (uint32_t)pg < (uint32_t)p.pv.n_pages, ok = e >= 0 && at < len && in;
       const uint32_t n = done + (uint32_t)j;
       const int slot = n % kSlots;
-      if (kHalves > 1 && lane == 0) s_ctl[warp].at[slot] = ok ? at : -1;
-      if (kHalves > 1) __syncwarp();
       if (lane == slot) {  // copies that one thread issues complete one after another
         uint64_t* bar = &wb[slot];
         if (ok) {
@@ -430,17 +450,32 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
           if (e >= 0 && !in) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
         }
       }
-      if ((j & 31) == 31) {
-        e_cur = e_nxt;
-        pg_cur = pg_nxt;
-        e_nxt = entry(j + 33 + lane);
-        pg_nxt = page_of(e_nxt);
-      }
+      next_pages(j);
       return ok ? at : -1;
     };
-    int at_slot[kSlots];  // one half: the slots' positions from the next unit's on
+    // Two halves (no lists): unit j into the slot, by the lane that holds its page.
+    const uint32_t ctl = kept(smem_u32(&s_ctl[warp])), tiles = kept(smem_u32(ring)), query = kept(smem_u32(query_s[kq]));
+    constexpr uint32_t kFree = offsetof(Ctl<kSlots>, free), kAt = offsetof(Ctl<kSlots>, at);
+    auto issue_at = [&](int j, uint32_t slot) {
+      if (lane == (j & 31)) {
+        const bool in = (uint32_t)pg_cur < (uint32_t)p.pv.n_pages;
+        sts32(ctl + kAt + 4 * slot, in ? R::kRows * (w0 + warp + kWarps * j) : -1);
+        mbar_expect_at(ctl + 8 * slot, in ? R::kUnit : 0);
+        if (in)
+          bulk_g2s_at(tiles + slot * R::kUnit, heads + (size_t)pg_cur * ((size_t)p.HKV * R::kBlock), R::kUnit, ctl + 8 * slot);
+        else
+          hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+      }
+      next_pages(j);
+    };
+    int at_slot[kHalves == 1 ? kSlots : 1];  // one half: the slots' positions from the next unit's on
+    if constexpr (kHalves == 1) {
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) at_slot[j] = half == 0 && j < nj && !dead ? issue(j) : -1;
+      for (int j = 0; j < kSlots; ++j) at_slot[j] = j < nj && !dead ? issue(j) : -1;
+    } else {
+      if (half == 0 && !dead)
+        for (int j = 0; j < min(kSlots, nj); ++j) issue_at(j, (done + j) % kSlots);
+    }
 
     // ---- the query rows: warp r prepares row r of each of its half's tiles --
 #pragma unroll
@@ -506,11 +541,8 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       }
     } else {
       uint32_t slot = done % kSlots, par = (done / kSlots) & 1u;
-      uint32_t ctl = smem_u32(&s_ctl[warp]), tiles = smem_u32(ring), query = smem_u32(query_s[kq]);
-      asm volatile("" : "+r"(ctl), "+r"(tiles), "+r"(query));  // kept, not formed anew in each pass
-      constexpr uint32_t kFree = offsetof(Ctl<kSlots>, free), kAt = offsetof(Ctl<kSlots>, at);
       for (int j = 0; j < nj && !dead; ++j) {
-        if (__any_sync(0xffffffffu, !mbar_wait_at(ctl + 8 * slot, par))) {
+        if (!mbar_wait_warp(ctl + 8 * slot, par)) {
           give_up(j, j + kSlots - (j > 0 ? 1 : 0));
           break;
         }
@@ -528,12 +560,12 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
         } else if (j > 0 && j - 1 + kSlots < nj) {
           // the slot of the unit before, which the other half has mostly left too
           const uint32_t s0 = slot ? slot - 1 : kSlots - 1, p0 = slot ? par : par ^ 1u;
-          if (__any_sync(0xffffffffu, !mbar_wait_at(ctl + kFree + 8 * s0, p0))) {
+          if (!mbar_wait_warp(ctl + kFree + 8 * s0, p0)) {
             give_up(j + 1, j - 1 + kSlots);
             break;
           }
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-          (void)issue(j - 1 + kSlots);
+          issue_at(j - 1 + kSlots, s0);
         }
         if (++slot == kSlots) slot = 0, par ^= 1u;
       }
@@ -628,17 +660,22 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   }
 }
 
-// Query tiles that a group takes together.  A pass of its own for each tile (the
+// Query tiles that a group takes together: one, or full fours.  One by one, the
 // groups of one KV head lie side by side and meet most of each other's reads in
-// L2) is as fast as four tiles a pass, whose one block an SM has eight warps to
-// hide latency with: 4-bit codes, 8 sequences of up to 16 thousand positions,
-// 8 KV heads, 4 / 8 / 16 tiles: 72 / 129 / 243 us one by one, 71 / 126 / 232 by
-// fours; one sequence of 32768: 36 / 57 / 102 against 38 / 61 / 101.  For wider
-// codes, whose cache passes L2 sooner, full fours pay: 8-bit 89 / 164 / 313 us one
-// by one, 69 / 120 / 221 by fours (6 tiles, two passes of four: 113 against 111).
+// L2, and the group's start is shorter; four at a time the codes are unpacked half
+// as often.  64 / 8 heads, 4 / 8 / 12 tiles, one by one and by fours, us:
+//   8-bit codes, 8 sequences of up to 16001   88 / 166 / 211    66 / 112 / 159
+//                32 of up to 2000             57 / 103 / 148    53 /  90 / 125
+//                one of 32768                 38 /  61 /  90    37 /  56 /  75
+//   4-bit codes, 8 of up to 16001             72 / 129 / 185    69 / 118 / 167
+//                32 of up to 2000             55 /  98 / 141    56 /  94 / 129
+//                one of 32768                 36 /  57 /  83    38 /  58 /  78
+// so 4-bit codes take fours from eight tiles on.  (Six 8-bit tiles as two passes of
+// four: 111 against 113.  Two at a time, one warp to a ring: between the two.)
 int group_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
   const int gq = c->num_q_heads / c->num_kv_heads, tiles = (n_q * gq + kRowsQ - 1) / kRowsQ;
-  return !blocks && hyq_bits_k(c) + hyq_bits_v(c) > 8 && tiles % kMaxNQ == 0 ? kMaxNQ : 1;
+  const bool wide = hyq_bits_k(c) + hyq_bits_v(c) > 8;
+  return !blocks && tiles % kMaxNQ == 0 && (wide || tiles > kMaxNQ) ? kMaxNQ : 1;
 }
 
 template <int BK, int BV, int NQ>
@@ -655,9 +692,7 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
 
 template <int BK, int BV>
 cudaError_t launch_nq(const Params& p, int nq, cudaStream_t s) {
-  if constexpr (BK + BV > 8)
-    if (nq == kMaxNQ) return launch<BK, BV, kMaxNQ>(p, s);
-  return launch<BK, BV, 1>(p, s);
+  return nq == kMaxNQ ? launch<BK, BV, kMaxNQ>(p, s) : launch<BK, BV, 1>(p, s);
 }
 
 // Partials of the largest grid: two slots of kMaxNQ query tiles on each SM

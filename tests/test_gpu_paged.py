@@ -888,13 +888,15 @@ def test_pages_hold_the_bytes_of_the_stream(hyq, bits):
     assert torch.equal(pages.transpose(0, 1), layer.qblocks()[0])
 
 
-# --- wide codes with 25 to 32 query rows a KV head (and multiples): four query tiles a pass ------------------------------
+# --- many query rows a KV head: from 25 to 32 on (wide codes; 4-bit: 57 to 64) fours of query tiles are taken together ----
 
-WIDE = [(8, 1, (8, 8), 4), (5, 1, (4, 8), 5), (14, 2, (8, 4), 4), (16, 2, (8, 8), 8), (6, 3, (8, 4), 14)]
+WIDE = [(8, 1, (8, 8), 4), (5, 1, (4, 8), 5), (14, 2, (8, 4), 4), (16, 2, (8, 8), 8), (6, 3, (8, 4), 14), (8, 1, (4, 4), 4),
+        (5, 1, (4, 4), 5), (8, 2, (4, 4), 4), (4, 1, (8, 8), 3), (8, 2, (4, 8), 4), (10, 2, (8, 4), 9), (8, 1, (4, 4), 6),
+        (8, 1, (4, 4), 8), (7, 1, (4, 4), 9)]
 
 
 @pytest.mark.parametrize("HQ,HKV,bits,n_q", WIDE)
-def test_wide_codes_and_many_query_rows_over_ragged_lengths(hyq, HQ, HKV, bits, n_q):
+def test_many_query_rows_over_ragged_lengths(hyq, HQ, HKV, bits, n_q):
     cache = make(HQ, HKV, 30, len(LENS), 6, bits=bits)
     hist = History(len(LENS), HKV)
     k, v, _, _ = grow(cache, list(range(len(LENS))), LENS, HQ + n_q)
@@ -911,9 +913,12 @@ def test_wide_codes_and_many_query_rows_over_ragged_lengths(hyq, HQ, HKV, bits, 
     assert torch.equal(outs[0], outs[1])
 
 
-@pytest.mark.parametrize("B,HQ,HKV,bits,n,n_q", [(1, 8, 1, (8, 8), 20011, 4), (2, 7, 1, (8, 4), 9000, 4), (1, 5, 1, (4, 8), 7777, 6)])
-def test_wide_codes_and_many_query_rows_joined(hyq, B, HQ, HKV, bits, n, n_q):
-    """Split over many blocks, whose partials (of 32, 28 and 30 rows) are joined; the same bits every time."""
+@pytest.mark.parametrize("B,HQ,HKV,bits,n,n_q", [(1, 8, 1, (8, 8), 20011, 4), (2, 7, 1, (8, 4), 9000, 4), (1, 5, 1, (4, 8), 7777, 6),
+                                                    (1, 8, 1, (4, 4), 12345, 4), (1, 4, 1, (4, 4), 20011, 4),
+                                                    (1, 3, 1, (8, 8), 15000, 5), (2, 6, 1, (4, 8), 5000, 7),
+                                                    (1, 8, 1, (4, 4), 9000, 8)])
+def test_many_query_rows_joined(hyq, B, HQ, HKV, bits, n, n_q):
+    """Split over many blocks, whose partials (15 to 64 rows) are joined; the same bits every time."""
     nb = -(-n // 64)
     cache = make(HQ, HKV, B * nb, B, nb, bits=bits)
     k = torch.randn(n * B, HKV, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
@@ -931,9 +936,10 @@ def test_wide_codes_and_many_query_rows_joined(hyq, B, HQ, HKV, bits, n, n_q):
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
-def test_wide_codes_and_many_query_rows_of_extreme_values(hyq):
+@pytest.mark.parametrize("bits,HQ,n_q", [((8, 8), 8, 4), ((4, 4), 8, 8), ((8, 8), 4, 4), ((4, 4), 4, 4)])
+def test_many_query_rows_of_extreme_values(hyq, bits, HQ, n_q):
     """Peaked logits late in the sequence (the maximum moves), equal ones, zero queries, large and tiny values."""
-    cache = make(8, 1, 25, 5, 5, bits=(8, 8))     # 290 rows: five pages each
+    cache = make(HQ, 1, 25, 5, 5, bits=bits)     # 290 rows: five pages each
     n = 290
     base = torch.randn(n, 1, 128, generator=torch.Generator().manual_seed(8))
     ks = [base * 200, torch.ones(n, 1, 128), base, base * 1e-5, base]
@@ -944,40 +950,42 @@ def test_wide_codes_and_many_query_rows_of_extreme_values(hyq):
         k, v = ks[s].to(torch.bfloat16), vs[s].to(torch.bfloat16)
         grow(cache, [s], [n], 0, rows=(k, v))
         hist.add([s], [n], k, v)
-    q = queries(9, 5, 4, 8)
+    q = queries(9, 5, n_q, HQ)
     q[4] = 0
     out = torch.full_like(q, float("nan"))
     cache.attention(0, q, out)
     check_attention(cache, hist, q, out, range(5))
 
 
-def test_wide_codes_and_many_query_rows_that_are_not_finite(hyq):
+@pytest.mark.parametrize("bits,HQ,n_q", [((8, 8), 8, 4), ((4, 4), 8, 8), ((8, 8), 4, 4), ((4, 4), 4, 4)])
+def test_many_query_rows_that_are_not_finite(hyq, bits, HQ, n_q):
     """A NaN or infinite query gives NaN in its own output row; all others are as without it."""
-    cache = make(8, 1, 8, 2, 4, bits=(8, 8))
+    cache = make(HQ, 1, 8, 2, 4, bits=bits)
     grow(cache, [0, 1], [200, 100], 3)
-    q = queries(4, 2, 4, 8)
+    q = queries(4, 2, n_q, HQ)
     outs = []
     for bad in (False, True):
         if bad:
-            q[0, 1, 3, 5], q[1, 3, 6, 100] = float("nan"), float("inf")
+            q[0, 1, 3, 5], q[1, 3, 2, 100] = float("nan"), float("inf")
         out = torch.zeros_like(q)
         cache.attention(0, q, out)
         outs.append(out)
-    same = torch.ones(2, 4, 8, dtype=torch.bool, device="cuda")
-    same[0, 1, 3] = same[1, 3, 6] = False
+    same = torch.ones(2, n_q, HQ, dtype=torch.bool, device="cuda")
+    same[0, 1, 3] = same[1, 3, 2] = False
     assert torch.equal(outs[0][same], outs[1][same])
     assert outs[1][~same].isnan().any(1).all()
 
 
-def test_wide_codes_and_many_query_rows_skip_pages_outside_the_pool(hyq):
+@pytest.mark.parametrize("bits,HQ,n_q", [((8, 8), 8, 4), ((4, 4), 8, 8), ((8, 8), 4, 4), ((4, 4), 4, 4)])
+def test_many_query_rows_skip_pages_outside_the_pool(hyq, bits, HQ, n_q):
     """A table entry outside the pool counts as nothing to see and is reported; the other sequences are as before."""
-    cache, hist = make(8, 1, 12, 2, 6, bits=(8, 8)), History(2, 1)
+    cache, hist = make(HQ, 1, 12, 2, 6, bits=bits), History(2, 1)
     k, v, _, _ = grow(cache, [0, 1], [300, 300], 3)
     hist.add([0, 1], [300, 300], k, v)
-    q = queries(4, 2, 4, 8)
+    q = queries(4, 2, n_q, HQ)
     cache.table()[0, 1], cache.table()[0, 3] = -5, 12
     out = torch.full_like(q, float("nan"))
     cache.attention(0, q, out)
     assert hyq_read_device_error(cache.err()) == L.DEVERR_INDEX
-    sel = [[[np.array([0, 2, 4])]] * 4, [[np.arange(5)]] * 4]
+    sel = [[[np.array([0, 2, 4])]] * n_q, [[np.arange(5)]] * n_q]
     check_attention(cache, hist, q, out, [0, 1], sel=sel)
