@@ -119,10 +119,14 @@ struct Segment {
   int64_t base;             // of the group's first unit in the line
 };
 
-// What the two warps of a ring share beside its bytes.
-template <int kSlots>
+// A ring's state beside its bytes: of one warp, or of two.
+template <int kHalves, int kSlots>
 struct Ctl {
   uint64_t full[kSlots];  // the slot's copy is there
+};
+template <int kSlots>
+struct Ctl<2, kSlots> {
+  uint64_t full[kSlots];
   uint64_t free[kSlots];  // the second half's warp is done with it
   int at[kSlots];         // position of the slot's first row, or -1 (nothing was copied)
 };
@@ -252,7 +256,8 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   __shared__ __align__(16) float rowc_s[NQ][kRowsQ][4];
   __shared__ uint32_t bz_s[NQ][kRowsQ][4];
   __shared__ int lim_s[NQ][kRowsQ];
-  __shared__ Ctl<kSlots> s_ctl[kWarps];
+  using RingCtl = Ctl<kHalves, kSlots>;
+  __shared__ __align__(8) RingCtl s_ctl[kWarps];
   __shared__ float red_m[kWarps][NQ][kRowsQ], red_l[kWarps][NQ][kRowsQ];
   __shared__ float s_wt[kRowsG][kWarps];                // weights of the warps' partials
   __shared__ float s_sum[kRowsG];
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   uint64_t* wb = s_ctl[warp].full;
   if (half == 0 && lane < kSlots) {
     mbar_init(&wb[lane], 1);
-    if (kHalves > 1) mbar_init(&s_ctl[warp].free[lane], 1);
+    if constexpr (kHalves > 1) mbar_init(&s_ctl[warp].free[lane], 1);
   }
   mbar_fence_init();
   chain_kernel();
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     };
     // Two halves (no lists): unit j into the slot, by the lane that holds its page.
     const uint32_t ctl = kept(smem_u32(&s_ctl[warp])), tiles = kept(smem_u32(ring)), query = kept(smem_u32(query_s[kq]));
-    constexpr uint32_t kFree = offsetof(Ctl<kSlots>, free), kAt = offsetof(Ctl<kSlots>, at);
+    constexpr uint32_t kFree = 8 * kSlots, kAt = 16 * kSlots;  // Ctl<2, kSlots>
     auto issue_at = [&](int j, uint32_t slot) {
       if (lane == (j & 31)) {
         const bool in = (uint32_t)pg_cur < (uint32_t)p.pv.n_pages;
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     }
     __syncthreads();
     // four elements of a row a thread (the warps' partials hold element d at d ^ (row / 2))
-    for (int i = tid; i < n_rows * (HYQ_D / 4); i += R::kBlockThreads) {
+    for (int i = tid; i < min(kRowsG, n_rows) * (HYQ_D / 4); i += R::kBlockThreads) {  // (the bound: a known count)
       const int r = i >> 5, d = 4 * (i & 31), x = (r & 7) >> 1;
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
