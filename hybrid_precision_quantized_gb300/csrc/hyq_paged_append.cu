@@ -10,14 +10,18 @@
 // page's 16-row tiles.  A lane holds eight elements (one 16-byte load) of the
 // rows 2t, 2t + 1, 2t + 8, 2t + 9 for two t: those whose codes share words in
 // either fragment order, so that a tile's words are assembled in registers,
-// without shared memory or barriers; a key warp carries the page's bounds.
+// without barriers; the next tile's rows come into shared memory meanwhile, each
+// lane's own part; a key warp carries the page's bounds.
 // Steps and reciprocals are costly: the rows are reduced together, halves
 // exchanged, so that each of a group's four lanes ends with two rows' (min, max)
 // and derives their steps, once per (row, group) instead of once per lane.
 //
-// What bounds it: instruction issue (84 per row and tensor, half of the slots
-// used at 16 warps an SM) and the loads' latency; prompts of 30 thousand rows of
-// 8 KV heads with the rows read back take 76 us, 0.63 of the copy rate.
+// What bounds it: instruction issue (85 per row and tensor, six in ten of the slots
+// used at 16 warps an SM) and the last round of blocks; prompts of 30 thousand
+// rows of 8 KV heads with the rows read back take 67 us, 0.70 of the copy rate.
+// Slower: 24 warps an SM with the rows read twice from shared memory (74 us),
+// blocks of four warps (80), resident blocks whose warps go from page to page (75,
+// and 70 with the values' tiles levelling the warps' shares).
 #include "hyq_paged.cuh"
 #include "hyq_qcode.cuh"
 
@@ -169,26 +173,25 @@ __device__ __noinline__ float2 exact_pair(uint32_t w, float s, float z, float r)
                      exact_code4<BITS>(x.y, z, s, __fmul_rn(__fsub_rn(x.y, z), ra)));
 }
 
-// Codes of a lane's eight elements: c as float pairs and, for packing, as the
+// Codes of a lane's eight elements: -c as float pairs and, for packing, as the
 // low bytes of b (the bits of 1.5 * 2^23 + c).  v becomes zeros in a marked group.
 struct Codes8 {
-  uint64_t c[4];
+  uint64_t nc[4];
   uint32_t b[8];
 };
 template <int BITS>
 __device__ __forceinline__ Codes8 codes8(uint4& v, float s, float z, float r) {
   Codes8 o;
-  const uint64_t nz2 = f2_splat(-z), r2 = f2_splat(r), m2 = f2_splat(kMagic), nm2 = f2_splat(-kMagic);
-  const uint64_t no2 = f2_splat(-1.f);
+  const uint64_t nz2 = f2_splat(-z), r2 = f2_splat(r), m2 = f2_splat(kMagic), no2 = f2_splat(-1.f);
   float far = 0.f;
-  // distance of an element pair's arguments from their codes, exact
+  // distance of an element pair's arguments from their codes
   auto code_pair = [&](int k) {
     const uint32_t w = (&v.x)[k];
     const uint64_t x = (uint64_t)(w << 16) | ((uint64_t)(w & 0xFFFF0000u) << 32);
-    const uint64_t t = f2_mul(f2_add(x, nz2), r2), b = f2_add(t, m2);
-    o.c[k] = f2_add(b, nm2);
+    const uint64_t y = f2_add(x, nz2), b = f2_fma(y, r2, m2);
+    o.nc[k] = f2_fma(b, no2, m2);
     o.b[2 * k] = lo32(b), o.b[2 * k + 1] = hi32(b);
-    const uint64_t d = f2_fma(o.c[k], no2, t);
+    const uint64_t d = f2_fma(y, r2, o.nc[k]);
     return fmaxf(fabsf(f2_lo(d)), fabsf(f2_hi(d)));
   };
 #pragma unroll
@@ -198,7 +201,7 @@ __device__ __forceinline__ Codes8 codes8(uint4& v, float s, float z, float r) {
     for (int k = 0; k < 4; ++k) {
       if (code_pair(k) > Near<BITS>::kTie || r < 0.f) {
         const float2 c = exact_pair<BITS>((&v.x)[k], s, z, r);
-        o.c[k] = f2_pack(c.x, c.y);
+        o.nc[k] = f2_pack(-c.x, -c.y);
         o.b[2 * k] = __float_as_uint(__fadd_rn(c.x, kMagic));
         o.b[2 * k + 1] = __float_as_uint(__fadd_rn(c.y, kMagic));
       }
@@ -230,11 +233,11 @@ __device__ __forceinline__ void store_meta(uint8_t* meta, int r, int q, uint32_t
 }
 
 __device__ __forceinline__ void store_hat(__nv_bfloat16* hat, const Codes8& c, float s, float z) {
-  const uint64_t s2 = f2_splat(s), z2 = f2_splat(z);
+  const uint64_t ns2 = f2_splat(-s), z2 = f2_splat(z);
   uint4 o;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint64_t x = f2_fma(c.c[k], s2, z2);
+    const uint64_t x = f2_fma(c.nc[k], ns2, z2);
     (&o.x)[k] = pack_bf16x2(f2_lo(x), f2_hi(x));
   }
   *reinterpret_cast<uint4*>(hat) = o;
@@ -265,24 +268,40 @@ __device__ __forceinline__ void merge_store(uint2* dst, uint2 x, uint32_t mask) 
   *dst = x;
 }
 
-// Rows `nm` (bits 0..15) of one tile, tensor T (0 = K, 1 = V): row i comes
-// from src + i ld.  bnd: bounds of the rows taken (K).  Returns whether a group
-// could not be held.
+// Row of step j of a lane, less 2 (lane / 16): rows 2t, 2t + 1, 2t + 8, 2t + 9 for
+// t = lane / 16 and lane / 16 + 2.
+__device__ __forceinline__ constexpr int step_row(int j) { return 4 * (j >> 2) + 8 * ((j >> 1) & 1) + (j & 1); }
+
+// A lane's elements of the rows `nm` (bits 0..15) of a tile on their way to shared
+// memory: step j to stage + 512 j, row i from src + i ld.  Each lane reads what
+// it fetched itself, so no barrier is needed.
+__device__ __forceinline__ void fetch_rows(uint32_t stage, const __nv_bfloat16* src, int64_t ld, uint32_t nm, int lane) {
+  const int row0 = 2 * (lane >> 4);
+  src += row0 * ld + 8 * (lane & 15);
+  nm >>= row0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if ((nm >> step_row(j)) & 1)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(stage + 512 * j), "l"(src + step_row(j) * ld)
+                   : "memory");
+}
+
+// Rows `nm` (bits 0..15) of one tile, tensor T (0 = K, 1 = V), that fetch_rows
+// brought.  bnd: bounds of the rows taken (K).  Returns whether a group could not
+// be held.
 template <int T, int BITS, int kCode, int kMeta>
-__device__ __forceinline__ bool tile_rows(uint8_t* tile, const __nv_bfloat16* src, int64_t ld, __nv_bfloat16* hat,
-                                          int64_t ldh, uint32_t nm, int lane, Bounds8& bnd) {
+__device__ __forceinline__ bool tile_rows(uint8_t* tile, const uint8_t* stage, __nv_bfloat16* hat, int64_t ldh,
+                                          uint32_t nm, int lane, Bounds8& bnd) {
   const int hw = lane >> 4, c = lane & 15, q = c >> 2, t4 = c & 3;
   // row of step j = 4 tt + 2 b + odd: 2 (2 tt + hw) + 8 b + odd
   const int row0 = 2 * hw;
-  src += row0 * ld + 8 * c;
   if (hat) hat += row0 * ldh + 8 * c;
   const uint32_t mine = nm >> row0;  // bit 4 tt + 8 b + odd: the lane's rows
   uint4 v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const int row = 4 * (j >> 2) + 8 * ((j >> 1) & 1) + (j & 1);
     v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if ((mine >> row) & 1) v[j] = *reinterpret_cast<const uint4*>(src + row * ld);
+    if ((mine >> step_row(j)) & 1) v[j] = *reinterpret_cast<const uint4*>(stage + 512 * j);
   }
   // ---- steps and zeros: lane t4 of a group ends with steps 2 t4 and 2 t4 + 1 --
   uint32_t m[8];
@@ -440,6 +459,7 @@ __device__ __forceinline__ void store_bounds(uint8_t* rec, int lane, const Bound
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kStageBytes = kWarps * 2 * 4096;
 
 // grid (pages that the call may reach / (8 / hb), KV heads / hb, {K, V}), with
 // hb = 1, 2, 4 or 8 heads a block: a block takes 8 / hb pages that get rows, in
@@ -448,6 +468,7 @@ constexpr int kWarps = kThreads / 32;
 template <int BK, int BV>
 __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendParams p, int hb) {
   using F = QFmt<BK, BV>;
+  extern __shared__ __align__(16) uint8_t s_stage[];  // [kWarps][2][4096]
   __shared__ int s_warp[kThreads / 32];
   __shared__ PageRows s_rows[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -495,18 +516,31 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
   Bounds8 b;
   b.clear();
   bool bad = false;
+  // Two tiles' worth of shared memory a warp: the next tile's rows are on their
+  // way while one is worked on (76 us without, 67 with).
+  uint8_t* stage = s_stage + 8192 * warp + 16 * lane;
+  auto rows_of = [&](int tile) -> uint32_t {  // rows of the tile: bits of [r0, r1) in [16 tile, 16 tile + 16)
+    const int a = max(r.r0 - 16 * tile, 0), z = min(r.r1 - 16 * tile, 16);
+    return ((1u << z) - 1u) & ~((1u << a) - 1u);
+  };
+  const int64_t tok = (int64_t)r.tok0 - r.r0;  // call row of the page's row 0 (may lie before the call's first)
+  auto fetch = [&](int tile) {
+    if (16 * tile < r.r1)
+      fetch_rows(smem_u32(stage) + 4096 * (tile & 1), src + (tok + 16 * tile) * p.ld, p.ld, rows_of(tile), lane);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  fetch(r.r0 >> 4);
 #pragma unroll 1
   for (int tile = r.r0 >> 4; 16 * tile < r.r1; ++tile) {
-    // rows of this tile: bits of [r0, r1) in [16 tile, 16 tile + 16)
-    const int a = max(r.r0 - 16 * tile, 0), z = min(r.r1 - 16 * tile, 16);
-    const uint32_t nm = ((1u << z) - 1u) & ~((1u << a) - 1u);
-    const int64_t row0 = (int64_t)r.tok0 + 16 * tile - r.r0;  // call row of the tile's row 0 (may lie before tok0)
+    fetch(tile + 1);
+    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
     uint8_t* tp = block + tile * F::kTile;
+    const uint8_t* from = stage + 4096 * (tile & 1);
+    __nv_bfloat16* to = hat ? hat + (tok + 16 * tile) * ldh : nullptr;
     if (T == 0)
-      bad |= tile_rows<0, BK, 0, F::kKMeta>(tp, src + row0 * p.ld, p.ld, hat ? hat + row0 * ldh : nullptr, ldh, nm, lane, b);
+      bad |= tile_rows<0, BK, 0, F::kKMeta>(tp, from, to, ldh, rows_of(tile), lane, b);
     else
-      bad |= tile_rows<1, BV, F::kVCode, F::kVMeta>(tp, src + row0 * p.ld, p.ld, hat ? hat + row0 * ldh : nullptr, ldh,
-                                                    nm, lane, b);
+      bad |= tile_rows<1, BV, F::kVCode, F::kVMeta>(tp, from, to, ldh, rows_of(tile), lane, b);
   }
   if (bad) hyq_set_err(p.pv.err, HYQ_DEVERR_QUANT_RANGE);
   if (T == 0) {
@@ -595,8 +629,13 @@ cudaError_t launch(const AppendParams& p, cudaStream_t s) {
   // a sequence with n rows reaches at most n / 64 + 2 pages
   const int pages = p.n_rows / HYQ_PAGE_ROWS + 2 * min(p.batch, p.n_rows);
   const int hb = p.HKV >= 8 ? 8 : p.HKV > 2 ? 4 : p.HKV, per = kWarps / hb;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = hyq_once_per_device(done, [] {
+    return cudaFuncSetAttribute(append_pages_kernel<BK, BV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
+  });
+  if (e != cudaSuccess) return e;
   return hyq_launch_chained(append_pages_kernel<BK, BV>, dim3((pages + per - 1) / per, (p.HKV + hb - 1) / hb, 2), kThreads,
-                            0, s, p, hb);
+                            kStageBytes, s, p, hb);
 }
 
 }  // namespace
