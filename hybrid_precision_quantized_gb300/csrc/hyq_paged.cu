@@ -290,39 +290,40 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     if (p.sel) n = R::kPerPage * min(p.k_sel, (len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS);
     return n == 0 ? 0 : n + R::kCost;
   };
-  // ---- the rows' units, summed up: a block of 4 rows per thread --------------
+  // ---- the rows' units, summed up: a row a thread (the loads of several rows in
+  // one thread would follow one another) --------------------------------------
   const int unit = p.HKV * p.QT;
   {
-    int64_t w[4], sum = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int b = 4 * tid + i;
-      int seq = -1;
-      const int len = b < p.batch ? row_len(p, b, &seq) : 0;
+    int64_t before = 0;
+    for (int row0 = 0; row0 < p.batch; row0 += R::kBlockThreads) {
+      const int b = row0 + tid;
+      int64_t w = 0;
       if (b < p.batch) {
+        int seq;
+        const int len = row_len(p, b, &seq);
         s_len[b] = len;
         s_seq[b] = seq;
         if (seq < 0 && blockIdx.x == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+        w = units_of(len);
       }
-      w[i] = units_of(len);
-      sum += w[i];
-    }
-    int64_t pre = sum;
+      int64_t pre = w;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += y;
+      }
+      if (row0 > 0) __syncthreads();  // the sums of the rows before have been read
+      if (lane == 31) s_warp[tid >> 5] = pre;
+      __syncthreads();
+      int64_t at = before + pre - w;
+      for (int i = 0; i < kWarps * kHalves; ++i) {
+        const int64_t x = s_warp[i];
+        if (i < tid >> 5) at += x;
+        before += x;
+      }
+      if (b < p.batch) s_cum[b] = at;
     }
-    if (lane == 31) s_warp[tid >> 5] = pre;
-    __syncthreads();
-    int64_t at = pre - sum;
-    for (int i = 0; i < tid >> 5; ++i) at += s_warp[i];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * tid + i <= p.batch) s_cum[4 * tid + i] = at;
-      at += w[i];
-    }
-    if (tid == R::kBlockThreads - 1 && p.batch == HYQ_PAGED_MAX_BATCH) s_cum[HYQ_PAGED_MAX_BATCH] = at;
+    if (tid == 0) s_cum[p.batch] = before;
   }
   __syncthreads();
   // rows without positions: their outputs are zero
@@ -390,7 +391,6 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     __syncthreads();
     const int w0 = seg.w0, w1 = seg.w1;
     if (w0 < 0) break;
-    const int len = seg.len;
     // Row r of the group is (token, head) pair flat0 + r of the KV head's.
     auto token_of = [&](int r) { return (seg.flat0 + r) / p.gq; };
     // the query rows, row `warp` of each query tile: loaded ahead of the page
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       if (NQ > 1 || !seg.sel) return x;  // several query tiles: never with lists
       const int e = seg.sel[x], pe = x > 0 ? seg.sel[x - 1] : -1;
       if (e < 0) return -1;
-      if ((x > 0 && pe < 0) || pe >= e || (int64_t)e * HYQ_PAGE_ROWS >= len) {
+      if ((x > 0 && pe < 0) || pe >= e || (int64_t)e * HYQ_PAGE_ROWS >= seg.len) {
         hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
         return -1;
       }
@@ -441,13 +441,13 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     auto issue = [&](int j) -> int {
       const int e = __shfl_sync(0xffffffffu, e_cur, j & 31), pg = __shfl_sync(0xffffffffu, pg_cur, j & 31);
       const int at = e * HYQ_PAGE_ROWS + part * R::kRows;
-      const bool in = (uint32_t)pg < (uint32_t)p.pv.n_pages, ok = e >= 0 && at < len && in;
+      const bool in = (uint32_t)pg < (uint32_t)p.pv.n_pages, ok = e >= 0 && at < seg.len && in;
       const uint32_t n = done + (uint32_t)j;
       const int slot = n % kSlots;
       if (lane == slot) {  // copies that one thread issues complete one after another
         uint64_t* bar = &wb[slot];
         if (ok) {
-          const uint32_t bytes = R::kTiles == 1 || at + 16 < len ? R::kUnit : R::kTile;
+          const uint32_t bytes = R::kTiles == 1 || at + 16 < seg.len ? R::kUnit : R::kTile;
           mbar_arrive_expect_tx(bar, bytes);
           bulk_g2s(ring + slot * R::kUnit, heads + (size_t)pg * ((size_t)p.HKV * R::kBlock), bytes, bar);
         } else {
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     for (int k = 0; k < kNW; ++k) {
       const int r = kRowsQ * (kq + k) + warp;
       prep_query_row<BK>(warp, lane, qv[k], bq_s(kq + k), rowc_s[kq + k], bz_s[kq + k]);
-      if (lane == 0) lim_s[kq + k][warp] = r < seg.n_rows ? max(0, len - p.n_q + 1 + token_of(r)) : len;
+      if (lane == 0) lim_s[kq + k][warp] = r < seg.n_rows ? max(0, seg.len - p.n_q + 1 + token_of(r)) : seg.len;
     }
     __syncthreads();
     uint32_t bq[8][2];
@@ -530,9 +530,9 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
             q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st);
           } else {
             const int lim0 = lim_s[0][2 * t], lim1 = lim_s[0][2 * t + 1];
-            for (int x = 0; x < R::kTiles && at + 16 * x < len; ++x) {
+            for (int x = 0; x < R::kTiles && at + 16 * x < seg.len; ++x) {
               const int a = at + 16 * x;
-              q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, len - a, bq, qc, st, lim0 - a, lim1 - a);
+              q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, seg.len - a, bq, qc, st, lim0 - a, lim1 - a);
             }
           }
         }
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
           if (at + R::kRows <= minlim)
             q_tile_pair<BK, BV, false>(tb, lane, query, 16, lim_s + kq, at, st);
           else
-            q_tile_pair<BK, BV, true>(tb, lane, query, len - at, lim_s + kq, at, st);
+            q_tile_pair<BK, BV, true>(tb, lane, query, seg.len - at, lim_s + kq, at, st);
         }
         __syncwarp();
         if (half == 1) {

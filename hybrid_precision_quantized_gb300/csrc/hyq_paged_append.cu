@@ -16,12 +16,15 @@
 // exchanged, so that each of a group's four lanes ends with two rows' (min, max)
 // and derives their steps, once per (row, group) instead of once per lane.
 //
-// What bounds it: instruction issue (85 per row and tensor, six in ten of the slots
-// used at 16 warps an SM) and the last round of blocks; prompts of 30 thousand
-// rows of 8 KV heads with the rows read back take 67 us, 0.70 of the copy rate.
-// Slower: 24 warps an SM with the rows read twice from shared memory (74 us),
-// blocks of four warps (80), resident blocks whose warps go from page to page (75,
-// and 70 with the values' tiles levelling the warps' shares).
+// What bounds it: instruction issue (85 per row and tensor at 16 warps an SM) and
+// the last round of blocks; prompts of 30 thousand rows of 8 KV heads with the rows
+// read back take 62 us, 0.77 of the copy rate.  A block lives about 15 us, so
+// its start counts: a call row a thread and the page's number asked for
+// after the first rows took 5 us off.  Slower than blocks of eight warps with a page
+// each: 24 warps an SM with the rows read twice from shared memory (+6 us), blocks of
+// four warps (+12), half pages of values a block (+3), resident blocks
+// whose warps go from page to page (+8, and +3 with the values' tiles levelling the
+// warps' shares).
 #include "hyq_paged.cuh"
 #include "hyq_qcode.cuh"
 
@@ -40,9 +43,10 @@ struct AppendParams {
 };
 
 // The rows that one page gets: rows [r0, r1) of the page, from row tok0 of
-// the call's rows on.
+// the call's rows on; the page's entry in the table.
 struct PageRows {
-  int page, r0, r1, tok0;
+  const int32_t* entry;
+  int r0, r1, tok0;
 };
 
 // First position and number of rows of call row i; n = 0 when there is
@@ -70,15 +74,17 @@ __device__ __forceinline__ CallRows call_rows(const AppendParams& p, int i) {
 __device__ __forceinline__ PageRows page_rows(const AppendParams& p, const CallRows& c, int nth) {
   const int blk = c.start / HYQ_PAGE_ROWS + nth, p0 = blk * HYQ_PAGE_ROWS;
   PageRows r;
-  r.page = p.pv.table[(size_t)c.seq * p.pv.max_blocks + blk];
+  r.entry = p.pv.table + (size_t)c.seq * p.pv.max_blocks + blk;
   r.r0 = max(0, c.start - p0);
   r.r1 = min(HYQ_PAGE_ROWS, c.start + c.n - p0);
   r.tok0 = c.tok + (p0 + r.r0 - c.start);
-  if (r.page < 0 || r.page >= p.pv.n_pages) {
-    hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-    r.r1 = r.r0;
-  }
   return r;
+}
+// The page is in the pool (reported if it is not).
+__device__ __forceinline__ bool page_ok(const AppendParams& p, int page) {
+  const bool ok = page >= 0 && page < p.pv.n_pages;
+  if (!ok) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+  return ok;
 }
 
 __device__ __forceinline__ uint32_t u32_of(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t*>(&x); }
@@ -473,42 +479,41 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
   __shared__ PageRows s_rows[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   chain_kernel();
-  // pages of the call rows 4 tid .. 4 tid + 3, summed up
-  CallRows c[4];
-  int n[4], sum = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    n[i] = 0;
-    if (4 * tid + i < p.batch) {
-      c[i] = call_rows(p, 4 * tid + i);
-      if (c[i].bad && blockIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-      if (c[i].n > 0) n[i] = (c[i].start + c[i].n - 1) / HYQ_PAGE_ROWS - c[i].start / HYQ_PAGE_ROWS + 1;
-    }
-    sum += n[i];
-  }
-  int pre = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += y;
-  }
-  if (lane == 31) s_warp[warp] = pre;
   const int per = kWarps / hb, first = (int)blockIdx.x * per;
   if (tid < kWarps) s_rows[tid].r0 = s_rows[tid].r1 = 0;  // no rows
-  __syncthreads();
-  int at = pre - sum;
-  for (int i = 0; i < warp; ++i) at += s_warp[i];
+  // Pages before each of the call's rows, a row a thread (the loads of several rows
+  // in one thread would follow one another), 256 rows at a time.
+  int before = 0;
+  for (int row0 = 0; row0 < p.batch; row0 += kThreads) {
+    const int row = row0 + tid;
+    CallRows c;
+    int n = 0;
+    if (row < p.batch) {
+      c = call_rows(p, row);
+      if (c.bad && blockIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+      if (c.n > 0) n = (c.start + c.n - 1) / HYQ_PAGE_ROWS - c.start / HYQ_PAGE_ROWS + 1;
+    }
+    int pre = n;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    for (int j = max(at - first, 0); j < per && first + j - at < n[i]; ++j) s_rows[j] = page_rows(p, c[i], first + j - at);
-    at += n[i];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    if (row0 > 0) __syncthreads();  // the sums of the 256 rows before have been read
+    if (lane == 31) s_warp[warp] = pre;
+    __syncthreads();
+    int at = before + pre - n;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) at += s_warp[i];
+      before += s_warp[i];
+    }
+    for (int j = max(at - first, 0); j < per && first + j - at < n; ++j) s_rows[j] = page_rows(p, c, first + j - at);
   }
   __syncthreads();
   const int h = blockIdx.y * hb + warp % hb, T = blockIdx.z;
   const PageRows r = s_rows[warp / hb];
   if (r.r1 <= r.r0 || h >= p.HKV) return;
-  const size_t ph = (size_t)r.page * p.HKV + h;
-  uint8_t* block = p.pv.pool + ph * F::kBlock;
+  const int page = *r.entry;  // not waited for before the first rows are on their way
   const int64_t ldh = (int64_t)p.HKV * HYQ_D;
   const __nv_bfloat16* src = (T == 0 ? p.k : p.v) + (int64_t)h * HYQ_D;
   __nv_bfloat16* hat = T == 0 ? p.k_hat : p.v_hat;
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
   b.clear();
   bool bad = false;
   // Two tiles' worth of shared memory a warp: the next tile's rows are on their
-  // way while one is worked on (76 us without, 67 with).
+  // way while one is worked on (11% faster).
   uint8_t* stage = s_stage + 8192 * warp + 16 * lane;
   auto rows_of = [&](int tile) -> uint32_t {  // rows of the tile: bits of [r0, r1) in [16 tile, 16 tile + 16)
     const int a = max(r.r0 - 16 * tile, 0), z = min(r.r1 - 16 * tile, 16);
@@ -530,6 +535,12 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
     asm volatile("cp.async.commit_group;\n" ::: "memory");
   };
   fetch(r.r0 >> 4);
+  if (!page_ok(p, page)) {
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    return;
+  }
+  const size_t ph = (size_t)page * p.HKV + h;
+  uint8_t* block = p.pv.pool + ph * F::kBlock;
 #pragma unroll 1
   for (int tile = r.r0 >> 4; 16 * tile < r.r1; ++tile) {
     fetch(tile + 1);
@@ -567,11 +578,12 @@ __global__ void __launch_bounds__(32 * kHeadsOne) append_one_kernel(const Append
   if (cr.bad && threadIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
   if (cr.n <= 0 || h >= p.HKV) return;
   const PageRows pr = page_rows(p, cr, 0);
-  if (pr.r1 <= pr.r0) return;
-  const size_t ph = (size_t)pr.page * p.HKV + h;
   const int T = lane >> 4, c = lane & 15, q = c >> 2, t4 = c & 3, row = pr.r0 & 15;
-  uint8_t* tile = p.pv.pool + ph * F::kBlock + (pr.r0 >> 4) * F::kTile;
   uint4 v = *reinterpret_cast<const uint4*>((T == 0 ? p.k : p.v) + (int64_t)pr.tok0 * p.ld + (int64_t)h * HYQ_D + 8 * c);
+  const int page = *pr.entry;
+  if (!page_ok(p, page)) return;
+  const size_t ph = (size_t)page * p.HKV + h;
+  uint8_t* tile = p.pv.pool + ph * F::kBlock + (pr.r0 >> 4) * F::kTile;
   uint32_t m = min_negmax(v);
   m = min2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = min2(m, __shfl_xor_sync(0xffffffffu, m, 2));
