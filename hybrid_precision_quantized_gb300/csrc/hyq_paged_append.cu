@@ -16,7 +16,7 @@
 // exchanged, so that each of a group's four lanes ends with two rows' (min, max)
 // and derives their steps, once per (row, group) instead of once per lane.
 //
-// What bounds it: instruction issue (85 per row and tensor at 16 warps an SM) and
+// What bounds it: instruction issue (81 per row and tensor at 16 warps an SM) and
 // the last round of blocks; prompts of 30 thousand rows of 8 KV heads with the rows
 // read back take 62 us, 0.77 of the copy rate.  A block lives about 15 us, so
 // its start counts: a call row a thread and the page's number asked for
