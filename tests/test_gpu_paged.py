@@ -989,3 +989,19 @@ def test_many_query_rows_skip_pages_outside_the_pool(hyq, bits, HQ, n_q):
     assert hyq_read_device_error(cache.err()) == L.DEVERR_INDEX
     sel = [[[np.array([0, 2, 4])]] * n_q, [[np.arange(5)]] * n_q]
     check_attention(cache, hist, q, out, [0, 1], sel=sel)
+
+
+@pytest.mark.parametrize("bits,n_q", [((8, 8), 4), ((4, 4), 8)])
+def test_many_query_rows_of_many_sequences(hyq, bits, n_q):
+    """1024 sequences, most of them shorter than the tokens asked for or empty: rows that see nothing are zeros."""
+    lens = [(5 * i) % 11 if i % 4 == 0 else 0 for i in range(1024)]
+    lens[5], lens[700], lens[1023] = 130, 70, 65
+    cache = make(8, 1, 300, 1024, 3, bits=bits)
+    k, v, _, _ = grow(cache, list(range(1024)), lens, 5)
+    hist = History(1024, 1)
+    hist.add(range(1024), lens, k, v)
+    q = queries(6, 1024, n_q, 8)
+    out = torch.full_like(q, float("nan"))
+    cache.attention(0, q, out)
+    assert hyq_read_device_error(cache.err()) == 0
+    check_attention(cache, hist, q, out, range(1024))
