@@ -202,9 +202,12 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   // for t >= 2), so a lane passes the zero pair of those groups.
   mma_f16(lg, (t & 1) ? ma.w : ma.z, (t & 1) ? mb.w : mb.z, 0u, 0u, qc.bz, 0u);
   // A vertical-line position (held in BF16 elsewhere) has NaN key steps in
-  // the stream: its logit is NaN, and the row is left out.
+  // the stream: its logit is NaN, and the row is left out.  Pages (kRows) hold no
+  // such rows: there a NaN is the query's own and goes on to its output.
+  if (!kRows) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) lg[i] = lg[i] != lg[i] ? -INFINITY : lg[i];
+    for (int i = 0; i < 4; ++i) lg[i] = lg[i] != lg[i] ? -INFINITY : lg[i];
+  }
   if (kRows) {
     if (g >= vh0) lg[0] = -INFINITY;
     if (g >= vh1) lg[1] = -INFINITY;

@@ -722,6 +722,8 @@ hyq_status hyq_paged_append(const hyq_config *cfg, const hyq_pages *pages, int32
  * (already appended).  out = softmax(q K^T / sqrt(128)) V over the
  * dequantised rows; a token at a negative position sees nothing and gives
  * zeros.  n_q = 1 is decoding, a few are drafted tokens or the end of a prompt.
+ * A query row that is not finite gives NaN in its own output row (if it sees
+ * anything) and changes no other.
  *   seqs  device int32 [batch] or NULL (sequence i); may repeat
  *   q     device bf16: token (b, i), head h, element d at
  *         (b n_q + i) ldq + 128 h + d; ldq >= 128 HQ, a multiple of 8
