@@ -4,7 +4,7 @@
 // For each query token i of a sequence and query head h of a KV head,
 //   out = sum_j 2^(x_j - M) v_j / sum_j 2^(x_j - M),  x_j = log2(e) q.k_j / sqrt(128),
 // over the positions j that the token sees, k_j and v_j = c s + z from the
-// pages: one pass with the running maximum and sum of a softmax (q_tile in
+// pages: one pass with the running maximum and sum of a softmax (q_tiles in
 // hyq_qtile.cuh: codes as fp16 subnormals on mma.sync, scales and zeros
 // applied outside).
 //
@@ -159,9 +159,6 @@ __device__ __forceinline__ void bulk_g2s_at(uint32_t dst, const void* src, uint3
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void sts32(uint32_t a, int v) {
-  asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(a), "r"(v) : "memory");
-}
 
 // Output row of (token, head) pair `flat` of a KV head whose first row is `out`.
 __device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, int gq, int flat) {
@@ -259,6 +256,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   using RingCtl = Ctl<kHalves, kSlots>;
   __shared__ __align__(8) RingCtl s_ctl[kWarps];
   __shared__ float red_m[kWarps][NQ][kRowsQ], red_l[kWarps][NQ][kRowsQ];
+  __shared__ __align__(16) uint32_t steps_s[kHalves == 1 ? 1 : kWarps * kHalves][32];  // each warp's scaled steps
   __shared__ float s_wt[kRowsG][kWarps];                // weights of the warps' partials
   __shared__ float s_sum[kRowsG];
   __shared__ int s_last;
@@ -459,12 +457,13 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       return ok ? at : -1;
     };
     // Two halves (no lists): unit j into the slot, by the lane that holds its page.
-    const uint32_t ctl = kept(smem_u32(&s_ctl[warp])), tiles = kept(smem_u32(ring)), query = kept(smem_u32(query_s[kq]));
+    const uint32_t ctl = kept(smem_u32(&s_ctl[warp])), tiles = kept(smem_u32(ring)), query = kept(smem_u32(query_s[kq])),
+                   scaled = kept(smem_u32(steps_s[kHalves == 1 ? 0 : tid >> 5]));
     constexpr uint32_t kFree = 8 * kSlots, kAt = 16 * kSlots;  // Ctl<2, kSlots>
     auto issue_at = [&](int j, uint32_t slot) {
       if (lane == (j & 31)) {
         const bool in = (uint32_t)pg_cur < (uint32_t)p.pv.n_pages;
-        sts32(ctl + kAt + 4 * slot, in ? R::kRows * (w0 + warp + kWarps * j) : -1);
+        sts32(ctl + kAt + 4 * slot, (uint32_t)(in ? R::kRows * (w0 + warp + kWarps * j) : -1));
         mbar_expect_at(ctl + 8 * slot, in ? R::kUnit : 0);
         if (in)
           bulk_g2s_at(tiles + slot * R::kUnit, heads + (size_t)pg_cur * ((size_t)p.HKV * R::kBlock), R::kUnit, ctl + 8 * slot);
@@ -493,15 +492,14 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     uint32_t bq[8][2];
     QConst qc;
     const int minlim = lim_s[0][0];  // the rows' tokens ascend
-    std::conditional_t<NQ == 1, State, PairState> st;
+    PageState<kNW> st;
     if constexpr (NQ == 1) {
       load_query_consts(g, t, bq_s(0), rowc_s[0], bz_s[0], bq, qc);
-      reset_state(st);
     } else {
       if (tid < 32 * NQ) spread_query_consts(query_s[tid >> 5], lane, rowc_s[tid >> 5], bz_s[tid >> 5]);
       __syncthreads();
-      reset_pair(st);
     }
+    reset_state(st);
 
     // A wait ran out: flag it, let this warp's other copies (units j0 .. j1 - 1)
     // land before shared memory is used for anything else, and stop.
@@ -524,7 +522,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
           break;
         }
         const int at = at_slot[0];
-        const uint8_t* tb = ring + slot * R::kUnit;
+        uint8_t* tb = ring + slot * R::kUnit;
         if (at >= 0) {
           if (at + R::kRows <= minlim) {
             q_tiles<BK, BV, R::kTiles>(tb, lane, bq, qc, st);
@@ -532,7 +530,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
             const int lim0 = lim_s[0][2 * t], lim1 = lim_s[0][2 * t + 1];
             for (int x = 0; x < R::kTiles && at + 16 * x < seg.len; ++x) {
               const int a = at + 16 * x;
-              q_tile<BK, BV, true, true>(tb + x * R::kTile, lane, seg.len - a, bq, qc, st, lim0 - a, lim1 - a);
+              q_tiles<BK, BV, 1, true>(tb + x * R::kTile, lane, bq, qc, st, seg.len - a, lim0 - a, lim1 - a);
             }
           }
         }
@@ -555,9 +553,9 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
         const uint32_t tb = tiles + slot * R::kUnit;
         if (at >= 0) {
           if (at + R::kRows <= minlim)
-            q_tile_pair<BK, BV, false>(tb, lane, query, 16, lim_s + kq, at, st);
+            q_tile_pair<BK, BV, false>(tb, lane, query, 16, lim_s + kq, at, scaled, st);
           else
-            q_tile_pair<BK, BV, true>(tb, lane, query, seg.len - at, lim_s + kq, at, st);
+            q_tile_pair<BK, BV, true>(tb, lane, query, seg.len - at, lim_s + kq, at, scaled, st);
         }
         __syncwarp();
         if (half == 1) {
@@ -583,17 +581,10 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     const bool whole = seg.w0 == 0 && seg.w1 == seg.n_units;
     float* pp = p.part + ((size_t)blockIdx.x * 2 + (seg.w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
     if (kHalves > 1) __syncthreads();  // both halves are done with the rings
-    if constexpr (NQ == 1) {
-      store_warp_partial<BV>(st, qc, g, t, reinterpret_cast<float*>(ring), red_m[warp][0], red_l[warp][0]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        load_query_consts(g, t, bq_s(kq + k), rowc_s[kq + k], bz_s[kq + k], bq, qc);
-        State one = pair_state(st, k, qc);
-        store_warp_partial<BV>(one, qc, g, t, reinterpret_cast<float*>(ring + 4096 * (kq + k)), red_m[warp][kq + k],
-                               red_l[warp][kq + k]);
-      }
-    }
+    for (int k = 0; k < kNW; ++k)
+      store_warp_partial<BV>(st, k, g, t, reinterpret_cast<float*>(ring + 4096 * (kq + k)), red_m[warp][kq + k],
+                             red_l[warp][kq + k]);
     __syncthreads();
     // eight lanes a row: its weights 2^(m_w - M) and its sum
     if (tid < kRowsG * kWarps) {

@@ -153,15 +153,10 @@ __device__ __forceinline__ uint32_t u4c(const uint4& v, int i) {
 //         + sum_q z_q (sum q)_q (one MMA: the zero pairs against qc.bz)
 //   out  += sum_j (p_j s_jq) c_jd  (P^T scaled by the V scale pairs in fp16)
 //         + sum_j p_j z_jq          (one MMA: the V zero pairs against P^T)
-//
-// kRows: the tile may lie at the end of what some query row sees, and its
-// rows past `vr` may hold anything (a page is reused without being cleared):
-// heads 2t, 2t+1 see the first vh[0], vh[1] rows, and the value metadata of
-// the rows past vr, which could be infinite or NaN, is taken as zero (their
-// probabilities are zero, and so must be their products).
-template <int BK, int BV, bool kLazy, bool kRows = false>
+// (the fixed-batch cache; q_tiles and q_tile_pair are the pages' forms)
+template <int BK, int BV, bool kLazy>
 __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, const uint32_t (&bq)[8][2],
-                                       const QConst& qc, State& st, int vh0 = 16, int vh1 = 16) {
+                                       const QConst& qc, State& st) {
   using F = QFmt<BK, BV>;
   const int g = lane >> 2, t = lane & 3;
   float C[4][4];
@@ -202,18 +197,10 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   // for t >= 2), so a lane passes the zero pair of those groups.
   mma_f16(lg, (t & 1) ? ma.w : ma.z, (t & 1) ? mb.w : mb.z, 0u, 0u, qc.bz, 0u);
   // A vertical-line position (held in BF16 elsewhere) has NaN key steps in
-  // the stream: its logit is NaN, and the row is left out.  Pages (kRows) hold no
-  // such rows: there a NaN is the query's own and goes on to its output.
-  if (!kRows) {
+  // the stream: its logit is NaN, and the row is left out.
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lg[i] = lg[i] != lg[i] ? -INFINITY : lg[i];
-  }
-  if (kRows) {
-    if (g >= vh0) lg[0] = -INFINITY;
-    if (g >= vh1) lg[1] = -INFINITY;
-    if (g + 8 >= vh0) lg[2] = -INFINITY;
-    if (g + 8 >= vh1) lg[3] = -INFINITY;
-  } else if (vr < 16) {
+  for (int i = 0; i < 4; ++i) lg[i] = lg[i] != lg[i] ? -INFINITY : lg[i];
+  if (vr < 16) {
     if (g >= vr) lg[0] = lg[1] = -INFINITY;
     if (g + 8 >= vr) lg[2] = lg[3] = -INFINITY;
   }
@@ -224,20 +211,13 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   const uint32_t pt1 = movmatrix_trans(pack_f16x2(p[2], p[3]));
   const uint8_t* vm = tb + F::kVMeta;
   // V scale pairs of tokens (2t, 2t+1) and (2t+8, 2t+9), groups 0..3.
-  uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
-  uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
+  const uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
+  const uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
   // sum_j p_j z_jq on the tensor core: A rows = groups (g < 4), k = tokens.
   uint32_t z0 = 0u, z1 = 0u;
   if (g < 4) {
     z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * g);
     z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * g);
-  }
-  if (kRows) {
-    // the halves of the pair (2t, 2t+1), and of (2t+8, 2t+9), that lie below vr
-    const uint32_t k0 = (2 * t < vr ? 0xFFFFu : 0u) | (2 * t + 1 < vr ? 0xFFFF0000u : 0u);
-    const uint32_t k1 = (2 * t + 8 < vr ? 0xFFFFu : 0u) | (2 * t + 9 < vr ? 0xFFFF0000u : 0u);
-    sv0.x &= k0, sv0.y &= k0, sv0.z &= k0, sv0.w &= k0, z0 &= k0;
-    sv1.x &= k1, sv1.y &= k1, sv1.z &= k1, sv1.w &= k1, z1 &= k1;
   }
   mma_f16(st.zd, z0, 0u, z1, 0u, pt0, pt1);
   uint32_t vw[BV == 4 ? 8 : 16];
@@ -259,31 +239,130 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
   }
 }
 
-// The running maximum of q_tiles and q_tile_pair is a reference that may lag:
-// it moves (and the accumulators are rescaled) only when a logit passes it by
-// more than kSlack<BV> in log2 units.  A probability is then at most 2^kSlack,
-// and p s still fits fp16: s is at most 2 * 65504 / qmax, 8734 for 4-bit and 514
-// for 8-bit values.  The first maximum of a row is seldom its last, so without
-// the slack short runs of tiles rescale at most of their tiles.  Each row's
-// maximum moves for its own logits alone: its result does not depend on the rows
-// that share its tile.
+// ---- pages ----------------------------------------------------------------------
+// A probability enters the value product in fp16, and so does its product with the
+// value step: both are kept at the upper end of what fp16 holds, whatever the
+// values' size, so that the small ones are not lost below it.  (With p at most 1 and
+// p s as it came, an output made of rows 12 nats below one large and empty row was off by
+// 0.28 of its size for 8-bit values of standard deviation 0.3 and by more than its
+// size from 0.1 down, for 4-bit ones by 0.11 at 0.02; now by 0.002, its rounding to BF16.)
+//
+// p.  The reference that a row's logits are taken from stands below a logit near
+// the row's maximum, so that p comes near 2^15.  It may lag: it moves (and the
+// accumulators are rescaled) only when some p would pass 2^top, top = 15, and then
+// to where that p is 2^(top - kSlack).  The first maximum of a row is seldom its
+// last, so without the slack short runs of tiles rescale at most of their tiles.
+// Each row's reference moves for its own logits alone: its result does not depend
+// on the rows that share its tile.  Sums and zero-point terms are of the same p.
+//
+// p s.  A warp takes the steps times a power of two 2^F >= 1 such that the
+// largest that it has met lies below 2: p s stays within 65504.  When a larger one
+// comes, F falls, to where that step lies in [0.5, 1), and the accumulators with
+// it.  Steps from 2 on (values that span 30, or 510 with 8-bit codes) lower top
+// instead: a step made smaller could leave fp16, beside others that are not large.
+// One lane scales each word of a tile's steps, in shared memory, before all read
+// them (one sequence of 1000 positions: 9.38 us without any of this, 9.55 with it,
+// 9.61 when each lane scaled the eight words that it read; drafts of 8-bit codes 65.5,
+// 66.8, 67.9).
 template <int BV>
 constexpr float kSlack = BV == 4 ? 2.f : 6.f;
-// The slack in the scaled domain of a row with inv = 2^-sigma.
-template <int BV>
-__device__ __forceinline__ float slack_of(float inv) {
-  return kSlack<BV> * __int_as_float((254 << 23) - __float_as_int(inv));
+
+// Of N query tiles and one warp, for the heads (2t, 2t+1) that a thread owns.
+template <int N>
+struct PageState {
+  float nm[N][2];      // minus the reference in log2 units (kNoMax before the first)
+  float l[N][2];       // running sums of this thread's probabilities
+  float acc[N][8][4];  // value products in units of 2^-24 2^F
+  float zd[N][4];      // sum_j p_j z_jq: rows g < 4 = group g, columns heads 2t, 2t+1
+  uint32_t lim;        // the largest step that F and top allow (its bits, twice)
+  float top;
+};
+constexpr float kNoMax = 3.402823466e38f;  // finite: a masked logit less it is still minus infinity
+
+template <int N>
+__device__ __forceinline__ void reset_state(PageState<N>& st) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    st.nm[k][0] = st.nm[k][1] = kNoMax;
+    st.l[k][0] = st.l[k][1] = 0.f;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) st.acc[k][mt][0] = st.acc[k][mt][1] = st.acc[k][mt][2] = st.acc[k][mt][3] = 0.f;
+    st.zd[k][0] = st.zd[k][1] = st.zd[k][2] = st.zd[k][3] = 0.f;
+  }
+  st.lim = 0x03FF03FFu;  // subnormal steps: F = 15
+  st.top = 15.f;
 }
 
-// q_tile for NT adjacent tiles, every row seen by every query row and no row
-// left out by NaN steps: the tiles' independent chains overlap, and the
-// running maximum is tested once for all of them.
-template <int BK, int BV, int NT>
-__device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint32_t (&bq)[8][2], const QConst& qc,
-                                        State& st) {
+// A step's bits ascend with its value.  The limit of F >= 0 has the exponent
+// field 15 - F (the steps below 2 2^-F), that of a lowered top 30 - top.
+constexpr uint32_t kLimitF0 = 0x3FFFu;
+__device__ __forceinline__ bool above_limit(uint32_t steps, uint32_t lim) { return __vmaxu2(steps, lim) != lim; }
+// The largest of all lanes' steps.
+__device__ __forceinline__ uint32_t most_step(uint32_t steps) {
+  return __reduce_max_sync(0xffffffffu, max(steps & 0xFFFFu, steps >> 16));
+}
+// 2^F, twice in fp16.
+__device__ __forceinline__ uint32_t step_scale(uint32_t lim) { return __vmaxu2(0x7BFF7BFFu - lim, 0x3C003C00u); }
+// 2^F of one limit (one half) over 2^F of another.
+__device__ __forceinline__ float scale_ratio(uint32_t a, uint32_t b) {
+  return __int_as_float(0x3F800000 + (int)((min(b, kLimitF0) - min(a, kLimitF0)) << 13));
+}
+// The limit for a step `most`: one above the present limit comes to lie in [0.5, 1) times 2^F.
+// Returns the change of F, which the value products take; top falls by `fell`.
+template <int N>
+__device__ __forceinline__ float raise_limit(uint32_t most, PageState<N>& st, float& fell) {
+  const uint32_t was = st.lim & 0xFFFFu, lim = most > was ? min((most | 0x3FFu) + 0x400u, 0x7BFFu) : was;
+  st.lim = lim * 0x00010001u;
+  const float top = (float)(30 - (int)(max(lim, kLimitF0) >> 10));
+  fell = st.top - top;
+  st.top = top;
+  return scale_ratio(lim, was);
+}
+
+// Query tile k's part of a raise: the reference of head 2t + j moves if one of its logits (tm: the
+// lane's largest, times inv = 2^-sigma) lies more than top above it, and by what top fell.
+template <int BV, int N>
+__device__ __forceinline__ void raise_head(PageState<N>& st, int k, int j, float tm, float inv, float fell, float fc) {
+  tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
+  tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
+  tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+  // inv is a power of two: the products are exact, and the sum rounded down keeps
+  // the largest p within 2^(top - kSlack)
+  const float old = st.nm[k][j], low = old - fell;
+  const float nm = fmaf(tm, inv, low) > st.top ? __fadd_rd(fmaxf(st.top - kSlack<BV>, 0.f), -tm * inv) : low;
+  const float corr = ex2(nm - old), ca = corr * fc;
+  st.nm[k][j] = nm;
+  st.l[k][j] *= corr;
+#pragma unroll
+  for (int mt = 0; mt < 8; ++mt) {
+    st.acc[k][mt][j] *= ca;
+    st.acc[k][mt][2 + j] *= ca;
+  }
+  st.zd[k][j] *= corr;
+}
+
+// The halves of a word about rows r, r + 1 that lie below vr.
+__device__ __forceinline__ uint32_t rows_below(int r, int vr) {
+  return (r < vr ? 0xFFFFu : 0u) | (r + 1 < vr ? 0xFFFF0000u : 0u);
+}
+
+// q_tile's products for NT adjacent tiles of a page: the tiles' independent chains
+// overlap, and reference and steps are tested once for all of them.
+//
+// kRows: the tile may lie at the end of what some query row sees, and its
+// rows past `vr` may hold anything (a page is reused without being cleared):
+// heads 2t, 2t+1 see the first vh0, vh1 rows, and the value metadata of
+// the rows past vr, which could be infinite or NaN, is taken as zero (their
+// probabilities are zero, and so must be their products).  Otherwise every row is
+// seen by every query row.  A NaN logit is its query's own and goes on to its output.
+template <int BK, int BV, int NT, bool kRows = false>
+__device__ __forceinline__ void q_tiles(uint8_t* tb0, int lane, const uint32_t (&bq)[8][2], const QConst& qc,
+                                        PageState<1>& st, int vr = 16, int vh0 = 16, int vh1 = 16) {
   using F = QFmt<BK, BV>;
+  static_assert(!kRows || NT == 1, "rows are left out of one tile at a time");
   const int g = lane >> 2, t = lane & 3;
   float lg[NT][4];
+  uint32_t step[NT];  // the steps of rows 2g, 2g + 1 and group t
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const uint8_t* tb = tb0 + n * F::kTile;
@@ -320,54 +399,71 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
                                          fmaf(b01.y, C[1][2 + c], fmaf(b23.x, C[2][2 + c], b23.y * C[3][2 + c])));
     }
     mma_f16(lg[n], (t & 1) ? ma.w : ma.z, (t & 1) ? mb.w : mb.z, 0u, 0u, qc.bz, 0u);
+    if (kRows) {
+      if (g >= vh0) lg[n][0] = -INFINITY;
+      if (g >= vh1) lg[n][1] = -INFINITY;
+      if (g + 8 >= vh0) lg[n][2] = -INFINITY;
+      if (g + 8 >= vh1) lg[n][3] = -INFINITY;
+    }
+    step[n] = *reinterpret_cast<const uint32_t*>(tb + F::kVMeta + 4 * lane);
+    if (kRows) step[n] &= rows_below(2 * g, vr);
   }
-  // ---- running maximum ------------------------------------------------------
-  float tm[2];
+  // ---- reference and steps ---------------------------------------------------
+  float x[NT][4];  // logits less the reference, in log2 units
+  uint32_t steps = step[0];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    tm[j] = fmaxf(lg[0][j], lg[0][2 + j]);
+  for (int n = 1; n < NT; ++n) steps = __vmaxu2(steps, step[n]);
+  const uint32_t most = most_step(steps);
+  bool above = most > (st.lim >> 16);
 #pragma unroll
-    for (int n = 1; n < NT; ++n) tm[j] = fmaxf(tm[j], fmaxf(lg[n][j], lg[n][2 + j]));
+  for (int n = 0; n < NT; ++n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[n][i] = fmaf(lg[n][i], qc.inv[i & 1], st.nm[0][i & 1]);
+    above |= fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])) > st.top;
   }
-  if (__any_sync(0xffffffffu, tm[0] > st.m[0] + slack_of<BV>(qc.inv[0]) || tm[1] > st.m[1] + slack_of<BV>(qc.inv[1]))) {
+  if (__any_sync(0xffffffffu, above)) {
+    float fell;
+    const float fc = raise_limit(most, st, fell);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 4));
-      tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 8));
-      tm[j] = fmaxf(tm[j], __shfl_xor_sync(0xffffffffu, tm[j], 16));
-      const float mn = tm[j] > st.m[j] + slack_of<BV>(qc.inv[j]) ? tm[j] : st.m[j];
-      const float nm = mn == -INFINITY ? 0.f : -mn * qc.inv[j];
-      const float corr = ex2(fmaf(st.m[j], qc.inv[j], nm));
-      st.m[j] = mn;
-      st.nm[j] = nm;
-      st.l[j] *= corr;
+      float tm = fmaxf(lg[0][j], lg[0][2 + j]);
 #pragma unroll
-      for (int mt = 0; mt < 8; ++mt) {
-        st.acc[mt][j] *= corr;
-        st.acc[mt][2 + j] *= corr;
+      for (int n = 1; n < NT; ++n) tm = fmaxf(tm, fmaxf(lg[n][j], lg[n][2 + j]));
+      raise_head<BV>(st, 0, j, tm, qc.inv[j], fell, fc);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        x[n][j] = fmaf(lg[n][j], qc.inv[j], st.nm[0][j]);
+        x[n][2 + j] = fmaf(lg[n][2 + j], qc.inv[j], st.nm[0][j]);
       }
-      st.zd[j] *= corr;
     }
   }
+  // the steps times 2^F, in their place: a lane's own word, read by all below
+  const uint32_t f2 = step_scale(st.lim);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    *reinterpret_cast<uint32_t*>(tb0 + n * F::kTile + F::kVMeta + 4 * lane) = hmul2_u32(step[n], f2);
+  __syncwarp();
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const uint8_t* tb = tb0 + n * F::kTile;
     float p[4];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      p[j] = ex2(fmaf(lg[n][j], qc.inv[j], st.nm[j]));
-      p[2 + j] = ex2(fmaf(lg[n][2 + j], qc.inv[j], st.nm[j]));
-      st.l[j] += p[j] + p[2 + j];
-    }
+    for (int i = 0; i < 4; ++i) p[i] = ex2(x[n][i]);
+    st.l[0][0] += p[0] + p[2];
+    st.l[0][1] += p[1] + p[3];
     const uint32_t pt0 = movmatrix_trans(pack_f16x2(p[0], p[1]));
     const uint32_t pt1 = movmatrix_trans(pack_f16x2(p[2], p[3]));
     const uint8_t* vm = tb + F::kVMeta;
     const uint4 sv0 = *reinterpret_cast<const uint4*>(vm + 16 * t);
     const uint4 sv1 = *reinterpret_cast<const uint4*>(vm + 16 * (t + 4));
     // rows g < 4 carry the zeros of group g; rows 4 .. 7 repeat them and are not used
-    const uint32_t z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * (g & 3));
-    const uint32_t z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * (g & 3));
-    mma_f16(st.zd, z0, 0u, z1, 0u, pt0, pt1);
+    uint32_t z0 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * t + 4 * (g & 3));
+    uint32_t z1 = *reinterpret_cast<const uint32_t*>(vm + 128 + 16 * (t + 4) + 4 * (g & 3));
+    if (kRows) {  // (the steps of those rows are zero already)
+      z0 &= rows_below(2 * t, vr);
+      z1 &= rows_below(2 * t + 8, vr);
+    }
+    mma_f16(st.zd[0], z0, 0u, z1, 0u, pt0, pt1);
     uint32_t vw[BV == 4 ? 8 : 16];
     load_words<BV == 4 ? 8 : 16>(tb + F::kVCode, lane, vw);
 #pragma unroll
@@ -377,10 +473,10 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
       for (int mm = 0; mm < 2; ++mm) {
         if (BV == 4) {
           const uint32_t x = vw[2 * q + mm], x8 = x >> 8;
-          mma_f16(st.acc[2 * q + mm], x & 0x000F000Fu, x & 0x00F000F0u, x8 & 0x000F000Fu, x8 & 0x00F000F0u, b0, b1);
+          mma_f16(st.acc[0][2 * q + mm], x & 0x000F000Fu, x & 0x00F000F0u, x8 & 0x000F000Fu, x8 & 0x00F000F0u, b0, b1);
         } else {
           const uint32_t y0 = vw[2 * (2 * q + mm)], y1 = vw[2 * (2 * q + mm) + 1];
-          mma_f16(st.acc[2 * q + mm], y0 & 0x00FF00FFu, y1 & 0x00FF00FFu, odd_bytes(y0), odd_bytes(y1), b0, b1);
+          mma_f16(st.acc[0][2 * q + mm], y0 & 0x00FF00FFu, y1 & 0x00FF00FFu, odd_bytes(y0), odd_bytes(y1), b0, b1);
         }
       }
     }
@@ -394,24 +490,6 @@ __device__ __forceinline__ void q_tiles(const uint8_t* tb0, int lane, const uint
 //   [2048, 2112)  per t: the code-product factor and 2^-sigma of head 2t, then of 2t + 1
 //   [2112, 2240)  per lane: the zero-point fragment
 constexpr int kPairQuery = 2240;  // bytes of a query tile
-struct PairState {
-  float nm[2][2];       // minus the running maximum in log2 units (kNoMax before the first)
-  float l[2][2];        // running sums of this thread's probabilities
-  float acc[2][8][4];   // as in State
-  float zd[2][4];       // sum_j p_j z_jq: rows g < 4, as in State
-};
-constexpr float kNoMax = 1e30f;  // above any slack, and finite: a masked logit less it is still minus infinity
-
-__device__ __forceinline__ void reset_pair(PairState& st) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    st.nm[k][0] = st.nm[k][1] = kNoMax;
-    st.l[k][0] = st.l[k][1] = 0.f;
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt) st.acc[k][mt][0] = st.acc[k][mt][1] = st.acc[k][mt][2] = st.acc[k][mt][3] = 0.f;
-    st.zd[k][0] = st.zd[k][1] = st.zd[k][2] = st.zd[k][3] = 0.f;
-  }
-}
 
 // The lane's constants of a query tile from what prep_query_row left.
 __device__ __forceinline__ void spread_query_consts(uint8_t* query, int lane, const float (&rowc_s)[HYQ_MAX_GQA][4],
@@ -440,13 +518,18 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(a), "r"(v) : "memory");
+}
+
 // One 16-row tile at address `tb` for two query tiles: a tile's codes are unpacked
 // and its scales converted once for both.  query: address of the first query tile's
-// operands.  kRows as in q_tile, with lim_s[k] the rows that query
+// operands; scaled: 128 bytes of the warp's own (two warps read a tile, each with
+// an F of its own).  kRows as in q_tiles, with lim_s[k] the rows that query
 // tile k's heads see, less `at`.
 template <int BK, int BV, bool kRows>
 __device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t query, int vr,
-                                            const int (*lim_s)[HYQ_MAX_GQA], int at, PairState& st) {
+                                            const int (*lim_s)[HYQ_MAX_GQA], int at, uint32_t scaled, PageState<2>& st) {
   using F = QFmt<BK, BV>;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t tl = tb + 16 * lane, tg = tb + 16 * g, tt = tb + 16 * t, tz = tt + 4 * (g & 3);
@@ -491,8 +574,10 @@ __device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t quer
   key_group(std::integral_constant<int, 1>{});
   key_group(std::integral_constant<int, 0>{});
   const uint32_t za = (t & 1) ? ma.w : ma.z, zb = (t & 1) ? mb.w : mb.z;
-  float x[2][4];  // lambda 2^-sigma - max, in log2 units
-  bool above = false;
+  float x[2][4];  // logits less the reference, in log2 units
+  uint32_t step = lds32<F::kVMeta>(tb + 4 * lane);  // of rows 2g, 2g + 1 and group t
+  if (kRows) step &= rows_below(2 * g, vr);
+  bool above = above_limit(step, st.lim);
   auto logits = [&](auto tile) {
     constexpr int k = decltype(tile)::value;
     float(&l)[4] = lg[k];
@@ -510,39 +595,28 @@ __device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t quer
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[k][i] = fmaf(l[i], __uint_as_float(i & 1 ? c.w : c.y), st.nm[k][i & 1]);
-    above |= fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3])) > kSlack<BV>;
+    above |= fmaxf(fmaxf(x[k][0], x[k][1]), fmaxf(x[k][2], x[k][3])) > st.top;
   };
   logits(std::integral_constant<int, 0>{});
   logits(std::integral_constant<int, 1>{});
   if (__any_sync(0xffffffffu, above)) {
+    float fell;
+    const float fc = raise_limit(most_step(step), st, fell);
     auto raise = [&](auto tile) {
       constexpr int k = decltype(tile)::value;
       const uint4 c = lds128<kPairQuery * k + 2048>(qt);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float inv = __uint_as_float(j ? c.w : c.y);
-        float tm = fmaxf(lg[k][j], lg[k][2 + j]);
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-        // inv is a power of two: the product is exact
-        const float old = st.nm[k][j], nm = fmaf(tm, inv, old) > kSlack<BV> ? -tm * inv : old;
-        const float corr = ex2(nm - old);
-        st.nm[k][j] = nm;
-        st.l[k][j] *= corr;
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          st.acc[k][mt][j] *= corr;
-          st.acc[k][mt][2 + j] *= corr;
-        }
-        st.zd[k][j] *= corr;
-        x[k][j] = fmaf(lg[k][j], inv, nm);
-        x[k][2 + j] = fmaf(lg[k][2 + j], inv, nm);
+        raise_head<BV>(st, k, j, fmaxf(lg[k][j], lg[k][2 + j]), inv, fell, fc);
+        x[k][j] = fmaf(lg[k][j], inv, st.nm[k][j]);
+        x[k][2 + j] = fmaf(lg[k][2 + j], inv, st.nm[k][j]);
       }
     };
     raise(std::integral_constant<int, 0>{});
     raise(std::integral_constant<int, 1>{});
   }
+  sts32(scaled + 4 * lane, hmul2_u32(step, step_scale(st.lim)));
   uint32_t pt0[2], pt1[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -554,14 +628,13 @@ __device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t quer
     pt0[k] = movmatrix_trans(pack_f16x2(p[0], p[1]));
     pt1[k] = movmatrix_trans(pack_f16x2(p[2], p[3]));
   }
-  uint4 sv0 = lds128<F::kVMeta>(tt), sv1 = lds128<F::kVMeta + 64>(tt);
+  __syncwarp();  // the scaled steps are there
+  const uint4 sv0 = lds128<0>(scaled + 16 * t), sv1 = lds128<64>(scaled + 16 * t);
   // rows g < 4 carry the zeros of group g; rows 4 .. 7 repeat them and are not used
   uint32_t z0 = lds32<F::kVMeta + 128>(tz), z1 = lds32<F::kVMeta + 192>(tz);
-  if (kRows) {
-    const uint32_t k0 = (2 * t < vr ? 0xFFFFu : 0u) | (2 * t + 1 < vr ? 0xFFFF0000u : 0u);
-    const uint32_t k1 = (2 * t + 8 < vr ? 0xFFFFu : 0u) | (2 * t + 9 < vr ? 0xFFFF0000u : 0u);
-    sv0.x &= k0, sv0.y &= k0, sv0.z &= k0, sv0.w &= k0, z0 &= k0;
-    sv1.x &= k1, sv1.y &= k1, sv1.z &= k1, sv1.w &= k1, z1 &= k1;
+  if (kRows) {  // (the steps of those rows are zero already)
+    z0 &= rows_below(2 * t, vr);
+    z1 &= rows_below(2 * t + 8, vr);
   }
 #pragma unroll
   for (int k = 0; k < 2; ++k) mma_f16(st.zd[k], z0, 0u, z1, 0u, pt0[k], pt1[k]);
@@ -589,23 +662,6 @@ __device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t quer
   value_group(std::integral_constant<int, 1>{});
   value_group(std::integral_constant<int, 2>{});
   value_group(std::integral_constant<int, 3>{});
-}
-
-// Query tile k of a pair as a State, for store_warp_partial.
-__device__ __forceinline__ State pair_state(const PairState& p, int k, const QConst& qc) {
-  State st;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    st.m[j] = p.nm[k][j] == kNoMax ? -INFINITY : -p.nm[k][j] / qc.inv[j];
-    st.l[j] = p.l[k][j];
-    st.zd[j] = p.zd[k][j];
-    st.nm[j] = st.zd[2 + j] = 0.f;
-  }
-#pragma unroll
-  for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) st.acc[mt][i] = p.acc[k][mt][i];
-  return st;
 }
 
 // A query row's operands: its fp16 B fragments (bq_s), scaled by an exact
@@ -693,20 +749,22 @@ __device__ __forceinline__ void reset_state(State& st) {
 // A warp's partial result to shared memory: acc[head][128] with the
 // zero-point terms in wpart ([8 heads][128] = 4 KB; element d of head hd at
 // hd*128 + (d ^ (hd/2)), so that the 32 lanes' stores of one accumulator
-// fall in 32 banks), the maximum (log2 units) and the sum per head.
+// fall in 32 banks), what the probabilities are relative to (m: log2 units) and
+// their sum per head.  unit: of the accumulators, times 2^24.
 template <int BV>
-__device__ __forceinline__ void store_warp_partial(State& st, const QConst& qc, int g, int t, float* wpart,
-                                                   float (&red_m)[HYQ_MAX_GQA], float (&red_l)[HYQ_MAX_GQA]) {
+__device__ __forceinline__ void store_partial(const float (&acc)[8][4], const float (&zd)[4], float (&l)[2], float m0,
+                                              float m1, float unit, int g, int t, float* wpart,
+                                              float (&red_m)[HYQ_MAX_GQA], float (&red_l)[HYQ_MAX_GQA]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) st.l[j] += __shfl_xor_sync(0xffffffffu, st.l[j], o);
+    for (int o = 4; o < 32; o <<= 1) l[j] += __shfl_xor_sync(0xffffffffu, l[j], o);
   // sum_j p_j z_jq of heads 2t, 2t+1 sits in lane (q, t): gather all four groups.
   float zt[4][2];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    zt[q][0] = __shfl_sync(0xffffffffu, st.zd[0], 4 * q + t);
-    zt[q][1] = __shfl_sync(0xffffffffu, st.zd[1], 4 * q + t);
+    zt[q][0] = __shfl_sync(0xffffffffu, zd[0], 4 * q + t);
+    zt[q][1] = __shfl_sync(0xffffffffu, zd[1], 4 * q + t);
   }
   // Accumulator (m-tile u, ci) of thread (g, t): element 32(u/2) + 4g +
   // 2(u%2) + (ci >> 1), head 2t + (ci & 1); with 4-bit values the rows
@@ -716,15 +774,31 @@ __device__ __forceinline__ void store_warp_partial(State& st, const QConst& qc, 
 #pragma unroll
     for (int ci = 0; ci < 4; ++ci) {
       const int d = 32 * (u >> 1) + 4 * g + 2 * (u & 1) + (ci >> 1), hd = 2 * t + (ci & 1);
-      const float f = (BV == 4 && ci >= 2) ? HYQ_F16_SUB_SCALE / 16.f : HYQ_F16_SUB_SCALE;
-      wpart[hd * HYQ_D + (d ^ t)] = fmaf(st.acc[u][ci], f, zt[u >> 1][ci & 1]);
+      const float f = (BV == 4 && ci >= 2) ? unit / 16.f : unit;
+      wpart[hd * HYQ_D + (d ^ t)] = fmaf(acc[u][ci], f, zt[u >> 1][ci & 1]);
     }
-  if (g == 0)
+  if (g == 0) {
+    red_m[2 * t] = m0, red_m[2 * t + 1] = m1;
+    red_l[2 * t] = l[0], red_l[2 * t + 1] = l[1];
+  }
+}
+template <int BV>
+__device__ __forceinline__ void store_warp_partial(State& st, const QConst& qc, int g, int t, float* wpart,
+                                                   float (&red_m)[HYQ_MAX_GQA], float (&red_l)[HYQ_MAX_GQA]) {
+  float m[2];  // back to log2 units
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      red_m[2 * t + j] = st.m[j] == -INFINITY ? -INFINITY : st.m[j] * qc.inv[j];  // back to log2 units
-      red_l[2 * t + j] = st.l[j];
-    }
+  for (int j = 0; j < 2; ++j) m[j] = st.m[j] == -INFINITY ? -INFINITY : st.m[j] * qc.inv[j];
+  store_partial<BV>(st.acc, st.zd, st.l, m[0], m[1], HYQ_F16_SUB_SCALE, g, t, wpart, red_m, red_l);
+}
+// Query tile k of a warp.
+template <int BV, int N>
+__device__ __forceinline__ void store_warp_partial(PageState<N>& st, int k, int g, int t, float* wpart,
+                                                   float (&red_m)[HYQ_MAX_GQA], float (&red_l)[HYQ_MAX_GQA]) {
+  float m[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) m[j] = st.nm[k][j] == kNoMax ? -INFINITY : -st.nm[k][j];
+  store_partial<BV>(st.acc[k], st.zd[k], st.l[k], m[0], m[1], HYQ_F16_SUB_SCALE * scale_ratio(kLimitF0, st.lim & 0xFFFFu), g, t, wpart, red_m,
+                    red_l);
 }
 
 }  // namespace

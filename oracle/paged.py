@@ -82,6 +82,33 @@ def attend_error(q, k, kparts, vparts, vcodes, vis, out):
     return 2.0 ** -8 * np.abs(out) + mean * (2.0 ** -10 + 2 * 2.0 ** -18 * size) + 2.0 ** -25 * total
 
 
+def attend_bound(q, k, kparts, vparts, vcodes, vsteps, vis, out, bits_v):
+    """attend_error without a part that does not shrink with the values: the
+    kernel keeps probabilities and their products with the value steps at the
+    upper end of fp16.
+
+    A row's largest probability is held as at least 2^lift, and every step s
+    is taken times 2^F, F >= 0, where
+      lift = top - 2 (4-bit values) or top - 6 (8-bit), at least 0, with
+      top = 15, less 1 for each power of two that the largest step reaches from 1 on;
+      2^-F <= 2 max s, or 2^-15 when that is smaller, and F = 0 from max s = 1/2 on.
+    Below the normal range of fp16 half a step is 2^-25: of a probability
+    2^(-25 - lift), which meets |c s| + |z|, of a product 2^(-25 - lift - F), which
+    meets c.  vsteps: the steps of all of the sequence's rows (those of rows that a
+    token does not see may count)."""
+    if not np.any(vis):
+        return np.zeros_like(out)
+    x = (k[vis] @ q) / math.sqrt(q.shape[-1])
+    p = np.exp(x - x.max())
+    size = ((kparts[vis] @ np.abs(q)) / math.sqrt(q.shape[-1])).max()
+    most = float(np.asarray(vsteps, np.float64).max())
+    top = 15 - (max(0, math.floor(math.log2(most)) + 1) if most > 0 else 0)
+    low = 2.0 ** (-25 - max(0, top - (2 if bits_v == 4 else 6)))
+    f = min(1.0, max(2 * most, 2.0 ** -15))
+    mean, parts, codes = (p @ vparts[vis]) / p.sum(), vparts[vis].sum(0) / p.sum(), vcodes[vis].sum(0) / p.sum()
+    return 2.0 ** -8 * np.abs(out) + mean * (2.0 ** -10 + 2 * 2.0 ** -18 * size) + low * (parts + f * codes)
+
+
 def dequantised(rows, bits):
     """Rows as the cache holds them, |c s| + |z| of each element, and the codes."""
     c, s, z = quantize(rows, bits)
