@@ -77,9 +77,16 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const SelectPa
   const int64_t lim = max((int64_t)0, len - p.n_q + 1 + tok);
   const int nb = (int)((lim + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS);
   int32_t* sel = p.sel + list * p.k;
+  auto query = [&] { return p.q + ((size_t)b * p.n_q + tok) * p.ldq + (size_t)h * p.gq * HYQ_D; };
   if (nb <= p.k) {  // every block that the token sees
-    if (blockIdx.x == 0)
+    if (blockIdx.x == 0) {
       for (int i = tid; i < p.k; i += kThreads) sel[i] = i < nb ? i : -1;
+      const __nv_bfloat16* q = query();
+      bool odd = false;
+      if (nb > 0)
+        for (int i = tid; i < p.gq * HYQ_D; i += kThreads) odd |= !isfinite(__bfloat162float(q[i]));
+      if (odd) hyq_set_err(p.pv.err, HYQ_DEVERR_SCORE);
+    }
     return;
   }
   // ---- the first records: lane i < 16 holds the page of record i, eight lanes
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) select_kernel(const SelectPa
   fetch();
   // ---- the query's codes: thread i < 128 holds element i of every head ------
   float x[HYQ_MAX_GQA], am = 0.f;
-  const __nv_bfloat16* q = p.q + ((size_t)b * p.n_q + tok) * p.ldq + (size_t)h * p.gq * HYQ_D;
+  const __nv_bfloat16* q = query();
   bool odd = false;
   if (tid < HYQ_D) {
 #pragma unroll

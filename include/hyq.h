@@ -753,7 +753,8 @@ hyq_status hyq_paged_attention(const hyq_config *cfg, const hyq_pages *pages, in
  *   seqs, q, ldq, n_q  as for hyq_paged_attention
  *   k      1 .. HYQ_PAGED_MAX_BLOCKS, n_first + n_last <= k
  *   sel    device int32 [batch][n_q][HKV][k]: block numbers, ascending, then -1
- * A query that is not finite counts as zeros and sets HYQ_DEVERR_SCORE.
+ * A query that is not finite counts as zeros and sets HYQ_DEVERR_SCORE, where
+ * every block is taken too; that of a token that sees nothing is not looked at.
  * Workspace: HYQ_OP_PAGED_SELECT, zero-filled before first use.
  */
 hyq_status hyq_paged_select(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
