@@ -467,52 +467,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageBytes = kWarps * 2 * 4096;
 
-// grid (pages that the call may reach / (8 / hb), KV heads / hb, {K, V}), with
-// hb = 1, 2, 4 or 8 heads a block: a block takes 8 / hb pages that get rows, in
-// the order of the call's rows, a warp for each (page, head).  Keys and values
-// in blocks of their own: the warps of a block run the same code (5% faster).
+// One warp: rows r of a page, keys (T = 0) or values of KV head h.  stage: two tiles'
+// worth of shared memory.
 template <int BK, int BV>
-__global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendParams p, int hb) {
+__device__ __forceinline__ void append_page(const AppendParams& p, const PageRows& r, int h, int T, uint8_t* stage, int lane) {
   using F = QFmt<BK, BV>;
-  extern __shared__ __align__(16) uint8_t s_stage[];  // [kWarps][2][4096]
-  __shared__ int s_warp[kThreads / 32];
-  __shared__ PageRows s_rows[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  chain_kernel();
-  const int per = kWarps / hb, first = (int)blockIdx.x * per;
-  if (tid < kWarps) s_rows[tid].r0 = s_rows[tid].r1 = 0;  // no rows
-  // Pages before each of the call's rows, a row a thread (the loads of several rows
-  // in one thread would follow one another), 256 rows at a time.
-  int before = 0;
-  for (int row0 = 0; row0 < p.batch; row0 += kThreads) {
-    const int row = row0 + tid;
-    CallRows c;
-    int n = 0;
-    if (row < p.batch) {
-      c = call_rows(p, row);
-      if (c.bad && blockIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-      if (c.n > 0) n = (c.start + c.n - 1) / HYQ_PAGE_ROWS - c.start / HYQ_PAGE_ROWS + 1;
-    }
-    int pre = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
-    }
-    if (row0 > 0) __syncthreads();  // the sums of the 256 rows before have been read
-    if (lane == 31) s_warp[warp] = pre;
-    __syncthreads();
-    int at = before + pre - n;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) at += s_warp[i];
-      before += s_warp[i];
-    }
-    for (int j = max(at - first, 0); j < per && first + j - at < n; ++j) s_rows[j] = page_rows(p, c, first + j - at);
-  }
-  __syncthreads();
-  const int h = blockIdx.y * hb + warp % hb, T = blockIdx.z;
-  const PageRows r = s_rows[warp / hb];
-  if (r.r1 <= r.r0 || h >= p.HKV) return;
   const int page = *r.entry;  // not waited for before the first rows are on their way
   const int64_t ldh = (int64_t)p.HKV * HYQ_D;
   const __nv_bfloat16* src = (T == 0 ? p.k : p.v) + (int64_t)h * HYQ_D;
@@ -521,9 +480,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
   Bounds8 b;
   b.clear();
   bool bad = false;
-  // Two tiles' worth of shared memory a warp: the next tile's rows are on their
-  // way while one is worked on (11% faster).
-  uint8_t* stage = s_stage + 8192 * warp + 16 * lane;
+  // The next tile's rows are on their way while one is worked on (11% faster).
+  stage += 16 * lane;
   auto rows_of = [&](int tile) -> uint32_t {  // rows of the tile: bits of [r0, r1) in [16 tile, 16 tile + 16)
     const int a = max(r.r0 - 16 * tile, 0), z = min(r.r1 - 16 * tile, 16);
     return ((1u << z) - 1u) & ~((1u << a) - 1u);
@@ -562,6 +520,79 @@ __global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const AppendP
     }
     store_bounds(p.pv.bounds + ph * HYQ_BOUND_BYTES, lane, b, r.r0 == 0);
   }
+}
+
+// A block's pages: the `per` from page `first` on among those that the call's rows get, in
+// the order of the rows.  Returns how many there are in all.  A row a thread (the
+// loads of several rows in one thread would follow one another), 256 rows at a time.
+__device__ __forceinline__ int find_pages(const AppendParams& p, int first, int per, PageRows* s_rows, int* s_warp) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < kWarps) s_rows[tid].r0 = s_rows[tid].r1 = 0;  // no rows
+  int before = 0;
+  for (int row0 = 0; row0 < p.batch; row0 += kThreads) {
+    const int row = row0 + tid;
+    CallRows c;
+    int n = 0;
+    if (row < p.batch) {
+      c = call_rows(p, row);
+      if (c.bad && blockIdx.x == 0 && blockIdx.y == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+      if (c.n > 0) n = (c.start + c.n - 1) / HYQ_PAGE_ROWS - c.start / HYQ_PAGE_ROWS + 1;
+    }
+    int pre = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    if (row0 > 0) __syncthreads();  // the sums of the 256 rows before have been read
+    if (lane == 31) s_warp[warp] = pre;
+    __syncthreads();
+    int at = before + pre - n;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) at += s_warp[i];
+      before += s_warp[i];
+    }
+    for (int j = max(at - first, 0); j < per && first + j - at < n; ++j) s_rows[j] = page_rows(p, c, first + j - at);
+  }
+  __syncthreads();
+  return before;
+}
+
+// The blocks take turns: when some of the call's rows are bad, the others may
+// share rows and reach more pages than the grid was made for.  Out of line, so
+// that the ordinary call's code is as if this were not (prompts in 62.4 us;
+// 63.8 with the turns in a loop of the kernel).
+template <int BK, int BV>
+__device__ __noinline__ void append_in_turns(const AppendParams& p, int hb, uint8_t* s_stage, PageRows* s_rows,
+                                             int* s_warp) {
+  const int warp = threadIdx.x >> 5, per = kWarps / hb, h = blockIdx.y * hb + warp % hb;
+  for (int first = (int)blockIdx.x * per;; first += (int)gridDim.x * per) {
+    __syncthreads();  // the rows of the turn before have been read
+    const int pages = find_pages(p, first, per, s_rows, s_warp);
+    const PageRows r = s_rows[warp / hb];
+    if (r.r1 > r.r0 && h < p.HKV) append_page<BK, BV>(p, r, h, blockIdx.z, s_stage + 8192 * warp, threadIdx.x & 31);
+    if (first + (int)gridDim.x * per >= pages) break;
+  }
+}
+
+// grid (pages that the call may reach / (8 / hb), KV heads / hb, {K, V}), with
+// hb = 1, 2, 4 or 8 heads a block: a block takes 8 / hb pages that get rows, in
+// the order of the call's rows, a warp for each (page, head).  Keys and values
+// in blocks of their own: the warps of a block run the same code (5% faster).
+template <int BK, int BV>
+__global__ void __launch_bounds__(kThreads, 2) append_pages_kernel(const __grid_constant__ AppendParams p, int hb) {
+  extern __shared__ __align__(16) uint8_t s_stage[];  // [kWarps][2][4096]
+  __shared__ int s_warp[kThreads / 32];
+  __shared__ PageRows s_rows[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  chain_kernel();
+  const int per = kWarps / hb, first = (int)blockIdx.x * per;
+  const int pages = find_pages(p, first, per, s_rows, s_warp);
+  if (pages > (int)gridDim.x * per) return append_in_turns<BK, BV>(p, hb, s_stage, s_rows, s_warp);
+  const int h = blockIdx.y * hb + warp % hb, T = blockIdx.z;
+  const PageRows r = s_rows[warp / hb];
+  if (r.r1 <= r.r0 || h >= p.HKV) return;
+  append_page<BK, BV>(p, r, h, T, s_stage + 8192 * warp, lane);
 }
 
 // One row per sequence: a warp per (sequence, KV head), the key in its first

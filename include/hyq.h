@@ -708,7 +708,8 @@ hyq_status hyq_pages_compact(const hyq_config *cfg, const hyq_pages *pages, int3
  *            the rows as the cache now holds them, c s + z rounded to BF16
  * A sequence that is out of range, that has fewer than n_i positions, or whose
  * table leaves the pool is left out and sets HYQ_DEVERR_INDEX; a pair of
- * cu_rows that descends or leaves [0, n_rows] likewise.  Pages that other
+ * cu_rows that descends or leaves [0, n_rows] likewise; the other sequences
+ * are written (after such a pair two of them may take the same rows).  Pages that other
  * sequences share are written too: reserve first.  Other rows of the pages keep their bits.
  */
 hyq_status hyq_paged_append(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,

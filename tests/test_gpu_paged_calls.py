@@ -1,11 +1,14 @@
 """Calls on the paged cache that its documentation allows, beside those of
 test_gpu_paged.py."""
+import numpy as np
 import pytest
 import torch
 
-from hybrid_precision_quantized_gb300 import hyq_read_device_error
+from hybrid_precision_quantized_gb300 import hyq_read_device_error, unpack_qblocks
 from hybrid_precision_quantized_gb300 import _lib as L
-from tests.test_gpu_paged import grow, ints, make, queries
+from oracle.quant import quantize
+from tests.gpu_util import mixed_rows
+from tests.test_gpu_paged import check_bounds, check_rows, grow, ints, make, np64, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +31,31 @@ def test_choice_reports_queries_that_are_not_finite_whatever_k_is(hyq):
             assert torch.equal(sel[:, :, 0], want[:, :, 0])
             if k >= 10 or err == 0:
                 assert torch.equal(sel, want)
+
+
+def test_append_with_a_bad_pair_between_two_good_ones(hyq):
+    """A pair of cu_rows that descends is left out and reported; the others are written whole, though they share rows and
+    so reach more pages than as many distinct rows could."""
+    for HKV, n in ((2, 640), (8, 1000)):
+        cache = make(HKV, HKV, 64, 3, 20)
+        cache.reserve(ints([0, 1, 2]), ints([n, 0, n + 7]))
+        before = cache.pool().clone()
+        k, v = (mixed_rows(s, (HKV, n, 128)).transpose(0, 1).contiguous() for s in (1, 2))
+        kh, vh = (torch.full((n, HKV, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        cache.append(0, k.cuda(), v.cuda(), seqs=ints([0, 1, 2]), cu_rows=ints([0, n, 0, n]), k_hat=kh, v_hat=vh)
+        assert hyq_read_device_error(cache.err()) == L.DEVERR_INDEX
+        assert kh.isfinite().all() and vh.isfinite().all()
+        for h in range(HKV):
+            check_rows(cache, 0, h, np64(k[:, h]), np64(v[:, h]))
+            check_bounds(cache, 0, h, np64(k[:, h]))
+        # sequence 2 begins with seven rows that no call wrote
+        pages = cache.table()[2, : -(-(n + 7) // 64)].long()
+        for h in range(HKV):
+            kc, vc, ks, kz, vs, vz = unpack_qblocks(cache.pool()[0, pages, h].cpu().numpy(), n + 7, 4, 4)
+            for got, want in zip((kc, ks, kz, vc, vs, vz), (*quantize(np64(k[:, h]), 4), *quantize(np64(v[:, h]), 4))):
+                got = got[7:]
+                if want.dtype == np.float16:
+                    got, want = got.view(np.uint16), want.view(np.uint16)
+                assert np.array_equal(got, want)
+        untouched = [p for p in range(64) if p not in set(pages.tolist()) | set(cache.table()[0, : -(-n // 64)].tolist())]
+        assert torch.equal(cache.pool()[0, untouched], before[0, untouched])
