@@ -159,16 +159,22 @@ class PagedCache:
 
     def workspace(self, op: int, batch: int, n_q: int = 1, stream=None) -> torch.Tensor:
         """The zero-filled workspace of an operation for calls of batch * n_q tokens, kept and grown as needed.  One that
-        has been outgrown stays allocated: work queued earlier may still use it."""
+        has been outgrown stays allocated: work queued earlier, or a captured graph, may still use it.  A larger one takes
+        at least twice the tokens of the last, so that there are few of them however the calls grow."""
         w = self._ws.get(op)
-        if w is None or w[0] < batch * n_q:
+        tokens = batch * n_q
+        if w is None or w[0] < tokens:
             n = L.hyq_pages_workspace_size(self.cfg, self.c, op, max(batch, 1), n_q)
             if n == 0:
                 raise ValueError(f"no call of this kind takes {batch} sequences with {n_q} tokens")
+            if w is not None:       # the size depends on the product alone
+                b = min(max(tokens, 2 * w[0]), L.PAGED_MAX_BATCH)
+                q = min(-(-max(tokens, 2 * w[0]) // b), L.PAGED_MAX_Q)
+                n, tokens = L.hyq_pages_workspace_size(self.cfg, self.c, op, b, q), b * q
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 t = torch.zeros(n, dtype=torch.uint8, device=self.device)
             self._kept.append(t)
-            w = self._ws[op] = (batch * n_q, t)
+            w = self._ws[op] = (tokens, t)
         return w[1]
 
     # tables ------------------------------------------------------------------

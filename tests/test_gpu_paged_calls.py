@@ -59,3 +59,30 @@ def test_append_with_a_bad_pair_between_two_good_ones(hyq):
                 assert np.array_equal(got, want)
         untouched = [p for p in range(64) if p not in set(pages.tolist()) | set(cache.table()[0, : -(-n // 64)].tolist())]
         assert torch.equal(cache.pool()[0, untouched], before[0, untouched])
+
+
+def test_workspaces_stay_few_as_calls_grow(hyq):
+    """One sequence more each time: what is kept stays within a few times the largest call's need."""
+    n = 300
+    cache = make(2, 2, 320, n, 200)
+    grow(cache, list(range(n)), [5 + i % 50 for i in range(n)], 1)
+    q = queries(1, n, 1, 2)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    other = make(2, 2, 320, n, 200)
+    grow(other, list(range(n)), [5 + i % 50 for i in range(n)], 1)
+    other.attention(0, q, want)
+    sel = torch.empty(n, 1, 2, 3, dtype=torch.int32, device="cuda")
+    for b in range(1, n + 1):
+        cache.attention(0, q[:b], out[:b])
+        cache.select(0, q[:b], sel[:b])
+        assert torch.equal(out[:b], want[:b])
+    kept = sum(t.nbytes for t in cache._kept)
+    need = [L.hyq_pages_workspace_size(cache.cfg, cache.c, op, n) for op in (L.OP_PAGED_ATTENTION, L.OP_PAGED_SELECT)]
+    assert len(cache._kept) <= 1 + 2 * 10 and kept <= 10 * sum(need)     # 1, 2, 4 .. 512, and the reserve's
+    for b, n_q in ((1024, 1), (1024, 33), (700, 64), (1024, 64)):        # up to the largest call there is
+        assert cache.workspace(L.OP_PAGED_ATTENTION, b, n_q).nbytes >= \
+            L.hyq_pages_workspace_size(cache.cfg, cache.c, L.OP_PAGED_ATTENTION, b, n_q)
+    for b, n_q in ((1025, 64), (1024, 65)):
+        with pytest.raises(ValueError):
+            cache.workspace(L.OP_PAGED_ATTENTION, b, n_q)
+    assert hyq_read_device_error(cache.err()) == 0
