@@ -71,6 +71,7 @@ class PagedCache:
             self.buf[name] = t
             setattr(self.c, name, t.data_ptr())
         self._ws, self._kept = {}, []
+        self._streams = {}      # that calls were queued on, by handle
         self._lib, self._index = L.load(), dev.index
         self._cfg, self._pages = ctypes.byref(cfg), ctypes.byref(self.c)
 
@@ -101,7 +102,8 @@ class PagedCache:
     # current one) are tested first and cost well under a microsecond each.
     def _run(self, name, args, stream, *tensors):
         """Call the C entry point on the given stream, or the current one of the cache's device.  A given stream is noted on
-        the call's tensors: one that the caller drops is not reused before the call has read it."""
+        the call's tensors, and every stream once on the cache's own: memory that is dropped is not reused before the
+        call has read it."""
         fn = getattr(self._lib, name)
         if stream is None:
             raw = torch._C._cuda_getCurrentRawStream(self._index)
@@ -110,6 +112,10 @@ class PagedCache:
             for t in tensors:
                 if t is not None:
                     t.record_stream(stream)
+        if raw not in self._streams:
+            self._streams[raw] = stream = stream if stream is not None else torch.cuda.current_stream(self.device)
+            for t in (*self.buf.values(), *self._kept):
+                t.record_stream(stream)
         if torch.cuda.current_device() == self._index:
             st = fn(self._cfg, self._pages, *args, raw)
         else:
@@ -174,6 +180,8 @@ class PagedCache:
             with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(self.device)):
                 t = torch.zeros(n, dtype=torch.uint8, device=self.device)
             self._kept.append(t)
+            for s in self._streams.values():
+                t.record_stream(s)
             w = self._ws[op] = (tokens, t)
         return w[1]
 

@@ -86,3 +86,29 @@ def test_workspaces_stay_few_as_calls_grow(hyq):
         with pytest.raises(ValueError):
             cache.workspace(L.OP_PAGED_ATTENTION, b, n_q)
     assert hyq_read_device_error(cache.err()) == 0
+
+
+def test_a_cache_may_be_dropped_while_its_calls_are_queued(hyq):
+    """Its memory is not reused before they have run, whichever stream they are on and however it was named."""
+    for named in (True, False):
+        cache = make(4, 2, 40, 2, 32)
+        grow(cache, [0, 1], [1500, 700], 3)
+        q = queries(1, 2, 1, 4)
+        want, out = torch.empty_like(q), torch.zeros_like(q)
+        cache.attention(0, q, want)
+        sizes = [t.nbytes for t in (*cache.buf.values(), *cache._kept)]
+        side = torch.cuda.Stream()
+        big = torch.randn(4096, 4096, device="cuda")
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(30):
+                big = big @ big * 1e-3
+            if not named:
+                cache.attention(0, q, out)
+        if named:
+            cache.attention(0, q, out, stream=side)
+        del cache
+        junk = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del junk, big

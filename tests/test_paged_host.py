@@ -165,3 +165,26 @@ def test_paged_cache_takes_given_buffers(lib):
     table = torch.ones(3, 5, dtype=torch.int32)
     c = hyq.PagedCache(cfg(), 10, 3, 5, device="cpu", buffers={"table": table})
     assert c.table() is table and c.c.table == table.data_ptr()
+
+
+def test_paged_cache_notes_every_stream_on_its_own_memory(lib, monkeypatch):
+    """The pool, the tables and the workspaces are not reused, once the cache is dropped, before the streams that its calls
+    were queued on have read them."""
+    from types import SimpleNamespace
+    seen = set()
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: seen.add((t.data_ptr(), s.cuda_stream)))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: SimpleNamespace(cuda_stream=5))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 5, raising=False)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: __import__("contextlib").nullcontext())
+    c = hyq.PagedCache(cfg(), 10, 3, 5, device="cpu")
+    c._lib = SimpleNamespace(**{n: lambda *a: 0 for n in ("hyq_pages_reset", "hyq_pages_reserve", "hyq_paged_attention")})
+    q = torch.zeros(2, 1, 8, 128, dtype=torch.bfloat16)
+    side = SimpleNamespace(cuda_stream=7)
+    c.reset(stream=side)
+    assert {(t.data_ptr(), 7) for t in c.buf.values()} <= seen
+    c.reserve(stream=side)
+    c.attention(0, q, torch.empty_like(q))              # the current stream
+    c.attention(0, q, torch.empty_like(q), stream=side)
+    own = [t.data_ptr() for t in (*c.buf.values(), *c._kept)]
+    assert len(own) == 8 and {(p, s) for p in own for s in (5, 7)} <= seen
