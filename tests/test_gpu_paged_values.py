@@ -181,3 +181,33 @@ def test_values_of_any_size_within_a_bound_that_shrinks_with_them(hyq, bits, HQ,
     cache.attention(0, q, out)
     assert hyq_read_device_error(cache.err()) == 0
     print(f"bits {bits} n_q {n_q} error / bound: {check_bound(cache, hist, q, out, range(m)):.3f}")
+
+
+@pytest.mark.parametrize("bits,HQ,n_q", [((4, 4), 2, 1), ((8, 8), 2, 1), ((8, 4), 8, 4), ((4, 4), 8, 8)])
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** 118, 2.0 ** 121, 2.0 ** -100, 2.0 ** -130])
+def test_queries_of_any_size(hyq, bits, HQ, n_q, size):
+    """Up to where logits leave float32 (one row takes all, and it has to be the right one) and down to nothing (all rows
+    count alike)."""
+    n = 200
+    cache, hist = make(HQ, 1, 4, 1, 4, bits=bits), History(1, 1)
+    gen = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(n, 1, 128, generator=gen).to(torch.bfloat16) for _ in range(2))
+    grow(cache, [0], [n], 0, rows=(k, v))
+    hist.add([0], [n], k, v)
+    q = (torch.randn(1, n_q, HQ, 128, generator=gen).to(torch.bfloat16).double() * size).to(torch.bfloat16)
+    out = torch.full((1, n_q, HQ, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    cache.attention(0, q.cuda(), out)
+    kd, kp, _ = P.dequantised(hist.k[0][:, 0], bits[0])
+    vd, vp, _ = P.dequantised(hist.v[0][:, 0], bits[1])
+    for i in range(n_q):
+        vis = np.arange(n) < n - n_q + 1 + i
+        for h in range(HQ):
+            x = kd[vis] @ np64(q[0, i, h])
+            if size > 1:     # the next row is far below, for logits off by 2^-18 of their products' sizes
+                second, first = np.sort(x)[-2:]
+                assert first - second > 2.0 ** -14 * (kp[vis] @ np.abs(np64(q[0, i, h]))).max()
+                want, mean = vd[vis][x.argmax()], vp[vis][x.argmax()]
+            else:
+                want, mean = vd[vis].mean(0), vp[vis].mean(0)
+            assert (np.abs(np64(out[0, i, h]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mean).all(), (i, h)
+    assert hyq_read_device_error(cache.err()) == 0
