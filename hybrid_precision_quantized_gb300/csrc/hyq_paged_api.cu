@@ -105,7 +105,8 @@ extern "C" hyq_status hyq_pages_fork(const hyq_config* c, const hyq_pages* p, co
 
 extern "C" hyq_status hyq_pages_truncate(const hyq_config* c, const hyq_pages* p, const int32_t* seqs,
                                          const int32_t* new_lens, int32_t n, hyq_stream_t s) {
-  const hyq_status st = call_ok(c, p, 0, seqs, n);
+  // without a list nothing is looked for in it: all rows of any table
+  const hyq_status st = call_ok(c, p, 0, seqs, seqs || n < 0 ? n : 0);
   if (st != HYQ_OK) return st;
   if ((!seqs && n > p->n_seqs) || (new_lens && !aligned(new_lens, 4))) return HYQ_ERR_INVALID_ARG;
   if (n == 0) return HYQ_OK;

@@ -31,7 +31,7 @@ class PagedCache:
 
     cfg        : heads and code widths (make_config; batch and capacity are not used)
     n_pages    : pages of 64 positions, each for every layer
-    n_seqs     : rows of the table
+    n_seqs     : rows of the table (a call takes 1024 of them at most; more are given in several calls)
     max_blocks : pages a sequence may have
     buffers    : tensors to use instead of new ones, by name (pool, bounds, table, lens, refs, err), contiguous, of
                  the C layout's types and sizes; those not given are allocated (and, without any, reset)
@@ -191,7 +191,8 @@ class PagedCache:
         self._run("hyq_pages_reset", (), stream)
 
     def reserve(self, seqs=None, n_new=None, stream=None):
-        """Room for n_new[i] (default 1) more positions of sequence seqs[i] (default: sequence i)."""
+        """Room for n_new[i] (default 1) more positions of sequence seqs[i] (default: sequence i; all of them without
+        n_new, in a cache of up to 1024)."""
         n = self._ints(n_new, "n_new", self._ints(seqs, "seqs"))
         ws = self.workspace(L.OP_PAGES_RESERVE, 1, stream=stream)
         self._run("hyq_pages_reserve", (L.ptr(seqs), self.n_seqs if n is None else n, L.ptr(n_new), ws.data_ptr(),
@@ -203,7 +204,8 @@ class PagedCache:
         self._run("hyq_pages_fork", (src.data_ptr(), dst.data_ptr(), n), stream, src, dst)
 
     def truncate(self, seqs=None, new_lens=None, stream=None):
-        """Shorten the sequences to new_lens (default 0: free them)."""
+        """Shorten the sequences (default: sequence i; all of them without new_lens, however many) to new_lens (default 0:
+        free them)."""
         n = self._ints(new_lens, "new_lens", self._ints(seqs, "seqs"))
         self._run("hyq_pages_truncate", (L.ptr(seqs), L.ptr(new_lens), self.n_seqs if n is None else n), stream, seqs,
                   new_lens)

@@ -565,7 +565,7 @@ hyq_status hyq_decode_attention_noalloc(const hyq_config *cfg, const void *q, co
  * Only num_q_heads, num_kv_heads, head_dim, group, bits_k and bits_v of
  * hyq_config are used by these entry points (the config must pass
  * hyq_config_check); every call gives its own number of sequences, at most
- * HYQ_PAGED_MAX_BATCH.  The pool and the tables need no initial contents
+ * HYQ_PAGED_MAX_BATCH (hyq_pages_truncate without a list: all of the table's rows).  The pool and the tables need no initial contents
  * beyond hyq_pages_reset; whatever a page's unwritten rows hold, they do not
  * reach a result.
  *
@@ -671,7 +671,7 @@ hyq_status hyq_pages_fork(const hyq_config *cfg, const hyq_pages *pages, const i
  * reaches loses one of its refs.  A sequence number out of range or listed
  * before, or a new length that is negative or above the present one, is left
  * out and sets HYQ_DEVERR_INDEX.
- *   seqs      device int32 [n] or NULL (sequence i)
+ *   seqs      device int32 [n], n <= HYQ_PAGED_MAX_BATCH, or NULL (sequence i, n <= n_seqs)
  *   new_lens  device int32 [n] or NULL (0 each)
  */
 hyq_status hyq_pages_truncate(const hyq_config *cfg, const hyq_pages *pages, const int32_t *seqs,

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from hybrid_precision_quantized_gb300 import hyq_read_device_error, unpack_qblocks
+from hybrid_precision_quantized_gb300 import HyqError, hyq_read_device_error, unpack_qblocks
 from hybrid_precision_quantized_gb300 import _lib as L
 from oracle.quant import quantize
 from tests.gpu_util import mixed_rows
@@ -112,3 +112,23 @@ def test_a_cache_may_be_dropped_while_its_calls_are_queued(hyq):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
         del junk, big
+
+
+def test_tables_of_more_rows_than_a_call_takes(hyq):
+    """3000 sequences: reserved in parts, refused as a whole, shortened and freed as a whole."""
+    n = 3000
+    cache = make(2, 1, 2 * n, n, 2)
+    for at in range(0, n, 1000):
+        cache.reserve(ints(list(range(at, at + 1000))), ints([100] * 1000))
+    with pytest.raises(HyqError) as e:
+        cache.reserve()
+    assert e.value.status == 2
+    assert (cache.lens() == 100).all() and int(cache.refs().sum()) == 2 * n
+    lens = torch.arange(n, dtype=torch.int32, device="cuda") % 100
+    cache.truncate(None, lens)
+    assert torch.equal(cache.lens(), lens) and int(cache.refs().sum()) == int(((lens + 63) // 64).sum())
+    with pytest.raises(HyqError):
+        cache.truncate(ints(list(range(1025))))
+    cache.truncate()
+    assert not cache.lens().any() and not cache.refs().any()
+    assert hyq_read_device_error(cache.err()) == 0
