@@ -746,9 +746,10 @@ hyq_status hyq_paged_attention(const hyq_config *cfg, const hyq_pages *pages, in
  * the token's g queries, c = rint(q 2^-e'), e' the smallest integer >=
  * HYQ_BOUND_EXP_MIN with max |q| <= 127 2^e' over the g heads, block j scores
  *   S(j) = 2^e_j sum_heads sum_d max(c_d lo_jd, c_d hi_jd),
- * up to a factor an upper bound of the summed logits of any of its rows
- * (Algorithm 1's score, bounded per block).  The sum is an integer below 2^24,
- * so S is exact.  Of the nb = ceil(visible / 64) blocks that the token sees,
+ * up to a factor an upper bound of what any of the block's rows, as appended, sums up to
+ * with the codes (Algorithm 1's score, bounded per block; the BF16 query itself and
+ * the rows as the cache holds them differ from those by their roundings, and may
+ * pass it by as much).  The sum is an integer below 2^24, so S is exact.  Of the nb = ceil(visible / 64) blocks that the token sees,
  * the first n_first and the last n_last are taken, then those of largest S,
  * ties to the lower block, min(nb, k) in all.
  *   seqs, q, ldq, n_q  as for hyq_paged_attention
