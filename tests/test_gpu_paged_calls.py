@@ -132,3 +132,49 @@ def test_tables_of_more_rows_than_a_call_takes(hyq):
     cache.truncate()
     assert not cache.lens().any() and not cache.refs().any()
     assert hyq_read_device_error(cache.err()) == 0
+
+
+def test_the_plain_bindings_make_the_same_calls(hyq):
+    """A step through hyq_pages_* and hyq_paged_* on raw sizes gives what PagedCache gives."""
+    HQ, HKV, n, nb = 4, 2, 3, 6
+    caches = [make(HQ, HKV, 24, n + 1, nb) for _ in range(2)]
+    rows = [mixed_rows(s, (HKV, 300, 128)).transpose(0, 1).contiguous().cuda() for s in (1, 2)]
+    one = [mixed_rows(s, (HKV, 2, 128)).transpose(0, 1).contiguous().cuda() for s in (3, 4)]
+    q, seqs, cu, counts = queries(5, 2, 1, HQ), ints([0, 1]), ints([0, 200, 300]), ints([200, 100])
+    results = []
+    for plain, c in zip((False, True), caches):
+        hats = [torch.zeros_like(rows[0]) for _ in range(2)]
+        out, sparse = torch.zeros_like(q), torch.zeros_like(q)
+        sel = torch.zeros(2, 1, HKV, 2, dtype=torch.int32, device="cuda")
+        if plain:
+            cfg, p = c.cfg, c.c
+            ws = {op: torch.zeros(L.hyq_pages_workspace_size(cfg, p, op, 2), dtype=torch.uint8, device="cuda")
+                  for op in (L.OP_PAGED_ATTENTION, L.OP_PAGED_SELECT, L.OP_PAGES_RESERVE, L.OP_PAGES_COMPACT)}
+            ld = HKV * 128
+            L.hyq_pages_reset(cfg, p)
+            L.hyq_pages_reserve(cfg, p, seqs, 2, counts, ws[L.OP_PAGES_RESERVE])
+            L.hyq_paged_append(cfg, p, 0, seqs, 2, cu, 300, *rows, ld, *hats)
+            L.hyq_pages_fork(cfg, p, seqs, ints([2, 3]), 2)
+            L.hyq_pages_truncate(cfg, p, ints([0, 3]), ints([70, 0]), 2)
+            L.hyq_pages_reserve(cfg, p, ints([2, 0]), 2, None, ws[L.OP_PAGES_RESERVE])
+            L.hyq_paged_append(cfg, p, 0, ints([2, 0]), 2, None, 2, *one, ld)
+            L.hyq_pages_compact(cfg, p, None, None, ws[L.OP_PAGES_COMPACT])
+            L.hyq_paged_attention(cfg, p, 0, ints([2, 1]), 2, 1, q, HQ * 128, out, ws[L.OP_PAGED_ATTENTION])
+            L.hyq_paged_select(cfg, p, 0, ints([2, 1]), 2, 1, q, HQ * 128, 2, 1, 1, sel, ws[L.OP_PAGED_SELECT])
+            L.hyq_paged_attention_blocks(cfg, p, 0, ints([2, 1]), 2, 1, q, HQ * 128, sel, 2, sparse,
+                                         ws[L.OP_PAGED_ATTENTION])
+        else:
+            c.reserve(seqs, counts)
+            c.append(0, *rows, seqs=seqs, cu_rows=cu, k_hat=hats[0], v_hat=hats[1])
+            c.fork(seqs, ints([2, 3]))
+            c.truncate(ints([0, 3]), ints([70, 0]))
+            c.reserve(ints([2, 0]))
+            c.append(0, *one, seqs=ints([2, 0]))
+            c.compact()
+            c.attention(0, q, out, seqs=ints([2, 1]))
+            c.select(0, q, sel, seqs=ints([2, 1]))
+            c.attention_blocks(0, q, sel, sparse, seqs=ints([2, 1]))
+        assert hyq_read_device_error(c.err()) == 0
+        results.append([*hats, out, sel, sparse, c.lens(), c.refs(), c.pool(), c.bounds()])
+    assert results[0][5].tolist() == [71, 100, 201, 0] and results[0][2].any() and results[0][4].any()
+    assert all(torch.equal(a, b) for a, b in zip(*results))
