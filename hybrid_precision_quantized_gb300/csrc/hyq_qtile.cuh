@@ -251,7 +251,9 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
 // the row's maximum, so that p comes near 2^15.  It may lag: it moves (and the
 // accumulators are rescaled) only when some p would pass 2^top, top = 15, and then
 // to where that p is 2^(top - kSlack).  The first maximum of a row is seldom its
-// last, so without the slack short runs of tiles rescale at most of their tiles.
+// last, so without the slack short runs of tiles rescale at most of their tiles (4-bit
+// codes, 64 query rows a KV head, 32 sequences of up to 2000: 99 us with a slack of 2, 90
+// with 6; p is rounded to half a step of fp16 down to 2^-23 of the row's largest).
 // Each row's reference moves for its own logits alone: its result does not depend
 // on the rows that share its tile.  Sums and zero-point terms are of the same p.
 //
@@ -261,11 +263,10 @@ __device__ __forceinline__ void q_tile(const uint8_t* tb, int lane, int vr, cons
 // it.  Steps from 2 on (values that span 30, or 510 with 8-bit codes) lower top
 // instead: a step made smaller could leave fp16, beside others that are not large.
 // One lane scales each word of a tile's steps, in shared memory, before all read
-// them (one sequence of 1000 positions: 9.38 us without any of this, 9.55 with it,
+// them (one sequence of 1000 positions: 9.37 us without any of this, 9.57 with it,
 // 9.61 when each lane scaled the eight words that it read; drafts of 8-bit codes 65.5,
 // 66.8, 67.9).
-template <int BV>
-constexpr float kSlack = BV == 4 ? 2.f : 6.f;
+constexpr float kSlack = 6.f;
 
 // Of N query tiles and one warp, for the heads (2t, 2t+1) that a thread owns.
 template <int N>
@@ -321,7 +322,7 @@ __device__ __forceinline__ float raise_limit(uint32_t most, PageState<N>& st, fl
 
 // Query tile k's part of a raise: the reference of head 2t + j moves if one of its logits (tm: the
 // lane's largest, times inv = 2^-sigma) lies more than top above it, and by what top fell.
-template <int BV, int N>
+template <int N>
 __device__ __forceinline__ void raise_head(PageState<N>& st, int k, int j, float tm, float inv, float fell, float fc) {
   tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 4));
   tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 8));
@@ -329,7 +330,7 @@ __device__ __forceinline__ void raise_head(PageState<N>& st, int k, int j, float
   // inv is a power of two: the products are exact, and the sum rounded down keeps
   // the largest p within 2^(top - kSlack)
   const float old = st.nm[k][j], low = old - fell;
-  const float nm = fmaf(tm, inv, low) > st.top ? __fadd_rd(fmaxf(st.top - kSlack<BV>, 0.f), -tm * inv) : low;
+  const float nm = fmaf(tm, inv, low) > st.top ? __fadd_rd(fmaxf(st.top - kSlack, 0.f), -tm * inv) : low;
   const float corr = ex2(nm - old), ca = corr * fc;
   st.nm[k][j] = nm;
   st.l[k][j] *= corr;
@@ -429,7 +430,7 @@ __device__ __forceinline__ void q_tiles(uint8_t* tb0, int lane, const uint32_t (
       float tm = fmaxf(lg[0][j], lg[0][2 + j]);
 #pragma unroll
       for (int n = 1; n < NT; ++n) tm = fmaxf(tm, fmaxf(lg[n][j], lg[n][2 + j]));
-      raise_head<BV>(st, 0, j, tm, qc.inv[j], fell, fc);
+      raise_head(st, 0, j, tm, qc.inv[j], fell, fc);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         x[n][j] = fmaf(lg[n][j], qc.inv[j], st.nm[0][j]);
@@ -608,7 +609,7 @@ __device__ __forceinline__ void q_tile_pair(uint32_t tb, int lane, uint32_t quer
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float inv = __uint_as_float(j ? c.w : c.y);
-        raise_head<BV>(st, k, j, fmaxf(lg[k][j], lg[k][2 + j]), inv, fell, fc);
+        raise_head(st, k, j, fmaxf(lg[k][j], lg[k][2 + j]), inv, fell, fc);
         x[k][j] = fmaf(lg[k][j], inv, st.nm[k][j]);
         x[k][2 + j] = fmaf(lg[k][2 + j], inv, st.nm[k][j]);
       }

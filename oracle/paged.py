@@ -82,14 +82,14 @@ def attend_error(q, k, kparts, vparts, vcodes, vis, out):
     return 2.0 ** -8 * np.abs(out) + mean * (2.0 ** -10 + 2 * 2.0 ** -18 * size) + 2.0 ** -25 * total
 
 
-def attend_bound(q, k, kparts, vparts, vcodes, vsteps, vis, out, bits_v):
+def attend_bound(q, k, kparts, vparts, vcodes, vsteps, vis, out):
     """attend_error without a part that does not shrink with the values: the
     kernel keeps probabilities and their products with the value steps at the
     upper end of fp16.
 
     A row's largest probability is held as at least 2^lift, and every step s
     is taken times 2^F, F >= 0, where
-      lift = top - 2 (4-bit values) or top - 6 (8-bit), at least 0, with
+      lift = top - 6, at least 0, with
       top = 15, less 1 for each power of two that the largest step reaches from 1 on;
       2^-F <= 2 max s, or 2^-15 when that is smaller, and F = 0 from max s = 1/2 on.
     Below the normal range of fp16 half a step is 2^-25: of a probability
@@ -103,7 +103,7 @@ def attend_bound(q, k, kparts, vparts, vcodes, vsteps, vis, out, bits_v):
     size = ((kparts[vis] @ np.abs(q)) / math.sqrt(q.shape[-1])).max()
     most = float(np.asarray(vsteps, np.float64).max())
     top = 15 - (max(0, math.floor(math.log2(most)) + 1) if most > 0 else 0)
-    low = 2.0 ** (-25 - max(0, top - (2 if bits_v == 4 else 6)))
+    low = 2.0 ** (-25 - max(0, top - 6))
     f = min(1.0, max(2 * most, 2.0 ** -15))
     mean, parts, codes = (p @ vparts[vis]) / p.sum(), vparts[vis].sum(0) / p.sum(), vcodes[vis].sum(0) / p.sum()
     return 2.0 ** -8 * np.abs(out) + mean * (2.0 ** -10 + 2 * 2.0 ** -18 * size) + low * (parts + f * codes)

@@ -150,7 +150,7 @@ def check_bound(cache, hist, q, out, seqs):
                 vis = np.arange(n) < n - q.shape[1] + 1 + i
                 for r in range(h * g, h * g + g):
                     want = P.attend(qn[b, i, r], kd, vd, vis)
-                    tol = P.attend_bound(qn[b, i, r], kd, kp, vp, vc, vs, vis, want, bits[1])
+                    tol = P.attend_bound(qn[b, i, r], kd, kp, vp, vc, vs, vis, want)
                     err = np.abs(on[b, i, r] - want)
                     assert (err <= tol).all(), (b, i, r, float((err / np.maximum(tol, 1e-300)).max()))
                     worst = max(worst, float((err / np.maximum(tol, 1e-300)).max()))
