@@ -656,22 +656,25 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   }
 }
 
-// Query tiles that a group takes together: one, or full fours.  One by one, the
+// Query tiles that a group takes together: one, or four.  One by one, the
 // groups of one KV head lie side by side and meet most of each other's reads in
 // L2, and the group's start is shorter; four at a time the codes are unpacked half
-// as often.  64 / 8 heads, 4 / 8 / 12 tiles, one by one and by fours, us:
-//   8-bit codes, 8 sequences of up to 16001   88 / 166 / 211    66 / 112 / 159
-//                32 of up to 2000             57 / 103 / 148    53 /  90 / 125
-//                one of 32768                 38 /  61 /  90    37 /  56 /  75
-//   4-bit codes, 8 of up to 16001             72 / 129 / 185    69 / 118 / 167
-//                32 of up to 2000             55 /  98 / 141    56 /  94 / 129
-//                one of 32768                 36 /  57 /  83    38 /  58 /  78
-// so 4-bit codes take fours from eight tiles on.  (Six 8-bit tiles as two passes of
-// four: 111 against 113.  Two at a time, one warp to a ring: between the two.)
+// as often, and the last four may lack one.  64 / 8 heads, 4 / 6 / 7 / 8 / 11 / 12 tiles, us:
+//                                            one by one                      by fours
+//   8-bit codes, 8 sequences of up to 16001   88 / 112 / 128 / 165 / 194 / 215   68 / 116 / 116 / 115 / 164 / 164
+//                32 of up to 2000             59 /  82 /  94 / 105 / 140 / 152   54 /  90 /  91 /  91 / 127 / 127
+//                one of 32768                 39 /  53 /  57 /  64 /  83 /  94   37 /  58 /  57 /  58 /  77 /  77
+//   4-bit codes, 8 of up to 16001             70 /  98 / 112 / 126 / 170 / 186   67 / 118 / 119 / 118 / 168 / 168
+//                32 of up to 2000             53 /  74 /  85 /  95 / 127 / 137   53 /  89 /  90 /  90 / 125 / 125
+//                one of 32768                 35 /  47 /  50 /  56 /  73 /  82   37 /  57 /  57 /  57 /  77 /  77
+// so 8-bit codes take fours when at most one is lacking (three tiles: 64 against 67), and
+// 4-bit codes full ones, from eight tiles on.  (Two at a time, one warp to a ring:
+// between the two.)
 int group_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
   const int gq = c->num_q_heads / c->num_kv_heads, tiles = (n_q * gq + kRowsQ - 1) / kRowsQ;
+  const int lack = (kMaxNQ - tiles % kMaxNQ) % kMaxNQ;
   const bool wide = hyq_bits_k(c) + hyq_bits_v(c) > 8;
-  return !blocks && tiles % kMaxNQ == 0 && (wide || tiles > kMaxNQ) ? kMaxNQ : 1;
+  return !blocks && (wide ? lack <= 1 && tiles >= kMaxNQ : lack == 0 && tiles > kMaxNQ) ? kMaxNQ : 1;
 }
 
 template <int BK, int BV, int NQ>

@@ -142,6 +142,9 @@ def check_bound(cache, hist, q, out, seqs):
     assert np.isfinite(on).all()
     for b, s in enumerate(seqs):
         n = len(hist.k[s])
+        if n == 0:
+            assert not on[b].any()
+            continue
         for h in range(hkv):
             kd, kp, _ = P.dequantised(hist.k[s][:, h], bits[0])
             vd, vp, vc = P.dequantised(hist.v[s][:, h], bits[1])
@@ -149,6 +152,9 @@ def check_bound(cache, hist, q, out, seqs):
             for i in range(q.shape[1]):
                 vis = np.arange(n) < n - q.shape[1] + 1 + i
                 for r in range(h * g, h * g + g):
+                    if not vis.any():
+                        assert not on[b, i, r].any()
+                        continue
                     want = P.attend(qn[b, i, r], kd, vd, vis)
                     tol = P.attend_bound(qn[b, i, r], kd, kp, vp, vc, vs, vis, want)
                     err = np.abs(on[b, i, r] - want)
@@ -211,3 +217,22 @@ def test_queries_of_any_size(hyq, bits, HQ, n_q, size):
                 want, mean = vd[vis].mean(0), vp[vis].mean(0)
             assert (np.abs(np64(out[0, i, h]) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * mean).all(), (i, h)
     assert hyq_read_device_error(cache.err()) == 0
+
+
+@pytest.mark.parametrize("HQ,HKV,bits,n_q", [(8, 1, (8, 8), 7), (7, 1, (8, 4), 8), (16, 2, (4, 8), 11), (5, 1, (8, 8), 11),
+                                             (8, 1, (8, 8), 3), (8, 1, (8, 8), 6), (8, 1, (4, 4), 7), (3, 1, (4, 8), 64)])
+def test_query_rows_that_end_early_in_a_four_of_tiles(hyq, HQ, HKV, bits, n_q):
+    """Three, six, seven and eleven tiles of query rows, the last of them filled or not, over ragged lengths and a long one."""
+    lens = [0, 1, 3, n_q - 1, n_q, 63, 65, 300, 9000]
+    m = len(lens)
+    cache, hist = make(HQ, HKV, 170, m, 150, bits=bits), History(m, HKV)
+    k, v, _, _ = grow(cache, list(range(m)), lens, HQ + n_q)
+    hist.add(range(m), lens, k, v)
+    q = queries(HQ, m, n_q, HQ)
+    outs = []
+    for _ in range(2):
+        out = torch.full_like(q, float("nan"))
+        cache.attention(0, q, out)
+        outs.append(out)
+    assert torch.equal(*outs) and hyq_read_device_error(cache.err()) == 0
+    check_bound(cache, hist, q, outs[0], range(m))
