@@ -18,7 +18,7 @@
 //
 // What bounds it: instruction issue (81 per row and tensor at 16 warps an SM) and
 // the last round of blocks; prompts of 30 thousand rows of 8 KV heads with the rows
-// read back take 62 us, 0.77 of the copy rate.  A block lives about 15 us, so
+// read back take 62 us, 0.76 of the copy rate.  A block lives about 15 us, so
 // its start counts: a call row a thread and the page's number asked for
 // after the first rows took 5 us off.  Slower than blocks of eight warps with a page
 // each: 24 warps an SM with the rows read twice from shared memory (+6 us), blocks of
