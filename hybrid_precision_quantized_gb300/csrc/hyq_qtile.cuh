@@ -708,7 +708,7 @@ __device__ __forceinline__ void prep_query_row(int r, int lane, uint2 v, uint32_
     bz_s[r][lane] = lane < 2 ? pack_f16x2(h0, h1) : pack_f16x2(y0 - h0, y1 - h1);
   }
   if (lane == 0) {
-    const float k0 = kScale * pow2i(24 - qe + sg);  // (each alone can leave float32)
+    const float k0 = kScale * 4096.f * (pow2i(12 - qe) * pow2i(sg));  // 2^(24 - qe) alone can leave float32
     rowc_s[r][0] = k0;
     rowc_s[r][1] = BK == 4 ? k0 * 0.0625f : k0;  // 4-bit tokens g+8 carry 16 c
     rowc_s[r][2] = pow2i(-sg);
