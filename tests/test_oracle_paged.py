@@ -66,3 +66,20 @@ def test_tables_by_hand():
     assert t.reserve([3], [57]) is None and t.reserve([2], [129]) is None     # past its table row; no pages left
     t.truncate([3], [0])
     assert t.compact() == [(6, 2)] and t.pages[:2] == [[0, 2], [0, 1]]
+
+
+def test_the_attention_bound_shrinks_with_the_values():
+    """Values times a power of two have the same codes while their steps (here from 0.003 on) stay normal in fp16, above
+    2^-14, and a bound times that power; the older bound keeps an absolute part."""
+    k, v, q, vis = rows(7, 50), rows(8, 50, 0.3), rows(9, 1, 2.0)[0], np.arange(50) < 43
+    found = []
+    for f in (1.0, 2.0 ** -4):
+        kd, kp, _ = P.dequantised(k, 4)
+        vd, vp, vc = P.dequantised(v * f, 8)
+        want = P.attend(q, kd, vd, vis)
+        found.append((want, P.attend_bound(q, kd, kp, vp, vc, P.quantize(v * f, 8)[1], vis, want),
+                      P.attend_error(q, kd, kp, vp, vc, vis, want)))
+    (w0, b0, e0), (w1, b1, e1) = found
+    assert np.array_equal(w0 * 2.0 ** -4, w1) and np.allclose(b0 * 2.0 ** -4, b1, rtol=1e-12)
+    assert (b0 <= e0).all() and (e1 > e0 * 2.0 ** -4).all()
+    assert not P.attend_bound(q, kd, kp, vp, vc, P.quantize(v, 8)[1], vis & False, 0 * want).any()
