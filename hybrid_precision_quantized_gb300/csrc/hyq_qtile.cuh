@@ -798,8 +798,8 @@ __device__ __forceinline__ void store_warp_partial(PageState<N>& st, int k, int 
   float m[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) m[j] = st.nm[k][j] == kNoMax ? -INFINITY : -st.nm[k][j];
-  store_partial<BV>(st.acc[k], st.zd[k], st.l[k], m[0], m[1], HYQ_F16_SUB_SCALE * scale_ratio(kLimitF0, st.lim & 0xFFFFu), g, t, wpart, red_m,
-                    red_l);
+  const float unit = HYQ_F16_SUB_SCALE * scale_ratio(kLimitF0, st.lim & 0xFFFFu);
+  store_partial<BV>(st.acc[k], st.zd[k], st.l[k], m[0], m[1], unit, g, t, wpart, red_m, red_l);
 }
 
 }  // namespace

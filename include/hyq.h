@@ -565,7 +565,8 @@ hyq_status hyq_decode_attention_noalloc(const hyq_config *cfg, const void *q, co
  * Only num_q_heads, num_kv_heads, head_dim, group, bits_k and bits_v of
  * hyq_config are used by these entry points (the config must pass
  * hyq_config_check); every call gives its own number of sequences, at most
- * HYQ_PAGED_MAX_BATCH (hyq_pages_truncate without a list: all of the table's rows).  The pool and the tables need no initial contents
+ * HYQ_PAGED_MAX_BATCH (hyq_pages_truncate without a list: all of the table's
+ * rows).  The pool and the tables need no initial contents
  * beyond hyq_pages_reset; whatever a page's unwritten rows hold, they do not
  * reach a result.
  *
@@ -749,7 +750,8 @@ hyq_status hyq_paged_attention(const hyq_config *cfg, const hyq_pages *pages, in
  * up to a factor an upper bound of what any of the block's rows, as appended, sums up to
  * with the codes (Algorithm 1's score, bounded per block; the BF16 query itself and
  * the rows as the cache holds them differ from those by their roundings, and may
- * pass it by as much).  The sum is an integer below 2^24, so S is exact.  Of the nb = ceil(visible / 64) blocks that the token sees,
+ * pass it by as much).  The sum is an integer below 2^24, so S is exact.  Of the
+ * nb = ceil(visible / 64) blocks that the token sees,
  * the first n_first and the last n_last are taken, then those of largest S,
  * ties to the lower block, min(nb, k) in all.
  *   seqs, q, ldq, n_q  as for hyq_paged_attention
