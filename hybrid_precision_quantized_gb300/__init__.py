@@ -14,6 +14,8 @@ from ._lib import (HyqConfig, HyqError, HyqLayout, HyqPages, load, lib_path, hyq
                    hyq_select_vertical_heads, hyq_select_vertical_mass, hyq_set_decode_plan, hyq_set_decode_overlap,
                    hyq_status_string, hyq_vl_count, hyq_workspace_size,
                    hyq_paged_append, hyq_paged_attention, hyq_paged_attention_blocks, hyq_paged_select,
+                   hyq_paged_attention_lse, hyq_paged_attention_shared, hyq_paged_cross_attention,
+                   hyq_paged_accumulate, hyq_pages_evict,
                    hyq_pages_compact, hyq_pages_fork, hyq_pages_reserve, hyq_pages_reset, hyq_pages_sizes,
                    hyq_pages_truncate, hyq_pages_workspace_size)
 from .cache import (HybridDecoder, HybridLayer, make_config, pack_qblocks, unpack_qblocks,

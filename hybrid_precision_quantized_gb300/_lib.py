@@ -51,6 +51,7 @@ BOUND_EXP_MIN = -40
 PAGED_MAX_BATCH, PAGED_MAX_Q = 1024, 64
 PAGES_FIELDS = ("pool", "bounds", "table", "lens", "refs", "err")
 OP_PAGED_ATTENTION, OP_PAGED_SELECT, OP_PAGES_RESERVE, OP_PAGES_COMPACT = 16, 17, 18, 19
+OP_PAGED_SHARED, OP_PAGED_CROSS, OP_PAGES_EVICT = 20, 21, 22
 
 # Every symbol include/hyq.h declares.
 SYMBOLS = ("hyq_status_string", "hyq_config_check", "hyq_vl_count", "hyq_layout_sizes",
@@ -62,7 +63,9 @@ SYMBOLS = ("hyq_status_string", "hyq_config_check", "hyq_vl_count", "hyq_layout_
            "hyq_prefill_attention_band", "hyq_select_vertical_heads", "hyq_pages_sizes",
            "hyq_pages_workspace_size", "hyq_pages_reset", "hyq_pages_reserve", "hyq_pages_fork",
            "hyq_pages_truncate", "hyq_pages_compact", "hyq_paged_append", "hyq_paged_attention",
-           "hyq_paged_select", "hyq_paged_attention_blocks")
+           "hyq_paged_select", "hyq_paged_attention_blocks", "hyq_paged_attention_lse",
+           "hyq_paged_attention_shared", "hyq_paged_cross_attention", "hyq_paged_accumulate",
+           "hyq_pages_evict")
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
 
@@ -157,6 +160,11 @@ def load() -> ctypes.CDLL:
         "hyq_paged_attention": (i32, [C, G, i32, vp, i32, i32, vp, i64, vp, vp, c_size_t, vp]),
         "hyq_paged_select": (i32, [C, G, i32, vp, i32, i32, vp, i64, i32, i32, i32, vp, vp, c_size_t, vp]),
         "hyq_paged_attention_blocks": (i32, [C, G, i32, vp, i32, i32, vp, i64, vp, i32, vp, vp, c_size_t, vp]),
+        "hyq_paged_attention_lse": (i32, [C, G, i32, vp, i32, i32, vp, i64, vp, vp, vp, c_size_t, vp]),
+        "hyq_paged_attention_shared": (i32, [C, G, i32, vp, i32, i32, vp, vp, i32, vp, i64, vp, vp, c_size_t, vp]),
+        "hyq_paged_cross_attention": (i32, [C, G, i32, vp, i32, vp, i32, vp, i64, vp, vp, c_size_t, vp]),
+        "hyq_paged_accumulate": (i32, [C, G, i32, vp, i32, i32, vp, i64, vp, vp, vp, vp]),
+        "hyq_pages_evict": (i32, [C, G, vp, i32, vp, i32, i32, vp, vp, c_size_t, vp]),
     })
     for name in SYMBOLS:
         fn = getattr(lib, name)
@@ -427,3 +435,37 @@ def hyq_paged_attention_blocks(cfg, pages: HyqPages, layer: int, seqs, batch: in
     _check("hyq_paged_attention_blocks", load().hyq_paged_attention_blocks(
         ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(q), ldq, ptr(sel), k, ptr(out),
         ptr(ws), ws.nbytes, stream_ptr(stream)))
+
+
+def hyq_paged_attention_lse(cfg, pages: HyqPages, layer: int, seqs, batch: int, n_q: int, q, ldq: int, out, lse, ws,
+                            stream=None):
+    _check("hyq_paged_attention_lse", load().hyq_paged_attention_lse(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(q), ldq, ptr(out), ptr(lse),
+        ptr(ws), ws.nbytes, stream_ptr(stream)))
+
+
+def hyq_paged_attention_shared(cfg, pages: HyqPages, layer: int, seqs, batch: int, n_q: int, cu_groups, n_shared,
+                               n_groups: int, q, ldq: int, out, ws, stream=None):
+    _check("hyq_paged_attention_shared", load().hyq_paged_attention_shared(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(cu_groups), ptr(n_shared), n_groups,
+        ptr(q), ldq, ptr(out), ptr(ws), ws.nbytes, stream_ptr(stream)))
+
+
+def hyq_paged_cross_attention(cfg, pages: HyqPages, layer: int, seqs, batch: int, cu_q, n_tokens: int, q, ldq: int,
+                              out, ws, stream=None):
+    _check("hyq_paged_cross_attention", load().hyq_paged_cross_attention(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, ptr(cu_q), n_tokens, ptr(q), ldq, ptr(out),
+        ptr(ws), ws.nbytes, stream_ptr(stream)))
+
+
+def hyq_paged_accumulate(cfg, pages: HyqPages, layer: int, seqs, batch: int, n_q: int, q, ldq: int, lse, n_new, mass,
+                         stream=None):
+    _check("hyq_paged_accumulate", load().hyq_paged_accumulate(
+        ctypes.byref(cfg), ctypes.byref(pages), layer, ptr(seqs), batch, n_q, ptr(q), ldq, ptr(lse), ptr(n_new),
+        ptr(mass), stream_ptr(stream)))
+
+
+def hyq_pages_evict(cfg, pages: HyqPages, seqs, batch: int, keep, n_first: int, n_last: int, mass, ws, stream=None):
+    _check("hyq_pages_evict", load().hyq_pages_evict(
+        ctypes.byref(cfg), ctypes.byref(pages), ptr(seqs), batch, ptr(keep), n_first, n_last, ptr(mass), ptr(ws),
+        ws.nbytes, stream_ptr(stream)))

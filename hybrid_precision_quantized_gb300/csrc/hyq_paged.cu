@@ -33,7 +33,7 @@ namespace {
 constexpr int kWarps = 8;              // warps that share out a group's units, each with a ring of its own
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowsQ = HYQ_MAX_GQA;    // query rows per tile (MMA N)
-constexpr int kPart = HYQ_D + 4;       // acc[128], m, l and two unused floats per query row
+constexpr int kPart = kPartFloats;
 constexpr int kMinUnits = 8;           // units per block before a group is split further
 constexpr int kMaxNQ = 4;             // query tiles that one block takes together
 
@@ -64,6 +64,12 @@ struct Ring : QFmt<BK, BV> {
   static_assert(kWarps % kPerPage == 0, "a warp's units take the same part of their pages");
 };
 
+// What a call leaves behind for a query row: its output; that and the logarithm of
+// its softmax sum (hyq_paged_attention_lse); or, over the positions behind what
+// its group shares, its accumulator, maximum and sum, which are joined with the
+// shared positions' later (hyq_paged_attention_shared).
+enum { kOut, kOutLse, kRest };
+
 struct Params {
   PageView pv;
   const int32_t* seqs;
@@ -75,6 +81,9 @@ struct Params {
   int32_t* tickets;    // [groups]
   int32_t batch, n_q, HQ, HKV, gq, k_sel;
   int32_t QT;          // groups per (sequence, KV head)
+  float* lse;          // kOutLse: [batch][n_q][HQ]
+  SharedRows shared;   // kRest
+  float* rest;         // kRest: [batch][n_q][HQ][kPart]
 };
 
 // Length of call row b, 0 for a sequence out of range.
@@ -166,6 +175,14 @@ __device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, in
   return out + ((size_t)tok * HQ + (flat - tok * gq)) * HYQ_D;
 }
 
+// The same row of an array with n floats a row.
+__device__ __forceinline__ float* extra_row(float* extra, int HQ, int gq, int flat, int n) {
+  const int tok = flat / gq;
+  return extra + ((size_t)tok * HQ + (flat - tok * gq)) * n;
+}
+// ln(2^M L): of nothing minus infinity.
+__device__ __forceinline__ float log_sum(float M, float L) { return (M + log2f(L)) * 0.6931471805599453f; }
+
 // One block: joins the n partials of a group's n_rows rows, eight rows per 256 threads.  Part i lies at
 // parts + i stride, the first one `first` further.  A thread takes four elements
 // of a row over every S-th part, kHold parts at a time, with an online softmax
@@ -173,9 +190,9 @@ __device__ __forceinline__ __nv_bfloat16* out_row(__nv_bfloat16* out, int HQ, in
 // one round of loads and nothing to wait for between them).  Out of line and
 // short: the code runs once a launch, cold, and its instructions are fetched
 // while the call waits (unrolled further it was slower).
-template <int kHalves>
+template <int kHalves, int kLeave>
 __device__ __noinline__ void join_parts(const float* parts, int first, int stride, int n, int n_rows, uint8_t* smem,
-                                        __nv_bfloat16* out, int HQ, int gq, int flat0) {
+                                        __nv_bfloat16* out, int HQ, int gq, int flat0, float* extra) {
   const int half = kHalves > 1 ? threadIdx.x / kThreads : 0, tid = threadIdx.x - kThreads * half;
   smem += half * kThreads * (sizeof(float4) + sizeof(float2));
   float4* sums = reinterpret_cast<float4*>(smem);                                // [kThreads]
@@ -229,6 +246,13 @@ __device__ __noinline__ void join_parts(const float* parts, int first, int strid
         L = fmaf(ml.y, w, L);
         a.x = fmaf(w, x.x, a.x), a.y = fmaf(w, x.y, a.y), a.z = fmaf(w, x.z, a.z), a.w = fmaf(w, x.w, a.w);
       }
+      if (kLeave == kRest) {
+        float* e = extra_row(extra, HQ, gq, flat0 + r, kPart);
+        *reinterpret_cast<float4*>(e + d) = a;
+        if (d == 0) *reinterpret_cast<float2*>(e + HYQ_D) = make_float2(top, L);
+        continue;
+      }
+      if (kLeave == kOutLse && d == 0) *extra_row(extra, HQ, gq, flat0 + r, 1) = log_sum(top, L);
       const float inv = L > 0.f ? 1.f / L : 0.f;
       *reinterpret_cast<uint2*>(out_row(out, HQ, gq, flat0 + r) + d) =
           make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
@@ -237,7 +261,7 @@ __device__ __noinline__ void join_parts(const float* parts, int first, int strid
   __syncthreads();
 }
 
-template <int BK, int BV, int NQ>
+template <int BK, int BV, int NQ, int kLeave>
 __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, NQ>::kPerSm)
     paged_kernel(const Params p) {
   using R = Ring<BK, BV, NQ>;
@@ -246,6 +270,8 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];  // units per (KV head, query tile) of the rows before b
   __shared__ int s_len[HYQ_PAGED_MAX_BATCH], s_seq[HYQ_PAGED_MAX_BATCH];
+  __shared__ int s_skip[kLeave == kRest ? HYQ_PAGED_MAX_BATCH : 1];  // pages that are left to the group
+  __shared__ float s_top[kLeave == kOut ? 1 : kRowsG];
   __shared__ int64_t s_warp[kWarps * kHalves];
   using Fragments = uint32_t[4][kRowsQ][4][4];
   __shared__ __align__(16) uint8_t query_s[NQ][R::kQuery];  // each begins with Fragments
@@ -298,7 +324,17 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       int64_t w = 0;
       if (b < p.batch) {
         int seq;
-        const int len = row_len(p, b, &seq);
+        int len = row_len(p, b, &seq);
+        if (kLeave == kRest) {
+          const int skip = shared_len(p.shared, p.pv, p.seqs, b, p.batch, p.n_q);
+          s_skip[b] = skip / HYQ_PAGE_ROWS;
+          if (skip == 0 && seq >= 0 && blockIdx.x == 0 && p.shared.n) {  // a row that cannot share what it should
+            const int i = group_of(p.shared, b);
+            if (p.shared.cu[i] <= b && b < p.shared.cu[i + 1] && p.shared.len[i] != 0)
+              hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+          }
+          len -= skip;
+        }
         s_len[b] = len;
         s_seq[b] = seq;
         if (seq < 0 && blockIdx.x == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
@@ -328,7 +364,16 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
     if (s_cum[b] == s_cum[b + 1]) {
       uint4* o = reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * p.HQ * HYQ_D);
-      for (int k = tid; k < p.n_q * p.HQ * (HYQ_D / 8); k += R::kBlockThreads) o[k] = make_uint4(0, 0, 0, 0);
+      if (kLeave != kRest)
+        for (int k = tid; k < p.n_q * p.HQ * (HYQ_D / 8); k += R::kBlockThreads) o[k] = make_uint4(0, 0, 0, 0);
+      if (kLeave == kOutLse)
+        for (int k = tid; k < p.n_q * p.HQ; k += R::kBlockThreads) p.lse[(size_t)b * p.n_q * p.HQ + k] = -INFINITY;
+      if (kLeave == kRest)
+        for (int k = tid; k < p.n_q * p.HQ; k += R::kBlockThreads) {
+          float* e = p.rest + ((size_t)b * p.n_q * p.HQ + k) * kPart;
+          for (int d = 0; d < HYQ_D; ++d) e[d] = 0.f;
+          e[HYQ_D] = -INFINITY, e[HYQ_D + 1] = 0.f;
+        }
     }
   // ---- this block's run -------------------------------------------------------
   // No more blocks than give each kMinUnits.  With few groups every group gets
@@ -379,7 +424,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
         seg.n_units = W - R::kCost;
         seg.n_rows = p.sel ? p.gq : min(kRowsG, p.n_q * p.gq - kRowsG * qt);
         seg.flat0 = p.sel ? qt * p.gq : qt * kRowsG;  // with block lists a group is one token's heads
-        seg.table = p.pv.table + (size_t)s_seq[lo] * p.pv.max_blocks;
+        seg.table = p.pv.table + (size_t)s_seq[lo] * p.pv.max_blocks + (kLeave == kRest ? s_skip[lo] : 0);
         seg.sel = p.sel ? p.sel + (((size_t)lo * p.n_q + qt) * p.HKV + h) * p.k_sel : nullptr;
         seg.out = p.out + ((size_t)lo * p.n_q * p.HQ + (size_t)h * p.gq) * HYQ_D;
         seg.base = s_cum[lo] * unit + (int64_t)grp * W + R::kCost;
@@ -580,6 +625,8 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
     const int n_rows = seg.n_rows;
     const bool whole = seg.w0 == 0 && seg.w1 == seg.n_units;
     float* pp = p.part + ((size_t)blockIdx.x * 2 + (seg.w0 == 0 ? 1 : 0)) * (NQ * kRowsQ * kPart);
+    float* extra = kLeave == kOut ? nullptr : (kLeave == kRest ? p.rest : p.lse) +
+                   ((size_t)seg.b * p.n_q * p.HQ + (size_t)seg.h * p.gq) * (kLeave == kRest ? kPart : 1);
     if (kHalves > 1) __syncthreads();  // both halves are done with the rings
 #pragma unroll
     for (int k = 0; k < kNW; ++k)
@@ -600,6 +647,7 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       s_wt[r][w] = wt;
       if (w == 0) {
         s_sum[r] = L;
+        if (kLeave != kOut) s_top[r] = M;
         if (!whole && r < n_rows) {
           pp[r * kPart + HYQ_D] = M;
           pp[r * kPart + HYQ_D + 1] = L;
@@ -620,7 +668,12 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
       }
       if (x & 1) a = make_float4(a.y, a.x, a.w, a.z);
       if (x & 2) a = make_float4(a.z, a.w, a.x, a.y);
-      if (whole) {
+      if (whole && kLeave == kRest) {
+        float* e = extra_row(extra, p.HQ, p.gq, seg.flat0 + r, kPart);
+        *reinterpret_cast<float4*>(e + d) = a;
+        if (d == 0) *reinterpret_cast<float2*>(e + HYQ_D) = make_float2(s_top[r], s_sum[r]);
+      } else if (whole) {
+        if (kLeave == kOutLse && d == 0) *extra_row(extra, p.HQ, p.gq, seg.flat0 + r, 1) = log_sum(s_top[r], s_sum[r]);
         const float L = s_sum[r], inv = L > 0.f ? 1.f / L : 0.f;
         *reinterpret_cast<uint2*>(out_row(seg.out, p.HQ, p.gq, seg.flat0 + r) + d) =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
@@ -646,8 +699,8 @@ __global__ void __launch_bounds__(Ring<BK, BV, NQ>::kBlockThreads, Ring<BK, BV, 
         // group; the first block, whose run holds the group's first unit, has it
         // in slot 1
         constexpr int kSlot = NQ * kRowsQ * kPart;
-        join_parts<kHalves>(p.part + (size_t)c0 * 2 * kSlot, kSlot, 2 * kSlot, c1 - c0 + 1, n_rows,
-                            smem, seg.out, p.HQ, p.gq, seg.flat0);
+        join_parts<kHalves, kLeave>(p.part + (size_t)c0 * 2 * kSlot, kSlot, 2 * kSlot, c1 - c0 + 1, n_rows,
+                                    smem, seg.out, p.HQ, p.gq, seg.flat0, extra);
       }
     }
     __syncthreads();  // the segment is done with
@@ -677,21 +730,24 @@ int group_tiles(const hyq_config* c, int32_t n_q, bool blocks) {
   return !blocks && (wide ? lack <= 1 && tiles >= kMaxNQ : lack == 0 && tiles > kMaxNQ) ? kMaxNQ : 1;
 }
 
-template <int BK, int BV, int NQ>
+template <int BK, int BV, int NQ, int kLeave>
 cudaError_t launch(const Params& p, cudaStream_t s) {
   using R = Ring<BK, BV, NQ>;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = hyq_once_per_device(done, [] {
-    return cudaFuncSetAttribute(paged_kernel<BK, BV, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmemBytes);
+    return cudaFuncSetAttribute(paged_kernel<BK, BV, NQ, kLeave>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                R::kSmemBytes);
   });
   if (e != cudaSuccess) return e;
   const int grid = R::kPerSm * hyq_num_sms();
-  return hyq_launch_chained(paged_kernel<BK, BV, NQ>, dim3(grid), R::kBlockThreads, R::kSmemBytes, s, p);
+  return hyq_launch_chained(paged_kernel<BK, BV, NQ, kLeave>, dim3(grid), R::kBlockThreads, R::kSmemBytes, s, p);
 }
 
 template <int BK, int BV>
 cudaError_t launch_nq(const Params& p, int nq, cudaStream_t s) {
-  return nq == kMaxNQ ? launch<BK, BV, kMaxNQ>(p, s) : launch<BK, BV, 1>(p, s);
+  if (p.rest) return nq == kMaxNQ ? launch<BK, BV, kMaxNQ, kRest>(p, s) : launch<BK, BV, 1, kRest>(p, s);
+  if (p.lse) return nq == kMaxNQ ? launch<BK, BV, kMaxNQ, kOutLse>(p, s) : launch<BK, BV, 1, kOutLse>(p, s);
+  return nq == kMaxNQ ? launch<BK, BV, kMaxNQ, kOut>(p, s) : launch<BK, BV, 1, kOut>(p, s);
 }
 
 // Partials of the largest grid: two slots of kMaxNQ query tiles on each SM
@@ -710,7 +766,8 @@ size_t hyq_paged_attention_ws_bytes(const hyq_config* c, int32_t batch, int32_t 
 
 cudaError_t hyq_launch_paged_attention(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
                                        int32_t n_q, const void* q, int64_t ldq, const int32_t* sel, int32_t k_sel,
-                                       void* out, void* ws, cudaStream_t s) {
+                                       void* out, float* lse, const SharedRows* shared, float* rest, void* ws,
+                                       cudaStream_t s) {
   const int nq = group_tiles(c, n_q, sel != nullptr);
   Params p;
   p.pv = pv;
@@ -728,6 +785,9 @@ cudaError_t hyq_launch_paged_attention(const hyq_config* c, const PageView& pv, 
   p.gq = c->num_q_heads / c->num_kv_heads;
   p.QT = sel ? n_q : (n_q * p.gq + nq * kRowsQ - 1) / (nq * kRowsQ);
   p.k_sel = k_sel;
+  p.lse = lse;
+  p.shared = shared ? *shared : SharedRows{};
+  p.rest = rest;
   const int bk = hyq_bits_k(c), bv = hyq_bits_v(c);
   if (bk == 4) return bv == 4 ? launch_nq<4, 4>(p, nq, s) : launch_nq<4, 8>(p, nq, s);
   return bv == 4 ? launch_nq<8, 4>(p, nq, s) : launch_nq<8, 8>(p, nq, s);

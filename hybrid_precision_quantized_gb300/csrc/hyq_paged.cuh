@@ -22,10 +22,38 @@ inline PageView hyq_page_view(const hyq_config* c, const hyq_pages* p, int32_t l
 
 inline size_t hyq_align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// Groups of call rows that begin with the same pages (hyq_paged_attention_shared).
+struct SharedRows {
+  const int32_t* cu;   // [n + 1] rows of the call
+  const int32_t* len;  // [n] positions shared, whole pages
+  int32_t n;
+};
+
+// A query row's partial result in memory: accumulator, maximum (log2 units), sum and two unused floats.
+constexpr int kPartFloats = HYQ_D + 4;
+
 size_t hyq_paged_attention_ws_bytes(const hyq_config* c, int32_t batch, int32_t n_q);
+// lse: logarithms of the softmax sums, or nullptr.  shared and rest: of the positions behind the shared ones, the
+// partial results [batch][n_q][HQ][kPartFloats] instead of outputs; or nullptr.
 cudaError_t hyq_launch_paged_attention(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
                                        int32_t n_q, const void* q, int64_t ldq, const int32_t* sel, int32_t k_sel,
-                                       void* out, void* ws, cudaStream_t s);
+                                       void* out, float* lse, const SharedRows* shared, float* rest, void* ws,
+                                       cudaStream_t s);
+size_t hyq_paged_shared_ws_bytes(const hyq_config* c, int32_t batch, int32_t n_q);
+cudaError_t hyq_launch_paged_shared(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
+                                    int32_t n_q, const SharedRows& shared, const void* q, int64_t ldq, void* out,
+                                    void* ws, cudaStream_t s);
+size_t hyq_paged_cross_ws_bytes(const hyq_config* c, int32_t batch);
+cudaError_t hyq_launch_paged_cross(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
+                                   const int32_t* cu_q, int32_t n_tokens, const void* q, int64_t ldq, void* out,
+                                   void* ws, cudaStream_t s);
+cudaError_t hyq_launch_paged_accumulate(const hyq_config* c, const PageView& pv, const int32_t* refs,
+                                        const int32_t* seqs, int32_t batch, int32_t n_q, const void* q, int64_t ldq,
+                                        const float* lse, const int32_t* n_new, float* mass, cudaStream_t s);
+size_t hyq_pages_evict_ws_bytes(const hyq_config* c, const hyq_pages* p, int32_t batch);
+cudaError_t hyq_launch_pages_evict(const hyq_config* c, const hyq_pages* p, const int32_t* seqs, int32_t batch,
+                                   const int32_t* keep, int32_t n_first, int32_t n_last, float* mass, void* ws,
+                                   cudaStream_t s);
 cudaError_t hyq_launch_paged_append(const hyq_config* c, const PageView& pv, const int32_t* seqs, int32_t batch,
                                     const int32_t* cu, int32_t n_rows, const void* k, const void* v, int64_t ld,
                                     void* k_hat, void* v_hat, cudaStream_t s);
@@ -88,3 +116,35 @@ __device__ __forceinline__ int bound_exp(float amax) {
 }
 // 2^k for -126 <= k <= 127.
 __device__ __forceinline__ float pow2_int(int k) { return __int_as_float((k + 127) << 23); }
+
+// Positions of group i that are read once for all of its rows, 0 when the group
+// cannot be: its rows are no part of the call, the positions no whole pages, or more
+// than the first row's tokens all see.  That row's table is the group's.
+__device__ __forceinline__ int group_len(const SharedRows& g, const PageView& pv, const int32_t* seqs, int i, int batch,
+                                         int n_q) {
+  const int b0 = g.cu[i], b1 = g.cu[i + 1], n = g.len[i];
+  if (b0 < 0 || b0 >= b1 || b1 > batch || n <= 0 || n % HYQ_PAGE_ROWS) return 0;
+  const int s = page_seq(seqs, b0, pv.n_seqs);
+  if (s < 0 || (int64_t)n > (int64_t)pv.max_blocks * HYQ_PAGE_ROWS) return 0;
+  return n <= (int64_t)pv.lens[s] - n_q + 1 ? n : 0;
+}
+// Group of call row b: the last one that begins at or before it.
+__device__ __forceinline__ int group_of(const SharedRows& g, int b) {
+  int lo = 0, hi = g.n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (g.cu[m] <= b) lo = m;
+    else hi = m;
+  }
+  return lo;
+}
+// Positions of call row b that its group reads for it.
+__device__ __forceinline__ int shared_len(const SharedRows& g, const PageView& pv, const int32_t* seqs, int b, int batch,
+                                          int n_q) {
+  if (g.n == 0) return 0;
+  const int i = group_of(g, b), s = page_seq(seqs, b, pv.n_seqs);
+  if (s < 0 || g.cu[i] > b || b >= g.cu[i + 1]) return 0;
+  const int n = group_len(g, pv, seqs, i, batch, n_q);
+  const int64_t len = min((int64_t)pv.lens[s], (int64_t)pv.max_blocks * HYQ_PAGE_ROWS);
+  return n <= len - n_q + 1 ? n : 0;
+}

@@ -71,6 +71,9 @@ extern "C" size_t hyq_pages_workspace_size(const hyq_config* c, const hyq_pages*
     case HYQ_OP_PAGED_SELECT: return q_ok ? hyq_paged_select_ws_bytes(c, p, batch, n_q) : 0;
     case HYQ_OP_PAGES_RESERVE: return hyq_pages_reserve_ws_bytes(p);
     case HYQ_OP_PAGES_COMPACT: return hyq_pages_compact_ws_bytes(p);
+    case HYQ_OP_PAGED_SHARED: return q_ok ? hyq_paged_shared_ws_bytes(c, batch, n_q) : 0;
+    case HYQ_OP_PAGED_CROSS: return hyq_paged_cross_ws_bytes(c, batch);
+    case HYQ_OP_PAGES_EVICT: return hyq_pages_evict_ws_bytes(c, p, batch);
     default: return 0;
   }
 }
@@ -138,19 +141,90 @@ extern "C" hyq_status hyq_paged_append(const hyq_config* c, const hyq_pages* p, 
                                            ld, k_hat, v_hat, s));
 }
 
-extern "C" hyq_status hyq_paged_attention(const hyq_config* c, const hyq_pages* p, int32_t layer, const int32_t* seqs,
-                                          int32_t batch, int32_t n_q, const void* q, int64_t ldq, void* out, void* ws,
-                                          size_t ws_bytes, hyq_stream_t s) {
+extern "C" hyq_status hyq_paged_attention_lse(const hyq_config* c, const hyq_pages* p, int32_t layer,
+                                              const int32_t* seqs, int32_t batch, int32_t n_q, const void* q,
+                                              int64_t ldq, void* out, float* lse, void* ws, size_t ws_bytes,
+                                              hyq_stream_t s) {
   hyq_status st = call_ok(c, p, layer, seqs, batch);
   if (st != HYQ_OK) return st;
   if (!seqs && batch > p->n_seqs) return HYQ_ERR_INVALID_ARG;
   if (batch == 0) return HYQ_OK;
   st = queries_ok(c, n_q, q, ldq);
   if (st != HYQ_OK) return st;
-  if (!out || !aligned(out, 16)) return HYQ_ERR_INVALID_ARG;
+  if (!out || !aligned(out, 16) || !aligned(lse, 4)) return HYQ_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, hyq_paged_attention_ws_bytes(c, batch, n_q))) return HYQ_ERR_WORKSPACE;
+  return from_cuda(hyq_launch_paged_attention(c, hyq_page_view(c, p, layer), seqs, batch, n_q, q, ldq, nullptr, 0, out,
+                                              lse, nullptr, nullptr, ws, s));
+}
+
+extern "C" hyq_status hyq_paged_attention(const hyq_config* c, const hyq_pages* p, int32_t layer, const int32_t* seqs,
+                                          int32_t batch, int32_t n_q, const void* q, int64_t ldq, void* out, void* ws,
+                                          size_t ws_bytes, hyq_stream_t s) {
+  return hyq_paged_attention_lse(c, p, layer, seqs, batch, n_q, q, ldq, out, nullptr, ws, ws_bytes, s);
+}
+
+extern "C" hyq_status hyq_paged_attention_shared(const hyq_config* c, const hyq_pages* p, int32_t layer,
+                                                 const int32_t* seqs, int32_t batch, int32_t n_q,
+                                                 const int32_t* cu_groups, const int32_t* n_shared, int32_t n_groups,
+                                                 const void* q, int64_t ldq, void* out, void* ws, size_t ws_bytes,
+                                                 hyq_stream_t s) {
+  hyq_status st = call_ok(c, p, layer, seqs, batch);
+  if (st != HYQ_OK) return st;
+  if ((!seqs && batch > p->n_seqs) || n_groups < 0) return HYQ_ERR_INVALID_ARG;
+  if (n_groups > HYQ_PAGED_MAX_BATCH) return HYQ_ERR_UNSUPPORTED;
+  if (batch == 0) return HYQ_OK;
+  st = queries_ok(c, n_q, q, ldq);
+  if (st != HYQ_OK) return st;
+  if (!out || !aligned(out, 16) || (n_groups && (!int32s(cu_groups) || !int32s(n_shared)))) return HYQ_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, hyq_paged_shared_ws_bytes(c, batch, n_q))) return HYQ_ERR_WORKSPACE;
+  return from_cuda(hyq_launch_paged_shared(c, hyq_page_view(c, p, layer), seqs, batch, n_q,
+                                           SharedRows{cu_groups, n_shared, n_groups}, q, ldq, out, ws, s));
+}
+
+extern "C" hyq_status hyq_paged_cross_attention(const hyq_config* c, const hyq_pages* p, int32_t layer,
+                                                const int32_t* seqs, int32_t batch, const int32_t* cu_q,
+                                                int32_t n_tokens, const void* q, int64_t ldq, void* out, void* ws,
+                                                size_t ws_bytes, hyq_stream_t s) {
+  hyq_status st = call_ok(c, p, layer, seqs, batch);
+  if (st != HYQ_OK) return st;
+  if (!seqs && batch > p->n_seqs) return HYQ_ERR_INVALID_ARG;
+  if (n_tokens < 0 || (cu_q ? !aligned(cu_q, 4) : n_tokens != batch)) return HYQ_ERR_INVALID_ARG;
+  if (batch == 0 || n_tokens == 0) return HYQ_OK;
+  st = queries_ok(c, 1, q, ldq);
+  if (st != HYQ_OK) return st;
+  if (!out || !aligned(out, 16)) return HYQ_ERR_INVALID_ARG;
+  if ((int64_t)n_tokens * c->num_q_heads > INT32_MAX) return HYQ_ERR_UNSUPPORTED;
+  if (!ws_ok(ws, ws_bytes, hyq_paged_cross_ws_bytes(c, batch))) return HYQ_ERR_WORKSPACE;
   return from_cuda(
-      hyq_launch_paged_attention(c, hyq_page_view(c, p, layer), seqs, batch, n_q, q, ldq, nullptr, 0, out, ws, s));
+      hyq_launch_paged_cross(c, hyq_page_view(c, p, layer), seqs, batch, cu_q, n_tokens, q, ldq, out, ws, s));
+}
+
+extern "C" hyq_status hyq_paged_accumulate(const hyq_config* c, const hyq_pages* p, int32_t layer, const int32_t* seqs,
+                                           int32_t batch, int32_t n_q, const void* q, int64_t ldq, const float* lse,
+                                           const int32_t* n_new, float* mass, hyq_stream_t s) {
+  hyq_status st = call_ok(c, p, layer, seqs, batch);
+  if (st != HYQ_OK) return st;
+  if (!seqs && batch > p->n_seqs) return HYQ_ERR_INVALID_ARG;
+  if (batch == 0) return HYQ_OK;
+  st = queries_ok(c, n_q, q, ldq);
+  if (st != HYQ_OK) return st;
+  if (!lse || !aligned(lse, 4) || !mass || !aligned(mass, 16) || !aligned(n_new, 4)) return HYQ_ERR_INVALID_ARG;
+  float* mine = mass + (size_t)layer * p->n_pages * c->num_kv_heads * HYQ_PAGE_ROWS;
+  return from_cuda(hyq_launch_paged_accumulate(c, hyq_page_view(c, p, layer), p->refs, seqs, batch, n_q, q, ldq, lse,
+                                               n_new, mine, s));
+}
+
+extern "C" hyq_status hyq_pages_evict(const hyq_config* c, const hyq_pages* p, const int32_t* seqs, int32_t batch,
+                                      const int32_t* keep, int32_t n_first, int32_t n_last, float* mass, void* ws,
+                                      size_t ws_bytes, hyq_stream_t s) {
+  const hyq_status st = call_ok(c, p, 0, seqs, batch);
+  if (st != HYQ_OK) return st;
+  if (!seqs && batch > p->n_seqs) return HYQ_ERR_INVALID_ARG;
+  if (n_first < 0 || n_last < 0 || n_first > INT32_MAX - n_last) return HYQ_ERR_INVALID_ARG;
+  if (batch == 0) return HYQ_OK;
+  if (!int32s(keep) || !mass || !aligned(mass, 16)) return HYQ_ERR_INVALID_ARG;
+  if (!ws_ok(ws, ws_bytes, hyq_pages_evict_ws_bytes(c, p, batch))) return HYQ_ERR_WORKSPACE;
+  return from_cuda(hyq_launch_pages_evict(c, p, seqs, batch, keep, n_first, n_last, mass, ws, s));
 }
 
 extern "C" hyq_status hyq_paged_attention_blocks(const hyq_config* c, const hyq_pages* p, int32_t layer,
@@ -166,7 +240,8 @@ extern "C" hyq_status hyq_paged_attention_blocks(const hyq_config* c, const hyq_
   if (!out || !aligned(out, 16) || !int32s(sel) || k < 1 || k > HYQ_PAGED_MAX_BLOCKS) return HYQ_ERR_INVALID_ARG;
   if (!ws_ok(ws, ws_bytes, hyq_paged_attention_ws_bytes(c, batch, n_q))) return HYQ_ERR_WORKSPACE;
   return from_cuda(
-      hyq_launch_paged_attention(c, hyq_page_view(c, p, layer), seqs, batch, n_q, q, ldq, sel, k, out, ws, s));
+      hyq_launch_paged_attention(c, hyq_page_view(c, p, layer), seqs, batch, n_q, q, ldq, sel, k, out, nullptr, nullptr,
+                                 nullptr, ws, s));
 }
 
 extern "C" hyq_status hyq_paged_select(const hyq_config* c, const hyq_pages* p, int32_t layer, const int32_t* seqs,

@@ -10,6 +10,16 @@ libhyq's kernels.  One step of a model with ``n_layers`` layers:
 
 ``fork`` lets sequences share what they have in common, ``truncate`` shortens
 or frees them, ``compact`` moves the pages in use to the front of the pool.
+``attention_shared`` reads what forked sequences share once for all of them;
+``cross_attention`` lets any number of tokens see all of a sequence.
+``accumulate`` sums up the weights that positions receive, and ``evict`` keeps
+those that received most:
+
+    mass = torch.zeros(cache.mass_shape, device="cuda")   # once
+    cache.attention(layer, q, out, seqs=seqs, lse=lse)    # each step and layer
+    cache.accumulate(layer, q, lse, mass, seqs=seqs)
+    cache.evict(mass, keep, seqs=seqs, n_first=4, n_last=128)   # now and then, all layers
+
 Nothing synchronises; errors that only the GPU can see collect in
 ``cache.err()`` (hyq_read_device_error).
 """
@@ -220,6 +230,15 @@ class PagedCache:
         ws = self.workspace(L.OP_PAGES_COMPACT, 1, stream=stream)
         self._run("hyq_pages_compact", (table, refs, ws.data_ptr(), ws.nbytes), stream, table_out, refs_out)
 
+    def evict(self, mass, keep, seqs=None, n_first: int = 0, n_last: int = 0, stream=None):
+        """Shorten the sequences to keep[i] positions (>= n_first + n_last), in every layer and KV head those that received
+        most besides the first n_first and the last n_last; their rows and masses move together (hyq_pages_evict)."""
+        n = self._ints(keep, "keep", self._ints(seqs, "seqs"))
+        m = self._dense(mass, "mass", torch.float32, self.mass_shape)
+        ws = self.workspace(L.OP_PAGES_EVICT, n, 1, stream)
+        self._run("hyq_pages_evict", (L.ptr(seqs), n, keep.data_ptr(), n_first, n_last, m, ws.data_ptr(), ws.nbytes),
+                  stream, seqs, keep, mass)
+
     # one layer -----------------------------------------------------------------
     def append(self, layer: int, k, v, seqs=None, cu_rows=None, k_hat=None, v_hat=None, stream=None):
         """Quantise rows k, v [rows, HKV, 128] into the last positions of their sequences: one row per sequence, or rows
@@ -252,13 +271,63 @@ class PagedCache:
         self._ints(seqs, "seqs", b)
         return b, n_q, self._heads(q, "q", self.cfg.num_q_heads)
 
-    def attention(self, layer: int, q, out, seqs=None, stream=None):
-        """Causal attention of the last n_q tokens of every sequence: q, out bf16 [sequences, n_q, HQ, 128]."""
+    def attention(self, layer: int, q, out, seqs=None, stream=None, lse=None):
+        """Causal attention of the last n_q tokens of every sequence: q, out bf16 [sequences, n_q, HQ, 128].  lse: a float32
+        tensor [sequences, n_q, HQ] for the logarithms of the softmax sums, which accumulate takes."""
         b, n_q, ldq = self._query(q, seqs)
         o = self._dense(out, "out", torch.bfloat16, q.shape)
+        e = self._dense(lse, "lse", torch.float32, q.shape[:3]) if lse is not None else None
         ws = self.workspace(L.OP_PAGED_ATTENTION, b, n_q, stream)
-        self._run("hyq_paged_attention", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, o, ws.data_ptr(), ws.nbytes),
-                  stream, seqs, q, out)
+        if e is None:
+            self._run("hyq_paged_attention", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, o, ws.data_ptr(),
+                                              ws.nbytes), stream, seqs, q, out)
+            return
+        self._run("hyq_paged_attention_lse", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, o, e, ws.data_ptr(),
+                                              ws.nbytes), stream, seqs, q, out, lse)
+
+    def attention_shared(self, layer: int, q, out, cu_groups, n_shared, seqs=None, stream=None):
+        """attention for sequences in groups that begin with the same pages (after fork): rows cu_groups[i] ..
+        cu_groups[i + 1] of the call share their first n_shared[i] positions, whole pages that all of their tokens see."""
+        b, n_q, ldq = self._query(q, seqs)
+        o = self._dense(out, "out", torch.bfloat16, q.shape)
+        n = self._ints(n_shared, "n_shared")
+        self._ints(cu_groups, "cu_groups", n + 1)
+        ws = self.workspace(L.OP_PAGED_SHARED, b, n_q, stream)
+        self._run("hyq_paged_attention_shared", (layer, L.ptr(seqs), b, n_q, cu_groups.data_ptr(), n_shared.data_ptr(), n,
+                                                 q.data_ptr(), ldq, o, ws.data_ptr(), ws.nbytes), stream, seqs,
+                  cu_groups, n_shared, q, out)
+
+    def cross_attention(self, layer: int, q, out, seqs=None, cu_q=None, stream=None):
+        """Attention of tokens that see all positions of their sequence: q, out bf16 [tokens, HQ, 128], tokens cu_q[i] ..
+        cu_q[i + 1] of sequence seqs[i], or one token each.  Tokens outside cu_q are left as they were."""
+        if q.dim() != 3:
+            raise ValueError("q: expected [tokens, HQ, 128]")
+        t = q.shape[0]
+        ldq = self._heads(q, "q", self.cfg.num_q_heads)
+        o = self._dense(out, "out", torch.bfloat16, q.shape)
+        if cu_q is None:
+            n = self._ints(seqs, "seqs", t)
+        else:
+            n = self._ints(cu_q, "cu_q") - 1
+            self._ints(seqs, "seqs", n)
+        ws = self.workspace(L.OP_PAGED_CROSS, n, 1, stream)
+        self._run("hyq_paged_cross_attention", (layer, L.ptr(seqs), n, L.ptr(cu_q), t, q.data_ptr(), ldq, o, ws.data_ptr(),
+                                                ws.nbytes), stream, seqs, cu_q, q, out)
+
+    @property
+    def mass_shape(self) -> tuple:
+        """Shape of the float32 tensor that accumulate and evict take: an entry per layer, page, KV head and position."""
+        return self.n_layers, self.n_pages, self.cfg.num_kv_heads, L.PAGE_ROWS
+
+    def accumulate(self, layer: int, q, lse, mass, seqs=None, n_new=None, stream=None):
+        """Add the attention weights that the last n_q tokens give (q and lse of the attention call) to what each position
+        of their sequences has received.  The last n_new[i] positions (default: n_q) are new and begin at zero."""
+        b, n_q, ldq = self._query(q, seqs)
+        e = self._dense(lse, "lse", torch.float32, q.shape[:3])
+        m = self._dense(mass, "mass", torch.float32, self.mass_shape)
+        self._ints(n_new, "n_new", b)
+        self._run("hyq_paged_accumulate", (layer, L.ptr(seqs), b, n_q, q.data_ptr(), ldq, e, L.ptr(n_new), m), stream,
+                  seqs, q, lse, n_new, mass)
 
     def select(self, layer: int, q, sel, seqs=None, n_first: int = 1, n_last: int = 1, stream=None):
         """The blocks worth reading for every token and KV head: sel int32 [sequences, n_q, HKV, k]."""

@@ -56,7 +56,8 @@ typedef enum {
 #define HYQ_DEVERR_COUNT 0x2       /* a device-side count exceeded the layout capacity */
 #define HYQ_DEVERR_INDEX 0x4       /* an index list was not strictly ascending in range */
 #define HYQ_DEVERR_SCORE 0x8       /* a selection score was NaN */
-#define HYQ_DEVERR_PAGES 0x20      /* no free page left, or a sequence past its table row */
+#define HYQ_DEVERR_PAGES 0x20      /* no free page left, a sequence past its table row, or a page that several
+                                      sequences hold where it must be one's own */
 #define HYQ_DEVERR_TIMEOUT 0x10    /* a bounded wait inside a kernel gave up (a bulk copy or a
                                       tensor-core commit did not complete); the kernel stopped
                                       issuing work, drained what it had in flight and returned */
@@ -617,6 +618,9 @@ typedef struct {
 #define HYQ_OP_PAGED_SELECT 17
 #define HYQ_OP_PAGES_RESERVE 18
 #define HYQ_OP_PAGES_COMPACT 19
+#define HYQ_OP_PAGED_SHARED 20
+#define HYQ_OP_PAGED_CROSS 21 /* n_q is not looked at: it serves any number of tokens */
+#define HYQ_OP_PAGES_EVICT 22
 
 /* Bytes of each buffer, in the order of HYQ_PAGES_FIELDS (out[HYQ_PAGES_FIELDS],
  * host), from the four sizes of `pages` (its pointers are not looked at). */
@@ -624,7 +628,7 @@ hyq_status hyq_pages_sizes(const hyq_config *cfg, const hyq_pages *pages, size_t
 
 /* Workspace bytes of an operation (HYQ_OP_PAGED_* / HYQ_OP_PAGES_*) for calls
  * of at most `batch` sequences with n_q query tokens each (n_q is used by
- * attention and select alone); 0 on invalid sizes.  A workspace must be zero-filled before its
+ * attention, shared and select alone); 0 on invalid sizes.  A workspace must be zero-filled before its
  * first use and is left ready for the next call; calls of any smaller size
  * may share it, one at a time. */
 size_t hyq_pages_workspace_size(const hyq_config *cfg, const hyq_pages *pages, int op, int32_t batch,
@@ -778,6 +782,110 @@ hyq_status hyq_paged_attention_blocks(const hyq_config *cfg, const hyq_pages *pa
                                       const int32_t *seqs, int32_t batch, int32_t n_q, const void *q, int64_t ldq,
                                       const int32_t *sel, int32_t k, void *out, void *ws, size_t ws_bytes,
                                       hyq_stream_t stream);
+
+/*
+ * hyq_paged_attention that also gives the logarithm of each query row's softmax
+ * sum, for hyq_paged_accumulate:
+ *   lse  device float32 [batch][n_q][HQ] or NULL: ln sum_j exp(q.k_j / sqrt(128));
+ *        minus infinity where nothing is seen, NaN for a query that is not finite
+ */
+hyq_status hyq_paged_attention_lse(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
+                                   int32_t batch, int32_t n_q, const void *q, int64_t ldq, void *out, float *lse,
+                                   void *ws, size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * hyq_paged_attention for sequences that begin alike (after hyq_pages_fork): what a
+ * group of them shares is read once for all of its query rows.
+ *   cu_groups  device int32 [n_groups + 1], ascending from 0 to batch: group i is
+ *              the call rows cu_groups[i] .. cu_groups[i + 1]
+ *   n_shared   device int32 [n_groups]: the group's first n_shared[i] positions, whole
+ *              pages (a multiple of 64; 0: nothing is shared), lie in the same
+ *              pages for all of its rows, and every query token sees them all
+ *              (n_shared <= length - n_q + 1)
+ *   n_groups   0 .. HYQ_PAGED_MAX_BATCH
+ * Other arguments and result as there, the shared positions being those of the
+ * group's first row.  What cannot be shared sets HYQ_DEVERR_INDEX and is read by
+ * each row for itself: a group whose n_shared is no multiple of 64 or more than its
+ * first row's tokens see, a row whose tokens do not see all of it, rows of
+ * a pair of cu_groups that descends or leaves [0, batch].
+ * The shared keys and values enter the products rounded to fp16 (2^-11 of an element), and so
+ * do the probabilities (of all positions).  Parts are joined in a fixed order.
+ * Workspace: HYQ_OP_PAGED_SHARED, zero-filled before first use.  Three launches.
+ */
+hyq_status hyq_paged_attention_shared(const hyq_config *cfg, const hyq_pages *pages, int32_t layer,
+                                      const int32_t *seqs, int32_t batch, int32_t n_q, const int32_t *cu_groups,
+                                      const int32_t *n_shared, int32_t n_groups, const void *q, int64_t ldq, void *out,
+                                      void *ws, size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * Cross attention: any number of query tokens a sequence (a decoder's), each of
+ * which sees all of its positions (an encoder's states, appended once):
+ * out = softmax(q K^T / sqrt(128)) V over the lens[s] dequantised rows, zeros
+ * where there are none.  A query row that is not finite gives NaN in its own output row
+ * and changes no other.
+ *   cu_q      device int32 [batch + 1], ascending: call row i's tokens are
+ *             cu_q[i] .. cu_q[i + 1]; or NULL: one each (n_tokens = batch).
+ *             Tokens outside [cu_q[0], cu_q[batch]) are left as they were
+ *   n_tokens  host, the number of tokens that q and out hold
+ *   seqs      device int32 [batch] or NULL (sequence i); may repeat
+ *   q         device bf16: token t, head h, element d at t ldq + 128 h + d; ldq >=
+ *             128 HQ, a multiple of 8
+ *   out       device bf16 [n_tokens][HQ][128]
+ * A sequence out of range or a table entry outside the pool sets
+ * HYQ_DEVERR_INDEX and counts as nothing to see; a pair of cu_q that descends or leaves
+ * [0, n_tokens] sets it too, and its tokens are left out.  Roundings as in
+ * hyq_paged_attention_shared (with cu_q = NULL as in hyq_paged_attention).
+ * Workspace: HYQ_OP_PAGED_CROSS, zero-filled before first use.  Two launches (one).
+ */
+hyq_status hyq_paged_cross_attention(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
+                                     int32_t batch, const int32_t *cu_q, int32_t n_tokens, const void *q, int64_t ldq,
+                                     void *out, void *ws, size_t ws_bytes, hyq_stream_t stream);
+
+/*
+ * Add the attention weights of the last n_q positions to what every position of
+ * their sequences has received: per KV head
+ *   mass[j] += sum over the tokens i that see j and the g heads of
+ *              exp(q.k_j / sqrt(128) - lse)
+ *   q, ldq, n_q  as for hyq_paged_attention (the same call's)
+ *   lse    device float32 [batch][n_q][HQ], from hyq_paged_attention_lse
+ *   n_new  device int32 [batch], 0 .. length, or NULL (n_q each): how many of the
+ *          sequence's last positions are new; they begin at zero, whatever mass holds
+ *   mass   device float32 [n_layers][n_pages][HKV][64], 16-byte aligned: of each page's
+ *          positions; entries of other positions are left as they were
+ * A query row that is not finite, or whose lse is not (where it sees anything), gives nothing
+ * and sets HYQ_DEVERR_SCORE.  A sequence that is out of range or listed before sets
+ * HYQ_DEVERR_INDEX and is left out, and so is a page outside the pool; a page that
+ * several sequences hold has no one owner: it sets HYQ_DEVERR_PAGES and is left out.
+ * Sums are float32, in a fixed order; a weight below 2^-126 counts as zero.  One launch, no workspace.
+ */
+hyq_status hyq_paged_accumulate(const hyq_config *cfg, const hyq_pages *pages, int32_t layer, const int32_t *seqs,
+                                int32_t batch, int32_t n_q, const void *q, int64_t ldq, const float *lse,
+                                const int32_t *n_new, float *mass, hyq_stream_t stream);
+
+/*
+ * Keep k = keep[i] of the n positions of every sequence seqs[i], in every layer and
+ * KV head those that received most: the first n_first, the last n_last and, of the
+ * others, the k - n_first - n_last of largest mass, ties to the lower position (NaN counts
+ * as larger than any number).  A sequence with n <= k stays as it is.
+ * With w = k - n_last: kept positions below w stay in their places; the r-th kept
+ * position of [w, n - n_last) goes to the r-th free place below w, both ascending;
+ * the last n_last go to [w, k) in their order.  Masses go with their
+ * rows.  The bound record of a page that received a row is taken anew over the
+ * rows below k that it holds, of their keys as held (c s + z in float32); other records
+ * and all other bytes stay.  lens = k; the pages behind are freed.
+ * Positions are those of the table: what the model puts into a row (a rotary
+ * angle) moves with it unchanged.
+ *   seqs  device int32 [batch] or NULL (sequence i)
+ *   keep  device int32 [batch], >= n_first + n_last
+ *   mass  as for hyq_paged_accumulate
+ * A sequence out of range or listed before, a keep that is too small or a table entry outside the
+ * pool sets HYQ_DEVERR_INDEX; a page among the ceil(k / 64) kept ones that another
+ * sequence holds too sets HYQ_DEVERR_PAGES: that sequence is left as it was.
+ * Workspace: HYQ_OP_PAGES_EVICT, no initial contents needed.  Four launches.
+ */
+hyq_status hyq_pages_evict(const hyq_config *cfg, const hyq_pages *pages, const int32_t *seqs, int32_t batch,
+                           const int32_t *keep, int32_t n_first, int32_t n_last, float *mass, void *ws, size_t ws_bytes,
+                           hyq_stream_t stream);
 
 /*
  * Copy a device error word to the host (synchronises `stream`).

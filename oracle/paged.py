@@ -117,6 +117,58 @@ def dequantised(rows, bits):
     return val, np.abs(val - zz) + np.abs(zz), c.astype(np.float64)
 
 
+def span_error(q, k, v, vis, out, far=0, ksize=None, vsize=None, vcodes=0.0):
+    """Elementwise bound of |gpu - attend| for one query row whose keys and values enter the products as fp16 (k, v: the
+    dequantised rows; far: the power of two by which rows beyond fp16 are taken down).  Where some of the rows enter them as
+    codes (attend_error), ksize and vsize are |c s| + |z| of the elements and vcodes the values' codes.
+
+    An element of a key or value is rounded by half a step of fp16: 2^-11 of it, or 2^(-25 + far) where the scaled element
+    is subnormal (c s + z is a multiple of 2^-24, so without scaling that is exact).  A logit is then off by the keys'
+    part of sum |q| |k| and by float32 sums that may truncate (2^-18 of the size, as in attend_error), numerator and
+    denominator alike.  A probability, held as 2^8 or more at the row's maximum, is rounded to fp16: 2^-11, or 2^-25
+    of what is held.  The exponential, its argument's rounding and the joins: 2^-18.  The output is rounded to BF16."""
+    if not np.any(vis):
+        return np.zeros_like(out)
+    mixed = vsize is not None
+    ksize, vsize = (np.abs(k[vis]), np.abs(v[vis])) if not mixed else (ksize[vis], vsize[vis])
+    x = (k[vis] @ q) / math.sqrt(q.shape[-1])
+    p = np.exp(x - x.max())
+    tiny = 2.0 ** (-25 + far) if far else 0.0
+    d = ((2.0 ** -11 + 2.0 ** -18) * (ksize @ np.abs(q)) + tiny * np.abs(q).sum()) / math.sqrt(q.shape[-1]) + 2.0 ** -18
+    total = p.sum()
+    first = ((p * d) @ vsize) / total + np.abs(out) * (p @ d) / total
+    low = 2.0 ** -25 * (vsize + vcodes[vis]).sum(0) if mixed else 2.0 ** -33 * vsize.sum(0)
+    return 2.0 ** -8 * np.abs(out) + 1.05 * first + (p @ vsize) / total * 2.0 ** -10 + tiny + low / total
+
+
+def weights(q, k, lse, lims):
+    """What every position receives from the query rows q [r, 128] of one KV head: sum of exp(q.k / sqrt(128) - lse) over
+    the rows that see it (row i the first lims[i] positions)."""
+    out = np.zeros(len(k))
+    for row, e, lim in zip(q, lse, lims):
+        if lim > 0:
+            out[:lim] += np.exp((k[:lim] @ row) / math.sqrt(k.shape[-1]) - e)
+    return out
+
+
+def keep_positions(mass, n, k, n_first, n_last):
+    """Where the rows of one (layer, KV head) come from after an eviction: entry j < k is the old position of new position
+    j.  NaN is the largest mass."""
+    if n <= k:
+        return list(range(n))
+    middle = range(n_first, n - n_last)
+    order = sorted(middle, key=lambda j: (-math.inf if math.isnan(mass[j]) else 0, 0 if math.isnan(mass[j]) else -mass[j], j))
+    kept = sorted(list(range(n_first)) + order[:k - n_first - n_last])
+    w = k - n_last
+    src = {j: j for j in kept if j < w}
+    free = [j for j in range(w) if j not in src]
+    for j, at in zip(free, [x for x in kept if x >= w]):
+        src[j] = at
+    for i in range(n_last):
+        src[w + i] = n - n_last + i
+    return [src[j] for j in range(k)]
+
+
 class Tables:
     """Page tables with the rules of hyq_pages_*, one sequence after another."""
 

@@ -83,3 +83,40 @@ def test_the_attention_bound_shrinks_with_the_values():
     assert np.array_equal(w0 * 2.0 ** -4, w1) and np.allclose(b0 * 2.0 ** -4, b1, rtol=1e-12)
     assert (b0 <= e0).all() and (e1 > e0 * 2.0 ** -4).all()
     assert not P.attend_bound(q, kd, kp, vp, vc, P.quantize(v, 8)[1], vis & False, 0 * want).any()
+
+
+def test_weights_of_whole_softmaxes_sum_to_the_number_of_rows():
+    k, q = rows(5, 40), rows(6, 6)
+    lims = [40, 39, 17, 1, 0, -3]
+    lse = [np.log(np.exp(k[:n] @ r / 128 ** 0.5).sum()) if n > 0 else -np.inf for r, n in zip(q, lims)]
+    w = P.weights(q, k, lse, lims)
+    assert np.isclose(w.sum(), 4.0) and w[39] < w.sum() and (w >= 0).all()
+    assert np.isclose(P.weights(q[3:4], k, lse[3:4], [1])[0], 1.0)
+
+
+@pytest.mark.parametrize("n, k, first, last", [(10, 7, 2, 3), (200, 64, 4, 32), (70, 69, 0, 69), (65, 1, 0, 0), (9, 5, 5, 0),
+                                               (30, 0, 0, 0), (12, 12, 1, 1), (5, 9, 0, 2)])
+def test_eviction_keeps_the_largest_and_moves_no_more_than_it_must(n, k, first, last):
+    mass = np.random.default_rng(n).integers(0, 5, n).astype(float)
+    src = P.keep_positions(mass, n, k, first, last)
+    m = min(n, k)
+    assert len(src) == m and len(set(src)) == m and all(0 <= s < n for s in src)
+    if n <= k:
+        assert src == list(range(n))
+        return
+    assert set(range(first)) | set(range(n - last, n)) <= set(src)
+    assert src[k - last:] == list(range(n - last, n))
+    out = [j for j in range(first, n - last) if j not in src]
+    chosen = [j for j in src if first <= j < n - last]
+    for a in out:
+        assert all(mass[b] > mass[a] or (mass[b] == mass[a] and b < a) for b in chosen)
+    w = k - last
+    assert all(src[j] == j for j in range(w) if j in src)          # below w a kept position keeps its place
+    moved = [src[j] for j in range(w) if src[j] != j]
+    assert moved == sorted(moved) and all(s >= w for s in moved)
+
+
+def test_eviction_takes_nan_for_the_largest():
+    mass = np.array([1.0, np.nan, 3.0, np.inf, np.nan, 2.0])
+    assert P.keep_positions(mass, 6, 2, 0, 0) == [4, 1]
+    assert sorted(P.keep_positions(mass, 6, 3, 0, 0)) == [1, 3, 4]
