@@ -15,20 +15,23 @@
 // two, which fp16 takes without rounding (BF16 has fewer bits; elements 2^-27 of
 // the row's largest and less are rounded).  Probabilities are rounded to fp16, kept
 // between 2^8 and 2^14 at the row's maximum so that the small ones are not lost.
+#include <type_traits>
+
+#include "hyq_f2.cuh"
 #include "hyq_paged.cuh"
 #include "hyq_tc.cuh"
 
 namespace {
 
-constexpr int kRows = 128;   // query rows of a tile (MMA M)
+constexpr int kRows = 128;   // query rows of a product (MMA M)
+constexpr int kPair = 2 * kRows;  // of a tile
 constexpr int kKeys = 128;   // positions of a unit: two pages (MMA N, and K of P V)
 constexpr int kUnitPages = kKeys / HYQ_PAGE_ROWS;
-constexpr int kThreads = 256;
-constexpr int kCost = 4;     // units that a tile's fixed work is worth
-constexpr int kRegion = 16384;           // 128 rows of 128 bytes, 128-byte swizzled
-constexpr uint32_t kColS = 0, kColP = 128, kColO = 256, kTmemCols = 512;
+constexpr int kCost = 6;     // jobs (128 rows of a unit) that a tile's fixed work is worth
+constexpr int kRegion = 16384;  // 128 rows of 128 bytes, 128-byte swizzled
+constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // two of each
 constexpr float kLog2Scale = 0.1275174307366466f;  // log2(e) / sqrt(128)
-constexpr float kSlack = 6.f, kLift = 8.f;         // probabilities at the row's maximum: 2^kLift .. 2^(kLift + kSlack)
+constexpr float kLift = 8.f;    // probabilities at a new maximum: 2^kLift
 
 // Values beyond fp16: a unit in which c s + z may pass 65504 is taken times 2^-kFar.
 template <int B>
@@ -43,16 +46,19 @@ struct Params {
   const __nv_bfloat16* q;
   int64_t ldq;
   __nv_bfloat16* out;
-  float* part;           // [grid][2] parts
   struct Plan* plan;
+  struct Entry* list;    // [grid][HYQ_PAGED_MAX_BATCH]
+  float* part;           // [grid][2] parts of tiles
+  float* half;           // [grid][2] states of 128 rows
   const float* rest;     // shared: partial results of the positions behind, [n_tokens][HQ][kPartFloats]
   int32_t HQ, HKV, gq;
 };
 
-// Part of a tile: [32][kRows] four elements each, then maximum and sum a row.
-constexpr int kPart = kRows * (HYQ_D + 2);
+// Part of a tile: [32][kPair] four elements each, then maximum and sum a row.
+constexpr int kPart = kPair * (HYQ_D + 2);
 
-// The units of all tiles laid end to end, cut into equal runs, a block each.
+// The jobs of all tiles laid end to end (a tile's begin with kCost that are not there), cut into equal runs, a
+// block each; a unit of a pair is its first job's block's.
 struct Shares {
   int64_t each, more;
   __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + min(c, more); }
@@ -63,7 +69,7 @@ struct Shares {
 };
 struct Plan {
   Shares sh;
-  int64_t cum[HYQ_PAGED_MAX_BATCH];  // units before segment i
+  int64_t cum[HYQ_PAGED_MAX_BATCH];  // jobs before segment i
   int32_t len[HYQ_PAGED_MAX_BATCH], t0[HYQ_PAGED_MAX_BATCH], rows[HYQ_PAGED_MAX_BATCH];
 };
 
@@ -95,7 +101,20 @@ __device__ __forceinline__ Seg segment(const Params& p, int i, bool report) {
   s.rows = ok ? (t1 - t0) * p.gq : 0;
   return s;
 }
-__device__ __forceinline__ int64_t units_of(int len) { return len ? (len + kKeys - 1) / kKeys + kCost : 0; }
+__device__ __forceinline__ int n_units(int len) { return (len + kKeys - 1) / kKeys; }
+// Jobs of one KV head: whole pairs, then the rows that are left.
+__device__ __forceinline__ int64_t head_slots(int len, int rows) {
+  if (len <= 0 || rows <= 0) return 0;
+  const int U = n_units(len), n = (rows + kPair - 1) / kPair, left = rows - (n - 1) * kPair;
+  return (int64_t)(n - 1) * (kCost + 2 * U) + kCost + (left > kRows ? 2 : 1) * U;
+}
+// First unit that begins at or behind job x of a tile with nt jobs a unit.
+__device__ __forceinline__ int unit_from(int x, int nt) { return max(0, (x - kCost + nt - 1) / nt); }
+// Whether block c has units of the tile whose first job (behind the fixed work) is `base`.
+__device__ __forceinline__ bool holds(const Shares& sh, int c, int64_t base, int nt, int U) {
+  const int64_t a = max((int64_t)0, sh.begin(c) - base), b = min((int64_t)nt * U, sh.begin(c + 1) - base);
+  return a < b && (a + nt - 1) / nt < (b + nt - 1) / nt;
+}
 
 // Byte offset of 16-byte chunk c of row r in a swizzled region.
 __device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
@@ -143,70 +162,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Whether some c s + z of a group may leave fp16: `vr` rows of the tile at tb, this lane's rows.
-template <int B>
-__device__ __forceinline__ bool key_meta_far(const uint8_t* meta, int lane, int vr) {
-  const uint32_t qmax = B == 4 ? 0x4B804B80u : 0x5BF85BF8u;  // 15, 255
-  if (lane >= vr || lane >= 16) return false;
-  const uint4 m = *reinterpret_cast<const uint4*>(meta + 16 * lane);
-  const uint32_t a = hfma2_u(m.x, qmax, m.z) & 0x7FFF7FFFu, b = hfma2_u(m.y, qmax, m.w) & 0x7FFF7FFFu;
-  const uint32_t top = __vmaxu2(a, b);
-  return (top >> 16) >= 0x7C00u || (top & 0xFFFFu) >= 0x7C00u;
-}
-template <int B>
-__device__ __forceinline__ bool value_meta_far(const uint8_t* meta, int lane, int vr) {
-  const uint32_t qmax = B == 4 ? 0x4B804B80u : 0x5BF85BF8u;
-  const int r = 2 * (lane >> 2);  // words: row pair, group
-  uint32_t a = hfma2_u(*reinterpret_cast<const uint32_t*>(meta + 4 * lane), qmax,
-                       *reinterpret_cast<const uint32_t*>(meta + 128 + 4 * lane)) & 0x7FFF7FFFu;
-  return (r < vr && (a & 0xFFFFu) >= 0x7C00u) || (r + 1 < vr && (a >> 16) >= 0x7C00u);
-}
-
-// One warp: the 16 keys of a tile as fp16 rows row0 .. row0 + 15 of the key operand at `dst`
-// (two regions of 64 elements).  Of 8-bit codes the four elements of each half of a
-// group of 32 lie beside those of the other half (query rows are ordered alike).
-template <int BK>
-__device__ __forceinline__ void keys_to_half(const uint8_t* tb, const uint8_t* meta, int lane, uint8_t* dst, int row0,
-                                             bool far) {
-  const int g = lane >> 2, t = lane & 3;
-  uint4 ma = *reinterpret_cast<const uint4*>(meta + 16 * g), mb = *reinterpret_cast<const uint4*>(meta + 16 * (g + 8));
-  if (far) {
-    const uint32_t f = (uint32_t)(15 - kFar<BK>) << 10, f2 = f | f << 16;
-    ma = make_uint4(hmul2_u(ma.x, f2), hmul2_u(ma.y, f2), hmul2_u(ma.z, f2), hmul2_u(ma.w, f2));
-    mb = make_uint4(hmul2_u(mb.x, f2), hmul2_u(mb.y, f2), hmul2_u(mb.z, f2), hmul2_u(mb.w, f2));
-  }
-  const int ra = key_row(row0 + g), rb = key_row(row0 + g + 8);
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {  // group v: 16 bytes of each row
-    uint32_t xa[4], xb[4];
-    if (BK == 4) {
-      const uint4 w4 = *reinterpret_cast<const uint4*>(tb + 512 * (v >> 1) + 16 * lane);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t w = u4at(w4, 2 * (v & 1) + u), w8 = w >> 8;
-        xa[2 * u] = low_codes(w), xa[2 * u + 1] = low_codes(w8);
-        xb[2 * u] = high_codes(w), xb[2 * u + 1] = high_codes(w8);
-      }
-    } else {
-      const uint4 w4 = *reinterpret_cast<const uint4*>(tb + 512 * v + 16 * lane);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint32_t wa = u4at(w4, 2 * u), wb = u4at(w4, 2 * u + 1);
-        xa[2 * u] = even_codes(wa), xa[2 * u + 1] = odd_codes(wa);
-        xb[2 * u] = even_codes(wb), xb[2 * u + 1] = odd_codes(wb);
-      }
-    }
-    const uint32_t sa = both(v < 2 ? ma.x : ma.y, v & 1), za = both(v < 2 ? ma.z : ma.w, v & 1);
-    const uint32_t sb = both(v < 2 ? mb.x : mb.y, v & 1), zb = both(v < 2 ? mb.z : mb.w, v & 1);
-    uint8_t* reg = dst + (v >> 1) * kRegion;
-    const int c = 4 * (v & 1) + t;
-    *reinterpret_cast<uint4*>(reg + swz(ra, c)) = make_uint4(hfma2_u(xa[0], sa, za), hfma2_u(xa[1], sa, za),
-                                                             hfma2_u(xa[2], sa, za), hfma2_u(xa[3], sa, za));
-    *reinterpret_cast<uint4*>(reg + swz(rb, c)) = make_uint4(hfma2_u(xb[0], sb, zb), hfma2_u(xb[1], sb, zb),
-                                                             hfma2_u(xb[2], sb, zb), hfma2_u(xb[3], sb, zb));
-  }
-}
-
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
@@ -216,50 +171,125 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t 
 __device__ __forceinline__ uint32_t halves_below(int r, int vr) {
   return (r < vr ? 0xFFFFu : 0u) | (r + 1 < vr ? 0xFFFF0000u : 0u);
 }
-// One warp: the 16 values of tile i of a page, transposed, as keys 16 i .. 16 i + 15 of the value operand's region
-// `dst` (rows: elements in the order of elem_of); rows from vr on are zero.
-template <int BV>
-__device__ __forceinline__ void values_to_half(const uint8_t* tb, const uint8_t* meta, int lane, uint32_t dst, int i,
-                                               int vr, bool far) {
-  const int g = lane >> 2, t = lane & 3;
-  uint4 s[2], z[2];  // of rows 2t + 8b and the next, groups 0 .. 3
-#pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    s[b] = *reinterpret_cast<const uint4*>(meta + 16 * (t + 4 * b));
-    z[b] = *reinterpret_cast<const uint4*>(meta + 128 + 16 * (t + 4 * b));
-    const uint32_t in = halves_below(2 * t + 8 * b, vr);
-    s[b] = make_uint4(s[b].x & in, s[b].y & in, s[b].z & in, s[b].w & in);
-    z[b] = make_uint4(z[b].x & in, z[b].y & in, z[b].z & in, z[b].w & in);
-    if (far) {
-      const uint32_t f = (uint32_t)(15 - kFar<BV>) << 10, f2 = f | f << 16;
-      s[b] = make_uint4(hmul2_u(s[b].x, f2), hmul2_u(s[b].y, f2), hmul2_u(s[b].z, f2), hmul2_u(s[b].w, f2));
-      z[b] = make_uint4(hmul2_u(z[b].x, f2), hmul2_u(z[b].y, f2), hmul2_u(z[b].z, f2), hmul2_u(z[b].w, f2));
-    }
-  }
-  // matrix m of a store: element 4 g + c of a group of 32, c = c0 + (m >> 1), keys of half m & 1; lane l gives the
-  // address of row l & 7 of matrix l >> 3
-  const int mb = (lane >> 3) & 1, mc = lane >> 4, r8 = lane & 7;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int c0 = 0; c0 < 4; c0 += 2) {
-      uint32_t x[4];
-      if (BV == 4) {
-        const uint4 w4 = *reinterpret_cast<const uint4*>(tb + 512 * (q >> 1) + 16 * lane);
-        const uint32_t w = u4at(w4, 2 * (q & 1) + (c0 >> 1)), w8 = w >> 8;
-        x[0] = low_codes(w), x[1] = low_codes(w8), x[2] = high_codes(w), x[3] = high_codes(w8);
-      } else {
-        const uint4 w4 = *reinterpret_cast<const uint4*>(tb + 512 * q + 16 * lane);
-        const uint32_t wa = u4at(w4, c0), wb = u4at(w4, c0 + 1);
-        x[0] = even_codes(wa), x[1] = odd_codes(wa), x[2] = even_codes(wb), x[3] = odd_codes(wb);
-      }
-#pragma unroll
-      for (int m = 0; m < 4; ++m) x[m] = hfma2_u(x[m], u4at(s[m & 1], q), u4at(z[m & 1], q));
-      const int n = 32 * q + 8 * (c0 + mc) + r8;
-      stmatrix_x4(dst + swz(n, 2 * i + mb), x[0], x[1], x[2], x[3]);
-    }
-  }
+__device__ __forceinline__ uint4 mul4(const uint4& v, uint32_t f) {
+  return make_uint4(hmul2_u(v.x, f), hmul2_u(v.y, f), hmul2_u(v.z, f), hmul2_u(v.w, f));
 }
+template <int B>
+__device__ __forceinline__ uint32_t far_scale() {  // 2^-kFar, twice
+  const uint32_t f = (uint32_t)(15 - kFar<B>) << 10;
+  return f | f << 16;
+}
+
+// A 16-row tile of codes in a warp's registers.
+template <int BK, int BV>
+struct TileCodes {
+  using F = QFmt<BK, BV>;
+  uint4 kc[BK / 2], vc[BV / 2];  // code words, 512 bytes of the region each
+  uint4 ka, kb;                  // keys' steps and zeros of rows g, g + 8
+  uint4 vs[2], vz[2];            // values' of rows 2t + 8b and the next, groups 0 .. 3
+
+  __device__ __forceinline__ void load(const uint8_t* tb, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < BK / 2; ++i) kc[i] = *reinterpret_cast<const uint4*>(tb + 512 * i + 16 * lane);
+#pragma unroll
+    for (int i = 0; i < BV / 2; ++i) vc[i] = *reinterpret_cast<const uint4*>(tb + F::kVCode + 512 * i + 16 * lane);
+    ka = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
+    kb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      vs[b] = *reinterpret_cast<const uint4*>(tb + F::kVMeta + 16 * (t + 4 * b));
+      vz[b] = *reinterpret_cast<const uint4*>(tb + F::kVMeta + 128 + 16 * (t + 4 * b));
+    }
+  }
+  // Whether some c s + z of this lane's rows below vr may leave fp16 (the largest code's does).
+  __device__ __forceinline__ bool far(int lane, int vr) const {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr uint32_t k = BK == 4 ? 0x4B804B80u : 0x5BF85BF8u, v = BV == 4 ? 0x4B804B80u : 0x5BF85BF8u;  // 15, 255
+    auto top = [](uint32_t s, uint32_t q, uint32_t z) { return hfma2_u(s, q, z) & 0x7FFF7FFFu; };
+    const uint32_t a = __vmaxu2(top(ka.x, k, ka.z), top(ka.y, k, ka.w)), b = __vmaxu2(top(kb.x, k, kb.z), top(kb.y, k, kb.w));
+    uint32_t most = __vmaxu2(g < vr ? a : 0u, g + 8 < vr ? b : 0u);
+#pragma unroll
+    for (int b2 = 0; b2 < 2; ++b2) {
+      const uint32_t c = __vmaxu2(__vmaxu2(top(vs[b2].x, v, vz[b2].x), top(vs[b2].y, v, vz[b2].y)),
+                                  __vmaxu2(top(vs[b2].z, v, vz[b2].z), top(vs[b2].w, v, vz[b2].w)));
+      most = __vmaxu2(most, c & halves_below(2 * t + 8 * b2, vr));
+    }
+    return (most >> 16) >= 0x7C00u || (most & 0xFFFFu) >= 0x7C00u;
+  }
+  // The keys as fp16 rows row0 .. row0 + 15 of the key operand at `dst` (two regions of 64 elements).  Of 8-bit codes
+  // the four elements of each half of a group of 32 lie beside those of the other half (query rows are ordered alike).
+  __device__ __forceinline__ void keys(uint8_t* dst, int lane, int row0, bool is_far) {
+    const int g = lane >> 2, t = lane & 3;
+    if (is_far) ka = mul4(ka, far_scale<BK>()), kb = mul4(kb, far_scale<BK>());
+    uint8_t* at = dst + 128 * key_row(row0 + g);  // row g + 8 lies 8 rows on, swizzled alike
+    const int x = key_row(g);                     // (row0 is a multiple of 8)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {  // group v: 16 bytes of each row
+      uint32_t xa[4], xb[4];
+      if (BK == 4) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t w = u4at(kc[v >> 1], 2 * (v & 1) + u), w8 = w >> 8;
+          xa[2 * u] = low_codes(w), xa[2 * u + 1] = low_codes(w8);
+          xb[2 * u] = high_codes(w), xb[2 * u + 1] = high_codes(w8);
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t wa = u4at(kc[BK == 4 ? 0 : v], 2 * u), wb = u4at(kc[BK == 4 ? 0 : v], 2 * u + 1);
+          xa[2 * u] = even_codes(wa), xa[2 * u + 1] = odd_codes(wa);
+          xb[2 * u] = even_codes(wb), xb[2 * u + 1] = odd_codes(wb);
+        }
+      }
+      const uint32_t sa = both(v < 2 ? ka.x : ka.y, v & 1), za = both(v < 2 ? ka.z : ka.w, v & 1);
+      const uint32_t sb = both(v < 2 ? kb.x : kb.y, v & 1), zb = both(v < 2 ? kb.z : kb.w, v & 1);
+      uint8_t* to = at + (v >> 1) * kRegion + (((4 * (v & 1) + t) ^ x) << 4);
+      *reinterpret_cast<uint4*>(to) = make_uint4(hfma2_u(xa[0], sa, za), hfma2_u(xa[1], sa, za),
+                                                 hfma2_u(xa[2], sa, za), hfma2_u(xa[3], sa, za));
+      *reinterpret_cast<uint4*>(to + 1024) = make_uint4(hfma2_u(xb[0], sb, zb), hfma2_u(xb[1], sb, zb),
+                                                        hfma2_u(xb[2], sb, zb), hfma2_u(xb[3], sb, zb));
+    }
+  }
+  // The values, transposed, as keys 16 i .. 16 i + 15 of the value operand's region `dst` (rows: elements in the
+  // order of elem_of); rows from vr on are zero.
+  __device__ __forceinline__ void values(uint32_t dst, int lane, int i, int vr, bool is_far) {
+    const int t = lane & 3;
+    if (vr < 16) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t in = halves_below(2 * t + 8 * b, vr);
+        vs[b] = make_uint4(vs[b].x & in, vs[b].y & in, vs[b].z & in, vs[b].w & in);
+        vz[b] = make_uint4(vz[b].x & in, vz[b].y & in, vz[b].z & in, vz[b].w & in);
+      }
+    }
+    if (is_far) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) vs[b] = mul4(vs[b], far_scale<BV>()), vz[b] = mul4(vz[b], far_scale<BV>());
+    }
+    // matrix m of a store: element 4 g + c of a group of 32, c = c0 + (m >> 1), keys of half m & 1; lane l gives the
+    // address of row l & 7 of matrix l >> 3
+    const int mb = (lane >> 3) & 1, mc = lane >> 4, r8 = lane & 7;
+    const uint32_t at = dst + 128 * (8 * mc + r8) + (((2 * i + mb) ^ r8) << 4);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+#pragma unroll
+      for (int c0 = 0; c0 < 4; c0 += 2) {
+        uint32_t x[4];
+        if (BV == 4) {
+          const uint32_t w = u4at(vc[q >> 1], 2 * (q & 1) + (c0 >> 1)), w8 = w >> 8;
+          x[0] = low_codes(w), x[1] = low_codes(w8), x[2] = high_codes(w), x[3] = high_codes(w8);
+        } else {
+          const uint32_t wa = u4at(vc[BV == 4 ? 0 : q], c0), wb = u4at(vc[BV == 4 ? 0 : q], c0 + 1);
+          x[0] = even_codes(wa), x[1] = odd_codes(wa), x[2] = even_codes(wb), x[3] = odd_codes(wb);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) x[m] = hfma2_u(x[m], u4at(vs[m & 1], q), u4at(vz[m & 1], q));
+        stmatrix_x4(at + 128 * (32 * q + 8 * c0), x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+};
 
 // One warp: query row r of a tile as fp16 in the order of the keys' elements, scaled by a power of two, and the
 // factor of its products (log2 units); v: the lane's elements 4 lane ..  A row that is not finite becomes NaN.
@@ -284,56 +314,113 @@ __device__ __forceinline__ void query_to_half(uint2 v, int lane, uint8_t* dst, i
   if (lane == 0) *factor = bad ? 1.f : kLog2Scale * __int_as_float((127 + max(-100, min(e - 14, 88))) << 23);
 }
 
+// ---- roles --------------------------------------------------------------------------------
+// The block's warps work apart and meet at mbarriers:
+//   softmax  two groups of four warps, a query row a thread: group t works on jobs t, t + 2, .. of a tile
+//   codes    four warps: query rows, then page by page the codes to fp16, a 16-row tile a warp
+//   mma      one thread: S = Q K^T and O += P V
+//   copy     the tiles of the block's run, one after another, and their pages
+// A tile of more than 128 query rows is a pair: each unit is two jobs, one for each half of the
+// rows, so that one half's products overlap the other's exponentials.  A smaller tile's
+// units are one job each and alternate between the groups, whose states are joined at the end.
+constexpr int kCodeWarp = 8, kMmaWarp = 12, kCopyWarp = 13, kThreads = 14 * 32;
+constexpr int kTiles = 4;   // tiles of the run that are known ahead
+constexpr int kVPages = 3;  // pages of values in fp16
+
 // Shared memory of the block.
 template <int BK, int BV>
 struct Smem {
-  static constexpr int kQ = 0, kK = kQ + 2 * kRegion, kV = kK + 2 * kRegion, kRaw = kV + 2 * kRegion;
-  static constexpr int kBytes = kRaw + kUnitPages * QFmt<BK, BV>::kBlock + 1024;
+  static constexpr int kQ = 0, kK = kQ + 4 * kRegion, kV = kK + 4 * kRegion, kRaw = kV + kVPages * kRegion;
+  static constexpr int kSlots = (227 * 1024 - 6 * 1024 - kRaw) / QFmt<BK, BV>::kBlock;  // pages of codes
+  static constexpr int kBytes = kRaw + kSlots * QFmt<BK, BV>::kBlock + 1024;
+  static_assert(kSlots >= 2, "two pages under way");
 };
 
+// A tile: units [w0, w1) of query rows row0 .. of KV head h of a segment.
+struct Tile {
+  const int32_t* table;
+  int w0, w1;            // w1 == 0: no tile is left
+  int len, t0, row0, n_rows, h;
+  int pair, whole;       // more than 128 rows; all of its units are this block's
+};
+// A segment that the block's run meets.
+struct Entry {
+  int64_t cum;
+  int32_t len, t0, rows, seq;
+};
+
+struct Bars {
+  uint64_t raw_full[8], raw_empty[8];
+  uint64_t k_full[2], k_empty[2], v_full[kVPages], v_empty[kVPages];
+  uint64_t q_full, q_empty;
+  uint64_t tile_full[kTiles], tile_empty[kTiles];
+  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], joined, drained;
+};
+// Barrier of the four code warps: whether some thread says so.
+__device__ __forceinline__ bool codes_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x)
+      : "memory");
+  return r;
+}
+
 template <int BK, int BV, bool kShared>
-__global__ void __launch_bounds__(kThreads, 1) span_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant__ Params p) {
   using F = QFmt<BK, BV>;
   using M = Smem<BK, BV>;
+  constexpr int kSlots = M::kSlots;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ __align__(8) uint64_t full, done;
+  __shared__ __align__(8) Bars bar;
   __shared__ uint32_t s_tmem;
-  __shared__ int64_t s_warp[kThreads / 32], s_pos, s_end;
-  __shared__ Shares s_sh;
-  __shared__ struct {
-    int64_t base, x0, x1;
-    int len, t0, rows, seq, W, grp;
-  } s_seg;
-  __shared__ float s_factor[kRows];
-  __shared__ int s_valid[kUnitPages];
+  __shared__ int64_t s_warp[kThreads / 32];
+  __shared__ int64_t s_pos, s_end;
+  __shared__ int s_first;
+  __shared__ Tile s_tile[kTiles];
+  __shared__ float s_factor[2][2 * kRows];
+  __shared__ int s_valid[8];            // rows of the page in a slot
+  __shared__ volatile uint32_t s_unit[4];  // rows of a unit's two pages (8 bits each), whether they are far (bits 16, 17)
+  __shared__ int s_abort;
+  volatile int* abort_flag = &s_abort;
   constexpr int kPer = (HYQ_PAGED_MAX_BATCH + kThreads - 1) / kThreads;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    mbar_init(&full, 1);
-    mbar_init(&done, 1);
+    s_abort = 0;
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.k_full[i], 4), mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.o_full[i], 1), mbar_init(&bar.o_empty[i], 4);
+    }
+    for (int i = 0; i < kVPages; ++i) mbar_init(&bar.v_full[i], 4), mbar_init(&bar.v_empty[i], 1);
+    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 13);
+    mbar_init(&bar.q_full, 4), mbar_init(&bar.q_empty, 1);
+    mbar_init(&bar.joined, 4), mbar_init(&bar.drained, 1);
     mbar_fence_init();
   }
-  if (warp == 0) tc_alloc(&s_tmem, kTmemCols);
+  if (warp == kMmaWarp) tc_alloc(&s_tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   chain_kernel();
 
-  // ---- the segments, kPer neighbours a thread ------------------------------------
-  Seg seg[kPer];
-  int64_t cum[kPer + 1];
+  // ---- the segments, kPer neighbours a thread; those of this block's run are listed ---------
+  Entry* list = p.list + (size_t)blockIdx.x * HYQ_PAGED_MAX_BATCH;
   {
-    int64_t w = 0;
+    Seg seg[kPer];
+    int64_t cum[kPer + 1], w = 0;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int i = tid * kPer + k;
       seg[k] = Seg{0, 0, 0, -1};
       if (i < p.n_seg) seg[k] = segment<kShared>(p, i, blockIdx.x == 0);
       cum[k] = w;
-      w += (int64_t)p.HKV * ((seg[k].rows + kRows - 1) / kRows) * units_of(seg[k].len);
+      w += (int64_t)p.HKV * head_slots(seg[k].len, seg[k].rows);
     }
     cum[kPer] = w;
     int64_t pre = w;
@@ -351,255 +438,542 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const Params p) {
     }
 #pragma unroll
     for (int k = 0; k <= kPer; ++k) cum[k] += before;
+    const int64_t nb = max((int64_t)1, min((int64_t)gridDim.x, total));
+    Shares sh;
+    sh.each = total / nb;
+    sh.more = total - sh.each * nb;
+    const int64_t pos = sh.begin(min((int64_t)blockIdx.x, nb)), end = sh.begin(min((int64_t)blockIdx.x + 1, nb));
     if (tid == 0) {
-      const int64_t nb = max((int64_t)1, min((int64_t)gridDim.x, total));
-      s_sh.each = total / nb;
-      s_sh.more = total - s_sh.each * nb;
-      s_pos = s_sh.begin(min((int64_t)blockIdx.x, nb));
-      s_end = s_sh.begin(min((int64_t)blockIdx.x + 1, nb));
-      if (blockIdx.x == 0) p.plan->sh = s_sh;
+      s_pos = pos, s_end = end;
+      if (blockIdx.x == 0) p.plan->sh = sh;
     }
-    if (blockIdx.x == 0)
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        const int i = tid * kPer + k;
-        if (i < p.n_seg) {
-          p.plan->cum[i] = cum[k];
-          p.plan->len[i] = seg[k].len;
-          p.plan->t0[i] = seg[k].t0;
-          p.plan->rows[i] = seg[k].rows;
-        }
+    for (int k = 0; k < kPer; ++k) {
+      const int i = tid * kPer + k;
+      if (i >= p.n_seg) break;
+      if (cum[k] < end && cum[k + 1] > pos) list[i] = Entry{cum[k], seg[k].len, seg[k].t0, seg[k].rows, seg[k].seq};
+      else if (cum[k] < end) list[i].rows = 0;
+      if (cum[k] <= pos && pos < cum[k + 1]) s_first = i;
+      if (blockIdx.x == 0) {
+        p.plan->cum[i] = cum[k];
+        p.plan->len[i] = seg[k].len;
+        p.plan->t0[i] = seg[k].t0;
+        p.plan->rows[i] = seg[k].rows;
       }
+    }
   }
   __syncthreads();
-  uint32_t nfull = 0, ndone = 0;  // phases waited for
-  bool dead = false;
 
-  while (true) {
-    // ---- the tile that the run meets next ------------------------------------------
-    const int64_t pos = s_pos, end = s_end;
-    __syncthreads();
-    if (pos >= end) break;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (cum[k] <= pos && pos < cum[k + 1]) {
-        const int W = (int)units_of(seg[k].len);
-        const int64_t off = pos - cum[k];
-        const int grp = (int)(off / W);
-        const int64_t x0 = off - (int64_t)grp * W, x1 = min((int64_t)W, x0 + (end - pos));
-        s_seg.base = cum[k] + (int64_t)grp * W + kCost;
-        s_seg.x0 = x0, s_seg.x1 = x1;
-        s_seg.len = seg[k].len, s_seg.t0 = seg[k].t0, s_seg.rows = seg[k].rows, s_seg.seq = seg[k].seq;
-        s_seg.W = W, s_seg.grp = grp;
-        s_pos = pos + (x1 - x0);
-      }
-    __syncthreads();
-    const int w0 = max(0, (int)s_seg.x0 - kCost), w1 = (int)s_seg.x1 - kCost, n_units = s_seg.W - kCost;
-    if (w1 <= 0) continue;  // the fixed work alone: the next block's
-    const int n_mt = (s_seg.rows + kRows - 1) / kRows, h = s_seg.grp / n_mt, mt = s_seg.grp - h * n_mt;
-    const int row0 = mt * kRows, n_rows = min(kRows, s_seg.rows - row0), len = s_seg.len;
-    const int32_t* table = p.pv.table + (size_t)s_seg.seq * p.pv.max_blocks;
-    // ---- the query rows ---------------------------------------------------------------
-    for (int r = warp; r < kRows; r += kThreads / 32) {
-      uint2 v = make_uint2(0, 0);
-      if (r < n_rows) {
-        const int tok = (row0 + r) / p.gq;
-        v = *reinterpret_cast<const uint2*>(p.q + (size_t)(s_seg.t0 + tok) * p.ldq +
-                                            (size_t)(h * p.gq + row0 + r - tok * p.gq) * HYQ_D + 4 * lane);
-      }
-      query_to_half<BK>(v, lane, sm + M::kQ, r, s_factor + r);
+  auto wait = [&](uint64_t& b, uint32_t parity) {
+    const bool ok = mbar_wait_or_abort(&b, parity & 1u, abort_flag);
+    if (!ok && !*abort_flag) {
+      *abort_flag = 1;
+      hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
     }
-    float m = -INFINITY, l = 0.f;
-    int vfar = 0;  // O is held times 2^-kFar
-    __syncthreads();
-    const float f = s_factor[tid & (kRows - 1)];
-    const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    return ok;
+  };
+  auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(b, parity)); };
+  auto units_jobs = [](const Tile& t) { return (t.w1 - t.w0) * (t.pair ? 2 : 1); };
 
-    for (int u = w0; u < w1 && !dead; ++u) {
-      // ---- the unit's pages ------------------------------------------------------------
-      if (tid == 0) {
-        uint32_t bytes = 0;
-        int page[kUnitPages];
-        for (int k = 0; k < kUnitPages; ++k) {
-          const int blk = u * kUnitPages + k, left = len - blk * HYQ_PAGE_ROWS;
-          page[k] = left > 0 ? table[blk] : -1;
-          const bool in = (uint32_t)page[k] < (uint32_t)p.pv.n_pages;
-          if (left > 0 && !in) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
-          s_valid[k] = in ? min(left, HYQ_PAGE_ROWS) : 0;
-          bytes += in ? F::kBlock : 0;
+  if (warp == kCopyWarp) {
+    // ---------------- the run's tiles and their pages ---------------------------------------
+    int64_t pos = s_pos;
+    const int64_t end = s_end;
+    int i = pos < end ? s_first : 0;
+    uint32_t n_tile = 0, n_page = 0;
+    bool ok = true;
+    while (ok) {
+      Tile t;
+      t.w1 = 0;
+      while (pos < end) {  // a tile of which the run has more than fixed work
+        const Entry e = list[i];
+        const int U = n_units(e.len);
+        const int64_t per = head_slots(e.len, e.rows);
+        if (e.rows == 0 || pos >= e.cum + per * p.HKV) {
+          ++i;
+          continue;
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        mbar_arrive_expect_tx(&full, bytes);
-        for (int k = 0; k < kUnitPages; ++k)
-          if (s_valid[k])
-            bulk_g2s(sm + M::kRaw + k * F::kBlock, p.pv.pool + ((size_t)page[k] * p.HKV + h) * F::kBlock, F::kBlock, &full);
-      }
-      __syncthreads();
-      if (!mbar_wait(&full, nfull & 1u)) dead = true;
-      ++nfull;
-      // ---- codes to fp16: a tile of 16 rows a warp -------------------------------------
-      const int pg = warp >> 2, ti = warp & 3, vr = s_valid[pg] - 16 * ti;
-      const uint8_t* tb = sm + M::kRaw + pg * F::kBlock + ti * F::kTile;
-      const bool kf = !dead && key_meta_far<BK>(tb + F::kKMeta, lane, vr);
-      const bool vf = !dead && value_meta_far<BV>(tb + F::kVMeta, lane, vr);
-      const bool kfar = __syncthreads_or(kf);
-      const int vnew = __syncthreads_or(vf) | vfar;
-      if (__syncthreads_or(dead)) {
-        dead = true;
-        if (tid == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
+        const int h = (int)((pos - e.cum) / per);
+        const int64_t off = pos - e.cum - per * h;
+        const int n_mt = (e.rows + kPair - 1) / kPair, mt = (int)min((int64_t)n_mt - 1, off / (kCost + 2 * U));
+        const int n_rows = min(kPair, e.rows - mt * kPair), nt = n_rows > kRows ? 2 : 1;
+        const int64_t x0 = off - (int64_t)mt * (kCost + 2 * U);
+        const int W = kCost + nt * U, x1 = (int)min((int64_t)W, x0 + (end - pos));
+        pos += x1 - x0;
+        const int a = unit_from((int)x0, nt), b = unit_from(x1, nt);
+        if (a >= b) continue;
+        t = Tile{p.pv.table + (size_t)e.seq * p.pv.max_blocks, a, b, e.len, e.t0, mt * kPair, n_rows, h, nt == 2, a == 0 && b == U};
         break;
       }
-      keys_to_half<BK>(tb, tb + F::kKMeta, lane, sm + M::kK, 64 * pg + 16 * ti, kfar);
-      values_to_half<BV>(tb + F::kVCode, tb + F::kVMeta, lane, smem_u32(sm + M::kV) + pg * kRegion, ti, vr, vnew);
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-        const uint32_t idesc = tc_idesc(0, 0, kRows, kKeys);
-        for (int k = 0; k < 8; ++k)
-          tc_mma_f16(tmem + kColS, tc_desc_sw128(smem_u32(sm + M::kQ) + (k >> 2) * kRegion + 32 * (k & 3)),
-                     tc_desc_sw128(smem_u32(sm + M::kK) + (k >> 2) * kRegion + 32 * (k & 3)), idesc, k > 0);
-        tc_commit(&done);
+      const uint32_t slot = n_tile % kTiles;
+      ok = wait_warp(bar.tile_empty[slot], (n_tile / kTiles) ^ 1);
+      if (!ok) break;
+      if (lane == 0) {
+        s_tile[slot] = t;
+        mbar_arrive(&bar.tile_full[slot]);
       }
-      if (!mbar_wait(&done, ndone & 1u)) dead = true;
-      ++ndone;
-      if (__syncthreads_or(dead)) {
-        dead = true;
-        if (tid == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
-        break;
-      }
-      tc_fence_after();
-      // ---- softmax: a row a thread --------------------------------------------------------
-      if (tid < kRows) {
-        const int v0 = s_valid[0], v1 = s_valid[1];
-        const bool whole = v0 == HYQ_PAGE_ROWS && v1 == HYQ_PAGE_ROWS;
-        // the maximum is kept as a product, in units of unscaled keys, and taken off before the factor is applied:
-        // a large logit's rounding then cannot come out as an exponent
-        const float up = kfar ? (float)(1 << kFar<BK>) : 1.f, fac = f * up;
-        auto load = [&](int c, float (&x)[32]) {
-          uint32_t r[32];
-          tc_ld32(t_lane + kColS + 32 * c, r);
-          tc_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(r[i]);
-            if (!whole && key_of(32 * (c & 1) + i) >= (c < 2 ? v0 : v1)) x[i] = -INFINITY;
-          }
-        };
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          float x[32];
-          load(c, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) mx = fmaxf(mx, x[i]);
-        }
-        const float top = mx * up;
-        float corr = 1.f;
-        if ((top - m) * f > kSlack) {
-          corr = ex2((m - top) * f);
-          m = top;
-          l *= corr;
-        }
-        if (vnew && !vfar) corr *= 1.f / (float)(1 << kFar<BV>);
-        if (u > w0 && __any_sync(0xffffffffu, corr != 1.f)) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t r[32];
-            tc_ld32(t_lane + kColO + 32 * c, r);
-            tc_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * corr);
-            tc_st32(t_lane + kColO + 32 * c, r);
-          }
-        }
-        const float nm = m == -INFINITY ? 0.f : -m / up;
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          uint32_t w[32];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x[32];
-            load(c + k, x);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              x[i] = ex2(fmaf(x[i] + nm, fac, kLift));
-              l += x[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)  // positions 2 i, 2 i + 1
-              w[16 * k + i] = pack_f16x2(x[key_row(2 * i)], x[key_row(2 * i + 1)]);
-          }
-          tc_st32(t_lane + kColP + 16 * c, w);
-        }
-        tc_wait_st();
-      }
-      vfar = vnew;
-      tc_fence_before();
-      __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-        const uint32_t idesc = tc_idesc(0, 0, kRows, HYQ_D);
-        for (int k = 0; k < 8; ++k)
-          tc_mma_f16_ts(tmem + kColO, tmem + kColP + 8 * k,
-                        tc_desc_sw128(smem_u32(sm + M::kV) + (k >> 2) * kRegion + 32 * (k & 3)), idesc, u > w0 || k > 0);
-        tc_commit(&done);
-      }
-      if (!mbar_wait(&done, ndone & 1u)) dead = true;
-      ++ndone;
-      tc_fence_after();
-      if (__syncthreads_or(dead)) {
-        dead = true;
-        if (tid == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
-      }
-    }
-    // ---- the tile's result, or this run's part of it --------------------------------------
-    if (tid < kRows && !dead) {
-      const bool whole = !kShared && w0 == 0 && w1 == n_units;
-      const float scale = vfar ? (float)(1 << kFar<BV>) : 1.f, inv = whole ? (l > 0.f ? scale / l : l) : scale;
-      float* part = p.part + ((size_t)blockIdx.x * 2 + (w0 == 0 ? 1 : 0)) * kPart;
-      const int tok = (row0 + tid) / p.gq;
-      __nv_bfloat16* out = p.out + ((size_t)(s_seg.t0 + tok) * p.HQ + h * p.gq + row0 + tid - tok * p.gq) * HYQ_D;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t r[32];
-        tc_ld32(t_lane + kColO + 32 * q, r);
-        tc_wait_ld();
-        if (tid < n_rows) {
-          float x[32];  // in the order of the elements
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[elem_of(i)] = __uint_as_float(r[i]) * inv;
-          if (whole) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(out + 32 * q + 8 * c) =
-                  make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
-                             pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              *reinterpret_cast<float4*>(part + ((8 * q + c) * kRows + tid) * 4) =
-                  make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
-          }
+      __syncwarp();
+      ++n_tile;
+      if (t.w1 == 0) break;
+      const int p0 = t.w0 * kUnitPages, np = min(t.w1 * kUnitPages, (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS) - p0;
+      const uint8_t* heads = p.pv.pool + (size_t)t.h * F::kBlock;
+      int cur = lane < np ? t.table[p0 + lane] : -1, nxt = 32 + lane < np ? t.table[p0 + 32 + lane] : -1;
+      for (int j = 0; j < np; ++j) {
+        const int pg = __shfl_sync(0xffffffffu, cur, j & 31);
+        const uint32_t sl = n_page % kSlots;
+        ok = wait_warp(bar.raw_empty[sl], (n_page / kSlots) ^ 1);
+        if (!ok) break;
+        if (lane == sl) {  // copies that one thread issues complete one after another
+          const bool in = (uint32_t)pg < (uint32_t)p.pv.n_pages;
+          if (!in) hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
+          s_valid[sl] = in ? min(HYQ_PAGE_ROWS, t.len - (p0 + j) * HYQ_PAGE_ROWS) : 0;
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+          mbar_arrive_expect_tx(&bar.raw_full[sl], in ? F::kBlock : 0);
+          if (in) bulk_g2s(sm + M::kRaw + sl * F::kBlock, heads + (size_t)pg * p.HKV * F::kBlock, F::kBlock, &bar.raw_full[sl]);
         }
         __syncwarp();
+        ++n_page;
+        if ((j & 31) == 31) {
+          cur = nxt;
+          nxt = j + 33 + lane < np ? t.table[p0 + j + 33 + lane] : -1;
+        }
       }
-      if (!whole && tid < n_rows)
-        *reinterpret_cast<float2*>(part + kRows * HYQ_D + 2 * tid) = make_float2(m * f - kLift, l);
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    if (!ok)  // copies in flight land before the block's shared memory goes
+      for (uint32_t n = n_page > kSlots ? n_page - kSlots : 0; n < n_page; ++n)
+        (void)mbar_wait(&bar.raw_full[n % kSlots], (n / kSlots) & 1u);
+  } else if (warp == kMmaWarp) {
+    // ---------------- products -----------------------------------------------------------------
+    if (lane == 0) {
+      struct Cursor {
+        Tile t;
+        uint32_t n;  // tiles before
+        int j, jobs;
+      } cq, cv;
+      bool ok = true;
+      auto open = [&](Cursor& c) {
+        ok = wait(bar.tile_full[c.n % kTiles], c.n / kTiles);
+        if (!ok) return;
+        c.t = s_tile[c.n % kTiles];
+        c.j = 0;
+        c.jobs = units_jobs(c.t);
+      };
+      const uint64_t dQ = tc_desc_sw128(smem_u32(sm + M::kQ)), dK = tc_desc_sw128(smem_u32(sm + M::kK)),
+                     dV = tc_desc_sw128(smem_u32(sm + M::kV));
+      constexpr uint64_t kStep = kRegion >> 4;
+      uint32_t kn = 0, vn = 0, pn[2] = {0, 0}, on[2] = {0, 0};
+      bool busy[2] = {false, false};
+      cq.n = cv.n = 0;
+      open(cq);
+      if (ok) open(cv);
+      while (ok) {
+        while (ok && cq.t.w1 && !busy[cq.j & 1]) {
+          const int t = cq.j & 1, u = cq.t.w0 + (cq.t.pair ? cq.j >> 1 : cq.j);
+          if (cq.j == 0) ok = wait(bar.q_full, cq.n);
+          if (ok && (!cq.t.pair || t == 0)) ok = wait(bar.k_full[kn & 1], kn >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          const bool half = u * kKeys + HYQ_PAGE_ROWS >= cq.t.len;  // one page
+          const uint32_t idesc = half ? tc_idesc(0, 0, kRows, HYQ_PAGE_ROWS) : tc_idesc(0, 0, kRows, kKeys);
+          const uint64_t a = dQ + (cq.t.pair ? t : 0) * 2 * kStep, b = dK + (kn & 1) * 2 * kStep;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t off = (k >> 2) * kStep + 2 * (k & 3);
+            tc_mma_f16(tmem + kColS + kKeys * t, a + off, b + off, idesc, k > 0);
+          }
+          tc_commit(&bar.s_full[t]);
+          busy[t] = true;
+          if (!cq.t.pair || t == 1) tc_commit(&bar.k_empty[kn & 1]), ++kn;
+          if (++cq.j == cq.jobs) {
+            tc_commit(&bar.q_empty);
+            ++cq.n;
+            open(cq);
+          }
+        }
+        if (!ok || cv.t.w1 == 0) break;
+        const int t = cv.j & 1, u = cv.t.w0 + (cv.t.pair ? cv.j >> 1 : cv.j);
+        const int pages = u * kKeys + HYQ_PAGE_ROWS >= cv.t.len ? 1 : 2;
+        if (cv.j < 2) ok = wait(bar.o_empty[t], on[t] ^ 1);
+        if (ok) ok = wait(bar.p_full[t], pn[t]);
+        if (!ok) break;
+        ++pn[t];
+        tc_fence_after();
+        for (int k = 0; ok && k < pages; ++k) {
+          const uint32_t n = vn + k, sl = n % kVPages;
+          if (!cv.t.pair || t == 0) {
+            ok = wait(bar.v_full[sl], n / kVPages);
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            tc_mma_f16_ts(tmem + kColO + HYQ_D * t, tmem + kColS + kKeys * t + 32 * k + 8 * x, dV + sl * kStep + 2 * x,
+                          tc_idesc(0, 0, kRows, HYQ_D), cv.j >= 2 || k > 0 || x > 0);
+          if (!cv.t.pair || t == 1) tc_commit(&bar.v_empty[sl]);
+        }
+        if (!ok) break;
+        if (!cv.t.pair || t == 1) vn += pages;
+        busy[t] = false;
+        if (cv.j + 2 >= cv.jobs) tc_commit(&bar.o_full[t]), ++on[t];
+        if (++cv.j == cv.jobs) {
+          mbar_arrive(&bar.tile_empty[cv.n % kTiles]);
+          ++cv.n;
+          open(cv);
+        }
+      }
+      tc_commit(&bar.drained);  // every product has finished
+      (void)mbar_wait(&bar.drained, 0);
+    }
+  } else if (warp >= kCodeWarp) {
+    // ---------------- query rows and codes ----------------------------------------------------
+    const int cw = warp - kCodeWarp;
+    uint32_t n_tile = 0, n_page = 0, kn = 0;
+    bool ok = true, stop = false, far = false;
+    while (true) {
+      // The four warps meet at the same barriers whatever becomes of a wait, and stop together.
+      ok = ok && wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
+      if (codes_any(!ok)) break;
+      const Tile t = s_tile[n_tile % kTiles];
+      if (t.w1 == 0) break;
+      ok = wait_warp(bar.q_empty, n_tile ^ 1);
+      if (ok) {
+        constexpr int kAhead = 16;
+        const int rows = t.pair ? kPair : kRows;
+        for (int r0 = cw; r0 < rows; r0 += 4 * kAhead) {
+          uint2 v[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int r = r0 + 4 * k;
+            v[k] = make_uint2(0, 0);
+            if (r < t.n_rows) {
+              const int tok = (t.row0 + r) / p.gq;
+              v[k] = *reinterpret_cast<const uint2*>(p.q + (size_t)(t.t0 + tok) * p.ldq +
+                                                     (size_t)(t.h * p.gq + t.row0 + r - tok * p.gq) * HYQ_D + 4 * lane);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            const int r = r0 + 4 * k;
+            if (r < rows)
+              query_to_half<BK>(v[k], lane, sm + M::kQ + (r / kRows) * 2 * kRegion, r % kRows, &s_factor[n_tile & 1][r]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.q_full);
+      }
+      far = false;  // a tile's own: O starts anew
+      const int last = (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS;
+      for (int u = t.w0; u < t.w1; ++u, ++kn) {
+        uint32_t info = 0;
+        const uint32_t ks = kn & 1;
+        uint8_t* kd = sm + M::kK + ks * 2 * kRegion;
+        ok = ok && wait_warp(bar.k_empty[ks], (kn >> 1) ^ 1);
+        const int pages = min(kUnitPages, last - u * kUnitPages);
+        for (int k = 0; k < pages; ++k, ++n_page) {
+          const uint32_t sl = n_page % kSlots;
+          ok = ok && wait_warp(bar.raw_full[sl], n_page / kSlots);
+          TileCodes<BK, BV> x;
+          int valid = 0;
+          bool mine = false;
+          if (ok) {
+            valid = s_valid[sl];
+            x.load(sm + M::kRaw + sl * F::kBlock + cw * F::kTile, lane);
+            mine = x.far(lane, valid - 16 * cw);
+          }
+          if (codes_any(mine || !ok)) {  // seldom: rows beyond fp16, or the end
+            if (codes_any(!ok)) {
+              stop = true;
+              break;
+            }
+            far = true;
+          }
+          if (lane == 0) mbar_arrive(&bar.raw_empty[sl]);  // (all lanes have met at the barrier)
+          x.keys(kd, lane, HYQ_PAGE_ROWS * k + 16 * cw, far);
+          info |= (uint32_t)valid << (8 * k) | (uint32_t)far << (16 + k);
+          if (k + 1 == pages) {
+            if (pages == 1) info |= (uint32_t)far << 17;
+            if (cw == 0 && lane == 0) s_unit[kn & 3] = info;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.k_full[ks]);
+          }
+          const uint32_t vs = n_page % kVPages;
+          ok = wait_warp(bar.v_empty[vs], (n_page / kVPages) ^ 1);
+          if (!ok) continue;
+          x.values(smem_u32(sm + M::kV) + vs * kRegion, lane, cw, valid - 16 * cw, far);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.v_full[vs]);
+        }
+        if (stop) break;
+      }
+      if (stop) break;
+      if (lane == 0) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
+      ++n_tile;
+    }
+  } else {
+    // ---------------- softmax: a query row a thread ---------------------------------------------
+    const int t = warp >> 2, rr = tid & (kRows - 1);
+    const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = t_lane + kColS + kKeys * t, tO = t_lane + kColO + HYQ_D * t;
+    uint32_t n_tile = 0, n_unit = 0, sn = 0, on = 0, joins = 0;
+    bool ok = true;
+    while (true) {
+      ok = wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
+      if (!ok) break;
+      const Tile tile = s_tile[n_tile % kTiles];
+      if (tile.w1 == 0) break;
+      const int U = tile.w1 - tile.w0, jobs = tile.pair ? U : (U + 1 - t) / 2;
+      const int r = rr + (tile.pair ? kRows * t : 0);
+      const bool idle = (r & ~31) >= tile.n_rows;  // no row of the warp is one
+      float m = -INFINITY, l = 0.f, f = 1.f;
+      bool far = false;
+      for (int j = 0; j < jobs; ++j) {
+        ok = wait_warp(bar.s_full[t], sn++);
+        if (!ok) break;
+        if (idle) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.p_full[t]);
+          continue;
+        }
+        tc_fence_after();
+        if (j == 0) f = s_factor[n_tile & 1][r];
+        const uint32_t info = s_unit[(n_unit + (tile.pair ? j : 2 * j + t)) & 3];
+        const int v0 = info & 0xFF, v1 = (info >> 8) & 0xFF;
+        const bool far0 = info & 0x10000, far1 = info & 0x20000, full = v0 == HYQ_PAGE_ROWS && v1 == HYQ_PAGE_ROWS;
+        const int chunks = (tile.w0 + (tile.pair ? j : 2 * j + t)) * kKeys + HYQ_PAGE_ROWS >= tile.len ? 2 : 4;
+        const float up0 = far0 ? (float)(1 << kFar<BK>) : 1.f, up1 = far1 ? (float)(1 << kFar<BK>) : 1.f;
+        const float lift0 = far1 && !far0 ? kLift - kFar<BV> : kLift;
+        uint32_t w[64];
+        float sum[2];
+        auto load = [&](int c, float (&x)[32]) {
+          uint32_t y[32];
+          tc_ld32(tS + 32 * c, y);
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(y[i]);
+          if (!full) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (key_of(32 * (c & 1) + i) >= (c < 2 ? v0 : v1)) x[i] = -INFINITY;
+          }
+        };
+        // probabilities of a page against the present reference.  kSafe: the reference is taken off first,
+        // so that a large logit's rounding cannot come out as an exponent.
+        auto probs = [&](auto safe) {
+          constexpr bool kSafe = decltype(safe)::value;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            sum[hf] = 0.f;
+            if (2 * hf >= chunks) continue;
+            const float fac = f * (hf ? up1 : up0), lift = hf ? kLift : lift0;
+            const uint64_t fac2 = f2_splat(fac), nm2 = f2_splat(kSafe ? (m == -INFINITY ? 0.f : -m / (hf ? up1 : up0)) : fmaf(-m, f, lift)),
+                           lift2 = f2_splat(lift);
+            uint64_t acc[2] = {0, 0};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float x[32];
+              load(2 * hf + c, x);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {  // positions 2 i, 2 i + 1
+                uint64_t e = f2_pack(x[key_row(2 * i)], x[key_row(2 * i + 1)]);
+                e = kSafe ? f2_fma(f2_add(e, nm2), fac2, lift2) : f2_fma(e, fac2, nm2);
+                e = f2_pack(ex2(f2_lo(e)), ex2(f2_hi(e)));
+                acc[i & 1] = f2_add(acc[i & 1], e);
+                w[32 * hf + 16 * c + i] = pack_f16x2(f2_lo(e), f2_hi(e));
+              }
+            }
+            acc[0] = f2_add(acc[0], acc[1]);
+            sum[hf] = f2_lo(acc[0]) + f2_hi(acc[0]);
+          }
+        };
+        float corr = 1.f;
+        bool again = __any_sync(0xffffffffu, !(fabsf(m * f) <= 4096.f));
+        if (!again) {
+          probs(std::false_type{});
+          again = __any_sync(0xffffffffu, !(fmaxf(sum[0], sum[1]) <= 32768.f));
+        }
+        if (again) {
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            float x[32];
+            load(c, x);
+            float y = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) y = fmax3(y, x[i], x[i + 1]);
+            mx = fmaxf(mx, y * (c < 2 ? up0 : up1));
+          }
+          if ((mx - m) * f > 0.f) {
+            corr = ex2((m - mx) * f);
+            m = mx;
+          }
+          probs(std::true_type{});
+        }
+        const float s0 = lift0 == kLift ? sum[0] : sum[0] * (float)(1 << kFar<BV>);
+        l = fmaf(l, corr, s0 + sum[1]);
+        if (far1 && !far) corr *= 1.f / (float)(1 << kFar<BV>);
+        far = far1;
+        if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {  // (the products so far are done: S came after them)
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            tc_ld32(tO + 32 * c, y);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+            tc_st32(tO + 32 * c, y);
+          }
+        }
+        // P takes the place of S
+        {
+          uint32_t y[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = w[i];
+          tc_st32(tS, y);
+          if (chunks > 2) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = w[32 + i];
+            tc_st32(tS + 32, y);
+          }
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.p_full[t]);
+      }
+      if (!ok) break;
+      n_unit += U;
+      // ---- the tile's result, or this run's part of it -----------------------------------------
+      const bool two = !tile.pair && U > 1;  // both groups have a state of the same rows
+      if (jobs) {
+        ok = wait_warp(bar.o_full[t], on++);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      float* half = p.half + ((size_t)blockIdx.x * 2 + (joins & 1)) * (kPart / 2);
+      if (two && t == 1 && !idle) {  // group 1 hands its state over
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t y[32];
+          tc_ld32(tO + 32 * q, y);
+          tc_wait_ld();
+          if (r < tile.n_rows) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(half + ((8 * q + c) * kRows + r) * 4) = make_uint4(y[c], y[8 + c], y[16 + c], y[24 + c]);
+          }
+          __syncwarp();
+        }
+        if (r < tile.n_rows)
+          *reinterpret_cast<float2*>(half + kRows * HYQ_D + 2 * r) = make_float2(m * f - kLift, far ? -l : l);
+      }
+      if (two && t == 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.joined);
+      }
+      if (two && t == 0) {
+        ok = wait_warp(bar.joined, joins);
+        if (!ok) break;
+      }
+      if (two) ++joins;
+      if (jobs && !idle && (tile.pair || t == 0)) {
+        // the group's own state and, with weights, the other group's and that of the rows' own positions
+        float M0 = m * f - kLift, w0 = far ? (float)(1 << kFar<BV>) : 1.f, w1 = 0.f, w2 = 0.f, L = l;
+        const int tok = tile.t0 + (tile.row0 + r) / p.gq, head = tile.h * p.gq + (tile.row0 + r) % p.gq;
+        const bool row = r < tile.n_rows;
+        if (two && row) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(half + kRows * HYQ_D) + r);
+          const bool far2 = ml.y < 0.f;
+          const float top = fmaxf(M0, ml.x), ref = top == -INFINITY ? 0.f : top, a = ex2(M0 - ref), b = ex2(ml.x - ref);
+          L = L * a + fabsf(ml.y) * b;
+          w0 *= a;
+          w1 = b * (far2 ? (float)(1 << kFar<BV>) : 1.f);
+          M0 = top;
+        }
+        const float* rest = nullptr;
+        bool write = row;
+        if (kShared && tile.whole && row) {
+          write = shared_len(p.shared, p.pv, p.seqs, tok / p.n_q, p.batch, p.n_q) > 0;  // (else the join's)
+          rest = p.rest + ((size_t)tok * p.HQ + head) * kPartFloats;
+          const float2 ml = *reinterpret_cast<const float2*>(rest + HYQ_D);
+          const float top = fmaxf(M0, ml.x), ref = top == -INFINITY ? 0.f : top, a = ex2(M0 - ref), b = ex2(ml.x - ref);
+          L = L * a + ml.y * b;
+          w0 *= a, w1 *= a, w2 = b;
+        }
+        if (tile.whole) {
+          const float inv = L > 0.f ? 1.f / L : L;
+          w0 *= inv, w1 *= inv, w2 *= inv;
+        }
+        float* part = p.part + ((size_t)blockIdx.x * 2 + (tile.w0 == 0 ? 1 : 0)) * kPart;
+        __nv_bfloat16* out = p.out + ((size_t)tok * p.HQ + head) * HYQ_D;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t y[32];
+          tc_ld32(tO + 32 * q, y);
+          tc_wait_ld();
+          if (write) {
+            float x[32];  // in the order of the elements
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[elem_of(i)] = __uint_as_float(y[i]) * w0;
+            if (two) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(half) + (8 * q + c) * kRows + r);
+                x[4 * c] = fmaf(v.x, w1, x[4 * c]), x[4 * c + 1] = fmaf(v.y, w1, x[4 * c + 1]);
+                x[4 * c + 2] = fmaf(v.z, w1, x[4 * c + 2]), x[4 * c + 3] = fmaf(v.w, w1, x[4 * c + 3]);
+              }
+            }
+            if (kShared && tile.whole) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const float4 v = *(reinterpret_cast<const float4*>(rest) + 8 * q + c);
+                x[4 * c] = fmaf(v.x, w2, x[4 * c]), x[4 * c + 1] = fmaf(v.y, w2, x[4 * c + 1]);
+                x[4 * c + 2] = fmaf(v.z, w2, x[4 * c + 2]), x[4 * c + 3] = fmaf(v.w, w2, x[4 * c + 3]);
+              }
+            }
+            if (tile.whole) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(out + 32 * q + 8 * c) =
+                    make_uint4(pack_bf16x2(x[8 * c], x[8 * c + 1]), pack_bf16x2(x[8 * c + 2], x[8 * c + 3]),
+                               pack_bf16x2(x[8 * c + 4], x[8 * c + 5]), pack_bf16x2(x[8 * c + 6], x[8 * c + 7]));
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<float4*>(part + ((8 * q + c) * kPair + r) * 4) =
+                    make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+            }
+          }
+          __syncwarp();
+        }
+        if (!tile.whole && row) *reinterpret_cast<float2*>(part + kPair * HYQ_D + 2 * r) = make_float2(M0, L);
+      }
+      if (jobs) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.o_empty[t]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
+      ++n_tile;
+    }
   }
+  tc_fence_before();
   __syncthreads();
-  if (warp == 0) tc_dealloc(tmem, kTmemCols);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tc_dealloc(tmem, kTmemCols);
+  }
 }
 
 // The parts of a row in run order, then (shared) what its own positions gave; eight rows of a KV head a block,
 // a thread four elements.
 constexpr int kJoinThreads = 256;
 template <bool kShared>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   chain_kernel();
   const int lane = threadIdx.x & 31, d4 = 4 * (threadIdx.x >> 5) + (lane >> 3);
   const int64_t per = ((int64_t)p.n_tokens * p.gq + 7) / 8, items = per * p.HKV;
@@ -634,15 +1008,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
       a.w = fmaf(a.w, c0, v.w * c1);
     };
     if (len > 0) {
-      const int r = (tok - plan.t0[i]) * p.gq + head, mt = r / kRows, rr = r - mt * kRows;
-      const int n_mt = (plan.rows[i] + kRows - 1) / kRows, n_units = (int)units_of(len) - kCost;
-      const int64_t base = plan.cum[i] + ((int64_t)h * n_mt + mt) * (n_units + kCost) + kCost;
-      const int c0 = plan.sh.owner(base), c1 = plan.sh.owner(base + n_units - 1);
-      if (!kShared && c0 == c1) continue;  // written by its block
+      const int U = n_units(len), r = (tok - plan.t0[i]) * p.gq + head, mt = r / kPair, rr = r - mt * kPair;
+      const int nt = min(kPair, plan.rows[i] - mt * kPair) > kRows ? 2 : 1;
+      const int64_t base = plan.cum[i] + h * head_slots(len, plan.rows[i]) + (int64_t)mt * (kCost + 2 * U) + kCost;
+      const int c0 = plan.sh.owner(base), c1 = plan.sh.owner(base + (int64_t)nt * (U - 1));
+      if (c0 == c1) continue;  // written by its block
       for (int c = c0; c <= c1; ++c) {
         const float* part = p.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart;
-        add(__ldcg(reinterpret_cast<const float2*>(part + kRows * HYQ_D) + rr),
-            __ldcg(reinterpret_cast<const float4*>(part) + d4 * kRows + rr));
+        // a run that ends before a pair's second half of a unit may have nothing of the tile
+        if (c > c0 && !holds(plan.sh, c, base, nt, U)) continue;
+        add(__ldcg(reinterpret_cast<const float2*>(part + kPair * HYQ_D) + rr),
+            __ldcg(reinterpret_cast<const float4*>(part) + d4 * kPair + rr));
       }
     }
     if (kShared) {
@@ -678,7 +1054,8 @@ cudaError_t launch_bits(const hyq_config* c, const Params& p, cudaStream_t s) {
 }
 
 size_t plan_bytes() { return hyq_align256(sizeof(Plan)); }
-size_t parts_bytes() { return hyq_align256((size_t)hyq_num_sms() * 2 * kPart * 4); }
+size_t list_bytes() { return hyq_align256((size_t)hyq_num_sms() * HYQ_PAGED_MAX_BATCH * sizeof(Entry)); }
+size_t parts_bytes() { return list_bytes() + hyq_align256((size_t)hyq_num_sms() * 3 * kPart * 4); }
 size_t rest_bytes(const hyq_config* c, int32_t batch, int32_t n_q) {
   return hyq_align256((size_t)batch * n_q * c->num_q_heads * kPartFloats * 4);
 }
@@ -693,7 +1070,9 @@ Params params(const hyq_config* c, const PageView& pv, const int32_t* seqs, int3
   p.ldq = ldq;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.plan = static_cast<Plan*>(ws);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + plan_bytes());
+  p.list = reinterpret_cast<Entry*>(static_cast<char*>(ws) + plan_bytes());
+  p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + plan_bytes() + list_bytes());
+  p.half = p.part + (size_t)hyq_num_sms() * 2 * kPart;
   p.HQ = c->num_q_heads;
   p.HKV = c->num_kv_heads;
   p.gq = p.HQ / p.HKV;
