@@ -31,7 +31,7 @@ constexpr int kCost = 6;     // jobs (128 rows of a unit) that a tile's fixed wo
 constexpr int kRegion = 16384;  // 128 rows of 128 bytes, 128-byte swizzled
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;  // two of each
 constexpr float kLog2Scale = 0.1275174307366466f;  // log2(e) / sqrt(128)
-constexpr float kLift = 8.f;    // probabilities at a new maximum: 2^kLift
+constexpr float kSlack = 6.f, kLift = 8.f;         // probabilities at the row's maximum: 2^kLift .. 2^(kLift + kSlack)
 
 // Values beyond fp16: a unit in which c s + z may pass 65504 is taken times 2^-kFar.
 template <int B>
@@ -180,46 +180,36 @@ __device__ __forceinline__ uint32_t far_scale() {  // 2^-kFar, twice
   return f | f << 16;
 }
 
-// A 16-row tile of codes in a warp's registers.
+// Whether a step and zero (two of each) may take c s + z out of fp16: the largest code's, as bits without sign.
+template <int B>
+__device__ __forceinline__ uint32_t largest(uint32_t s, uint32_t z) {
+  return hfma2_u(s, B == 4 ? 0x4B804B80u : 0x5BF85BF8u, z) & 0x7FFF7FFFu;  // 15, 255
+}
+__device__ __forceinline__ bool leaves_fp16(uint32_t most) { return (most >> 16) >= 0x7C00u || (most & 0xFFFFu) >= 0x7C00u; }
+
+// The keys of a 16-row tile of codes in a warp's registers.
 template <int BK, int BV>
-struct TileCodes {
+struct KeyTile {
   using F = QFmt<BK, BV>;
-  uint4 kc[BK / 2], vc[BV / 2];  // code words, 512 bytes of the region each
-  uint4 ka, kb;                  // keys' steps and zeros of rows g, g + 8
-  uint4 vs[2], vz[2];            // values' of rows 2t + 8b and the next, groups 0 .. 3
+  uint4 kc[BK / 2];  // code words, 512 bytes of the region each
+  uint4 ka, kb;      // steps and zeros of rows g, g + 8
 
   __device__ __forceinline__ void load(const uint8_t* tb, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2;
 #pragma unroll
     for (int i = 0; i < BK / 2; ++i) kc[i] = *reinterpret_cast<const uint4*>(tb + 512 * i + 16 * lane);
-#pragma unroll
-    for (int i = 0; i < BV / 2; ++i) vc[i] = *reinterpret_cast<const uint4*>(tb + F::kVCode + 512 * i + 16 * lane);
     ka = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
     kb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      vs[b] = *reinterpret_cast<const uint4*>(tb + F::kVMeta + 16 * (t + 4 * b));
-      vz[b] = *reinterpret_cast<const uint4*>(tb + F::kVMeta + 128 + 16 * (t + 4 * b));
-    }
   }
-  // Whether some c s + z of this lane's rows below vr may leave fp16 (the largest code's does).
-  __device__ __forceinline__ bool far(int lane, int vr) const {
-    const int g = lane >> 2, t = lane & 3;
-    constexpr uint32_t k = BK == 4 ? 0x4B804B80u : 0x5BF85BF8u, v = BV == 4 ? 0x4B804B80u : 0x5BF85BF8u;  // 15, 255
-    auto top = [](uint32_t s, uint32_t q, uint32_t z) { return hfma2_u(s, q, z) & 0x7FFF7FFFu; };
-    const uint32_t a = __vmaxu2(top(ka.x, k, ka.z), top(ka.y, k, ka.w)), b = __vmaxu2(top(kb.x, k, kb.z), top(kb.y, k, kb.w));
-    uint32_t most = __vmaxu2(g < vr ? a : 0u, g + 8 < vr ? b : 0u);
-#pragma unroll
-    for (int b2 = 0; b2 < 2; ++b2) {
-      const uint32_t c = __vmaxu2(__vmaxu2(top(vs[b2].x, v, vz[b2].x), top(vs[b2].y, v, vz[b2].y)),
-                                  __vmaxu2(top(vs[b2].z, v, vz[b2].z), top(vs[b2].w, v, vz[b2].w)));
-      most = __vmaxu2(most, c & halves_below(2 * t + 8 * b2, vr));
-    }
-    return (most >> 16) >= 0x7C00u || (most & 0xFFFFu) >= 0x7C00u;
+  __device__ __forceinline__ bool far(int lane, int vr) const {  // of this lane's rows below vr
+    const int g = lane >> 2;
+    const uint32_t a = __vmaxu2(largest<BK>(ka.x, ka.z), largest<BK>(ka.y, ka.w));
+    const uint32_t b = __vmaxu2(largest<BK>(kb.x, kb.z), largest<BK>(kb.y, kb.w));
+    return leaves_fp16(__vmaxu2(g < vr ? a : 0u, g + 8 < vr ? b : 0u));
   }
   // The keys as fp16 rows row0 .. row0 + 15 of the key operand at `dst` (two regions of 64 elements).  Of 8-bit codes
   // the four elements of each half of a group of 32 lie beside those of the other half (query rows are ordered alike).
-  __device__ __forceinline__ void keys(uint8_t* dst, int lane, int row0, bool is_far) {
+  __device__ __forceinline__ void store(uint8_t* dst, int lane, int row0, bool is_far) {
     const int g = lane >> 2, t = lane & 3;
     if (is_far) ka = mul4(ka, far_scale<BK>()), kb = mul4(kb, far_scale<BK>());
     uint8_t* at = dst + 128 * key_row(row0 + g);  // row g + 8 lies 8 rows on, swizzled alike
@@ -251,9 +241,33 @@ struct TileCodes {
                                                         hfma2_u(xb[2], sb, zb), hfma2_u(xb[3], sb, zb));
     }
   }
+};
+
+// Its values.
+template <int BK, int BV>
+struct ValueTile {
+  using F = QFmt<BK, BV>;
+  uint4 vc[BV / 2];
+  uint4 vs[2], vz[2];  // steps and zeros of rows 2t + 8b and the next, groups 0 .. 3
+
+  // Word `lane` of the steps (rows 2 (lane / 4) and the next, group lane % 4) and of the zeros: whether one below vr is far.
+  static __device__ __forceinline__ bool far(const uint8_t* tb, int lane, int vr) {
+    const uint32_t* m = reinterpret_cast<const uint32_t*>(tb + F::kVMeta) + lane;
+    return leaves_fp16(largest<BV>(m[0], m[32]) & halves_below(2 * (lane >> 2), vr));
+  }
+  __device__ __forceinline__ void load(const uint8_t* tb, int lane) {
+    const int t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < BV / 2; ++i) vc[i] = *reinterpret_cast<const uint4*>(tb + F::kVCode + 512 * i + 16 * lane);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      vs[b] = *reinterpret_cast<const uint4*>(tb + F::kVMeta + 16 * (t + 4 * b));
+      vz[b] = *reinterpret_cast<const uint4*>(tb + F::kVMeta + 128 + 16 * (t + 4 * b));
+    }
+  }
   // The values, transposed, as keys 16 i .. 16 i + 15 of the value operand's region `dst` (rows: elements in the
   // order of elem_of); rows from vr on are zero.
-  __device__ __forceinline__ void values(uint32_t dst, int lane, int i, int vr, bool is_far) {
+  __device__ __forceinline__ void store(uint32_t dst, int lane, int i, int vr, bool is_far) {
     const int t = lane & 3;
     if (vr < 16) {
 #pragma unroll
@@ -291,39 +305,17 @@ struct TileCodes {
   }
 };
 
-// One warp: query row r of a tile as fp16 in the order of the keys' elements, scaled by a power of two, and the
-// factor of its products (log2 units); v: the lane's elements 4 lane ..  A row that is not finite becomes NaN.
-template <int BK>
-__device__ __forceinline__ void query_to_half(uint2 v, int lane, uint8_t* dst, int r, float* factor) {
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-  float am = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y)));
-  const bool nan = a.x != a.x || a.y != a.y || b.x != b.x || b.y != b.y;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  const bool bad = __any_sync(0xffffffffu, nan) || !(am <= 3.402823466e38f);
-  // 2^(e - 1) <= am < 2^e; subnormal queries count as 2^-126
-  const int e = am > 0.f ? max((__float_as_int(am) >> 23) - 126, -125) : 14;
-  // two steps: 2^(14 - e) alone may leave float32
-  const float s1 = __int_as_float((127 + (14 - e) / 2) << 23), s2 = __int_as_float((127 + (14 - e) - (14 - e) / 2) << 23);
-  uint2 w = make_uint2(pack_f16x2(a.x * s1 * s2, a.y * s1 * s2), pack_f16x2(b.x * s1 * s2, b.y * s1 * s2));
-  if (bad) w = make_uint2(0x7FFF7FFFu, 0x7FFF7FFFu);
-  const int vg = lane >> 3, el = BK == 4 ? 4 * lane : 32 * vg + 8 * (lane & 3) + 4 * ((lane >> 2) & 1);
-  *reinterpret_cast<uint2*>(dst + (el >> 6) * kRegion + swz(r, (el & 63) >> 3) + 2 * (el & 7)) = w;
-  // past 2^88 logits differ by more than any exponent holds, or not at all; below 2^-100 they are all alike
-  if (lane == 0) *factor = bad ? 1.f : kLog2Scale * __int_as_float((127 + max(-100, min(e - 14, 88))) << 23);
-}
-
 // ---- roles --------------------------------------------------------------------------------
 // The block's warps work apart and meet at mbarriers:
 //   softmax  two groups of four warps, a query row a thread: group t works on jobs t, t + 2, .. of a tile
-//   codes    four warps: query rows, then page by page the codes to fp16, a 16-row tile a warp
+//   codes    four warps for keys, four for values: a tile's query rows, then page by page the codes to fp16, 16 rows a
+//            warp
 //   mma      one thread: S = Q K^T and O += P V
 //   copy     the tiles of the block's run, one after another, and their pages
 // A tile of more than 128 query rows is a pair: each unit is two jobs, one for each half of the
 // rows, so that one half's products overlap the other's exponentials.  A smaller tile's
 // units are one job each and alternate between the groups, whose states are joined at the end.
-constexpr int kCodeWarp = 8, kMmaWarp = 12, kCopyWarp = 13, kThreads = 14 * 32;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kCopyWarp = 17, kThreads = 18 * 32;
 constexpr int kTiles = 4;   // tiles of the run that are known ahead
 constexpr int kVPages = 3;  // pages of values in fp16
 
@@ -349,6 +341,68 @@ struct Entry {
   int32_t len, t0, rows, seq;
 };
 
+// The query rows of a tile as fp16 in the order of the keys' elements, each scaled by a power of two, and the factors of
+// their products (log2 units).  A row that is not finite becomes NaN.  Eight warps, two rows of each at a time, a lane
+// eight elements of one.
+template <int BK>
+__device__ __noinline__ void load_queries(const Params& p, const Tile& t, int warp, int lane, uint8_t* dst, float* factor) {
+  constexpr int kAhead = 4;  // pairs of rows under way, and as many in hand
+  const int half = lane >> 4, l = lane & 15, rows = t.pair ? kPair : kRows;
+  const int dt = 16 / p.gq, dh = 16 - dt * p.gq;
+  int tok = (t.row0 + 2 * warp + half) / p.gq, head = t.row0 + 2 * warp + half - tok * p.gq;
+  const __nv_bfloat16* q = p.q + (size_t)t.t0 * p.ldq + (size_t)t.h * p.gq * HYQ_D + 8 * l;
+  auto fetch = [&](int r0, uint4 (&v)[kAhead]) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (r0 + 16 * k + half < t.n_rows) v[k] = *reinterpret_cast<const uint4*>(q + (size_t)tok * p.ldq + head * HYQ_D);
+      tok += dt, head += dh;
+      if (head >= p.gq) head -= p.gq, ++tok;
+    }
+  };
+  uint4 v[kAhead], next[kAhead];
+  fetch(2 * warp, v);
+#pragma unroll 1
+  for (int r0 = 2 * warp; r0 < rows; r0 += 16 * kAhead) {
+    fetch(r0 + 16 * kAhead, next);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int r = r0 + 16 * k + half;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u4at(v[k], i) << 16);
+        x[2 * i + 1] = __uint_as_float(u4at(v[k], i) & 0xFFFF0000u);
+      }
+      float am = 0.f, z = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) am = fmaxf(am, fabsf(x[i])), z = fmaf(x[i], 0.f, z);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+      const bool bad = (__ballot_sync(0xffffffffu, z != 0.f) >> (16 * half)) & 0xFFFFu;  // (NaN: infinities too)
+      // 2^(e - 1) <= am < 2^e; subnormal queries count as 2^-126
+      const int e = am > 0.f ? max((__float_as_int(am) >> 23) - 126, -125) : 14;
+      // two steps: 2^(14 - e) alone may leave float32
+      const float s1 = __int_as_float((127 + (14 - e) / 2) << 23), s2 = __int_as_float((127 + (14 - e) - (14 - e) / 2) << 23);
+      uint4 w = make_uint4(pack_f16x2(x[0] * s1 * s2, x[1] * s1 * s2), pack_f16x2(x[2] * s1 * s2, x[3] * s1 * s2),
+                           pack_f16x2(x[4] * s1 * s2, x[5] * s1 * s2), pack_f16x2(x[6] * s1 * s2, x[7] * s1 * s2));
+      if (bad) w = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+      uint8_t* to = dst + (r / kRows) * 2 * kRegion + (l >> 3) * kRegion;
+      const int rr = r % kRows;
+      if (BK == 4) {
+        *reinterpret_cast<uint4*>(to + swz(rr, l & 7)) = w;
+      } else {  // elements 32 v + 16 i + 4 t lie at 32 v + 8 t + 4 i
+        const int c = 4 * ((l >> 2) & 1) + 2 * (l & 1), h8 = 8 * ((l >> 1) & 1);
+        *reinterpret_cast<uint2*>(to + swz(rr, c) + h8) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(to + swz(rr, c + 1) + h8) = make_uint2(w.z, w.w);
+      }
+      // past 2^88 logits differ by more than any exponent holds, or not at all; below 2^-100 they are all alike
+      if (l == 0) factor[r] = bad ? 1.f : kLog2Scale * __int_as_float((127 + max(-100, min(e - 14, 88))) << 23);
+      v[k] = next[k];
+    }
+  }
+}
+
 struct Bars {
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k_full[2], k_empty[2], v_full[kVPages], v_empty[kVPages];
@@ -356,15 +410,37 @@ struct Bars {
   uint64_t tile_full[kTiles], tile_empty[kTiles];
   uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], joined, drained;
 };
-// Barrier of the four code warps: whether some thread says so.
+// Barrier of the four key or value warps: whether some thread says so.
+template <int kId>
 __device__ __forceinline__ bool codes_any(bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)x)
+      : "r"((uint32_t)x), "n"(kId)
       : "memory");
   return r;
+}
+
+__device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done;
+}
+// Out of line, as the loops below are rolled: the roles' code has to stay in the SM's
+// instruction cache together (unrolled and inlined throughout, two of three fetches missed it,
+// and the whole took three times as long).
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
+  if (mbar_wait_or_abort(bar, parity, abort_flag)) return true;
+  if (!*abort_flag) {
+    *abort_flag = 1;
+    hyq_set_err(err, HYQ_DEVERR_TIMEOUT);
+  }
+  return false;
 }
 
 template <int BK, int BV, bool kShared>
@@ -382,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   __shared__ Tile s_tile[kTiles];
   __shared__ float s_factor[2][2 * kRows];
   __shared__ int s_valid[8];            // rows of the page in a slot
-  __shared__ volatile uint32_t s_unit[4];  // rows of a unit's two pages (8 bits each), whether they are far (bits 16, 17)
+  __shared__ volatile uint32_t s_unit[4];  // rows of a unit's two pages (8 bits each), whether their keys are far (bits 16, 17), their values (18, 19)
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   constexpr int kPer = (HYQ_PAGED_MAX_BATCH + kThreads - 1) / kThreads;
@@ -390,15 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 4);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4), mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_full[i], 1), mbar_init(&bar.o_empty[i], 4);
     }
     for (int i = 0; i < kVPages; ++i) mbar_init(&bar.v_full[i], 4), mbar_init(&bar.v_empty[i], 1);
-    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 13);
-    mbar_init(&bar.q_full, 4), mbar_init(&bar.q_empty, 1);
+    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 17);
+    mbar_init(&bar.q_full, 8), mbar_init(&bar.q_empty, 1);
     mbar_init(&bar.joined, 4), mbar_init(&bar.drained, 1);
     mbar_fence_init();
   }
@@ -465,12 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   __syncthreads();
 
   auto wait = [&](uint64_t& b, uint32_t parity) {
-    const bool ok = mbar_wait_or_abort(&b, parity & 1u, abort_flag);
-    if (!ok && !*abort_flag) {
-      *abort_flag = 1;
-      hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
-    }
-    return ok;
+    return mbar_try(&b, parity & 1u) || wait_long(&b, parity & 1u, abort_flag, p.pv.err);
   };
   auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(b, parity)); };
   auto units_jobs = [](const Tile& t) { return (t.w1 - t.w0) * (t.pair ? 2 : 1); };
@@ -624,94 +695,85 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
       tc_commit(&bar.drained);  // every product has finished
       (void)mbar_wait(&bar.drained, 0);
     }
-  } else if (warp >= kCodeWarp) {
+  } else if (warp >= kKeyWarp) {
     // ---------------- query rows and codes ----------------------------------------------------
-    const int cw = warp - kCodeWarp;
-    uint32_t n_tile = 0, n_page = 0, kn = 0;
-    bool ok = true, stop = false, far = false;
-    while (true) {
-      // The four warps meet at the same barriers whatever becomes of a wait, and stop together.
-      ok = ok && wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
-      if (codes_any(!ok)) break;
-      const Tile t = s_tile[n_tile % kTiles];
-      if (t.w1 == 0) break;
-      ok = wait_warp(bar.q_empty, n_tile ^ 1);
-      if (ok) {
-        constexpr int kAhead = 16;
-        const int rows = t.pair ? kPair : kRows;
-        for (int r0 = cw; r0 < rows; r0 += 4 * kAhead) {
-          uint2 v[kAhead];
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int r = r0 + 4 * k;
-            v[k] = make_uint2(0, 0);
-            if (r < t.n_rows) {
-              const int tok = (t.row0 + r) / p.gq;
-              v[k] = *reinterpret_cast<const uint2*>(p.q + (size_t)(t.t0 + tok) * p.ldq +
-                                                     (size_t)(t.h * p.gq + t.row0 + r - tok * p.gq) * HYQ_D + 4 * lane);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int r = r0 + 4 * k;
-            if (r < rows)
-              query_to_half<BK>(v[k], lane, sm + M::kQ + (r / kRows) * 2 * kRegion, r % kRows, &s_factor[n_tile & 1][r]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.q_full);
-      }
-      far = false;  // a tile's own: O starts anew
-      const int last = (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS;
-      for (int u = t.w0; u < t.w1; ++u, ++kn) {
-        uint32_t info = 0;
-        const uint32_t ks = kn & 1;
-        uint8_t* kd = sm + M::kK + ks * 2 * kRegion;
-        ok = ok && wait_warp(bar.k_empty[ks], (kn >> 1) ^ 1);
-        const int pages = min(kUnitPages, last - u * kUnitPages);
-        for (int k = 0; k < pages; ++k, ++n_page) {
-          const uint32_t sl = n_page % kSlots;
-          ok = ok && wait_warp(bar.raw_full[sl], n_page / kSlots);
-          TileCodes<BK, BV> x;
-          int valid = 0;
-          bool mine = false;
-          if (ok) {
-            valid = s_valid[sl];
-            x.load(sm + M::kRaw + sl * F::kBlock + cw * F::kTile, lane);
-            mine = x.far(lane, valid - 16 * cw);
-          }
-          if (codes_any(mine || !ok)) {  // seldom: rows beyond fp16, or the end
-            if (codes_any(!ok)) {
-              stop = true;
-              break;
-            }
-            far = true;
-          }
-          if (lane == 0) mbar_arrive(&bar.raw_empty[sl]);  // (all lanes have met at the barrier)
-          x.keys(kd, lane, HYQ_PAGE_ROWS * k + 16 * cw, far);
-          info |= (uint32_t)valid << (8 * k) | (uint32_t)far << (16 + k);
-          if (k + 1 == pages) {
-            if (pages == 1) info |= (uint32_t)far << 17;
-            if (cw == 0 && lane == 0) s_unit[kn & 3] = info;
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.k_full[ks]);
-          }
-          const uint32_t vs = n_page % kVPages;
-          ok = wait_warp(bar.v_empty[vs], (n_page / kVPages) ^ 1);
-          if (!ok) continue;
-          x.values(smem_u32(sm + M::kV) + vs * kRegion, lane, cw, valid - 16 * cw, far);
+    // The four warps of a kind meet at the same barriers whatever becomes of a wait, and stop together.  A page
+    // whose c s + z may leave fp16 is taken down; values then stay so to the end of the tile, whose O has one scale.
+    auto codes = [&](auto kind) {
+      constexpr bool kKeys = decltype(kind)::value;
+      constexpr int kId = kKeys ? 1 : 2;
+      const int cw = warp & 3;
+      uint32_t n_tile = 0, n_page = 0, kn = 0;
+      bool ok = true;
+      while (true) {
+        ok = ok && wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
+        if (codes_any<kId>(!ok)) return;
+        const Tile& t = s_tile[n_tile % kTiles];
+        const int w0 = t.w0, w1 = t.w1, last = (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS;
+        if (w1 == 0) return;
+        ok = wait_warp(bar.q_empty, n_tile ^ 1);
+        if (ok) {
+          load_queries<BK>(p, t, warp - kKeyWarp, lane, sm + M::kQ, s_factor[n_tile & 1]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.v_full[vs]);
+          if (lane == 0) mbar_arrive(&bar.q_full);
         }
-        if (stop) break;
+        bool vfar = false;
+        uint32_t info = 0;
+#pragma unroll 1
+        for (int pg = w0 * kUnitPages; pg < min(w1 * kUnitPages, last); ++pg, ++n_page) {
+          const uint32_t sl = n_page % kSlots;
+          ok = ok && wait_warp(bar.raw_full[sl], n_page / kSlots);
+          typename std::conditional<kKeys, KeyTile<BK, BV>, ValueTile<BK, BV>>::type x;
+          int valid = 0;
+          bool kf = false, vf = false;
+          if (ok) {
+            const uint8_t* tb = sm + M::kRaw + sl * F::kBlock + cw * F::kTile;
+            valid = s_valid[sl];
+            x.load(tb, lane);
+            if constexpr (kKeys) kf = x.far(lane, valid - 16 * cw);
+            vf = ValueTile<BK, BV>::far(tb, lane, valid - 16 * cw);
+          }
+          if (codes_any<kId>(kf || vf || !ok)) {  // seldom
+            if (codes_any<kId>(!ok)) return;
+            kf = codes_any<kId>(kf);
+            vfar |= codes_any<kId>(vf);
+          }
+          if (lane == 0) mbar_arrive(&bar.raw_empty[sl]);  // (all lanes have met at the barrier)
+          if constexpr (kKeys) {
+            const uint32_t ks = kn & 1, k = pg & 1;
+            if (k == 0) {
+              ok = wait_warp(bar.k_empty[ks], (kn >> 1) ^ 1);
+              info = 0;
+            }
+            if (!ok) continue;
+            x.store(sm + M::kK + ks * 2 * kRegion, lane, HYQ_PAGE_ROWS * k + 16 * cw, kf);
+            info |= (uint32_t)valid << (8 * k) | (uint32_t)kf << (16 + k) | (uint32_t)vfar << (18 + k);
+            if (k == 1 || pg + 1 == last) {
+              if (k == 0) info |= (uint32_t)vfar << 19;
+              if (cw == 0 && lane == 0) s_unit[kn & 3] = info;
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar.k_full[ks]);
+              ++kn;
+            }
+          } else {
+            const uint32_t vs = n_page % kVPages;
+            ok = wait_warp(bar.v_empty[vs], (n_page / kVPages) ^ 1);
+            if (!ok) continue;
+            x.store(smem_u32(sm + M::kV) + vs * kRegion, lane, cw, valid - 16 * cw, vfar);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.v_full[vs]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
+        ++n_tile;
       }
-      if (stop) break;
-      if (lane == 0) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
-      ++n_tile;
-    }
+    };
+    if (warp < kValueWarp) codes(std::true_type{});
+    else codes(std::false_type{});
   } else {
     // ---------------- softmax: a query row a thread ---------------------------------------------
     const int t = warp >> 2, rr = tid & (kRows - 1);
@@ -742,12 +804,9 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
         if (j == 0) f = s_factor[n_tile & 1][r];
         const uint32_t info = s_unit[(n_unit + (tile.pair ? j : 2 * j + t)) & 3];
         const int v0 = info & 0xFF, v1 = (info >> 8) & 0xFF;
-        const bool far0 = info & 0x10000, far1 = info & 0x20000, full = v0 == HYQ_PAGE_ROWS && v1 == HYQ_PAGE_ROWS;
+        const bool far0 = info & 0x40000, far1 = info & 0x80000, full = v0 == HYQ_PAGE_ROWS && v1 == HYQ_PAGE_ROWS;
         const int chunks = (tile.w0 + (tile.pair ? j : 2 * j + t)) * kKeys + HYQ_PAGE_ROWS >= tile.len ? 2 : 4;
-        const float up0 = far0 ? (float)(1 << kFar<BK>) : 1.f, up1 = far1 ? (float)(1 << kFar<BK>) : 1.f;
-        const float lift0 = far1 && !far0 ? kLift - kFar<BV> : kLift;
-        uint32_t w[64];
-        float sum[2];
+        const float up0 = info & 0x10000 ? (float)(1 << kFar<BK>) : 1.f, up1 = info & 0x20000 ? (float)(1 << kFar<BK>) : 1.f;
         auto load = [&](int c, float (&x)[32]) {
           uint32_t y[32];
           tc_ld32(tS + 32 * c, y);
@@ -755,65 +814,36 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(y[i]);
           if (!full) {
+            const int v = (c < 2 ? v0 : v1) - 32 * (c & 1);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (key_of(32 * (c & 1) + i) >= (c < 2 ? v0 : v1)) x[i] = -INFINITY;
+              if (key_of(i) >= v) x[i] = -INFINITY;
           }
         };
-        // probabilities of a page against the present reference.  kSafe: the reference is taken off first,
-        // so that a large logit's rounding cannot come out as an exponent.
-        auto probs = [&](auto safe) {
-          constexpr bool kSafe = decltype(safe)::value;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            sum[hf] = 0.f;
-            if (2 * hf >= chunks) continue;
-            const float fac = f * (hf ? up1 : up0), lift = hf ? kLift : lift0;
-            const uint64_t fac2 = f2_splat(fac), nm2 = f2_splat(kSafe ? (m == -INFINITY ? 0.f : -m / (hf ? up1 : up0)) : fmaf(-m, f, lift)),
-                           lift2 = f2_splat(lift);
-            uint64_t acc[2] = {0, 0};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float x[32];
-              load(2 * hf + c, x);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {  // positions 2 i, 2 i + 1
-                uint64_t e = f2_pack(x[key_row(2 * i)], x[key_row(2 * i + 1)]);
-                e = kSafe ? f2_fma(f2_add(e, nm2), fac2, lift2) : f2_fma(e, fac2, nm2);
-                e = f2_pack(ex2(f2_lo(e)), ex2(f2_hi(e)));
-                acc[i & 1] = f2_add(acc[i & 1], e);
-                w[32 * hf + 16 * c + i] = pack_f16x2(f2_lo(e), f2_hi(e));
-              }
-            }
-            acc[0] = f2_add(acc[0], acc[1]);
-            sum[hf] = f2_lo(acc[0]) + f2_hi(acc[0]);
-          }
-        };
-        float corr = 1.f;
-        bool again = __any_sync(0xffffffffu, !(fabsf(m * f) <= 4096.f));
-        if (!again) {
-          probs(std::false_type{});
-          again = __any_sync(0xffffffffu, !(fmaxf(sum[0], sum[1]) <= 32768.f));
-        }
-        if (again) {
-          float mx = -INFINITY;
+        float mx = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < chunks; ++c) {
-            float x[32];
-            load(c, x);
-            float y = -INFINITY;
+        for (int c = 0; c < chunks; ++c) {
+          float x[32];
+          load(c, x);
+          float y[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) y = fmax3(y, x[i], x[i + 1]);
-            mx = fmaxf(mx, y * (c < 2 ? up0 : up1));
+          for (int i = 4; i < 32; i += 8) {
+            y[0] = fmax3(y[0], x[i], x[i + 1]);
+            y[1] = fmax3(y[1], x[i + 2], x[i + 3]);
+            if (i + 4 < 32) {
+              y[2] = fmax3(y[2], x[i + 4], x[i + 5]);
+              y[3] = fmax3(y[3], x[i + 6], x[i + 7]);
+            }
           }
-          if ((mx - m) * f > 0.f) {
-            corr = ex2((m - mx) * f);
-            m = mx;
-          }
-          probs(std::true_type{});
+          mx = fmaxf(mx, fmax3(fmaxf(y[0], y[1]), y[2], y[3]) * (c < 2 ? up0 : up1));
         }
-        const float s0 = lift0 == kLift ? sum[0] : sum[0] * (float)(1 << kFar<BV>);
-        l = fmaf(l, corr, s0 + sum[1]);
+        // The reference stands at a maximum that may lag by kSlack, in units of products.
+        float corr = 1.f;
+        if ((mx - m) * f > kSlack) {
+          corr = ex2((m - mx) * f);
+          m = mx;
+          l *= corr;
+        }
         if (far1 && !far) corr *= 1.f / (float)(1 << kFar<BV>);
         far = far1;
         if (j > 0 && __any_sync(0xffffffffu, corr != 1.f)) {  // (the products so far are done: S came after them)
@@ -827,18 +857,43 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
             tc_st32(tO + 32 * c, y);
           }
         }
-        // P takes the place of S
-        {
-          uint32_t y[32];
+        // Probabilities; they take the place of products that have been read.  Of rows whose logits are large the
+        // reference is taken off before the factor is applied: its rounding would come out as an exponent.
+        const float ref = m == -INFINITY ? 0.f : m;  // (nothing is seen yet, or the row is NaN)
+        auto probs = [&](auto large) {
+          constexpr bool kLarge = decltype(large)::value;
+#pragma unroll 1
+          for (int c = 0; c < chunks; ++c) {
+            const bool low = far1 && !far0 && c < 2;  // of values that are not taken down in a unit whose others are
+            const float up = c < 2 ? up0 : up1, lift = low ? kLift - kFar<BV> : kLift;
+            const uint64_t nm2 = f2_splat(kLarge ? -ref / up : fmaf(-ref, f, lift)),
+                           fac2 = f2_splat(f * up), lift2 = f2_splat(lift);
+            float x[32];
+            load(c, x);
+            uint64_t acc[2] = {0, 0};
+            uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = w[i];
-          tc_st32(tS, y);
-          if (chunks > 2) {
+            for (int b = 0; b < 4; ++b) {
+              float e[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = w[32 + i];
-            tc_st32(tS + 32, y);
+              for (int i = 0; i < 4; ++i) {
+                uint64_t y = f2_pack(x[8 * b + 2 * i], x[8 * b + 2 * i + 1]);
+                y = kLarge ? f2_fma(f2_add(y, nm2), fac2, lift2) : f2_fma(y, fac2, nm2);
+                e[2 * i] = ex2(f2_lo(y)), e[2 * i + 1] = ex2(f2_hi(y));
+                acc[i & 1] = f2_add(acc[i & 1], f2_pack(e[2 * i], e[2 * i + 1]));
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)  // positions 2 i, 2 i + 1
+                w[4 * b + i] = pack_f16x2(e[key_row(2 * i)], e[key_row(2 * i + 1)]);
+            }
+            acc[0] = f2_add(acc[0], acc[1]);
+            const float sum = f2_lo(acc[0]) + f2_hi(acc[0]);
+            l += low ? sum * (float)(1 << kFar<BV>) : sum;
+            tc_st16(tS + 16 * c, w);
           }
-        }
+        };
+        if (__any_sync(0xffffffffu, fabsf(ref * f) > 4096.f)) probs(std::true_type{});
+        else probs(std::false_type{});
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
