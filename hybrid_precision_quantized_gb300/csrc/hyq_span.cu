@@ -310,12 +310,12 @@ struct ValueTile {
 //   softmax  two groups of four warps, a query row a thread: group t works on jobs t, t + 2, .. of a tile
 //   codes    four warps for keys, four for values: a tile's query rows, then page by page the codes to fp16, 16 rows a
 //            warp
-//   mma      one thread: S = Q K^T and O += P V
+//   mma      two warps, one thread of each issues: S = Q K^T; O += P V
 //   copy     the tiles of the block's run, one after another, and their pages
 // A tile of more than 128 query rows is a pair: each unit is two jobs, one for each half of the
 // rows, so that one half's products overlap the other's exponentials.  A smaller tile's
 // units are one job each and alternate between the groups, whose states are joined at the end.
-constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kCopyWarp = 17, kThreads = 18 * 32;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kPvWarp = 17, kCopyWarp = 18, kThreads = 19 * 32;
 constexpr int kTiles = 4;   // tiles of the run that are known ahead
 constexpr int kVPages = 3;  // pages of values in fp16
 
@@ -408,7 +408,7 @@ struct Bars {
   uint64_t k_full[2], k_empty[2], v_full[kVPages], v_empty[kVPages];
   uint64_t q_full, q_empty;
   uint64_t tile_full[kTiles], tile_empty[kTiles];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2], joined, drained;
+  uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_empty[2], joined, drained;
 };
 // Barrier of the four key or value warps: whether some thread says so.
 template <int kId>
@@ -469,13 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
     for (int i = 0; i < kSlots; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4), mbar_init(&bar.k_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.s_full[i], 1), mbar_init(&bar.s_free[i], 1), mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_full[i], 1), mbar_init(&bar.o_empty[i], 4);
     }
     for (int i = 0; i < kVPages; ++i) mbar_init(&bar.v_full[i], 4), mbar_init(&bar.v_empty[i], 1);
-    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 17);
+    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 18);
     mbar_init(&bar.q_full, 8), mbar_init(&bar.q_empty, 1);
-    mbar_init(&bar.joined, 4), mbar_init(&bar.drained, 1);
+    mbar_init(&bar.joined, 4), mbar_init(&bar.drained, 2);
     mbar_fence_init();
   }
   if (warp == kMmaWarp) tc_alloc(&s_tmem, kTmemCols);
@@ -544,7 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
     return mbar_try(&b, parity & 1u) || wait_long(&b, parity & 1u, abort_flag, p.pv.err);
   };
   auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(b, parity)); };
-  auto units_jobs = [](const Tile& t) { return (t.w1 - t.w0) * (t.pair ? 2 : 1); };
 
   if (warp == kCopyWarp) {
     // ---------------- the run's tiles and their pages ---------------------------------------
@@ -613,88 +612,95 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
     if (!ok)  // copies in flight land before the block's shared memory goes
       for (uint32_t n = n_page > kSlots ? n_page - kSlots : 0; n < n_page; ++n)
         (void)mbar_wait(&bar.raw_full[n % kSlots], (n / kSlots) & 1u);
-  } else if (warp == kMmaWarp) {
-    // ---------------- products -----------------------------------------------------------------
-    if (lane == 0) {
-      struct Cursor {
-        Tile t;
-        uint32_t n;  // tiles before
-        int j, jobs;
-      } cq, cv;
-      bool ok = true;
-      auto open = [&](Cursor& c) {
-        ok = wait(bar.tile_full[c.n % kTiles], c.n / kTiles);
-        if (!ok) return;
-        c.t = s_tile[c.n % kTiles];
-        c.j = 0;
-        c.jobs = units_jobs(c.t);
-      };
-      const uint64_t dQ = tc_desc_sw128(smem_u32(sm + M::kQ)), dK = tc_desc_sw128(smem_u32(sm + M::kK)),
-                     dV = tc_desc_sw128(smem_u32(sm + M::kV));
-      constexpr uint64_t kStep = kRegion >> 4;
-      uint32_t kn = 0, vn = 0, pn[2] = {0, 0}, on[2] = {0, 0};
-      bool busy[2] = {false, false};
-      cq.n = cv.n = 0;
-      open(cq);
-      if (ok) open(cv);
-      while (ok) {
-        while (ok && cq.t.w1 && !busy[cq.j & 1]) {
-          const int t = cq.j & 1, u = cq.t.w0 + (cq.t.pair ? cq.j >> 1 : cq.j);
-          if (cq.j == 0) ok = wait(bar.q_full, cq.n);
-          if (ok && (!cq.t.pair || t == 0)) ok = wait(bar.k_full[kn & 1], kn >> 1);
+  } else if (warp >= kMmaWarp) {
+    // ---------------- products ---------------------------------------------------------------
+    // Each warp's flow is uniform and one lane issues: a product of 128 x 128 x 16 takes 64 cycles, and descriptors
+    // put together by a single thread took longer than that.  P takes the place of S, so the next S of a group waits
+    // for the product that reads P, and is itself the sign that all products of the group so far are done.
+    constexpr uint64_t kStep = kRegion >> 4;
+    const bool one = lane == 0, pv = warp == kPvWarp;
+    auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    uint32_t n_tile = 0, kn = 0, sn[2] = {0, 0}, on[2] = {0, 0};
+    bool ok = true;
+    while (true) {
+      ok = wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
+      if (!ok) break;
+      const Tile& tile = s_tile[n_tile % kTiles];
+      const int w0 = same(tile.w0), w1 = same(tile.w1), len = same(tile.len), pair = same(tile.pair);
+      if (w1 == 0) break;
+      const int jobs = (w1 - w0) << pair;
+      if (!pv) {
+        const uint64_t dQ = tc_desc_sw128(smem_u32(sm + M::kQ)), dK = tc_desc_sw128(smem_u32(sm + M::kK));
+        ok = wait_warp(bar.q_full, n_tile);
+#pragma unroll 1
+        for (int j = 0; ok && j < jobs; ++j) {
+          const int t = j & 1, u = w0 + (j >> pair);
+          if (!pair || t == 0) ok = wait_warp(bar.k_full[kn & 1], kn >> 1);
+          ok = ok && wait_warp(bar.s_free[t], sn[t]++ ^ 1);
           if (!ok) break;
           tc_fence_after();
-          const bool half = u * kKeys + HYQ_PAGE_ROWS >= cq.t.len;  // one page
+          const bool half = u * kKeys + HYQ_PAGE_ROWS >= len;  // one page
           const uint32_t idesc = half ? tc_idesc(0, 0, kRows, HYQ_PAGE_ROWS) : tc_idesc(0, 0, kRows, kKeys);
-          const uint64_t a = dQ + (cq.t.pair ? t : 0) * 2 * kStep, b = dK + (kn & 1) * 2 * kStep;
+          const uint64_t a = dQ + (pair ? t : 0) * 2 * kStep, b = dK + (kn & 1) * 2 * kStep;
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t off = (k >> 2) * kStep + 2 * (k & 3);
-            tc_mma_f16(tmem + kColS + kKeys * t, a + off, b + off, idesc, k > 0);
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t off = (k >> 2) * kStep + 2 * (k & 3);
+              tc_mma_f16(tmem + kColS + kKeys * t, a + off, b + off, idesc, k > 0);
+            }
+            tc_commit(&bar.s_full[t]);
+            if (!pair || t == 1) tc_commit(&bar.k_empty[kn & 1]);
+            if (j + 1 == jobs) tc_commit(&bar.q_empty);
           }
-          tc_commit(&bar.s_full[t]);
-          busy[t] = true;
-          if (!cq.t.pair || t == 1) tc_commit(&bar.k_empty[kn & 1]), ++kn;
-          if (++cq.j == cq.jobs) {
-            tc_commit(&bar.q_empty);
-            ++cq.n;
-            open(cq);
-          }
+          if (!pair || t == 1) ++kn;
         }
-        if (!ok || cv.t.w1 == 0) break;
-        const int t = cv.j & 1, u = cv.t.w0 + (cv.t.pair ? cv.j >> 1 : cv.j);
-        const int pages = u * kKeys + HYQ_PAGE_ROWS >= cv.t.len ? 1 : 2;
-        if (cv.j < 2) ok = wait(bar.o_empty[t], on[t] ^ 1);
-        if (ok) ok = wait(bar.p_full[t], pn[t]);
-        if (!ok) break;
-        ++pn[t];
-        tc_fence_after();
-        for (int k = 0; ok && k < pages; ++k) {
-          const uint32_t n = vn + k, sl = n % kVPages;
-          if (!cv.t.pair || t == 0) {
-            ok = wait(bar.v_full[sl], n / kVPages);
-            if (!ok) break;
-            tc_fence_after();
-          }
+      } else {
+        const uint64_t dV = tc_desc_sw128(smem_u32(sm + M::kV));
+#pragma unroll 1
+        for (int j = 0; ok && j < jobs; ++j) {
+          const int t = j & 1, u = w0 + (j >> pair);
+          const int pages = u * kKeys + HYQ_PAGE_ROWS >= len ? 1 : 2;
+          if (j < 2) ok = wait_warp(bar.o_empty[t], on[t] ^ 1);
+          ok = ok && wait_warp(bar.p_full[t], sn[t]++);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < pages; ++k) {
+            const uint32_t n = kn + k, sl = n % kVPages;
+            if (!pair || t == 0) {
+              ok = wait_warp(bar.v_full[sl], n / kVPages);
+              if (!ok) break;
+              tc_fence_after();
+            }
+            const uint64_t b = dV + sl * kStep;
+            const uint32_t a = tmem + kColS + kKeys * t + 32 * k;
+            if (one) {
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            tc_mma_f16_ts(tmem + kColO + HYQ_D * t, tmem + kColS + kKeys * t + 32 * k + 8 * x, dV + sl * kStep + 2 * x,
-                          tc_idesc(0, 0, kRows, HYQ_D), cv.j >= 2 || k > 0 || x > 0);
-          if (!cv.t.pair || t == 1) tc_commit(&bar.v_empty[sl]);
-        }
-        if (!ok) break;
-        if (!cv.t.pair || t == 1) vn += pages;
-        busy[t] = false;
-        if (cv.j + 2 >= cv.jobs) tc_commit(&bar.o_full[t]), ++on[t];
-        if (++cv.j == cv.jobs) {
-          mbar_arrive(&bar.tile_empty[cv.n % kTiles]);
-          ++cv.n;
-          open(cv);
+              for (int x = 0; x < 4; ++x)
+                tc_mma_f16_ts(tmem + kColO + HYQ_D * t, a + 8 * x, b + 2 * x, tc_idesc(0, 0, kRows, HYQ_D),
+                              j >= 2 || k > 0 || x > 0);
+              if (!pair || t == 1) tc_commit(&bar.v_empty[sl]);
+            }
+          }
+          if (!ok) break;
+          if (one) {
+            tc_commit(&bar.s_free[t]);
+            if (j + 2 >= jobs) tc_commit(&bar.o_full[t]);
+          }
+          if (j + 2 >= jobs) ++on[t];
+          if (!pair || t == 1) kn += pages;
         }
       }
+      if (!ok) break;
+      __syncwarp();
+      if (one) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
+      ++n_tile;
+    }
+    if (one) {
       tc_commit(&bar.drained);  // every product has finished
       (void)mbar_wait(&bar.drained, 0);
     }
+    __syncwarp();
   } else if (warp >= kKeyWarp) {
     // ---------------- query rows and codes ----------------------------------------------------
     // The four warps of a kind meet at the same barriers whatever becomes of a wait, and stop together.  A page
