@@ -201,44 +201,42 @@ struct KeyTile {
     ka = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * g);
     kb = *reinterpret_cast<const uint4*>(tb + F::kKMeta + 16 * (g + 8));
   }
-  __device__ __forceinline__ bool far(int lane, int vr) const {  // of this lane's rows below vr
-    const int g = lane >> 2;
-    const uint32_t a = __vmaxu2(largest<BK>(ka.x, ka.z), largest<BK>(ka.y, ka.w));
-    const uint32_t b = __vmaxu2(largest<BK>(kb.x, kb.z), largest<BK>(kb.y, kb.w));
-    return leaves_fp16(__vmaxu2(g < vr ? a : 0u, g + 8 < vr ? b : 0u));
-  }
   // The keys as fp16 rows row0 .. row0 + 15 of the key operand at `dst` (two regions of 64 elements).  Of 8-bit codes
   // the four elements of each half of a group of 32 lie beside those of the other half (query rows are ordered alike).
   __device__ __forceinline__ void store(uint8_t* dst, int lane, int row0, bool is_far) {
     const int g = lane >> 2, t = lane & 3;
-    if (is_far) ka = mul4(ka, far_scale<BK>()), kb = mul4(kb, far_scale<BK>());
-    uint8_t* at = dst + 128 * key_row(row0 + g);  // row g + 8 lies 8 rows on, swizzled alike
-    const int x = key_row(g);                     // (row0 is a multiple of 8)
+    if (__builtin_expect(is_far, 0)) ka = mul4(ka, far_scale<BK>()), kb = mul4(kb, far_scale<BK>());
+    const int x = key_row(g);  // (row0 is a multiple of 8; row g + 8 lies 8 rows on, swizzled alike)
+    uint8_t* at = dst + 128 * (row0 + x);
+    // groups 2 i and 2 i + 1: 16 bytes of each row apiece.  (Rolled: see the waits.)
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {  // group v: 16 bytes of each row
-      uint32_t xa[4], xb[4];
-      if (BK == 4) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t w = u4at(kc[v >> 1], 2 * (v & 1) + u), w8 = w >> 8;
-          xa[2 * u] = low_codes(w), xa[2 * u + 1] = low_codes(w8);
-          xb[2 * u] = high_codes(w), xb[2 * u + 1] = high_codes(w8);
-        }
-      } else {
+      for (int v = 0; v < 2; ++v) {
+        uint32_t xa[4], xb[4];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t wa = u4at(kc[BK == 4 ? 0 : v], 2 * u), wb = u4at(kc[BK == 4 ? 0 : v], 2 * u + 1);
-          xa[2 * u] = even_codes(wa), xa[2 * u + 1] = odd_codes(wa);
-          xb[2 * u] = even_codes(wb), xb[2 * u + 1] = odd_codes(wb);
+          if (BK == 4) {
+            const uint32_t w = u4at(kc[0], 2 * v + u), w8 = w >> 8;
+            xa[2 * u] = low_codes(w), xa[2 * u + 1] = low_codes(w8);
+            xb[2 * u] = high_codes(w), xb[2 * u + 1] = high_codes(w8);
+          } else {
+            const uint32_t wa = u4at(kc[BK == 4 ? 0 : v], 2 * u), wb = u4at(kc[BK == 4 ? 0 : v], 2 * u + 1);
+            xa[2 * u] = even_codes(wa), xa[2 * u + 1] = odd_codes(wa);
+            xb[2 * u] = even_codes(wb), xb[2 * u + 1] = odd_codes(wb);
+          }
         }
+        const uint32_t sa = both(ka.x, v), za = both(ka.z, v), sb = both(kb.x, v), zb = both(kb.z, v);
+        uint8_t* to = at + (((4 * v + t) ^ x) << 4);
+        *reinterpret_cast<uint4*>(to) = make_uint4(hfma2_u(xa[0], sa, za), hfma2_u(xa[1], sa, za),
+                                                   hfma2_u(xa[2], sa, za), hfma2_u(xa[3], sa, za));
+        *reinterpret_cast<uint4*>(to + 1024) = make_uint4(hfma2_u(xb[0], sb, zb), hfma2_u(xb[1], sb, zb),
+                                                          hfma2_u(xb[2], sb, zb), hfma2_u(xb[3], sb, zb));
       }
-      const uint32_t sa = both(v < 2 ? ka.x : ka.y, v & 1), za = both(v < 2 ? ka.z : ka.w, v & 1);
-      const uint32_t sb = both(v < 2 ? kb.x : kb.y, v & 1), zb = both(v < 2 ? kb.z : kb.w, v & 1);
-      uint8_t* to = at + (v >> 1) * kRegion + (((4 * (v & 1) + t) ^ x) << 4);
-      *reinterpret_cast<uint4*>(to) = make_uint4(hfma2_u(xa[0], sa, za), hfma2_u(xa[1], sa, za),
-                                                 hfma2_u(xa[2], sa, za), hfma2_u(xa[3], sa, za));
-      *reinterpret_cast<uint4*>(to + 1024) = make_uint4(hfma2_u(xb[0], sb, zb), hfma2_u(xb[1], sb, zb),
-                                                        hfma2_u(xb[2], sb, zb), hfma2_u(xb[3], sb, zb));
+      at += kRegion;
+      ka.x = ka.y, ka.z = ka.w, kb.x = kb.y, kb.z = kb.w;
+      if (BK == 4) kc[0] = kc[1];
+      else kc[0] = kc[BK / 2 - 2], kc[1] = kc[BK / 2 - 1];
     }
   }
 };
@@ -250,11 +248,6 @@ struct ValueTile {
   uint4 vc[BV / 2];
   uint4 vs[2], vz[2];  // steps and zeros of rows 2t + 8b and the next, groups 0 .. 3
 
-  // Word `lane` of the steps (rows 2 (lane / 4) and the next, group lane % 4) and of the zeros: whether one below vr is far.
-  static __device__ __forceinline__ bool far(const uint8_t* tb, int lane, int vr) {
-    const uint32_t* m = reinterpret_cast<const uint32_t*>(tb + F::kVMeta) + lane;
-    return leaves_fp16(largest<BV>(m[0], m[32]) & halves_below(2 * (lane >> 2), vr));
-  }
   __device__ __forceinline__ void load(const uint8_t* tb, int lane) {
     const int t = lane & 3;
 #pragma unroll
@@ -269,7 +262,7 @@ struct ValueTile {
   // order of elem_of); rows from vr on are zero.
   __device__ __forceinline__ void store(uint32_t dst, int lane, int i, int vr, bool is_far) {
     const int t = lane & 3;
-    if (vr < 16) {
+    if (__builtin_expect(vr < 16, 0)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const uint32_t in = halves_below(2 * t + 8 * b, vr);
@@ -277,7 +270,7 @@ struct ValueTile {
         vz[b] = make_uint4(vz[b].x & in, vz[b].y & in, vz[b].z & in, vz[b].w & in);
       }
     }
-    if (is_far) {
+    if (__builtin_expect(is_far, 0)) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) vs[b] = mul4(vs[b], far_scale<BV>()), vz[b] = mul4(vz[b], far_scale<BV>());
     }
@@ -285,22 +278,31 @@ struct ValueTile {
     // address of row l & 7 of matrix l >> 3
     const int mb = (lane >> 3) & 1, mc = lane >> 4, r8 = lane & 7;
     const uint32_t at = dst + 128 * (8 * mc + r8) + (((2 * i + mb) ^ r8) << 4);
+    uint32_t to = at;
+#pragma unroll 1
+    for (int i2 = 0; i2 < 2; ++i2) {  // groups 2 i2 and 2 i2 + 1
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+      for (int v = 0; v < 2; ++v) {
 #pragma unroll
-      for (int c0 = 0; c0 < 4; c0 += 2) {
-        uint32_t x[4];
-        if (BV == 4) {
-          const uint32_t w = u4at(vc[q >> 1], 2 * (q & 1) + (c0 >> 1)), w8 = w >> 8;
-          x[0] = low_codes(w), x[1] = low_codes(w8), x[2] = high_codes(w), x[3] = high_codes(w8);
-        } else {
-          const uint32_t wa = u4at(vc[BV == 4 ? 0 : q], c0), wb = u4at(vc[BV == 4 ? 0 : q], c0 + 1);
-          x[0] = even_codes(wa), x[1] = odd_codes(wa), x[2] = even_codes(wb), x[3] = odd_codes(wb);
+        for (int c0 = 0; c0 < 4; c0 += 2) {
+          uint32_t x[4];
+          if (BV == 4) {
+            const uint32_t w = u4at(vc[0], 2 * v + (c0 >> 1)), w8 = w >> 8;
+            x[0] = low_codes(w), x[1] = low_codes(w8), x[2] = high_codes(w), x[3] = high_codes(w8);
+          } else {
+            const uint32_t wa = u4at(vc[BV == 4 ? 0 : v], c0), wb = u4at(vc[BV == 4 ? 0 : v], c0 + 1);
+            x[0] = even_codes(wa), x[1] = odd_codes(wa), x[2] = even_codes(wb), x[3] = odd_codes(wb);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) x[m] = hfma2_u(x[m], v ? vs[m & 1].y : vs[m & 1].x, v ? vz[m & 1].y : vz[m & 1].x);
+          stmatrix_x4(to + 128 * (32 * v + 8 * c0), x[0], x[1], x[2], x[3]);
         }
-#pragma unroll
-        for (int m = 0; m < 4; ++m) x[m] = hfma2_u(x[m], u4at(vs[m & 1], q), u4at(vz[m & 1], q));
-        stmatrix_x4(at + 128 * (32 * q + 8 * c0), x[0], x[1], x[2], x[3]);
       }
+      to += 128 * 64;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) vs[b].x = vs[b].z, vs[b].y = vs[b].w, vz[b].x = vz[b].z, vz[b].y = vz[b].w;
+      if (BV == 4) vc[0] = vc[1];
+      else vc[0] = vc[BV / 2 - 2], vc[1] = vc[BV / 2 - 1];
     }
   }
 };
@@ -312,10 +314,11 @@ struct ValueTile {
 //            warp
 //   mma      two warps, one thread of each issues: S = Q K^T; O += P V
 //   copy     the tiles of the block's run, one after another, and their pages
+//   scan     whether a page has rows beyond fp16
 // A tile of more than 128 query rows is a pair: each unit is two jobs, one for each half of the
 // rows, so that one half's products overlap the other's exponentials.  A smaller tile's
 // units are one job each and alternate between the groups, whose states are joined at the end.
-constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kPvWarp = 17, kCopyWarp = 18, kThreads = 19 * 32;
+constexpr int kKeyWarp = 8, kValueWarp = 12, kMmaWarp = 16, kPvWarp = 17, kCopyWarp = 18, kScanWarp = 19, kThreads = 20 * 32;
 constexpr int kTiles = 4;   // tiles of the run that are known ahead
 constexpr int kVPages = 3;  // pages of values in fp16
 
@@ -404,24 +407,12 @@ __device__ __noinline__ void load_queries(const Params& p, const Tile& t, int wa
 }
 
 struct Bars {
-  uint64_t raw_full[8], raw_empty[8];
+  uint64_t raw_full[8], raw_seen[8], raw_empty[8];
   uint64_t k_full[2], k_empty[2], v_full[kVPages], v_empty[kVPages];
   uint64_t q_full, q_empty;
   uint64_t tile_full[kTiles], tile_empty[kTiles];
   uint64_t s_full[2], s_free[2], p_full[2], o_full[2], o_empty[2], joined, drained;
 };
-// Barrier of the four key or value warps: whether some thread says so.
-template <int kId>
-__device__ __forceinline__ bool codes_any(bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)x), "n"(kId)
-      : "memory");
-  return r;
-}
-
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -430,17 +421,6 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
       : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return done;
-}
-// Out of line, as the loops below are rolled: the roles' code has to stay in the SM's
-// instruction cache together (unrolled and inlined throughout, two of three fetches missed it,
-// and the whole took three times as long).
-__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* err) {
-  if (mbar_wait_or_abort(bar, parity, abort_flag)) return true;
-  if (!*abort_flag) {
-    *abort_flag = 1;
-    hyq_set_err(err, HYQ_DEVERR_TIMEOUT);
-  }
-  return false;
 }
 
 template <int BK, int BV, bool kShared>
@@ -457,8 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   __shared__ int s_first;
   __shared__ Tile s_tile[kTiles];
   __shared__ float s_factor[2][2 * kRows];
-  __shared__ int s_valid[8];            // rows of the page in a slot
-  __shared__ volatile uint32_t s_unit[4];  // rows of a unit's two pages (8 bits each), whether their keys are far (bits 16, 17), their values (18, 19)
+  __shared__ int s_valid[8];  // rows of the page in a slot
+  // Of the last pages: their rows, whether the keys are taken down (bit 8), the values (bit 9).  Pages are scanned
+  // ahead of the softmax by the slots and two units at most.
+  __shared__ volatile uint32_t s_page[16];
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   constexpr int kPer = (HYQ_PAGED_MAX_BATCH + kThreads - 1) / kThreads;
@@ -466,14 +448,14 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 8);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_seen[i], 1), mbar_init(&bar.raw_empty[i], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.k_full[i], 4), mbar_init(&bar.k_empty[i], 1);
       mbar_init(&bar.s_full[i], 1), mbar_init(&bar.s_free[i], 1), mbar_init(&bar.p_full[i], 4);
       mbar_init(&bar.o_full[i], 1), mbar_init(&bar.o_empty[i], 4);
     }
     for (int i = 0; i < kVPages; ++i) mbar_init(&bar.v_full[i], 4), mbar_init(&bar.v_empty[i], 1);
-    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 18);
+    for (int i = 0; i < kTiles; ++i) mbar_init(&bar.tile_full[i], 1), mbar_init(&bar.tile_empty[i], 19);
     mbar_init(&bar.q_full, 8), mbar_init(&bar.q_empty, 1);
     mbar_init(&bar.joined, 4), mbar_init(&bar.drained, 2);
     mbar_fence_init();
@@ -540,8 +522,16 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   }
   __syncthreads();
 
+  // The code of all roles has to stay in the SM's instruction cache together: a wait is a few instructions, and the
+  // loops are rolled.  One that runs out leaves a flag, which is reported at the end.
   auto wait = [&](uint64_t& b, uint32_t parity) {
-    return mbar_try(&b, parity & 1u) || wait_long(&b, parity & 1u, abort_flag, p.pv.err);
+#pragma unroll 1
+    for (int it = 0; it < (1 << 22); ++it) {
+      if (mbar_try(&b, parity & 1u)) return true;
+      if (*abort_flag) return false;
+    }
+    *abort_flag = 1;
+    return false;
   };
   auto wait_warp = [&](uint64_t& b, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(b, parity)); };
 
@@ -612,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
     if (!ok)  // copies in flight land before the block's shared memory goes
       for (uint32_t n = n_page > kSlots ? n_page - kSlots : 0; n < n_page; ++n)
         (void)mbar_wait(&bar.raw_full[n % kSlots], (n / kSlots) & 1u);
-  } else if (warp >= kMmaWarp) {
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ---------------- products ---------------------------------------------------------------
     // Each warp's flow is uniform and one lane issues: a product of 128 x 128 x 16 takes 64 cycles, and descriptors
     // put together by a single thread took longer than that.  P takes the place of S, so the next S of a group waits
@@ -701,91 +691,102 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
       (void)mbar_wait(&bar.drained, 0);
     }
     __syncwarp();
-  } else if (warp >= kKeyWarp) {
+  } else if (warp >= kKeyWarp && warp < kMmaWarp) {
     // ---------------- query rows and codes ----------------------------------------------------
-    // The four warps of a kind meet at the same barriers whatever becomes of a wait, and stop together.  A page
-    // whose c s + z may leave fp16 is taken down; values then stay so to the end of the tile, whose O has one scale.
+    // A page whose c s + z may leave fp16 is taken down; values then stay so to the end of the tile, whose O has one scale.
     auto codes = [&](auto kind) {
-      constexpr bool kKeys = decltype(kind)::value;
-      constexpr int kId = kKeys ? 1 : 2;
+      constexpr bool kIsKeys = decltype(kind)::value;
       const int cw = warp & 3;
       uint32_t n_tile = 0, n_page = 0, kn = 0;
-      bool ok = true;
-      while (true) {
-        ok = ok && wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
-        if (codes_any<kId>(!ok)) return;
+      while (wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles)) {
         const Tile& t = s_tile[n_tile % kTiles];
-        const int w0 = t.w0, w1 = t.w1, last = (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS;
-        if (w1 == 0) return;
-        ok = wait_warp(bar.q_empty, n_tile ^ 1);
-        if (ok) {
-          load_queries<BK>(p, t, warp - kKeyWarp, lane, sm + M::kQ, s_factor[n_tile & 1]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.q_full);
+        const int last = (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS, end = min(t.w1 * kUnitPages, last);
+        int pg = t.w0 * kUnitPages;
+        if (t.w1 == 0 || !wait_warp(bar.q_empty, n_tile ^ 1)) return;
+        load_queries<BK>(p, t, warp - kKeyWarp, lane, sm + M::kQ, s_factor[n_tile & 1]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar.q_full);
+          mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
         }
-        bool vfar = false;
-        uint32_t info = 0;
 #pragma unroll 1
-        for (int pg = w0 * kUnitPages; pg < min(w1 * kUnitPages, last); ++pg, ++n_page) {
+        for (; pg < end; ++pg, ++n_page) {
           const uint32_t sl = n_page % kSlots;
-          ok = ok && wait_warp(bar.raw_full[sl], n_page / kSlots);
-          typename std::conditional<kKeys, KeyTile<BK, BV>, ValueTile<BK, BV>>::type x;
-          int valid = 0;
-          bool kf = false, vf = false;
-          if (ok) {
-            const uint8_t* tb = sm + M::kRaw + sl * F::kBlock + cw * F::kTile;
-            valid = s_valid[sl];
-            x.load(tb, lane);
-            if constexpr (kKeys) kf = x.far(lane, valid - 16 * cw);
-            vf = ValueTile<BK, BV>::far(tb, lane, valid - 16 * cw);
-          }
-          if (codes_any<kId>(kf || vf || !ok)) {  // seldom
-            if (codes_any<kId>(!ok)) return;
-            kf = codes_any<kId>(kf);
-            vfar |= codes_any<kId>(vf);
-          }
-          if (lane == 0) mbar_arrive(&bar.raw_empty[sl]);  // (all lanes have met at the barrier)
-          if constexpr (kKeys) {
+          if (!wait_warp(bar.raw_seen[sl], n_page / kSlots)) return;
+          (void)mbar_try(&bar.raw_full[sl], (n_page / kSlots) & 1u);  // (it is: what the copy brought is visible)
+          const uint32_t info = s_page[n_page & 15];
+          typename std::conditional<kIsKeys, KeyTile<BK, BV>, ValueTile<BK, BV>>::type x;
+          x.load(sm + M::kRaw + sl * F::kBlock + cw * F::kTile, lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.raw_empty[sl]);
+          if constexpr (kIsKeys) {
             const uint32_t ks = kn & 1, k = pg & 1;
-            if (k == 0) {
-              ok = wait_warp(bar.k_empty[ks], (kn >> 1) ^ 1);
-              info = 0;
-            }
-            if (!ok) continue;
-            x.store(sm + M::kK + ks * 2 * kRegion, lane, HYQ_PAGE_ROWS * k + 16 * cw, kf);
-            info |= (uint32_t)valid << (8 * k) | (uint32_t)kf << (16 + k) | (uint32_t)vfar << (18 + k);
+            if (k == 0 && !wait_warp(bar.k_empty[ks], (kn >> 1) ^ 1)) return;
+            x.store(sm + M::kK + ks * 2 * kRegion, lane, HYQ_PAGE_ROWS * k + 16 * cw, info & 0x100);
+            fence_proxy_async_smem();
+            __syncwarp();
             if (k == 1 || pg + 1 == last) {
-              if (k == 0) info |= (uint32_t)vfar << 19;
-              if (cw == 0 && lane == 0) s_unit[kn & 3] = info;
-              fence_proxy_async_smem();
-              __syncwarp();
               if (lane == 0) mbar_arrive(&bar.k_full[ks]);
               ++kn;
             }
           } else {
             const uint32_t vs = n_page % kVPages;
-            ok = wait_warp(bar.v_empty[vs], (n_page / kVPages) ^ 1);
-            if (!ok) continue;
-            x.store(smem_u32(sm + M::kV) + vs * kRegion, lane, cw, valid - 16 * cw, vfar);
+            if (!wait_warp(bar.v_empty[vs], (n_page / kVPages) ^ 1)) return;
+            x.store(smem_u32(sm + M::kV) + vs * kRegion, lane, cw, (int)(info & 0xFF) - 16 * cw, info & 0x200);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.v_full[vs]);
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
         ++n_tile;
       }
     };
     if (warp < kValueWarp) codes(std::true_type{});
     else codes(std::false_type{});
+  } else if (warp == kScanWarp) {
+    // ---------------- rows beyond fp16 --------------------------------------------------------------
+    uint32_t n_tile = 0, n_page = 0;
+    bool ok = true;
+    while (ok && wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles)) {
+      const Tile& t = s_tile[n_tile % kTiles];
+      int pages = min(t.w1 * kUnitPages, (t.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS) - t.w0 * kUnitPages;
+      if (t.w1 == 0) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.tile_empty[n_tile % kTiles]);
+      ++n_tile;
+      bool vfar = false;
+#pragma unroll 1
+      for (; pages > 0; --pages, ++n_page) {
+        const uint32_t sl = n_page % kSlots;
+        ok = wait_warp(bar.raw_full[sl], n_page / kSlots);
+        if (!ok) break;
+        const int valid = s_valid[sl];
+        uint32_t km = 0, vm = 0;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // lane: words of row lane / 2 and of row pair lane / 4
+          const uint8_t* tb = sm + M::kRaw + sl * F::kBlock + i * F::kTile;
+          const uint32_t* k = reinterpret_cast<const uint32_t*>(tb + F::kKMeta) + 4 * (lane >> 1) + (lane & 1);
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(tb + F::kVMeta) + lane;
+          const int r = valid - 16 * i;
+          if ((lane >> 1) < r) km = __vmaxu2(km, largest<BK>(k[0], k[2]));
+          vm = __vmaxu2(vm, largest<BV>(v[0], v[32]) & halves_below(2 * (lane >> 2), r));
+        }
+        const bool kf = __any_sync(0xffffffffu, leaves_fp16(km));
+        vfar |= __any_sync(0xffffffffu, leaves_fp16(vm)) != 0;
+        if (lane == 0) {
+          s_page[n_page & 15] = (uint32_t)valid | (uint32_t)kf << 8 | (uint32_t)vfar << 9;
+          mbar_arrive(&bar.raw_seen[sl]);
+        }
+        __syncwarp();
+      }
+    }
   } else {
     // ---------------- softmax: a query row a thread ---------------------------------------------
     const int t = warp >> 2, rr = tid & (kRows - 1);
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t tS = t_lane + kColS + kKeys * t, tO = t_lane + kColO + HYQ_D * t;
-    uint32_t n_tile = 0, n_unit = 0, sn = 0, on = 0, joins = 0;
+    uint32_t n_tile = 0, n_page = 0, sn = 0, on = 0, joins = 0;
     bool ok = true;
     while (true) {
       ok = wait_warp(bar.tile_full[n_tile % kTiles], n_tile / kTiles);
@@ -808,18 +809,19 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
         }
         tc_fence_after();
         if (j == 0) f = s_factor[n_tile & 1][r];
-        const uint32_t info = s_unit[(n_unit + (tile.pair ? j : 2 * j + t)) & 3];
-        const int v0 = info & 0xFF, v1 = (info >> 8) & 0xFF;
-        const bool far0 = info & 0x40000, far1 = info & 0x80000, full = v0 == HYQ_PAGE_ROWS && v1 == HYQ_PAGE_ROWS;
-        const int chunks = (tile.w0 + (tile.pair ? j : 2 * j + t)) * kKeys + HYQ_PAGE_ROWS >= tile.len ? 2 : 4;
-        const float up0 = info & 0x10000 ? (float)(1 << kFar<BK>) : 1.f, up1 = info & 0x20000 ? (float)(1 << kFar<BK>) : 1.f;
+        const int u = tile.pair ? j : 2 * j + t;
+        const bool one = (tile.w0 + u) * kKeys + HYQ_PAGE_ROWS >= tile.len;  // one page
+        const uint32_t i0 = s_page[(n_page + 2 * u) & 15], i1 = one ? i0 & 0x200 : s_page[(n_page + 2 * u + 1) & 15];
+        const int v0 = i0 & 0xFF, v1 = i1 & 0xFF, chunks = one ? 2 : 4;
+        const bool far0 = i0 & 0x200, far1 = i1 & 0x200, full = v0 == HYQ_PAGE_ROWS && v1 == HYQ_PAGE_ROWS;
+        const float up0 = i0 & 0x100 ? (float)(1 << kFar<BK>) : 1.f, up1 = i1 & 0x100 ? (float)(1 << kFar<BK>) : 1.f;
         auto load = [&](int c, float (&x)[32]) {
           uint32_t y[32];
           tc_ld32(tS + 32 * c, y);
           tc_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(y[i]);
-          if (!full) {
+          if (__builtin_expect(!full, 0)) {
             const int v = (c < 2 ? v0 : v1) - 32 * (c & 1);
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -898,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
             tc_st16(tS + 16 * c, w);
           }
         };
-        if (__any_sync(0xffffffffu, fabsf(ref * f) > 4096.f)) probs(std::true_type{});
+        if (__builtin_expect(__any_sync(0xffffffffu, fabsf(ref * f) > 4096.f), 0)) probs(std::true_type{});
         else probs(std::false_type{});
         tc_wait_st();
         tc_fence_before();
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
         if (lane == 0) mbar_arrive(&bar.p_full[t]);
       }
       if (!ok) break;
-      n_unit += U;
+      n_page += min(tile.w1 * kUnitPages, (tile.len + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS) - tile.w0 * kUnitPages;
       // ---- the tile's result, or this run's part of it -----------------------------------------
       const bool two = !tile.pair && U > 1;  // both groups have a state of the same rows
       if (jobs) {
@@ -1024,6 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && s_abort) hyq_set_err(p.pv.err, HYQ_DEVERR_TIMEOUT);
   if (warp == kMmaWarp) {
     tc_fence_after();
     tc_dealloc(tmem, kTmemCols);
