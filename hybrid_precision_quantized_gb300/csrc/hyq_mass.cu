@@ -12,7 +12,7 @@
 //
 // A group is one (sequence, KV head).  Its half pages (units of two 16-row tiles) go round the
 // block's warps, each with a ring of asynchronous copies of its own, and a warp takes a unit
-// against all query rows: a position's sum has one writer and one order, so there is nothing
+// against all query rows (with more than one tile of those a unit is a single tile): a position's sum has one writer and one order, so there is nothing
 // to join and results do not vary from run to run.  The codes are unpacked once a unit and
 // the query rows' operands read once for both tiles.  The pages of all groups, laid end to end,
 // are cut into equal runs, a block each.
@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kMaxWarps = 16;
 constexpr int kCost = 4;   // pages that a group's fixed work is worth
-constexpr int kRows = 32;  // positions of a unit
 
 struct Params {
   PageView pv;
@@ -46,10 +45,11 @@ struct __align__(16) Query {
   int lim[HYQ_MAX_GQA];  // positions that the row sees
 };
 
-template <int BK, int BV>
+template <int BK, int BV, int kTiles>
 struct Unit {
   using F = QFmt<BK, BV>;
-  static constexpr int kCodes = 256 * BK, kTile = kCodes + 256, kBytes = 2 * kTile;  // of the keys alone
+  static constexpr int kCodes = 256 * BK, kTile = kCodes + 256, kBytes = kTiles * kTile;  // of the keys alone
+  static constexpr int kRows = 16 * kTiles, kPerPage = HYQ_PAGE_ROWS / kRows;
 };
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -68,7 +68,9 @@ __device__ __forceinline__ void copies_wait() {
 template <int BK, int BV, int kSlots, bool kOne>
 __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p) {
   using F = QFmt<BK, BV>;
-  using U = Unit<BK, BV>;
+  constexpr int kT = kOne ? 2 : 1;
+  using U = Unit<BK, BV, kT>;
+  constexpr int kRows = U::kRows, kPer = U::kPerPage;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1], s_warp[kMaxWarps];
   __shared__ __align__(16) int s_seq[HYQ_PAGED_MAX_BATCH];
@@ -132,11 +134,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
     const int len = s_len[lo], fresh = len - (p.n_new ? p.n_new[lo] : p.n_q);
     const int32_t* table = p.pv.table + (size_t)s_seq[lo] * p.pv.max_blocks;
     // ---- this warp's units: half page u0, u0 + n_warps, ..; their pages 32 ahead --------
-    const int u0 = 2 * max(0, x0 - kCost) + warp, u1 = min(2 * (x1 - kCost), (len + kRows - 1) / kRows);
+    const int u0 = kPer * max(0, x0 - kCost) + warp, u1 = min(kPer * (x1 - kCost), (len + kRows - 1) / kRows);
     const int nj = u1 > u0 ? (u1 - u0 + n_warps - 1) / n_warps : 0;
     auto page_of = [&](int j) -> int {  // of unit j, or -1 for one that is left out
       if (j >= nj) return -1;
-      const int pg = table[(u0 + j * n_warps) >> 1];
+      const int pg = table[(u0 + j * n_warps) / kPer];
       if ((uint32_t)pg >= (uint32_t)p.pv.n_pages) {
         hyq_set_err(p.pv.err, HYQ_DEVERR_INDEX);
         return -1;
@@ -152,19 +154,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
     auto issue = [&](int j) {  // (a group of copies whether there are any or not)
       const int pg = j < nj ? page(j) : -1;
       if (pg >= 0) {
-        const uint8_t* from = p.pv.pool + ((size_t)pg * p.HKV + h) * F::kBlock + 2 * ((u0 + j * n_warps) & 1) * F::kTile;
+        const uint8_t* from = p.pv.pool + ((size_t)pg * p.HKV + h) * F::kBlock + kT * ((u0 + j * n_warps) % kPer) * F::kTile;
         const uint32_t to = smem_u32(ring) + (j % kSlots) * U::kBytes;
 #pragma unroll
-        for (int i = 0; i < U::kBytes / 512; ++i) {
+        for (int i = 0; i < (U::kBytes + 511) / 512; ++i) {
           const int x = 16 * lane + 512 * i, tile = x / U::kTile, at = x - tile * U::kTile;
-          copy16(to + x, from + tile * F::kTile + (at < U::kCodes ? at : F::kKMeta + at - U::kCodes));
+          if (U::kBytes % 512 == 0 || x < U::kBytes) copy16(to + x, from + tile * F::kTile + (at < U::kCodes ? at : F::kKMeta + at - U::kCodes));
         }
       }
       copies_end();
     };
-    auto weights = [&](int j, int pg) { return p.mass + ((size_t)pg * p.HKV + h) * HYQ_PAGE_ROWS + kRows * ((u0 + j * n_warps) & 1); };
+    auto weights = [&](int j, int pg) { return p.mass + ((size_t)pg * p.HKV + h) * HYQ_PAGE_ROWS + kRows * ((u0 + j * n_warps) % kPer); };
     auto held = [&](int j, int pg) {  // what this lane's position of unit j has so far
-      return j < nj && pg >= 0 && kRows * (u0 + j * n_warps) + lane < fresh ? weights(j, pg)[lane] : 0.f;
+      return j < nj && pg >= 0 && lane < kRows && kRows * (u0 + j * n_warps) + lane < fresh ? weights(j, pg)[lane] : 0.f;
     };
 #pragma unroll 1
     for (int j = 0; j < kSlots; ++j) issue(j);
@@ -172,26 +174,33 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
     float old = held(0, pg);
     // ---- the query rows, a warp each ------------------------------------------------
     __syncthreads();
-    for (int r = warp; r < p.QT * HYQ_MAX_GQA; r += n_warps) {
-      Query& qt = query[r / HYQ_MAX_GQA];
-      const int r8 = r & 7, tok = r / p.gq, head = h * p.gq + r - tok * p.gq;
-      uint2 v = make_uint2(0, 0);
-      float nl = -INFINITY;
-      int lim = 0;
-      if (tok < p.n_q) {
-        v = *reinterpret_cast<const uint2*>(p.q + ((size_t)lo * p.n_q + tok) * p.ldq + (size_t)head * HYQ_D + 4 * lane);
-        const float lse = p.lse[((size_t)lo * p.n_q + tok) * p.HQ + head];
-        lim = max(0, len - p.n_q + 1 + tok);
-        const uint32_t e = 0x7F807F80u, a = v.x & e, b = v.y & e;
+#pragma unroll 1
+    for (int r0 = warp; r0 < p.QT * HYQ_MAX_GQA; r0 += 4 * n_warps) {
+      uint2 v[4];
+      float lse[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // four rows under way
+        const int r = r0 + k * n_warps, tok = r / p.gq, head = h * p.gq + r - tok * p.gq;
+        v[k] = make_uint2(0, 0), lse[k] = 0.f;
+        if (tok < p.n_q) {
+          v[k] = *reinterpret_cast<const uint2*>(p.q + ((size_t)lo * p.n_q + tok) * p.ldq + (size_t)head * HYQ_D + 4 * lane);
+          lse[k] = p.lse[((size_t)lo * p.n_q + tok) * p.HQ + head];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = r0 + k * n_warps, tok = r / p.gq;
+        if (r >= p.QT * HYQ_MAX_GQA) break;
+        const int lim = tok < p.n_q ? max(0, len - p.n_q + 1 + tok) : 0;
+        const uint32_t e = 0x7F807F80u, a = v[k].x & e, b = v[k].y & e;
         bool bad = (a >> 16) == 0x7F80u || (a & 0xFFFFu) == 0x7F80u || (b >> 16) == 0x7F80u || (b & 0xFFFFu) == 0x7F80u;
-        bad |= !(fabsf(lse) <= 3.402823466e38f);
+        bad |= !(fabsf(lse[k]) <= 3.402823466e38f);
         bad = __any_sync(0xffffffffu, bad);
         if (bad && lim > 0 && lane == 0) hyq_set_err(p.pv.err, HYQ_DEVERR_SCORE);
-        if (bad) v = make_uint2(0, 0);
-        else nl = lse * -1.4426950408889634f;
+        Query& qt = query[r / HYQ_MAX_GQA];
+        prep_query_row<BK>(r & 7, lane, bad ? make_uint2(0, 0) : v[k], qt.bq, qt.rowc, qt.bz);
+        if (lane == 0) qt.nl[r & 7] = bad || lim == 0 ? -INFINITY : lse[k] * -1.4426950408889634f, qt.lim[r & 7] = lim;
       }
-      prep_query_row<BK>(r8, lane, v, qt.bq, qt.rowc, qt.bz);
-      if (lane == 0) qt.nl[r8] = nl, qt.lim[r8] = lim;
     }
     __syncthreads();
     uint32_t bq1[8][2];
@@ -205,13 +214,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
       copies_wait<kSlots - 1>();
       __syncwarp();
       const float next = held(j + 1, pg_next);
-      float sums[4] = {0.f, 0.f, 0.f, 0.f};  // of rows g, g + 8 of the two tiles
+      float sums[2 * kT];  // of rows g, g + 8 of the tiles
+#pragma unroll
+      for (int i = 0; i < 2 * kT; ++i) sums[i] = 0.f;
       if (pg >= 0) {
         const bool all = at + kRows <= minlim;  // every row sees every position
-        uint4 ma[2], mb[2];                     // steps and zeros of rows g, g + 8
-        uint32_t kw[2][BK == 4 ? 8 : 16];
+        uint4 ma[kT], mb[kT];                   // steps and zeros of rows g, g + 8
+        uint32_t kw[kT][BK == 4 ? 8 : 16];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kT; ++i) {
           const uint8_t* tb = ring + (j % kSlots) * U::kBytes + i * U::kTile;
           load_words<BK == 4 ? 8 : 16>(tb, lane, kw[i]);
           ma[i] = *reinterpret_cast<const uint4*>(tb + U::kCodes + 16 * g);
@@ -259,16 +270,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
         };
         if (kOne) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < kT; ++i)
             give(i, [&](float (&C)[4], int ks, uint32_t b0, uint32_t b1) {
               uint32_t a[4];
               fragment(i, ks, a);
               mma_f16(C, a[0], a[1], a[2], a[3], b0, b1);
             }, bq1, qc1, nl1[0], nl1[1], query[0].lim);
         } else {
-          uint32_t a[2][8][4];
+          uint32_t a[kT][8][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < kT; ++i)
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) fragment(i, ks, a[i][ks]);
 #pragma unroll 1
@@ -278,25 +289,25 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
             load_query_consts(g, t, query[k].bq, query[k].rowc, query[k].bz, bq, qc);
             const float2 nl = *reinterpret_cast<const float2*>(&query[k].nl[2 * t]);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kT; ++i)
               give(i, [&](float (&C)[4], int ks, uint32_t b0, uint32_t b1) {
                 mma_f16(C, a[i][ks][0], a[i][ks][1], a[i][ks][2], a[i][ks][3], b0, b1);
               }, bq, qc, nl.x, nl.y, query[k].lim);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kT; ++i) {
           sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 1);
           sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 2);
         }
         // row r of the unit: sums[r / 8] of the lanes 4 (r % 8) ..
         float add = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2 * kT; ++i) {
           const float x = __shfl_sync(0xffffffffu, sums[i], 4 * (lane & 7));
           if (lane >> 3 == i) add = x;
         }
-        if (at + lane < len) weights(j, pg)[lane] = old + add;
+        if (lane < kRows && at + lane < len) weights(j, pg)[lane] = old + add;
       } else {
         issue(j + kSlots);
       }
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
 // Reads are what bounds a single tile of query rows: a ring holds four units where there is room, else two.
 template <int BK, int BV, bool kOne>
 cudaError_t launch_one(const Params& p, cudaStream_t s) {
-  constexpr int kSlots = kOne && BK == 4 ? 4 : 2, kRoom = 208 * 1024, kRing = kSlots * Unit<BK, BV>::kBytes;
+  constexpr int kSlots = kOne && BK == 4 ? 4 : 2, kRoom = 208 * 1024, kRing = kSlots * Unit<BK, BV, kOne ? 2 : 1>::kBytes;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = hyq_once_per_device(done, [] {
     return cudaFuncSetAttribute(mass_kernel<BK, BV, kSlots, kOne>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
