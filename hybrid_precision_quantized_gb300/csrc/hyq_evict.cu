@@ -15,6 +15,8 @@
 // tables.  What bounds it: the mass is read once, each moved row read and written
 // once, and of each page that changes the keys for its bounds: HBM for long
 // prompts, latency (dependent launches and reads) for small calls.
+#include "hyq_codes.cuh"
+#include "hyq_f2.cuh"
 #include "hyq_paged.cuh"
 
 namespace {
@@ -119,115 +121,148 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   }
 }
 
-// A mass as an integer that orders like it: NaN above everything, -0 as 0.
+// A mass as an integer above 0 that orders like it: NaN above everything, -0 as 0.
 __device__ __forceinline__ uint32_t mass_key(float x) {
   if (x != x) return 0xFFFFFFFFu;
   const uint32_t u = __float_as_uint(x + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelThreads = 512;
-// One block per (layer, row, KV head); a thread takes whole pages.
+constexpr int kPiece = 16;          // positions that a thread takes at a time
+constexpr int kSmall = 8192;        // positions that a small block holds
+static_assert(HYQ_PAGE_ROWS == 4 * kPiece, "four lanes a page");
+
+// One block per (layer, row, KV head).  The threshold is found two bits at a time by counting the keys at and above
+// three candidates: the keys stay in registers (read again for each pair of bits past the first 32768 positions), and
+// counting needs no atomics, whose bins the exponents of masses share (by a histogram of eight bits at a time, a page a
+// thread: 229 us for 4096 selections of 4160, with this NNN).
+// kSelThreads threads hold kHeld pieces each.  Two sizes, three small blocks or a large one an SM, each for the
+// sequences of its size (all in large ones: 975 us instead of NNN for the whole eviction of 16 x 4096 in 32 layers).
+template <int kSelThreads, int kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
-  __shared__ int s_hist[256], s_scan[kSelThreads / 32], s_bin, s_left;
+  constexpr int kSelWarps = kSelThreads / 32, kPass = kSelThreads * kPiece;  // positions of a pass
+  __shared__ int s_count[2][3][kSelWarps], s_scan[kSelWarps];
   chain_kernel();
   const int h = blockIdx.x % p.HKV, b = blockIdx.x / p.HKV, layer = blockIdx.y, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   const Row row = p.ws.row[b];
   if (row.k < 0) return;
   const int hi = row.n - p.n_last, w = row.k - p.n_last, want = w - p.n_first;  // of [n_first, hi)
-  const int nb = (hi + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS;
+  if ((hi <= kSmall) != (kHeld * kPass == kSmall)) return;  // the other size's
   const int32_t* table = p.pages.table + (size_t)row.seq * p.pages.max_blocks;
   const float* mass = p.mass + (size_t)layer * p.pages.n_pages * p.HKV * HYQ_PAGE_ROWS;
-  // keys of a page's positions that may be chosen
-  auto each = [&](int j, auto f) {
-    const float4* at = reinterpret_cast<const float4*>(mass + ((size_t)table[j] * p.HKV + h) * HYQ_PAGE_ROWS);
-#pragma unroll 4
-    for (int c = 0; c < HYQ_PAGE_ROWS / 4; ++c) {
-      const float4 x = at[c];
-      const float v[4] = {x.x, x.y, x.z, x.w};
+  // the keys of the piece that begins at `pos`; those that are not to be chosen from are 0 (no mass's key)
+  auto keys = [&](int pos, uint32_t (&key)[kPiece]) {
+    float4 v[kPiece / 4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 4 * c + e, pos = j * HYQ_PAGE_ROWS + r;
-        if (pos >= p.n_first && pos < hi) f(r, mass_key(v[e]));
-      }
+    for (int c = 0; c < kPiece / 4; ++c) v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pos < hi) {
+      const float4* at = reinterpret_cast<const float4*>(
+          mass + ((size_t)table[pos / HYQ_PAGE_ROWS] * p.HKV + h) * HYQ_PAGE_ROWS + pos % HYQ_PAGE_ROWS);
+#pragma unroll
+      for (int c = 0; c < kPiece / 4; ++c) v[c] = at[c];
+    }
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      const float x = i & 2 ? (i & 1 ? v[i >> 2].w : v[i >> 2].z) : (i & 1 ? v[i >> 2].y : v[i >> 2].x);
+      key[i] = pos + i >= p.n_first && pos + i < hi ? mass_key(x) : 0u;
     }
   };
-  // the want-th largest key: eight bits at a time
+  uint32_t held[kHeld][kPiece];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) keys(k * kPass + kPiece * tid, held[k]);
+  // the want-th largest key: the largest one that at least `want` keys reach
   uint32_t key = 0;
-  int left = want;  // of the keys that share the bits so far
-  for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
-    if (tid < 256) s_hist[tid] = 0;
-    __syncthreads();
-    for (int j = tid; j < nb; j += kSelThreads)
-      each(j, [&](int, uint32_t x) {
-        if (shift == 24 || (x >> (shift + 8)) == (key >> (shift + 8))) atomicAdd(&s_hist[(x >> shift) & 255], 1);
-      });
-    __syncthreads();
-    if (tid < 32) {  // lane l: bins 8 l .. 8 l + 7; how many lie above
-      int mine = 0;
-      for (int k = 0; k < 8; ++k) mine += s_hist[8 * lane + k];
-      int above = mine;
+#pragma unroll 1
+  for (int shift = 30; shift >= 0 && want > 0; shift -= 2) {
+    const uint32_t c1 = key | 1u << shift, c2 = key | 2u << shift, c3 = key | 3u << shift;
+    int n1 = 0, n2 = 0, n3 = 0;
+    auto count = [&](const uint32_t (&x)[kPiece]) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_down_sync(0xffffffffu, above, o);
-        if (lane + o < 32) above += y;
-      }
-      above -= mine;
-      for (int k = 7; k >= 0; --k) {
-        const int c = s_hist[8 * lane + k];
-        if (above < left && left <= above + c) {
-          s_bin = 8 * lane + k;
-          s_left = left - above;
-        }
-        above += c;
-      }
-    }
-    __syncthreads();
-    key |= (uint32_t)s_bin << shift;
-    left = s_left;
-    __syncthreads();
-  }
-  // the mask: what lies above the key, and the first `left` that equal it
-  const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
-  int kept = 0, ties = 0;  // in the pages before
-  for (int j0 = 0; j0 < nb; j0 += kSelThreads) {
-    const int j = j0 + tid;
-    uint64_t gt = 0, eq = 0;
-    if (j < nb) {
-      each(j, [&](int r, uint32_t x) {
-        gt |= (uint64_t)(want > 0 && x > key) << r;
-        eq |= (uint64_t)(want > 0 && x == key) << r;
-      });
-      const int nf = p.n_first - j * HYQ_PAGE_ROWS;
-      if (nf > 0) gt |= nf >= 64 ? ~0ull : (1ull << nf) - 1;
-    }
-    auto scan = [&](int v, int& before) {  // exclusive over the block, on top of `before`
-      int pre = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = pre;
-      __syncthreads();
-      int at = before + pre - v;
-      for (int k = 0; k < kSelThreads / 32; ++k) {
-        if (k < warp) at += s_scan[k];
-        before += s_scan[k];
-      }
-      return at;
+      for (int i = 0; i < kPiece; ++i) n1 += x[i] >= c1, n2 += x[i] >= c2, n3 += x[i] >= c3;
     };
-    const int ne = __popcll(eq), tie_at = scan(ne, ties);
-    int take = max(0, min(ne, left - tie_at));
-    while (__popcll(eq) > take) eq &= ~(1ull << (63 - __clzll(eq)));
-    const uint64_t m = gt | eq;
-    const int at = scan(__popcll(m), kept);
-    if (j < nb) {
-      p.ws.mask[base + j] = m;
-      p.ws.before[base + j] = at;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (k * kPass < hi) count(held[k]);
+    for (int pos = kHeld * kPass + kPiece * tid; pos < hi; pos += kPass) {
+      uint32_t x[kPiece];
+      keys(pos, x);
+      count(x);
     }
+    n1 = __reduce_add_sync(0xffffffffu, n1), n2 = __reduce_add_sync(0xffffffffu, n2), n3 = __reduce_add_sync(0xffffffffu, n3);
+    int(&s)[3][kSelWarps] = s_count[(shift >> 1) & 1];
+    if (lane == 0) s[0][warp] = n1, s[1][warp] = n2, s[2][warp] = n3;
+    __syncthreads();
+    const bool in = lane < kSelWarps;  // every warp sums up the warps' counts
+    n1 = __reduce_add_sync(0xffffffffu, in ? s[0][lane] : 0), n2 = __reduce_add_sync(0xffffffffu, in ? s[1][lane] : 0);
+    n3 = __reduce_add_sync(0xffffffffu, in ? s[2][lane] : 0);
+    key = n3 >= want ? c3 : n2 >= want ? c2 : n1 >= want ? c1 : key;
+  }
+  // the mask: what lies above the key, and the first of those that equal it
+  const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
+  int kept = 0, ties = 0;  // in the pieces before
+  auto scan = [&](int v, int& before) {  // exclusive over the block, on top of `before`
+    int pre = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[warp] = pre;
+    __syncthreads();
+    int at = before + pre - v;
+    for (int k = 0; k < kSelWarps; ++k) {
+      if (k < warp) at += s_scan[k];
+      before += s_scan[k];
+    }
+    return at;
+  };
+  // how many of those that equal the key are kept: all above it are
+  int above = 0;
+  auto over = [&](const uint32_t (&x)[kPiece]) {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) above += x[i] > key;
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k * kPass < hi) over(held[k]);
+  for (int pos = kHeld * kPass + kPiece * tid; pos < hi; pos += kPass) {
+    uint32_t x[kPiece];
+    keys(pos, x);
+    over(x);
+  }
+  int total = 0;
+  (void)scan(above, total);
+  const int left = want - total;
+  auto finish = [&](int pos, const uint32_t (&x)[kPiece]) {  // (all threads)
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i) {
+      gt |= (uint32_t)(want > 0 && x[i] > key) << i;
+      eq |= (uint32_t)(want > 0 && x[i] == key && key != 0) << i;
+    }
+    const int nf = p.n_first - pos;
+    if (nf > 0) gt |= nf >= kPiece ? (1u << kPiece) - 1 : (1u << nf) - 1;
+    const int tie_at = scan(__popc(eq), ties);
+    int drop = __popc(eq) - max(0, min(__popc(eq), left - tie_at));
+    for (; drop > 0; --drop) eq &= ~(1u << (31 - __clz(eq)));
+    const uint32_t m = pos < hi ? gt | eq : 0u;
+    const int at = scan(__popc(m), kept);
+    // four lanes' pieces are a page
+    const uint32_t lo = m | __shfl_down_sync(0xffffffffu, m, 1) << 16, up = __shfl_down_sync(0xffffffffu, lo, 2);
+    if ((lane & 3) == 0 && pos < hi) {
+      p.ws.mask[base + pos / HYQ_PAGE_ROWS] = (uint64_t)lo | (uint64_t)up << 32;
+      p.ws.before[base + pos / HYQ_PAGE_ROWS] = at;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k * kPass < hi) finish(k * kPass + kPiece * tid, held[k]);
+  for (int first = kHeld * kPass; first < hi; first += kPass) {
+    uint32_t x[kPiece];
+    keys(first + kPiece * tid, x);
+    finish(first + kPiece * tid, x);
   }
 }
 
@@ -369,17 +404,112 @@ __device__ __forceinline__ void write_record(const uint8_t* page, int rows, uint
   if (d < 4) reinterpret_cast<int32_t*>(rec + 2 * HYQ_D)[d] = d == 0 ? e : 0;
 }
 
-// The free places below w: a block takes one page of one (layer, row, KV head).
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One warp: least and largest keys of a page, element by element, as they are held.
+template <int BK, int BV>
+struct Extremes {
+  float lo[32], hi[32];  // of the lane's rows so far: elements 32 v + .. of its eight of each group v
+  uint4 kc[BK / 2], ka, kb;
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
+  }
+  __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
+    using F = QFmt<BK, BV>;
+#pragma unroll
+    for (int i = 0; i < BK / 2; ++i) kc[i] = *reinterpret_cast<const uint4*>(tile + 512 * i + 16 * lane);
+    ka = *reinterpret_cast<const uint4*>(tile + F::kKMeta + 16 * (lane >> 2));
+    kb = *reinterpret_cast<const uint4*>(tile + F::kKMeta + 16 * ((lane >> 2) + 8));
+  }
+  // The tile's rows below vr (kAll: all sixteen).
+  template <bool kAll>
+  __device__ __forceinline__ void take(int lane, int vr) {
+    const bool ina = (lane >> 2) < vr, inb = (lane >> 2) + 8 < vr;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      uint32_t xa[4], xb[4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (BK == 4) {
+          const uint32_t w = u4at(kc[v >> 1], 2 * (v & 1) + u), w8 = w >> 8;
+          xa[2 * u] = low_codes(w), xa[2 * u + 1] = low_codes(w8);
+          xb[2 * u] = high_codes(w), xb[2 * u + 1] = high_codes(w8);
+        } else {
+          const uint32_t wa = u4at(kc[BK == 4 ? 0 : v], 2 * u), wb = u4at(kc[BK == 4 ? 0 : v], 2 * u + 1);
+          xa[2 * u] = even_codes(wa), xa[2 * u + 1] = odd_codes(wa);
+          xb[2 * u] = even_codes(wb), xb[2 * u + 1] = odd_codes(wb);
+        }
+      }
+      auto half = [&](uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(v & 1 ? w >> 16 : w & 0xFFFFu))); };
+      const float sa = half(v < 2 ? ka.x : ka.y), za = half(v < 2 ? ka.z : ka.w);
+      const float sb = half(v < 2 ? kb.x : kb.y), zb = half(v < 2 ? kb.z : kb.w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 ca = *reinterpret_cast<const __half2*>(&xa[i]), cb = *reinterpret_cast<const __half2*>(&xb[i]);
+        const float a[2] = {fmaf(__low2float(ca), sa, za), fmaf(__high2float(ca), sa, za)};
+        const float b[2] = {fmaf(__low2float(cb), sb, zb), fmaf(__high2float(cb), sb, zb)};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int at = 8 * v + 2 * i + e;
+          lo[at] = fmin3(lo[at], kAll || ina ? a[e] : INFINITY, kAll || inb ? b[e] : INFINITY);
+          hi[at] = fmax3(hi[at], kAll || ina ? a[e] : -INFINITY, kAll || inb ? b[e] : -INFINITY);
+        }
+      }
+    }
+  }
+  // The record of what has been taken: lanes that differ in g exchange halves until each has four elements of all rows.
+  __device__ __forceinline__ void write(uint8_t* rec, int lane) {
+    auto halve = [&](int n, int bit) {  // of the first 2 n elements a lane keeps the half that its bit says
+      const bool up = lane & bit;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) {
+          const float l = __shfl_xor_sync(0xffffffffu, up ? lo[i] : lo[n + i], bit), h = __shfl_xor_sync(0xffffffffu, up ? hi[i] : hi[n + i], bit);
+          lo[i] = fminf(up ? lo[n + i] : lo[i], l);
+          hi[i] = fmaxf(up ? hi[n + i] : hi[i], h);
+        }
+    };
+    halve(16, 16);
+    halve(8, 8);
+    halve(4, 4);
+    float am = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) am = fmax3(am, fabsf(lo[i]), fabsf(hi[i]));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+    const int e = bound_exp(am), t = lane & 3, v = lane >> 3, i4 = (lane >> 2) & 1;
+    const float f = pow2_int(-e);
+    uint32_t l = 0, h = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      l |= (uint32_t)(uint8_t)(int8_t)(int)floorf(lo[i] * f) << (8 * i);
+      h |= (uint32_t)(uint8_t)(int8_t)(int)ceilf(hi[i] * f) << (8 * i);
+    }
+    const int at = 32 * v + (BK == 4 ? 8 * t + 4 * i4 : 16 * i4 + 4 * t);
+    *reinterpret_cast<uint32_t*>(rec + at) = l;
+    *reinterpret_cast<uint32_t*>(rec + HYQ_D + at) = h;
+    if (lane < 4) reinterpret_cast<int32_t*>(rec + 2 * HYQ_D)[lane] = lane == 0 ? e : 0;
+  }
+};
+
+// The free places below w: a warp takes one page of one (layer, row, KV head).  A tile without free places is read for its
+// keys alone, straight into registers, the next one ahead.
 template <int BK, int BV>
 __global__ void __launch_bounds__(kMoveThreads) fill_kernel(const Params p) {
   using F = QFmt<BK, BV>;
-  __shared__ __align__(16) uint8_t s_page[F::kBlock];
-  __shared__ float s_red[4];
+  __shared__ __align__(16) uint8_t s_tile[kMoveThreads / 32][F::kTile];
   chain_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* held = s_tile[warp];
   const int64_t per = (int64_t)p.HKV * p.pages.n_layers, items = p.ws.cum[p.batch] * per;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int64_t x = it / per;
+  for (int64_t it = (int64_t)blockIdx.x * (kMoveThreads / 32) + warp; it < items; it += (int64_t)gridDim.x * (kMoveThreads / 32)) {
+    const int64_t x = items >> 32 ? it / per : (uint32_t)it / (uint32_t)per;
     const int lh = (int)(it - x * per), layer = lh / p.HKV, h = lh - layer * p.HKV;
     int b = 0, hi = p.batch;
     while (hi - b > 1) {
@@ -388,45 +518,55 @@ __global__ void __launch_bounds__(kMoveThreads) fill_kernel(const Params p) {
       else hi = m;
     }
     const Row row = p.ws.row[b];
-    const int j = (int)(x - p.ws.cum[b]), w = row.k - p.n_last;
+    const int j = (int)(x - p.ws.cum[b]), w = row.k - p.n_last, at = j * HYQ_PAGE_ROWS;
     const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
-    const uint64_t mask = p.ws.mask[base + j];
-    const int here = min(HYQ_PAGE_ROWS, w - j * HYQ_PAGE_ROWS);  // its rows below w
-    uint64_t holes = ~mask & (here == 64 ? ~0ull : (1ull << here) - 1);
+    const int here = min(HYQ_PAGE_ROWS, w - at);  // its rows below w
+    const uint64_t holes = ~p.ws.mask[base + j] & (here == 64 ? ~0ull : (1ull << here) - 1);
     if (!holes) continue;
     const Place pl = place_of<BK, BV>(p, row, layer, h);
     // the r-th free place takes the r-th kept position from w on, the (kw + r)-th of all
     const int nb = (row.n - p.n_last + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS, jw = w / HYQ_PAGE_ROWS;
     const uint64_t mw = jw < nb ? p.ws.mask[base + jw] & ((1ull << (w % HYQ_PAGE_ROWS)) - 1) : 0;
     const int kw = jw < nb ? p.ws.before[base + jw] + __popcll(mw) : 0;
-    const int first = j * HYQ_PAGE_ROWS - p.ws.before[base + j];  // free places in the pages before
-    const int r = 16 * warp + lane;
-    int from = -1;
-    if (lane < 16 && (holes >> r) & 1) {
-      const int rank = kw + first + __popcll(holes & ((1ull << r) - 1));
-      int lo = jw, up = nb;  // the last page with `before` <= rank
-      while (up - lo > 1) {
-        const int m = (lo + up) >> 1;
-        if (p.ws.before[base + m] <= rank) lo = m;
-        else up = m;
-      }
-      uint64_t m = p.ws.mask[base + lo];
-      for (int s = rank - p.ws.before[base + lo]; s > 0; --s) m &= m - 1;
-      from = lo * HYQ_PAGE_ROWS + __ffsll(m) - 1;
-    }
-    uint8_t* tile = pl.tile<BK, BV>(j * HYQ_PAGE_ROWS + 16 * warp);
-    uint8_t* held = s_page + warp * F::kTile;
-    copy_tile<BK, BV>(held, tile, lane);
-    __syncwarp();
-    const float weight = gather_rows<BK, BV>(pl, held, lane, from);
-    if (__any_sync(0xffffffffu, from >= 0)) copy_tile<BK, BV>(tile, held, lane);
-    if (from >= 0) *pl.weight(j * HYQ_PAGE_ROWS + r) = weight;
-    __syncthreads();
+    const int rank0 = kw + at - p.ws.before[base + j];  // of the page's first free place
     // a page with rows of the last n_last gets its record when they are there
-    if (j * HYQ_PAGE_ROWS + HYQ_PAGE_ROWS <= w || p.n_last == 0)
-      write_record<BK, BV>(s_page, min(HYQ_PAGE_ROWS, row.k - j * HYQ_PAGE_ROWS),
-                           pl.bounds + (size_t)pl.table[j] * p.HKV * HYQ_BOUND_BYTES, s_red);
-    __syncthreads();
+    const bool record = at + HYQ_PAGE_ROWS <= w || p.n_last == 0;
+    const int valid = min(HYQ_PAGE_ROWS, row.k - at);
+    uint8_t* tile0 = pl.tile<BK, BV>(at);
+    Extremes<BK, BV> x2;
+    x2.reset();
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      uint8_t* tile = tile0 + i * F::kTile;
+      const uint32_t mine = (uint32_t)(holes >> (16 * i)) & 0xFFFFu;
+      if (mine) {
+        int from = -1;
+        if (lane < 16 && (mine >> lane) & 1) {
+          const int rank = rank0 + __popcll(holes & ((1ull << (16 * i + lane)) - 1));
+          int lo = jw, up = nb;  // the last page with `before` <= rank
+          while (up - lo > 1) {
+            const int m = (lo + up) >> 1;
+            if (p.ws.before[base + m] <= rank) lo = m;
+            else up = m;
+          }
+          uint64_t m = p.ws.mask[base + lo];
+          for (int s = rank - p.ws.before[base + lo]; s > 0; --s) m &= m - 1;
+          from = lo * HYQ_PAGE_ROWS + __ffsll(m) - 1;
+        }
+        copy_tile<BK, BV>(held, tile, lane);
+        __syncwarp();
+        const float weight = gather_rows<BK, BV>(pl, held, lane, from);
+        copy_tile<BK, BV>(tile, held, lane);
+        if (from >= 0) *pl.weight(at + 16 * i + lane) = weight;
+      }
+      if (record && 16 * i < valid) {
+        x2.load(mine ? held : tile, lane);
+        if (valid - 16 * i >= 16) x2.template take<true>(lane, 16);
+        else x2.template take<false>(lane, valid - 16 * i);
+      }
+      __syncwarp();
+    }
+    if (record) x2.write(pl.bounds + (size_t)pl.table[j] * p.HKV * HYQ_BOUND_BYTES, lane);
   }
 }
 
@@ -470,9 +610,13 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   cudaError_t e = hyq_launch_chained(plan_kernel, dim3(1), kPlanThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   const dim3 heads(p.batch * p.HKV, p.pages.n_layers);
-  e = hyq_launch_chained(select_kernel, heads, kSelThreads, 0, s, p);
+  e = hyq_launch_chained(select_kernel<256, 2>, heads, 256, 0, s, p);
   if (e != cudaSuccess) return e;
-  e = hyq_launch_chained(fill_kernel<BK, BV>, dim3(12 * hyq_num_sms()), kMoveThreads, 0, s, p);
+  if ((int64_t)p.pages.max_blocks * HYQ_PAGE_ROWS > kSmall) {  // longer sequences may be there
+    e = hyq_launch_chained(select_kernel<512, 4>, heads, 512, 0, s, p);
+    if (e != cudaSuccess) return e;
+  }
+  e = hyq_launch_chained(fill_kernel<BK, BV>, dim3(4 * hyq_num_sms()), kMoveThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   return hyq_launch_chained(shift_kernel<BK, BV>, heads, kMoveThreads, 0, s, p);
 }

@@ -17,6 +17,7 @@
 // between 2^8 and 2^14 at the row's maximum so that the small ones are not lost.
 #include <type_traits>
 
+#include "hyq_codes.cuh"
 #include "hyq_f2.cuh"
 #include "hyq_paged.cuh"
 #include "hyq_tc.cuh"
@@ -63,8 +64,9 @@ struct Shares {
   int64_t each, more;
   __device__ __forceinline__ int64_t begin(int64_t c) const { return c * each + min(c, more); }
   __device__ __forceinline__ int owner(int64_t x) const {
-    const int64_t wide = more * (each + 1);
-    return (int)(x < wide ? x / (each + 1) : more + (x - wide) / each);
+    const int64_t wide = more * (each + 1), y = x < wide ? x : x - wide, d = x < wide ? each + 1 : each;
+    const int64_t q = ((y | d) >> 32) == 0 ? (int64_t)((uint32_t)y / (uint32_t)d) : y / d;
+    return (int)(x < wide ? q : more + q);
   }
 };
 struct Plan {
@@ -113,7 +115,7 @@ __device__ __forceinline__ int unit_from(int x, int nt) { return max(0, (x - kCo
 // Whether block c has units of the tile whose first job (behind the fixed work) is `base`.
 __device__ __forceinline__ bool holds(const Shares& sh, int c, int64_t base, int nt, int U) {
   const int64_t a = max((int64_t)0, sh.begin(c) - base), b = min((int64_t)nt * U, sh.begin(c + 1) - base);
-  return a < b && (a + nt - 1) / nt < (b + nt - 1) / nt;
+  return a < b && (a + nt - 1) >> (nt - 1) < (b + nt - 1) >> (nt - 1);  // (nt is 1 or 2)
 }
 
 // Byte offset of 16-byte chunk c of row r in a swizzled region.
@@ -125,36 +127,6 @@ __host__ __device__ constexpr int key_of(int row) { return (row & ~7) | ((row & 
 // Element of the head dimension that column n of O holds (the rows of the value
 // tile are ordered so that a stmatrix's eight rows meet distinct banks).
 __host__ __device__ constexpr int elem_of(int n) { return (n & ~31) | ((n & 7) << 2) | ((n >> 3) & 3); }
-
-__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
-                            *reinterpret_cast<const __half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b) {
-  const __half2 r = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Codes as an fp16 pair, exactly: their bits under 1024, less 1024.
-__device__ __forceinline__ uint32_t low_codes(uint32_t w) {  // nibbles 0 and 4
-  return hadd2_u((w & 0x000F000Fu) | 0x64006400u, 0xE400E400u);
-}
-__device__ __forceinline__ uint32_t high_codes(uint32_t w) {  // nibbles 1 and 5, which count 16 each
-  return hfma2_u((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
-}
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) {  // bytes 0 and 2
-  return hadd2_u((w & 0x00FF00FFu) | 0x64006400u, 0xE400E400u);
-}
-__device__ __forceinline__ uint32_t odd_codes(uint32_t w) {  // bytes 1 and 3
-  return hadd2_u(__byte_perm(w, 0x64646464u, 0x4341), 0xE400E400u);
-}
-__device__ __forceinline__ uint32_t u4at(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-// Halves 0 or 1 of a word, twice.
-__device__ __forceinline__ uint32_t both(uint32_t w, int half) { return __byte_perm(w, 0, half ? 0x3232 : 0x1010); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -1040,13 +1012,14 @@ template <bool kShared>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
   chain_kernel();
   const int lane = threadIdx.x & 31, d4 = 4 * (threadIdx.x >> 5) + (lane >> 3);
-  const int64_t per = ((int64_t)p.n_tokens * p.gq + 7) / 8, items = per * p.HKV;
+  // (the query rows of all heads are fewer than 2^31)
+  const uint32_t rows = (uint32_t)p.n_tokens * p.gq, per = (rows + 7) / 8, items = per * p.HKV;
   const Plan& plan = *p.plan;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+  for (uint32_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int h = (int)(it / per);
-    const int64_t R = (it - h * per) * 8 + (lane & 7);
-    if (R >= (int64_t)p.n_tokens * p.gq) continue;
-    const int tok = (int)(R / p.gq), head = (int)(R - (int64_t)tok * p.gq);
+    const uint32_t R = (it - h * per) * 8 + (lane & 7);
+    if (R >= rows) continue;
+    const int tok = (int)(R / p.gq), head = (int)(R - (uint32_t)tok * p.gq);
     int i, len = 0;
     if (kShared) {
       i = p.n_seg ? group_of(p.shared, tok / p.n_q) : 0;
@@ -1077,12 +1050,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       const int64_t base = plan.cum[i] + h * head_slots(len, plan.rows[i]) + (int64_t)mt * (kCost + 2 * U) + kCost;
       const int c0 = plan.sh.owner(base), c1 = plan.sh.owner(base + (int64_t)nt * (U - 1));
       if (c0 == c1) continue;  // written by its block
-      for (int c = c0; c <= c1; ++c) {
-        const float* part = p.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * kPart;
-        // a run that ends before a pair's second half of a unit may have nothing of the tile
-        if (c > c0 && !holds(plan.sh, c, base, nt, U)) continue;
-        add(__ldcg(reinterpret_cast<const float2*>(part + kPair * HYQ_D) + rr),
-            __ldcg(reinterpret_cast<const float4*>(part) + d4 * kPair + rr));
+      constexpr int kHold = 8;  // parts under way
+      for (int c = c0; c <= c1; c += kHold) {
+        float2 ml[kHold];
+        float4 v[kHold];
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) {
+          const float* part = p.part + ((size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0)) * kPart;
+          // (a run that ends before a pair's second half of a unit may have nothing of the tile)
+          const bool in = c + k <= c1 && holds(plan.sh, c + k, base, nt, U);
+          ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(part + kPair * HYQ_D) + rr) : make_float2(-INFINITY, 0.f);
+          v[k] = in ? __ldcg(reinterpret_cast<const float4*>(part) + d4 * kPair + rr) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) add(ml[k], v[k]);
       }
     }
     if (kShared) {
