@@ -28,7 +28,7 @@ struct Row {
   int32_t seq, n, k;  // k < 0: nothing to do
 };
 struct EvictWs {
-  int64_t* cum;     // [batch + 1] pages below w of the rows before
+  int64_t* cum;     // [batch + 1] kept pages of the rows before
   Row* row;         // [batch]
   uint64_t* mask;   // [n_layers][batch][HKV][max_blocks] kept positions below n - n_last
   int32_t* before;  // likewise: how many are kept in the pages before
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const Params p) {
   if (err) hyq_set_err(pg.err, err);
   __syncthreads();
   k = s_k[i];
-  int64_t w = i < p.batch && k >= 0 ? (k - p.n_last + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS : 0, pre = w;
+  int64_t w = i < p.batch && k >= 0 ? (k + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS : 0, pre = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, pre, o);
@@ -197,6 +197,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
     n1 = __reduce_add_sync(0xffffffffu, in ? s[0][lane] : 0), n2 = __reduce_add_sync(0xffffffffu, in ? s[1][lane] : 0);
     n3 = __reduce_add_sync(0xffffffffu, in ? s[2][lane] : 0);
     key = n3 >= want ? c3 : n2 >= want ? c2 : n1 >= want ? c1 : key;
+    if (n3 == want || n2 == want || n1 == want) {  // just as many reach a candidate: no need to know the key itself
+      key = (n3 == want ? c3 : n2 == want ? c2 : c1) - 1;
+      break;
+    }
   }
   // the mask: what lies above the key, and the first of those that equal it
   const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
@@ -337,7 +341,11 @@ __device__ __forceinline__ Place place_of(const Params& p, const Row& row, int l
 template <int BK, int BV>
 __device__ __forceinline__ float gather_rows(const Place& pl, uint8_t* held, int lane, int from) {
   float weight = 0.f;
-  if (lane < 16 && from >= 0) weight = *pl.weight(from);
+  uint64_t src = 0;  // the tile that the row comes from: all rows' table entries are read at once
+  if (lane < 16 && from >= 0) {
+    weight = *pl.weight(from);
+    src = reinterpret_cast<uint64_t>(pl.tile<BK, BV>(from));
+  }
   uint32_t todo = __ballot_sync(0xffffffffu, lane < 16 && from >= 0);
   while (todo) {
     HeldRow<BK, BV> x[kHold];
@@ -346,8 +354,9 @@ __device__ __forceinline__ float gather_rows(const Place& pl, uint8_t* held, int
     for (int i = 0; i < kHold; ++i) {
       r[i] = todo ? __ffs(todo) - 1 : -1;
       todo &= todo - 1;
-      const int src = __shfl_sync(0xffffffffu, from, r[i] < 0 ? 0 : r[i]);
-      if (r[i] >= 0) x[i].load(pl.tile<BK, BV>(src), src % 16, lane);
+      const int at = r[i] < 0 ? 0 : r[i], row = __shfl_sync(0xffffffffu, from, at) & 15;
+      const uint8_t* tile = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, src, at));
+      if (r[i] >= 0) x[i].load(tile, row, lane);
     }
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
@@ -364,57 +373,23 @@ __device__ __forceinline__ void copy_tile(uint8_t* to, const uint8_t* from, int 
     if (32 * i + lane < n) reinterpret_cast<uint4*>(to)[32 * i + lane] = reinterpret_cast<const uint4*>(from)[32 * i + lane];
 }
 
-// One block: the bound record of a page's rows [0, rows) as they are held, from its tiles in shared memory.
-template <int BK, int BV>
-__device__ __forceinline__ void write_record(const uint8_t* page, int rows, uint8_t* rec, float* red /* [4] */) {
-  using F = QFmt<BK, BV>;
-  const int d = threadIdx.x;  // kMoveThreads = 128 elements
-  float mn = INFINITY, mx = -INFINITY;
-  // byte and nibble of element d in row 0 (4-bit: rows g, g + 8 share it)
-  const int q = d >> 5;
-  int at;
-  if (BK == 4) {
-    const int t = (d >> 3) & 3, u = 2 * q + ((d >> 2) & 1);
-    at = 512 * (u >> 2) + 16 * t + 4 * (u & 3) + ((d >> 1) & 1) + 2 * (d & 1);
-  } else {
-    const int t = (d >> 2) & 3, u = 2 * (d >> 4), e = d & 3;
-    at = 512 * (u >> 2) + 16 * t + 4 * (u & 3) + (e >> 1) + 2 * (e & 1);
-  }
-  for (int r = 0; r < rows; ++r) {
-    const uint8_t* tile = page + (r >> 4) * F::kTile;
-    const int i = r & 15;
-    int c = tile[at + 64 * (i & 7) + (BK == 8 ? 4 * (i >> 3) : 0)];
-    if (BK == 4) c = (c >> (4 * (i >> 3))) & 15;
-    const __half* m = reinterpret_cast<const __half*>(tile + F::kKMeta + 16 * i);
-    const float x = fmaf((float)c, __half2float(m[q]), __half2float(m[4 + q]));
-    mn = fminf(mn, x);
-    mx = fmaxf(mx, x);
-  }
-  float am = fmaxf(fabsf(mn), fabsf(mx));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  __syncthreads();
-  if ((d & 31) == 0) red[d >> 5] = am;
-  __syncthreads();
-  am = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const int e = bound_exp(am);
-  const float f = pow2_int(-e);
-  rec[d] = (uint8_t)(int8_t)(int)floorf(mn * f);
-  rec[HYQ_D + d] = (uint8_t)(int8_t)(int)ceilf(mx * f);
-  if (d < 4) reinterpret_cast<int32_t*>(rec + 2 * HYQ_D)[d] = d == 0 ? e : 0;
-}
-
 __device__ __forceinline__ float fmin3(float a, float b, float c) {
   float d;
   asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
+// A lane's key codes of a 16-row tile, and steps and zeros of rows g and g + 8.
+template <int BK>
+struct Keys {
+  uint4 kc[BK / 2], ka, kb;
+};
+
 // One warp: least and largest keys of a page, element by element, as they are held.
 template <int BK, int BV>
 struct Extremes {
   float lo[32], hi[32];  // of the lane's rows so far: elements 32 v + .. of its eight of each group v
-  uint4 kc[BK / 2], ka, kb;
+  Keys<BK> next;         // the tile that is on its way
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -423,13 +398,13 @@ struct Extremes {
   __device__ __forceinline__ void load(const uint8_t* tile, int lane) {
     using F = QFmt<BK, BV>;
 #pragma unroll
-    for (int i = 0; i < BK / 2; ++i) kc[i] = *reinterpret_cast<const uint4*>(tile + 512 * i + 16 * lane);
-    ka = *reinterpret_cast<const uint4*>(tile + F::kKMeta + 16 * (lane >> 2));
-    kb = *reinterpret_cast<const uint4*>(tile + F::kKMeta + 16 * ((lane >> 2) + 8));
+    for (int i = 0; i < BK / 2; ++i) next.kc[i] = *reinterpret_cast<const uint4*>(tile + 512 * i + 16 * lane);
+    next.ka = *reinterpret_cast<const uint4*>(tile + F::kKMeta + 16 * (lane >> 2));
+    next.kb = *reinterpret_cast<const uint4*>(tile + F::kKMeta + 16 * ((lane >> 2) + 8));
   }
   // The tile's rows below vr (kAll: all sixteen).
   template <bool kAll>
-  __device__ __forceinline__ void take(int lane, int vr) {
+  __device__ __forceinline__ void take(const Keys<BK>& k, int lane, int vr) {
     const bool ina = (lane >> 2) < vr, inb = (lane >> 2) + 8 < vr;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -437,18 +412,18 @@ struct Extremes {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (BK == 4) {
-          const uint32_t w = u4at(kc[v >> 1], 2 * (v & 1) + u), w8 = w >> 8;
+          const uint32_t w = u4at(k.kc[v >> 1], 2 * (v & 1) + u), w8 = w >> 8;
           xa[2 * u] = low_codes(w), xa[2 * u + 1] = low_codes(w8);
           xb[2 * u] = high_codes(w), xb[2 * u + 1] = high_codes(w8);
         } else {
-          const uint32_t wa = u4at(kc[BK == 4 ? 0 : v], 2 * u), wb = u4at(kc[BK == 4 ? 0 : v], 2 * u + 1);
+          const uint32_t wa = u4at(k.kc[BK == 4 ? 0 : v], 2 * u), wb = u4at(k.kc[BK == 4 ? 0 : v], 2 * u + 1);
           xa[2 * u] = even_codes(wa), xa[2 * u + 1] = odd_codes(wa);
           xb[2 * u] = even_codes(wb), xb[2 * u + 1] = odd_codes(wb);
         }
       }
       auto half = [&](uint32_t w) { return __half2float(__ushort_as_half((unsigned short)(v & 1 ? w >> 16 : w & 0xFFFFu))); };
-      const float sa = half(v < 2 ? ka.x : ka.y), za = half(v < 2 ? ka.z : ka.w);
-      const float sb = half(v < 2 ? kb.x : kb.y), zb = half(v < 2 ? kb.z : kb.w);
+      const float sa = half(v < 2 ? k.ka.x : k.ka.y), za = half(v < 2 ? k.ka.z : k.ka.w);
+      const float sb = half(v < 2 ? k.kb.x : k.kb.y), zb = half(v < 2 ? k.kb.z : k.kb.w);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const __half2 ca = *reinterpret_cast<const __half2*>(&xa[i]), cb = *reinterpret_cast<const __half2*>(&xb[i]);
@@ -498,75 +473,126 @@ struct Extremes {
   }
 };
 
-// The free places below w: a warp takes one page of one (layer, row, KV head).  A tile without free places is read for its
-// keys alone, straight into registers, the next one ahead.
+// A kept page of one (layer, row, KV head): item `it` of all.
+struct Item {
+  Row row;
+  int b, layer, h, page;  // call row; page of the sequence
+};
+__device__ __forceinline__ Item item_of(const Params& p, const int64_t* cum, int64_t it) {
+  const int64_t per = (int64_t)p.HKV * p.pages.n_layers, x = it >> 32 ? it / per : (uint32_t)it / (uint32_t)per;
+  const int lh = (int)(it - x * per);
+  Item r;
+  r.layer = lh / p.HKV;
+  r.h = lh - r.layer * p.HKV;
+  int hi = p.batch;
+  r.b = 0;
+  while (hi - r.b > 1) {
+    const int m = (r.b + hi) >> 1;
+    if (cum[m] <= x) r.b = m;
+    else hi = m;
+  }
+  r.row = p.ws.row[r.b];
+  r.page = (int)(x - cum[r.b]);
+  return r;
+}
+__device__ __forceinline__ size_t mask_of(const Params& p, const Item& it) {
+  return (((size_t)it.layer * p.batch + it.b) * p.HKV + it.h) * p.pages.max_blocks;
+}
+// Its places below w that are free.
+__device__ __forceinline__ uint64_t free_places(const Params& p, const Item& it) {
+  const int here = it.row.k - p.n_last - it.page * HYQ_PAGE_ROWS;  // rows below w
+  if (here <= 0) return 0;
+  return ~p.ws.mask[mask_of(p, it) + it.page] & (here >= 64 ? ~0ull : (1ull << here) - 1);
+}
+
+// The free places below w: a warp takes a page.  (Its time is a chain of dependent reads; a block a page, a tile a warp,
+// left three of four warps without work where a page has one free place: 385 against NNN us for 16 x 4096 in 32 layers.)
 template <int BK, int BV>
 __global__ void __launch_bounds__(kMoveThreads) fill_kernel(const Params p) {
   using F = QFmt<BK, BV>;
+  constexpr int kWords = F::kTile / 16, kLoads = (kWords + 31) / 32;
   __shared__ __align__(16) uint8_t s_tile[kMoveThreads / 32][F::kTile];
+  __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];
   chain_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i <= p.batch; i += kMoveThreads) s_cum[i] = p.ws.cum[i];
+  __syncthreads();
   uint8_t* held = s_tile[warp];
-  const int64_t per = (int64_t)p.HKV * p.pages.n_layers, items = p.ws.cum[p.batch] * per;
+  const int64_t items = s_cum[p.batch] * p.HKV * p.pages.n_layers;
   for (int64_t it = (int64_t)blockIdx.x * (kMoveThreads / 32) + warp; it < items; it += (int64_t)gridDim.x * (kMoveThreads / 32)) {
-    const int64_t x = items >> 32 ? it / per : (uint32_t)it / (uint32_t)per;
-    const int lh = (int)(it - x * per), layer = lh / p.HKV, h = lh - layer * p.HKV;
-    int b = 0, hi = p.batch;
-    while (hi - b > 1) {
-      const int m = (b + hi) >> 1;
-      if (p.ws.cum[m] <= x) b = m;
-      else hi = m;
-    }
-    const Row row = p.ws.row[b];
-    const int j = (int)(x - p.ws.cum[b]), w = row.k - p.n_last, at = j * HYQ_PAGE_ROWS;
-    const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
-    const int here = min(HYQ_PAGE_ROWS, w - at);  // its rows below w
-    const uint64_t holes = ~p.ws.mask[base + j] & (here == 64 ? ~0ull : (1ull << here) - 1);
+    const Item x = item_of(p, s_cum, it);
+    const uint64_t holes = free_places(p, x);
     if (!holes) continue;
-    const Place pl = place_of<BK, BV>(p, row, layer, h);
+    const Place pl = place_of<BK, BV>(p, x.row, x.layer, x.h);
+    const size_t base = mask_of(p, x);
     // the r-th free place takes the r-th kept position from w on, the (kw + r)-th of all
-    const int nb = (row.n - p.n_last + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS, jw = w / HYQ_PAGE_ROWS;
+    const int w = x.row.k - p.n_last, at = x.page * HYQ_PAGE_ROWS;
+    const int nb = (x.row.n - p.n_last + HYQ_PAGE_ROWS - 1) / HYQ_PAGE_ROWS, jw = w / HYQ_PAGE_ROWS;
     const uint64_t mw = jw < nb ? p.ws.mask[base + jw] & ((1ull << (w % HYQ_PAGE_ROWS)) - 1) : 0;
-    const int kw = jw < nb ? p.ws.before[base + jw] + __popcll(mw) : 0;
-    const int rank0 = kw + at - p.ws.before[base + j];  // of the page's first free place
-    // a page with rows of the last n_last gets its record when they are there
-    const bool record = at + HYQ_PAGE_ROWS <= w || p.n_last == 0;
-    const int valid = min(HYQ_PAGE_ROWS, row.k - at);
-    uint8_t* tile0 = pl.tile<BK, BV>(at);
-    Extremes<BK, BV> x2;
-    x2.reset();
+    const int rank0 = (jw < nb ? p.ws.before[base + jw] + __popcll(mw) : 0) + at - p.ws.before[base + x.page];
+    uint8_t* tile = pl.tile<BK, BV>(at);
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      uint8_t* tile = tile0 + i * F::kTile;
+    for (int i = 0; i < 4; ++i, tile += F::kTile) {
       const uint32_t mine = (uint32_t)(holes >> (16 * i)) & 0xFFFFu;
-      if (mine) {
-        int from = -1;
-        if (lane < 16 && (mine >> lane) & 1) {
-          const int rank = rank0 + __popcll(holes & ((1ull << (16 * i + lane)) - 1));
-          int lo = jw, up = nb;  // the last page with `before` <= rank
-          while (up - lo > 1) {
-            const int m = (lo + up) >> 1;
-            if (p.ws.before[base + m] <= rank) lo = m;
-            else up = m;
-          }
-          uint64_t m = p.ws.mask[base + lo];
-          for (int s = rank - p.ws.before[base + lo]; s > 0; --s) m &= m - 1;
-          from = lo * HYQ_PAGE_ROWS + __ffsll(m) - 1;
+      if (!mine) continue;
+      uint4 v[kLoads];  // the tile arrives while its rows' sources are looked for
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        if (32 * k + lane < kWords) v[k] = reinterpret_cast<const uint4*>(tile)[32 * k + lane];
+      const int r = 16 * i + lane;
+      int from = -1;
+      if (lane < 16 && (mine >> lane) & 1) {
+        const int rank = rank0 + __popcll(holes & ((1ull << r) - 1));
+        int lo = jw, up = nb;  // the last page with `before` <= rank
+        while (up - lo > 1) {
+          const int m = (lo + up) >> 1;
+          if (p.ws.before[base + m] <= rank) lo = m;
+          else up = m;
         }
-        copy_tile<BK, BV>(held, tile, lane);
-        __syncwarp();
-        const float weight = gather_rows<BK, BV>(pl, held, lane, from);
-        copy_tile<BK, BV>(tile, held, lane);
-        if (from >= 0) *pl.weight(at + 16 * i + lane) = weight;
+        uint64_t m = p.ws.mask[base + lo];
+        for (int s = rank - p.ws.before[base + lo]; s > 0; --s) m &= m - 1;
+        from = lo * HYQ_PAGE_ROWS + __ffsll(m) - 1;
       }
-      if (record && 16 * i < valid) {
-        x2.load(mine ? held : tile, lane);
-        if (valid - 16 * i >= 16) x2.template take<true>(lane, 16);
-        else x2.template take<false>(lane, valid - 16 * i);
-      }
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        if (32 * k + lane < kWords) reinterpret_cast<uint4*>(held)[32 * k + lane] = v[k];
+      __syncwarp();
+      const float weight = gather_rows<BK, BV>(pl, held, lane, from);
+      copy_tile<BK, BV>(tile, held, lane);
+      if (from >= 0) *pl.weight(at + r) = weight;
       __syncwarp();
     }
-    if (record) x2.write(pl.bounds + (size_t)pl.table[j] * p.HKV * HYQ_BOUND_BYTES, lane);
+  }
+}
+
+// The records of pages that received a row, a warp each: their keys alone, straight into registers, a tile ahead.
+template <int BK, int BV>
+__global__ void __launch_bounds__(kMoveThreads, 4) record_kernel(const Params p) {
+  using F = QFmt<BK, BV>;
+  __shared__ int64_t s_cum[HYQ_PAGED_MAX_BATCH + 1];
+  chain_kernel();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i <= p.batch; i += kMoveThreads) s_cum[i] = p.ws.cum[i];
+  __syncthreads();
+  const int64_t items = s_cum[p.batch] * p.HKV * p.pages.n_layers;
+  for (int64_t it = (int64_t)blockIdx.x * (kMoveThreads / 32) + warp; it < items; it += (int64_t)gridDim.x * (kMoveThreads / 32)) {
+    const Item x = item_of(p, s_cum, it);
+    const int at = x.page * HYQ_PAGE_ROWS, valid = min(HYQ_PAGE_ROWS, x.row.k - at);
+    const bool shifted = p.n_last > 0 && at + HYQ_PAGE_ROWS > x.row.k - p.n_last;
+    if (!shifted && !free_places(p, x)) continue;
+    const Place pl = place_of<BK, BV>(p, x.row, x.layer, x.h);
+    const uint8_t* tile = pl.tile<BK, BV>(at);
+    Extremes<BK, BV> e;
+    e.reset();
+    e.load(tile, lane);
+#pragma unroll 1
+    for (int i = 0; 16 * i < valid; ++i) {
+      Keys<BK> now = e.next;
+      if (16 * (i + 1) < valid) e.load(tile + (i + 1) * F::kTile, lane);
+      if (valid - 16 * i >= 16) e.template take<true>(now, lane, 16);
+      else e.template take<false>(now, lane, valid - 16 * i);
+    }
+    e.write(pl.bounds + (size_t)pl.table[x.page] * p.HKV * HYQ_BOUND_BYTES, lane);
   }
 }
 
@@ -575,7 +601,6 @@ template <int BK, int BV>
 __global__ void __launch_bounds__(kMoveThreads) shift_kernel(const Params p) {
   using F = QFmt<BK, BV>;
   __shared__ __align__(16) uint8_t s_page[F::kBlock];
-  __shared__ float s_red[4];
   chain_kernel();
   const int h = blockIdx.x % p.HKV, b = blockIdx.x / p.HKV, layer = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -594,8 +619,6 @@ __global__ void __launch_bounds__(kMoveThreads) shift_kernel(const Params p) {
     __syncthreads();  // all of the page's sources have been read: some lie in the page
     if (__any_sync(0xffffffffu, from >= 0)) copy_tile<BK, BV>(tile, held, lane);
     if (from >= 0) *pl.weight(pos) = weight;
-    write_record<BK, BV>(s_page, min(HYQ_PAGE_ROWS, row.k - j * HYQ_PAGE_ROWS),
-                         pl.bounds + (size_t)pl.table[j] * p.HKV * HYQ_BOUND_BYTES, s_red);
     __syncthreads();  // the stores are made before the next page's reads
   }
   if (layer == 0 && h == 0) {  // the other blocks have n and k from the plan
@@ -613,12 +636,14 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   e = hyq_launch_chained(select_kernel<256, 2>, heads, 256, 0, s, p);
   if (e != cudaSuccess) return e;
   if ((int64_t)p.pages.max_blocks * HYQ_PAGE_ROWS > kSmall) {  // longer sequences may be there
-    e = hyq_launch_chained(select_kernel<512, 4>, heads, 512, 0, s, p);
+    e = hyq_launch_chained(select_kernel<1024, 2>, heads, 1024, 0, s, p);
     if (e != cudaSuccess) return e;
   }
-  e = hyq_launch_chained(fill_kernel<BK, BV>, dim3(4 * hyq_num_sms()), kMoveThreads, 0, s, p);
+  e = hyq_launch_chained(fill_kernel<BK, BV>, dim3(12 * hyq_num_sms()), kMoveThreads, 0, s, p);
   if (e != cudaSuccess) return e;
-  return hyq_launch_chained(shift_kernel<BK, BV>, heads, kMoveThreads, 0, s, p);
+  e = hyq_launch_chained(shift_kernel<BK, BV>, heads, kMoveThreads, 0, s, p);
+  if (e != cudaSuccess) return e;
+  return hyq_launch_chained(record_kernel<BK, BV>, dim3(4 * hyq_num_sms()), kMoveThreads, 0, s, p);
 }
 
 }  // namespace
