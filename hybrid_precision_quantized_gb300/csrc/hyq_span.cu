@@ -48,6 +48,7 @@ struct Params {
   int64_t ldq;
   __nv_bfloat16* out;
   struct Plan* plan;
+  struct Split* split;   // [grid]
   struct Entry* list;    // [grid][HYQ_PAGED_MAX_BATCH]
   float* part;           // [grid][2] parts of tiles
   float* half;           // [grid][2] states of 128 rows
@@ -73,6 +74,12 @@ struct Plan {
   Shares sh;
   int64_t cum[HYQ_PAGED_MAX_BATCH];  // jobs before segment i
   int32_t len[HYQ_PAGED_MAX_BATCH], t0[HYQ_PAGED_MAX_BATCH], rows[HYQ_PAGED_MAX_BATCH];
+};
+
+// The tile whose first units are a block's and the others the next blocks'; n_rows is 0 when there is none.
+struct Split {
+  int64_t base;  // its first job behind the fixed work
+  int32_t t0, row0, n_rows, h, nt, units;
 };
 
 struct Seg {
@@ -513,6 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
     const int64_t end = s_end;
     int i = pos < end ? s_first : 0;
     uint32_t n_tile = 0, n_page = 0;
+    Split cut;
+    cut.n_rows = 0;
     bool ok = true;
     while (ok) {
       Tile t;
@@ -534,6 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
         pos += x1 - x0;
         const int a = unit_from((int)x0, nt), b = unit_from(x1, nt);
         if (a >= b) continue;
+        if (a == 0 && b < U)
+          cut = Split{e.cum + per * h + (int64_t)mt * (kCost + 2 * U) + kCost, e.t0, mt * kPair, n_rows, h, nt, U};
         t = Tile{p.pv.table + (size_t)e.seq * p.pv.max_blocks, a, b, e.len, e.t0, mt * kPair, n_rows, h, nt == 2, a == 0 && b == U};
         break;
       }
@@ -571,6 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
         }
       }
     }
+    if (lane == 0) p.split[blockIdx.x] = cut;
     if (!ok)  // copies in flight land before the block's shared memory goes
       for (uint32_t n = n_page > kSlots ? n_page - kSlots : 0; n < n_page; ++n)
         (void)mbar_wait(&bar.raw_full[n % kSlots], (n / kSlots) & 1u);
@@ -1005,11 +1017,47 @@ __global__ void __launch_bounds__(kThreads, 1) span_kernel(const __grid_constant
   }
 }
 
-// The parts of a row in run order, then (shared) what its own positions gave; eight rows of a KV head a block,
-// a thread four elements.
 constexpr int kJoinThreads = 256;
-template <bool kShared>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Params p) {
+// Four elements of a row, summed up over parts.
+struct Joined {
+  float top = -INFINITY, L = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx, c0 = ex2(top - ref), c1 = ex2(ml.x - ref);
+    top = mx;
+    L = fmaf(L, c0, ml.y * c1);
+    a.x = fmaf(a.x, c0, v.x * c1), a.y = fmaf(a.y, c0, v.y * c1), a.z = fmaf(a.z, c0, v.z * c1),
+    a.w = fmaf(a.w, c0, v.w * c1);
+  }
+  // Blocks c0 .. c1 of a tile, row r of it; eight parts under way.
+  __device__ __forceinline__ void parts(const Params& p, const Shares& sh, int c0, int c1, int64_t base, int nt, int U, int r,
+                                        int d4) {
+    constexpr int kHold = 8;
+    for (int c = c0; c <= c1; c += kHold) {
+      float2 ml[kHold];
+      float4 v[kHold];
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {
+        const float* part = p.part + ((size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0)) * kPart;
+        // (a run that ends before a pair's second half of a unit may have nothing of the tile)
+        const bool in = c + k <= c1 && holds(sh, c + k, base, nt, U);
+        ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(part + kPair * HYQ_D) + r) : make_float2(-INFINITY, 0.f);
+        v[k] = in ? __ldcg(reinterpret_cast<const float4*>(part) + d4 * kPair + r) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) add(ml[k], v[k]);
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* out) const {
+    const float inv = L > 0.f ? 1.f / L : L;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  }
+};
+
+// Shared: the parts of a row in run order, then what its own positions gave; eight rows of a KV head a block, a thread
+// four elements.  Rows that the span kernel has finished are left out.
+__global__ void __launch_bounds__(kJoinThreads) join_shared_kernel(const __grid_constant__ Params p) {
   chain_kernel();
   const int lane = threadIdx.x & 31, d4 = 4 * (threadIdx.x >> 5) + (lane >> 3);
   // (the query rows of all heads are fewer than 2^31)
@@ -1020,59 +1068,43 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const uint32_t R = (it - h * per) * 8 + (lane & 7);
     if (R >= rows) continue;
     const int tok = (int)(R / p.gq), head = (int)(R - (uint32_t)tok * p.gq);
-    int i, len = 0;
-    if (kShared) {
-      i = p.n_seg ? group_of(p.shared, tok / p.n_q) : 0;
-      if (p.n_seg) len = shared_len(p.shared, p.pv, p.seqs, tok / p.n_q, p.batch, p.n_q);
-    } else {
-      i = 0;
-      int hi = p.n_seg;
-      while (hi - i > 1) {
-        const int mid = (i + hi) >> 1;
-        if (p.cu[mid] <= tok) i = mid;
-        else hi = mid;
-      }
-      if (p.cu[i] > tok || tok >= p.cu[i + 1] || p.cu[i] < 0 || p.cu[i + 1] > p.n_tokens) continue;  // nobody's token
-      len = plan.len[i];
-    }
-    float top = -INFINITY, L = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float2 ml, float4 v) {
-      const float mx = fmaxf(top, ml.x), ref = mx == -INFINITY ? 0.f : mx, c0 = ex2(top - ref), c1 = ex2(ml.x - ref);
-      top = mx;
-      L = fmaf(L, c0, ml.y * c1);
-      a.x = fmaf(a.x, c0, v.x * c1), a.y = fmaf(a.y, c0, v.y * c1), a.z = fmaf(a.z, c0, v.z * c1),
-      a.w = fmaf(a.w, c0, v.w * c1);
-    };
+    const int i = p.n_seg ? group_of(p.shared, tok / p.n_q) : 0;
+    const int len = p.n_seg ? shared_len(p.shared, p.pv, p.seqs, tok / p.n_q, p.batch, p.n_q) : 0;
+    Joined sum;
     if (len > 0) {
       const int U = n_units(len), r = (tok - plan.t0[i]) * p.gq + head, mt = r / kPair, rr = r - mt * kPair;
       const int nt = min(kPair, plan.rows[i] - mt * kPair) > kRows ? 2 : 1;
       const int64_t base = plan.cum[i] + h * head_slots(len, plan.rows[i]) + (int64_t)mt * (kCost + 2 * U) + kCost;
       const int c0 = plan.sh.owner(base), c1 = plan.sh.owner(base + (int64_t)nt * (U - 1));
       if (c0 == c1) continue;  // written by its block
-      constexpr int kHold = 8;  // parts under way
-      for (int c = c0; c <= c1; c += kHold) {
-        float2 ml[kHold];
-        float4 v[kHold];
-#pragma unroll
-        for (int k = 0; k < kHold; ++k) {
-          const float* part = p.part + ((size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0)) * kPart;
-          // (a run that ends before a pair's second half of a unit may have nothing of the tile)
-          const bool in = c + k <= c1 && holds(plan.sh, c + k, base, nt, U);
-          ml[k] = in ? __ldcg(reinterpret_cast<const float2*>(part + kPair * HYQ_D) + rr) : make_float2(-INFINITY, 0.f);
-          v[k] = in ? __ldcg(reinterpret_cast<const float4*>(part) + d4 * kPair + rr) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-#pragma unroll
-        for (int k = 0; k < kHold; ++k) add(ml[k], v[k]);
-      }
+      sum.parts(p, plan.sh, c0, c1, base, nt, U, rr, d4);
     }
-    if (kShared) {
-      const float* e = p.rest + ((size_t)tok * p.HQ + h * p.gq + head) * kPartFloats;
-      add(*reinterpret_cast<const float2*>(e + HYQ_D), *(reinterpret_cast<const float4*>(e) + d4));
-    }
-    const float inv = L > 0.f ? 1.f / L : L;
-    *reinterpret_cast<uint2*>(p.out + ((size_t)tok * p.HQ + h * p.gq + head) * HYQ_D + 4 * d4) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    const float* e = p.rest + ((size_t)tok * p.HQ + h * p.gq + head) * kPartFloats;
+    sum.add(*reinterpret_cast<const float2*>(e + HYQ_D), *(reinterpret_cast<const float4*>(e) + d4));
+    sum.store(p.out + ((size_t)tok * p.HQ + h * p.gq + head) * HYQ_D + 4 * d4);
+  }
+}
+
+// Cross: eight rows of a tile that several blocks share, found where its first block has noted it; and zeros for the
+// tokens of empty sequences.
+__global__ void __launch_bounds__(kJoinThreads) join_cross_kernel(const __grid_constant__ Params p) {
+  chain_kernel();
+  const int lane = threadIdx.x & 31, d4 = 4 * (threadIdx.x >> 5) + (lane >> 3), c0 = blockIdx.x;
+  const Split tile = p.split[c0];
+  const int r = 8 * blockIdx.y + (lane & 7);
+  if (r < tile.n_rows) {
+    const Shares sh = p.plan->sh;
+    Joined sum;
+    sum.parts(p, sh, c0, sh.owner(tile.base + (int64_t)tile.nt * (tile.units - 1)), tile.base, tile.nt, tile.units, r, d4);
+    const int tok = (tile.row0 + r) / p.gq, head = tile.h * p.gq + tile.row0 + r - tok * p.gq;
+    sum.store(p.out + ((size_t)(tile.t0 + tok) * p.HQ + head) * HYQ_D + 4 * d4);
+  }
+  for (int i = blockIdx.x; i < p.n_seg; i += gridDim.x) {
+    if (p.plan->len[i] > 0) continue;
+    const size_t n = (size_t)(p.plan->rows[i] / p.gq) * p.HQ * (HYQ_D / 8);  // (whole tokens)
+    uint4* out = reinterpret_cast<uint4*>(p.out + (size_t)p.plan->t0[i] * p.HQ * HYQ_D);
+    for (size_t x = blockIdx.y * kJoinThreads + threadIdx.x; x < n; x += (size_t)gridDim.y * kJoinThreads)
+      out[x] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -1087,8 +1119,10 @@ cudaError_t launch(const Params& p, cudaStream_t s) {
   const int sms = hyq_num_sms();
   e = hyq_launch_chained(span_kernel<BK, BV, kShared>, dim3(sms), kThreads, bytes, s, p);
   if (e != cudaSuccess) return e;
+  if (!kShared)
+    return hyq_launch_chained(join_cross_kernel, dim3(sms, kPair / 8), kJoinThreads, 0, s, p);
   const int64_t items = ((int64_t)p.n_tokens * p.gq + 7) / 8 * p.HKV;
-  return hyq_launch_chained(join_kernel<kShared>, dim3((int)(items < 8 * sms ? items : 8 * sms)), kJoinThreads, 0, s, p);
+  return hyq_launch_chained(join_shared_kernel, dim3((int)(items < 8 * sms ? items : 8 * sms)), kJoinThreads, 0, s, p);
 }
 
 template <bool kShared>
@@ -1098,7 +1132,7 @@ cudaError_t launch_bits(const hyq_config* c, const Params& p, cudaStream_t s) {
   return bv == 4 ? launch<8, 4, kShared>(p, s) : launch<8, 8, kShared>(p, s);
 }
 
-size_t plan_bytes() { return hyq_align256(sizeof(Plan)); }
+size_t plan_bytes() { return hyq_align256(sizeof(Plan)) + hyq_align256((size_t)hyq_num_sms() * sizeof(Split)); }
 size_t list_bytes() { return hyq_align256((size_t)hyq_num_sms() * HYQ_PAGED_MAX_BATCH * sizeof(Entry)); }
 size_t parts_bytes() { return list_bytes() + hyq_align256((size_t)hyq_num_sms() * 3 * kPart * 4); }
 size_t rest_bytes(const hyq_config* c, int32_t batch, int32_t n_q) {
@@ -1115,6 +1149,7 @@ Params params(const hyq_config* c, const PageView& pv, const int32_t* seqs, int3
   p.ldq = ldq;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.plan = static_cast<Plan*>(ws);
+  p.split = reinterpret_cast<Split*>(static_cast<char*>(ws) + hyq_align256(sizeof(Plan)));
   p.list = reinterpret_cast<Entry*>(static_cast<char*>(ws) + plan_bytes());
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws) + plan_bytes() + list_bytes());
   p.half = p.part + (size_t)hyq_num_sms() * 2 * kPart;
