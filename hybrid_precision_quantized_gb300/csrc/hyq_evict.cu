@@ -8,13 +8,15 @@
 // moved row is read and written once, and nothing is read after it has been written: the
 // free places lie below w, what goes there at or behind it.
 //
-// Four launches: which sequences and how many pages (one block); the kept positions of
+// Launches: which sequences and how many pages (one block); the kept positions of
 // every (layer, sequence, KV head) as a bit mask a page with the number kept before it;
-// the free places, a block a page; the last n_last positions, which may overlap their
+// the free places, a warp a page; the last n_last positions, which may overlap their
 // new places and are therefore taken a page after another by one block, and the
-// tables.  What bounds it: the mass is read once, each moved row read and written
-// once, and of each page that changes the keys for its bounds: HBM for long
-// prompts, latency (dependent launches and reads) for small calls.
+// tables; the bound records of the pages that received a row, a warp each.  What bounds it: the
+// mass is read once, each moved row read and written once, and of each page that changes
+// the keys for its bounds: in part HBM (2.8 TB/s of these bytes for 16 x 4096 in 32
+// layers), in part dependent reads (page numbers, masks, rows) and the records'
+// arithmetic; small calls are bound by the launches' latencies.
 #include "hyq_codes.cuh"
 #include "hyq_f2.cuh"
 #include "hyq_paged.cuh"
@@ -135,9 +137,9 @@ static_assert(HYQ_PAGE_ROWS == 4 * kPiece, "four lanes a page");
 // One block per (layer, row, KV head).  The threshold is found two bits at a time by counting the keys at and above
 // three candidates: the keys stay in registers (read again for each pair of bits past the first 32768 positions), and
 // counting needs no atomics, whose bins the exponents of masses share (by a histogram of eight bits at a time, a page a
-// thread: 229 us for 4096 selections of 4160, with this NNN).
+// thread: 229 us for 4096 selections of 4160 in a cold launch, with this 132; 512 of 32512 took 86 and take 128).
 // kSelThreads threads hold kHeld pieces each.  Two sizes, three small blocks or a large one an SM, each for the
-// sequences of its size (all in large ones: 975 us instead of NNN for the whole eviction of 16 x 4096 in 32 layers).
+// sequences of its size (all in large ones: 975 us instead of 545 for a whole eviction of 16 x 4096 in 32 layers).
 template <int kSelThreads, int kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
   constexpr int kSelWarps = kSelThreads / 32, kPass = kSelThreads * kPiece;  // positions of a pass
@@ -506,7 +508,7 @@ __device__ __forceinline__ uint64_t free_places(const Params& p, const Item& it)
 }
 
 // The free places below w: a warp takes a page.  (Its time is a chain of dependent reads; a block a page, a tile a warp,
-// left three of four warps without work where a page has one free place: 385 against NNN us for 16 x 4096 in 32 layers.)
+// left three of four warps without work where a page has one free place: 385 against 184 us for 16 x 4096 in 32 layers, cold.)
 template <int BK, int BV>
 __global__ void __launch_bounds__(kMoveThreads) fill_kernel(const Params p) {
   using F = QFmt<BK, BV>;

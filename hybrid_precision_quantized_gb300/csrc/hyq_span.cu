@@ -15,6 +15,15 @@
 // two, which fp16 takes without rounding (BF16 has fewer bits; elements 2^-27 of
 // the row's largest and less are rounded).  Probabilities are rounded to fp16, kept
 // between 2^8 and 2^14 at the row's maximum so that the small ones are not lost.
+//
+// What bounds it: 4 x 128 x 128 x 128 flops a job (128 query rows and a unit) are 1024 cycles
+// of the tensor cores; the kernel takes about three times that (2000 tokens of four
+// sequences of up to 16001, 8-bit codes: 829 us, 0.40 of the product rate; one sequence of
+// 32768 for 64 requests: 0.19 of the rate for the whole call).  Each role waits for its own
+// dependent instructions and for the one before it (products, exponentials, products),
+// two jobs in flight; tensor cores are busy a third of the time, issue slots a half.
+// Few query rows: the codes are read once, and the fixed work of a block (its tiles, the
+// query rows, the join of parts) is most of the time.
 #include <type_traits>
 
 #include "hyq_codes.cuh"
@@ -329,7 +338,8 @@ struct Entry {
 template <int BK>
 __device__ __noinline__ void load_queries(const Params& p, const Tile& t, int warp, int lane, uint8_t* dst, float* factor) {
   constexpr int kAhead = 4;  // pairs of rows under way, and as many in hand
-  const int half = lane >> 4, l = lane & 15, rows = t.pair ? kPair : kRows;
+  const int half = lane >> 4, l = lane & 15;
+  const int rows = (t.n_rows + 31) & ~31;  // (no warp looks at the rows behind: their products are their own)
   const int dt = 16 / p.gq, dh = 16 - dt * p.gq;
   int tok = (t.row0 + 2 * warp + half) / p.gq, head = t.row0 + 2 * warp + half - tok * p.gq;
   const __nv_bfloat16* q = p.q + (size_t)t.t0 * p.ldq + (size_t)t.h * p.gq * HYQ_D + 8 * l;

@@ -881,7 +881,8 @@ hyq_status hyq_paged_accumulate(const hyq_config *cfg, const hyq_pages *pages, i
  * A sequence out of range or listed before, a keep that is too small or a table entry outside the
  * pool sets HYQ_DEVERR_INDEX; a page among the ceil(k / 64) kept ones that another
  * sequence holds too sets HYQ_DEVERR_PAGES: that sequence is left as it was.
- * Workspace: HYQ_OP_PAGES_EVICT, no initial contents needed.  Four launches.
+ * Workspace: HYQ_OP_PAGES_EVICT, no initial contents needed.  Five launches (six where max_blocks
+ * allows more than 8192 positions).
  */
 hyq_status hyq_pages_evict(const hyq_config *cfg, const hyq_pages *pages, const int32_t *seqs, int32_t batch,
                            const int32_t *keep, int32_t n_first, int32_t n_last, float *mass, void *ws, size_t ws_bytes,
