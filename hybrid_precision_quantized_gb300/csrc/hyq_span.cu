@@ -18,7 +18,7 @@
 //
 // What bounds it: 4 x 128 x 128 x 128 flops a job (128 query rows and a unit) are 1024 cycles
 // of the tensor cores; the kernel takes about three times that (2000 tokens of four
-// sequences of up to 16001, 8-bit codes: 829 us, 0.40 of the product rate; one sequence of
+// sequences of up to 16001, 8-bit codes: 824 us, 0.40 of the product rate; one sequence of
 // 32768 for 64 requests: 0.19 of the rate for the whole call).  Each role waits for its own
 // dependent instructions and for the one before it (products, exponentials, products),
 // two jobs in flight; tensor cores are busy a third of the time, issue slots a half.
