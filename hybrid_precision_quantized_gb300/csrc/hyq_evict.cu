@@ -143,7 +143,8 @@ static_assert(HYQ_PAGE_ROWS == 4 * kPiece, "four lanes a page");
 template <int kSelThreads, int kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
   constexpr int kSelWarps = kSelThreads / 32, kPass = kSelThreads * kPiece;  // positions of a pass
-  __shared__ int s_count[2][3][kSelWarps], s_scan[kSelWarps];
+  __shared__ int s_count[2][3][kSelWarps];
+  __shared__ uint32_t s_scan[2][kSelWarps];
   chain_kernel();
   const int h = blockIdx.x % p.HKV, b = blockIdx.x / p.HKV, layer = blockIdx.y, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -206,24 +207,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
   }
   // the mask: what lies above the key, and the first of those that equal it
   const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
-  int kept = 0, ties = 0;  // in the pieces before
-  auto scan = [&](int v, int& before) {  // exclusive over the block, on top of `before`
-    int pre = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_scan[warp] = pre;
-    __syncthreads();
-    int at = before + pre - v;
-    for (int k = 0; k < kSelWarps; ++k) {
-      if (k < warp) at += s_scan[k];
-      before += s_scan[k];
-    }
-    return at;
-  };
   // how many of those that equal the key are kept: all above it are
   int above = 0;
   auto over = [&](const uint32_t (&x)[kPiece]) {
@@ -238,9 +221,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
     keys(pos, x);
     over(x);
   }
-  int total = 0;
-  (void)scan(above, total);
-  const int left = want - total;
+  // (a block's sum: the warps' sums, which every warp adds up; `upto`: those of the warps before it)
+  auto sums = [&](uint32_t v, uint32_t* s, int upto) {
+    const uint32_t x = lane < kSelWarps ? s[lane] : 0u;
+    return make_uint2(__reduce_add_sync(0xffffffffu, x), v + __reduce_add_sync(0xffffffffu, lane < upto ? x : 0u));
+  };
+  above = __reduce_add_sync(0xffffffffu, above);
+  if (lane == 0) s_scan[0][warp] = above;
+  __syncthreads();
+  const int left = max(0, want - (int)sums(0u, s_scan[0], 0).x);  // (none wanted: the key is 0)
+  int above_before = 0, ties_before = 0, turn = 1;  // in the pieces before
   auto finish = [&](int pos, const uint32_t (&x)[kPiece]) {  // (all threads)
     uint32_t gt = 0, eq = 0;
 #pragma unroll
@@ -250,11 +240,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
     }
     const int nf = p.n_first - pos;
     if (nf > 0) gt |= nf >= kPiece ? (1u << kPiece) - 1 : (1u << nf) - 1;
-    const int tie_at = scan(__popc(eq), ties);
-    int drop = __popc(eq) - max(0, min(__popc(eq), left - tie_at));
-    for (; drop > 0; --drop) eq &= ~(1u << (31 - __clz(eq)));
+    // what the threads before have of both, a half word each (a pass has 2^14 positions at most)
+    const uint32_t mine = (uint32_t)__popc(gt) | (uint32_t)__popc(eq) << 16;
+    uint32_t pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += y;
+    }
+    uint32_t* s = s_scan[turn];
+    turn ^= 1;
+    if (lane == 31) s[warp] = pre;
+    __syncthreads();
+    const uint2 both = sums(pre - mine, s, warp);
+    const int tie_at = ties_before + (int)(both.y >> 16), room = max(0, left - tie_at);
+    const int at = above_before + (int)(both.y & 0xffffu) + min(tie_at, left);
+    above_before += (int)(both.x & 0xffffu), ties_before += (int)(both.x >> 16);
+    for (int drop = __popc(eq) - room; drop > 0; --drop) eq &= ~(1u << (31 - __clz(eq)));
     const uint32_t m = pos < hi ? gt | eq : 0u;
-    const int at = scan(__popc(m), kept);
     // four lanes' pieces are a page
     const uint32_t lo = m | __shfl_down_sync(0xffffffffu, m, 1) << 16, up = __shfl_down_sync(0xffffffffu, lo, 2);
     if ((lane & 3) == 0 && pos < hi) {
