@@ -14,7 +14,7 @@
 // new places and are therefore taken a page after another by one block, and the
 // tables; the bound records of the pages that received a row, a warp each.  What bounds it: the
 // mass is read once, each moved row read and written once, and of each page that changes
-// the keys for its bounds: in part HBM (2.8 TB/s of these bytes for 16 x 4096 in 32
+// the keys for its bounds: in part HBM (2.9 TB/s of these bytes for 16 x 4096 in 32
 // layers), in part dependent reads (page numbers, masks, rows) and the records'
 // arithmetic; small calls are bound by the launches' latencies.
 #include "hyq_codes.cuh"
@@ -134,17 +134,19 @@ constexpr int kPiece = 16;          // positions that a thread takes at a time
 constexpr int kSmall = 8192;        // positions that a small block holds
 static_assert(HYQ_PAGE_ROWS == 4 * kPiece, "four lanes a page");
 
-// One block per (layer, row, KV head).  The threshold is found two bits at a time by counting the keys at and above
-// three candidates: the keys stay in registers (read again for each pair of bits past the first 32768 positions), and
-// counting needs no atomics, whose bins the exponents of masses share (by a histogram of eight bits at a time, a page a
-// thread: 229 us for 4096 selections of 4160 in a cold launch, with this 132; 512 of 32512 took 86 and take 128).
+// One block per (layer, row, KV head).  The threshold is found a bit at a time by counting the keys at and above a
+// candidate: the keys stay in registers (read again for each bit past the first 32768 positions), and counting needs no
+// atomics, whose bins the exponents of masses share (a histogram of eight bits at a time, a page a thread: 229 us
+// for 4096 selections of 4160 in a cold launch, with this 43; 512 of up to 32512 took 86 and take 99).  Comparisons
+// bound it: two bits by three candidates at a time took 474 and 243 us where whole evictions of 16 x 4096 in 32 layers and of
+// eight prompts of up to 32768 in eight take 453 and 222.  Many positions receive nothing, and the threshold is among them:
+// that is seen after four bits (143 to 45 us for the 4096 selections).
 // kSelThreads threads hold kHeld pieces each.  Two sizes, three small blocks or a large one an SM, each for the
 // sequences of its size (all in large ones: 975 us instead of 545 for a whole eviction of 16 x 4096 in 32 layers).
 template <int kSelThreads, int kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
   constexpr int kSelWarps = kSelThreads / 32, kPass = kSelThreads * kPiece;  // positions of a pass
-  __shared__ int s_count[2][3][kSelWarps];
-  __shared__ uint32_t s_scan[2][kSelWarps];
+  __shared__ uint32_t s_count[2][kSelWarps], s_scan[2][kSelWarps];
   chain_kernel();
   const int h = blockIdx.x % p.HKV, b = blockIdx.x / p.HKV, layer = blockIdx.y, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -174,15 +176,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
   uint32_t held[kHeld][kPiece];
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) keys(k * kPass + kPiece * tid, held[k]);
-  // the want-th largest key: the largest one that at least `want` keys reach
+  // a block's sum: the warps' sums, which every warp adds up; and that of the warps before `upto`
+  auto sums = [&](const uint32_t* s, int upto) {
+    const uint32_t x = lane < kSelWarps ? s[lane] : 0u;
+    return make_uint2(__reduce_add_sync(0xffffffffu, x), __reduce_add_sync(0xffffffffu, lane < upto ? x : 0u));
+  };
   uint32_t key = 0;
-#pragma unroll 1
-  for (int shift = 30; shift >= 0 && want > 0; shift -= 2) {
-    const uint32_t c1 = key | 1u << shift, c2 = key | 2u << shift, c3 = key | 3u << shift;
-    int n1 = 0, n2 = 0, n3 = 0;
+  auto reach = [&](uint32_t c, uint32_t* s) {  // how many keys are c or more
+    int n = 0;
     auto count = [&](const uint32_t (&x)[kPiece]) {
 #pragma unroll
-      for (int i = 0; i < kPiece; ++i) n1 += x[i] >= c1, n2 += x[i] >= c2, n3 += x[i] >= c3;
+      for (int i = 0; i < kPiece; ++i) n += x[i] >= c;
     };
 #pragma unroll
     for (int k = 0; k < kHeld; ++k)
@@ -192,44 +196,35 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
       keys(pos, x);
       count(x);
     }
-    n1 = __reduce_add_sync(0xffffffffu, n1), n2 = __reduce_add_sync(0xffffffffu, n2), n3 = __reduce_add_sync(0xffffffffu, n3);
-    int(&s)[3][kSelWarps] = s_count[(shift >> 1) & 1];
-    if (lane == 0) s[0][warp] = n1, s[1][warp] = n2, s[2][warp] = n3;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) s[warp] = n;
     __syncthreads();
-    const bool in = lane < kSelWarps;  // every warp sums up the warps' counts
-    n1 = __reduce_add_sync(0xffffffffu, in ? s[0][lane] : 0), n2 = __reduce_add_sync(0xffffffffu, in ? s[1][lane] : 0);
-    n3 = __reduce_add_sync(0xffffffffu, in ? s[2][lane] : 0);
-    key = n3 >= want ? c3 : n2 >= want ? c2 : n1 >= want ? c1 : key;
-    if (n3 == want || n2 == want || n1 == want) {  // just as many reach a candidate: no need to know the key itself
-      key = (n3 == want ? c3 : n2 == want ? c2 : c1) - 1;
+    return (int)sums(s, 0).x;
+  };
+  // the want-th largest key: the largest one that at least `want` keys reach
+  int above = -1;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0 && want > 0; --bit) {
+    const uint32_t c = key | 1u << bit;
+    const int n = reach(c, s_count[bit & 1]);
+    if (n >= want) key = c;
+    if (n == want) {  // just as many reach the candidate: no need to know the key itself
+      key = c - 1;
       break;
+    }
+    if (bit == 28 && key == 0x80000000u) {  // [0, 2^-95): zeros as a rule, and then no further bit tells more
+      const int more = reach(key + 1, s_scan[0]);
+      if (more < want) {
+        above = more;
+        break;
+      }
     }
   }
   // the mask: what lies above the key, and the first of those that equal it
   const size_t base = (((size_t)layer * p.batch + b) * p.HKV + h) * p.pages.max_blocks;
-  // how many of those that equal the key are kept: all above it are
-  int above = 0;
-  auto over = [&](const uint32_t (&x)[kPiece]) {
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) above += x[i] > key;
-  };
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k)
-    if (k * kPass < hi) over(held[k]);
-  for (int pos = kHeld * kPass + kPiece * tid; pos < hi; pos += kPass) {
-    uint32_t x[kPiece];
-    keys(pos, x);
-    over(x);
-  }
-  // (a block's sum: the warps' sums, which every warp adds up; `upto`: those of the warps before it)
-  auto sums = [&](uint32_t v, uint32_t* s, int upto) {
-    const uint32_t x = lane < kSelWarps ? s[lane] : 0u;
-    return make_uint2(__reduce_add_sync(0xffffffffu, x), v + __reduce_add_sync(0xffffffffu, lane < upto ? x : 0u));
-  };
-  above = __reduce_add_sync(0xffffffffu, above);
-  if (lane == 0) s_scan[0][warp] = above;
-  __syncthreads();
-  const int left = max(0, want - (int)sums(0u, s_scan[0], 0).x);  // (none wanted: the key is 0)
+  // of those that equal the key, as many are kept as those above it leave
+  if (above < 0) above = key == ~0u ? 0 : reach(key + 1, s_scan[0]);
+  const int left = max(0, want - above);  // (none wanted: the key is 0)
   int above_before = 0, ties_before = 0, turn = 1;  // in the pieces before
   auto finish = [&](int pos, const uint32_t (&x)[kPiece]) {  // (all threads)
     uint32_t gt = 0, eq = 0;
@@ -252,7 +247,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
     turn ^= 1;
     if (lane == 31) s[warp] = pre;
     __syncthreads();
-    const uint2 both = sums(pre - mine, s, warp);
+    uint2 both = sums(s, warp);
+    both.y += pre - mine;
     const int tie_at = ties_before + (int)(both.y >> 16), room = max(0, left - tie_at);
     const int at = above_before + (int)(both.y & 0xffffu) + min(tie_at, left);
     above_before += (int)(both.x & 0xffffu), ties_before += (int)(both.x >> 16);

@@ -662,6 +662,28 @@ def test_eviction_by_masses_of_any_kind(hyq):
     check_evicted(cache, mass, want)
 
 
+@pytest.mark.parametrize("n,keep", [(400, 90), (9000, 700)])
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf", "zero", "tiny", "mostly zero", "half nan"])
+def test_eviction_by_masses_that_tie(hyq, n, keep, what):
+    """More equal masses than places: the lower positions stay."""
+    cache, _ = filled(2, 1, [n, 100])
+    mass = random_mass(cache, 6)
+    own = mass[:, cache.table()[0, :(n + 63) // 64].long()]
+    some = torch.rand(own.shape, generator=torch.Generator("cuda").manual_seed(n), device="cuda")
+    if what == "half nan":
+        own[some < 0.5] = float("nan")
+    elif what == "mostly zero":
+        own[some < 0.97] = 0.0
+    else:
+        own.fill_({"nan": float("nan"), "inf": float("inf"), "-inf": float("-inf"), "zero": 0.0, "tiny": 1e-42}[what])
+        own[some < 0.01] = 1e-43 if what == "tiny" else 0.0
+    mass[:, cache.table()[0, :(n + 63) // 64].long()] = own
+    want = expect_evicted(cache, mass, [0], [keep], 3, 20)
+    cache.evict(mass, ints([keep]), seqs=ints([0]), n_first=3, n_last=20)
+    assert err(cache) == 0
+    check_evicted(cache, mass, want)
+
+
 def test_eviction_leaves_out_what_it_reports(hyq):
     def start():
         cache, _ = filled(2, 1, [200, 150, 300], spare=12)
