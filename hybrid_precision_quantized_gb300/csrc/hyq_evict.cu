@@ -142,7 +142,8 @@ static_assert(HYQ_PAGE_ROWS == 4 * kPiece, "four lanes a page");
 // eight prompts of up to 32768 in eight take 453 and 222.  Many positions receive nothing, and the threshold is among them:
 // that is seen after four bits (143 to 45 us for the 4096 selections).
 // kSelThreads threads hold kHeld pieces each.  Two sizes, three small blocks or a large one an SM, each for the
-// sequences of its size (all in large ones: 975 us instead of 545 for a whole eviction of 16 x 4096 in 32 layers).
+// sequences of its size (all in large ones: 975 us instead of 545 for an eviction of 16 x 4096 in
+// 32 layers, when it took two bits at a time).
 template <int kSelThreads, int kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const Params p) {
   constexpr int kSelWarps = kSelThreads / 32, kPass = kSelThreads * kPiece;  // positions of a pass
