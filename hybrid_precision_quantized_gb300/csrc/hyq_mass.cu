@@ -12,10 +12,11 @@
 // product, an exponential and a sum per query row and position) for many (64 tokens of eight
 // sequences of up to 8192: 119 us, 0.09 of the product rate).
 //
-// A group is one (sequence, KV head).  Its half pages (units of two 16-row tiles) go round the
-// block's warps, each with a ring of asynchronous copies of its own, and a warp takes a unit
-// against all query rows (with more than one tile of those a unit is a single tile): a position's sum has one writer and one order, so there is nothing
-// to join and results do not vary from run to run.  The codes are unpacked once a unit and
+// A group is one (sequence, KV head).  Its units (two 16-row tiles; with more than one tile
+// of query rows a single one) go round the block's warps, each with a ring of asynchronous
+// copies of its own, and a warp takes a unit against all query rows: a position's sum has one
+// writer and one order, so there is nothing to join and results do not vary from run to run.
+// The codes are unpacked once a unit and
 // the query rows' operands read once for both tiles.  The pages of all groups, laid end to end,
 // are cut into equal runs, a block each.
 #include "hyq_paged.cuh"
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 1) mass_kernel(const Params p)
     if (x1 <= kCost) continue;
     const int len = s_len[lo], fresh = len - (p.n_new ? p.n_new[lo] : p.n_q);
     const int32_t* table = p.pv.table + (size_t)s_seq[lo] * p.pv.max_blocks;
-    // ---- this warp's units: half page u0, u0 + n_warps, ..; their pages 32 ahead --------
+    // ---- this warp's units of kRows positions: u0, u0 + n_warps, ..; their pages 32 ahead --------
     const int u0 = kPer * max(0, x0 - kCost) + warp, u1 = min(kPer * (x1 - kCost), (len + kRows - 1) / kRows);
     const int nj = u1 > u0 ? (u1 - u0 + n_warps - 1) / n_warps : 0;
     auto page_of = [&](int j) -> int {  // of unit j, or -1 for one that is left out
